@@ -69,6 +69,8 @@ typedef struct CUstream_st *kpool_stream_t;
 /* Device status word bits (kpool_read_status). */
 #define KPOOL_STATUS_TIMEOUT 1      /* a pipeline wait gave up; results invalid */
 #define KPOOL_STATUS_BAD_SEQLENS 2  /* cu_seqlens not 0..T non-decreasing */
+#define KPOOL_STATUS_BAD_PAGE 4     /* a sequence, page, length or count out of range */
+#define KPOOL_STATUS_NO_PAGES 8     /* too few free pages: the pool is unchanged */
 
 /* Message for the last failing call on this host thread ("" if none). */
 KPOOL_API const char *kpool_last_error(void);
@@ -454,6 +456,173 @@ KPOOL_API int kpool_sparse_mla_fwd_pools_at(const void *q, const void *kv, const
                                             float softmax_scale, void *o_out, float *lse_out,
                                             void *workspace, size_t workspace_bytes,
                                             kpool_stream_t stream);
+
+/*
+ * Paged cache.  A store keeps the cached rows of tokens in pages; sequences
+ * list their pages, and sequences forked from one parent list the same whole
+ * pages.  (The pages have no counterpart in the sources: a rollout, as in
+ * SkyRL PR "GLM-5.3-Flash (glm5_next) Megatron support", samples several
+ * answers to one prompt, and their caches share the prompt's pages.)
+ *
+ * kpool_page_pool -- which pages the sequences hold.  Device arrays of the
+ * caller, int32, 4-byte aligned:
+ *   page_table [n_seqs, max_pages]   entry j of row s is the page of the tokens
+ *                 j * page_size .. (j + 1) * page_size - 1 of sequence s;
+ *                 entries behind its length mean nothing
+ *   seq_lens [n_seqs]                tokens of each sequence (0 = none held)
+ *   ref_count [n_pages]              sequences that hold the page
+ *   free_list [n_pages], free_count [1]   the first free_count entries are the
+ *                 unreferenced pages; allocation takes the last of them first
+ * page_size tokens fill a page; max_pages <= 2^20, (max_pages + 1) * page_size
+ * < 2^31.
+ *
+ * kpool_page_store -- the rows of one kind, in every layer: row r of page p of
+ * layer l at data + l * layer_stride + p * page_stride + r * row_bytes (strides
+ * in bytes; address, strides and row_bytes multiples of 16).  rows_per_page is
+ * page_size for latents, page_size / kpool for pooled keys, and divides
+ * page_size.
+ *
+ * Conventions of the calls that change a pool: they check the whole list on
+ * the device first.  A sequence or page id out of range or listed twice, a
+ * negative count, a length that the table has no room for, or free_count
+ * outside 0..n_pages sets KPOOL_STATUS_BAD_PAGE; too few free pages set
+ * KPOOL_STATUS_NO_PAGES.  Either way the call changes nothing.  Page ids out of
+ * range inside the used part of a page-table row are skipped, with
+ * KPOOL_STATUS_BAD_PAGE.  No id is followed out of its array.  Calls on one
+ * pool are ordered by the caller (one stream, or events).
+ * workspace: kpool_pages_workspace_size(n, n_seqs, n_pages) bytes, n the
+ * listed items (0 for kpool_pages_compact), 256-byte aligned; its status word
+ * belongs to the last call that used it.
+ */
+#define KPOOL_MAX_STORES 8
+typedef struct kpool_page_pool {
+    int32_t *page_table, *seq_lens, *ref_count, *free_list, *free_count;
+    int32_t n_seqs, max_pages, n_pages, page_size;
+} kpool_page_pool;
+typedef struct kpool_page_store {
+    void *data;
+    int64_t layer_stride, page_stride;
+    int32_t n_layers, rows_per_page, row_bytes, reserved;
+} kpool_page_store;
+
+/* 0 for sizes out of range. */
+KPOOL_API size_t kpool_pages_workspace_size(int64_t n, int n_seqs, int n_pages);
+
+/*
+ * kpool_pages_copy -- page dst[i] becomes a copy of page src[i], in every store
+ * and layer (contents only: no table or count changes).  A source may be
+ * listed several times; a destination listed twice, or also as a source, is
+ * refused (KPOOL_STATUS_BAD_PAGE, nothing copied).
+ */
+KPOOL_API int kpool_pages_copy(const int32_t *src, const int32_t *dst, int64_t n, int n_pages,
+                               const kpool_page_store *stores, int n_stores, void *workspace,
+                               size_t workspace_bytes, kpool_stream_t stream);
+
+/*
+ * kpool_pages_fork -- sequence children[i], which must hold nothing, becomes a
+ * copy of sequence parents[i]: it lists the parent's whole pages (one more
+ * reference each), and the rows that the parent uses of a last, partial page
+ * are copied to a page of the child's own, popped from the free pages in list
+ * order.  A parent may have several children; parents are read as they were
+ * before the call.
+ */
+KPOOL_API int kpool_pages_fork(const kpool_page_pool *pool, const int32_t *parents,
+                               const int32_t *children, int64_t n, const kpool_page_store *stores,
+                               int n_stores, void *workspace, size_t workspace_bytes,
+                               kpool_stream_t stream);
+
+/*
+ * kpool_pages_extend -- sequence seqs[i] grows by n_new[i] >= 0 tokens; the
+ * pages that it lacks are popped from the free pages in list order.
+ * begin_out[i] (int32 [n]) gets its length before the call, or -1 everywhere
+ * when the call is refused.  A sequence whose last, partial page is held by
+ * others as well is refused (KPOOL_STATUS_BAD_PAGE): fork copies such pages.
+ */
+KPOOL_API int kpool_pages_extend(const kpool_page_pool *pool, const int32_t *seqs,
+                                 const int32_t *n_new, int64_t n, int32_t *begin_out,
+                                 void *workspace, size_t workspace_bytes, kpool_stream_t stream);
+
+/*
+ * kpool_pages_write -- rows cu_rows[i] .. cu_rows[i + 1] - 1 of `rows` go to the
+ * rows begin[i], begin[i] + 1, ... of sequence seqs[i] in the store (for
+ * latents the token positions that kpool_pages_extend returned).
+ *   rows   [n_layers, total, row_bytes]: layer l at rows + l * rows_layer_stride
+ *          bytes, 16-byte aligned
+ *   cu_rows  int32 [n + 1]
+ * A row outside its sequence's length (rows_per_page of every page_size
+ * tokens), in a page that other sequences hold too, or with no sequence to go
+ * to is left out, with KPOOL_STATUS_BAD_PAGE.  Rows that go to one place twice
+ * leave either.
+ */
+KPOOL_API int kpool_pages_write(const kpool_page_pool *pool, const int32_t *seqs,
+                                const int32_t *begin, const int32_t *cu_rows, int64_t n,
+                                int64_t total, const void *rows, int64_t rows_layer_stride,
+                                const kpool_page_store *store, void *workspace,
+                                size_t workspace_bytes, kpool_stream_t stream);
+
+/*
+ * kpool_pages_free -- the listed sequences give up their pages: their table
+ * entries become -1, their lengths 0, and the pages that nobody holds any more
+ * are pushed on the free list in ascending order.
+ */
+KPOOL_API int kpool_pages_free(const kpool_page_pool *pool, const int32_t *seqs, int64_t n,
+                               void *workspace, size_t workspace_bytes, kpool_stream_t stream);
+
+/*
+ * kpool_pages_compact -- with k pages referenced, moves them to the pages
+ * 0 .. k - 1: the i-th referenced page at or above k to the i-th unreferenced
+ * page below k, in every store and layer, and rewrites the page tables and
+ * counts.  The free list becomes n_pages - 1 .. k (so that k is taken first).
+ * What the pages at or above k hold afterwards means nothing.
+ */
+KPOOL_API int kpool_pages_compact(const kpool_page_pool *pool, const kpool_page_store *stores,
+                                  int n_stores, void *workspace, size_t workspace_bytes,
+                                  kpool_stream_t stream);
+
+/*
+ * kpool_shared_prefix_mla_fwd -- attention over a paged cache for a batch whose
+ * sequences share prefixes, in the absorbed latent form of
+ * kpool_sparse_mla_fwd, over all of a query's tokens instead of a selection.
+ * The shared tokens of a group are read and multiplied once for all of its
+ * queries.  For row (t, h), query t of sequence b being the i-th of its n_q:
+ *     J(t)       = tokens 0 .. len_b - n_q + i of sequence b
+ *     s_j        = softmax_scale * sum_d q[t, h, d] * kv_b[j, d]   (FP32)
+ *     o[t, h, :] = sum_j softmax_j(s) kv_b[j, :]                    (BF16 out)
+ *     lse[t, h]  = ln sum_j exp(s_j)                                (FP32 out)
+ * (the queries are the sequence's last tokens, already in the cache); a row
+ * with no token gets o = 0 and lse = -inf.  Softmax weights are rounded to
+ * BF16 before they multiply kv; sums and statistics are FP32.
+ *   q            bf16 [Tq, H, Dc], 16-byte aligned
+ *   kv           bf16 [n_pages, page_size, Dc], pages kv_page_stride elements
+ *                apart (a multiple of 8, >= page_size * Dc); 16-byte aligned
+ *   page_table   int32 [n_rows, max_pages], seq_lens int32 [n_rows], as in
+ *                kpool_page_pool
+ *   seq_ids      int32 [B]: the table row of each sequence of the batch, or
+ *                NULL for rows 0 .. B - 1 (then n_rows >= B)
+ *   cu_seqlens_q int32 [B + 1]: the query rows of each sequence (any number)
+ *   cu_groups    int32 [G + 1]: sequences cu_groups[g] .. cu_groups[g+1] - 1
+ *                share their first prefix_lens[g] tokens, which are read
+ *                through the group's first sequence (a length above a
+ *                sequence's own is cut to it; 0 = nothing shared)
+ *   workspace    kpool_shared_prefix_mla_workspace_size(Tq, H, B, G) bytes,
+ *                256-byte aligned
+ * Cached values at positions below a sequence's length must be finite; what
+ * pages hold behind it is not read into any result.
+ * Device status: KPOOL_STATUS_BAD_SEQLENS when cu_seqlens_q or cu_groups is
+ * not 0 .. Tq or 0 .. B non-decreasing (nothing is written);
+ * KPOOL_STATUS_BAD_PAGE when a table row, length or page id that the call uses
+ * is out of range (results of the rows that use it are not valid; a length is
+ * cut to its table's room); KPOOL_STATUS_TIMEOUT as for the sparse attention.
+ * Supported: 1 <= H <= 128, Dc = 512, page_size 16, 32, 64 or 128
+ * (UNSUPPORTED otherwise); softmax_scale finite and > 0.
+ */
+KPOOL_API size_t kpool_shared_prefix_mla_workspace_size(int64_t Tq, int H, int B, int G);
+KPOOL_API int kpool_shared_prefix_mla_fwd(
+    const void *q, const void *kv, int64_t kv_page_stride, int n_pages, int page_size,
+    const int32_t *page_table, const int32_t *seq_lens, int n_rows, int max_pages,
+    const int32_t *seq_ids, const int32_t *cu_seqlens_q, int B, const int32_t *cu_groups,
+    const int32_t *prefix_lens, int G, int64_t Tq, int H, int Dc, float softmax_scale,
+    void *o_out, float *lse_out, void *workspace, size_t workspace_bytes, kpool_stream_t stream);
 
 /*
  * kpool_read_status -- debug helper: synchronously copy the device status

@@ -11,8 +11,9 @@ __version__ = "1.0.0"
 
 
 def __getattr__(name):
-    if name.startswith("kpool_") or name in ("KPoolError", "new_workspace", "LIB_PATH",
-                                             "STATUS_TIMEOUT", "STATUS_BAD_SEQLENS"):
+    if name.startswith("kpool_") or name in ("KPoolError", "KPoolPages", "new_workspace",
+                                             "LIB_PATH", "STATUS_TIMEOUT", "STATUS_BAD_SEQLENS",
+                                             "STATUS_BAD_PAGE", "STATUS_NO_PAGES"):
         mod = importlib.import_module(".binding", __name__)
         return getattr(mod, name)
     raise AttributeError(name)

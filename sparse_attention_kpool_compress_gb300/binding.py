@@ -63,6 +63,16 @@ _SIGS = {
                                         ctypes.c_float, _P, _P, _P, _SZ, _P]),
     "kpool_sparse_mla_fwd_pools_at": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _L, _L, _I, _I, _I,
                                            _I, _I, ctypes.c_float, _P, _P, _P, _SZ, _P]),
+    "kpool_pages_workspace_size": (_SZ, [_L, _I, _I]),
+    "kpool_pages_copy": (_I, [_P, _P, _L, _I, _P, _I, _P, _SZ, _P]),
+    "kpool_pages_fork": (_I, [_P, _P, _P, _L, _P, _I, _P, _SZ, _P]),
+    "kpool_pages_extend": (_I, [_P, _P, _P, _L, _P, _P, _SZ, _P]),
+    "kpool_pages_write": (_I, [_P, _P, _P, _P, _L, _L, _P, _L, _P, _P, _SZ, _P]),
+    "kpool_pages_free": (_I, [_P, _P, _L, _P, _SZ, _P]),
+    "kpool_pages_compact": (_I, [_P, _P, _I, _P, _SZ, _P]),
+    "kpool_shared_prefix_mla_workspace_size": (_SZ, [_L, _I, _I, _I]),
+    "kpool_shared_prefix_mla_fwd": (_I, [_P, _P, _L, _I, _I, _P, _P, _I, _I, _P, _P, _I, _P, _P,
+                                         _I, _L, _I, _I, ctypes.c_float, _P, _P, _P, _SZ, _P]),
     "kpool_read_status": (_I, [_P, _P]),
     "kpool_score_topk_noalloc_status": (_I, [_P]),
     "kpool_debug_set_wait_limit_ns": (ctypes.c_uint64, [ctypes.c_uint64]),
@@ -77,6 +87,8 @@ for _name, (_res, _args) in _SIGS.items():
 
 STATUS_TIMEOUT = 1
 STATUS_BAD_SEQLENS = 2
+STATUS_BAD_PAGE = 4
+STATUS_NO_PAGES = 8
 
 
 class KPoolError(RuntimeError):
@@ -443,6 +455,296 @@ def kpool_sparse_mla_fwd_pools_at(q, kv, pool_idx, kpool: int, index_topk: int,
     return o, lse
 
 
+# ---- paged cache ------------------------------------------------------------
+
+class _Pool(ctypes.Structure):
+    _fields_ = [("page_table", _P), ("seq_lens", _P), ("ref_count", _P), ("free_list", _P),
+                ("free_count", _P), ("n_seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32)]
+
+
+class _Store(ctypes.Structure):
+    _fields_ = [("data", _P), ("layer_stride", _L), ("page_stride", _L),
+                ("n_layers", ctypes.c_int32), ("rows_per_page", ctypes.c_int32),
+                ("row_bytes", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class _on(object):
+    """Makes a device the current one for a call, when it is not already."""
+
+    def __init__(self, device):
+        self.index = device.index
+        self.before = None
+
+    def __enter__(self):
+        now = torch.cuda.current_device()
+        if self.index is not None and now != self.index:
+            self.before = now
+            torch.cuda.set_device(self.index)
+
+    def __exit__(self, *exc):
+        if self.before is not None:
+            torch.cuda.set_device(self.before)
+
+
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError("%s is on %s, not on %s" % (name, t.device, device))
+
+
+class KPoolPages:
+    """Which pages the sequences of a paged cache hold: page_table int32
+    [n_seqs, max_pages], seq_lens [n_seqs], ref_count [n_pages], free_list
+    [n_pages] and free_count [1], CUDA tensors of one device that the
+    kpool_pages_* calls read and change in place (include/kpool.h,
+    kpool_page_pool).  kpool_pages_new makes an empty one."""
+
+    __slots__ = ("page_table", "seq_lens", "ref_count", "free_list", "free_count", "page_size",
+                 "device", "_c")
+
+    def __init__(self, page_table, seq_lens, ref_count, free_list, free_count, page_size: int):
+        arrays = dict(page_table=page_table, seq_lens=seq_lens, ref_count=ref_count,
+                      free_list=free_list, free_count=free_count)
+        for name, t in arrays.items():
+            _need(t, name, torch.int32)
+        _same_device(page_table.device, **arrays)
+        if page_table.dim() != 2 or seq_lens.numel() != page_table.shape[0]:
+            raise ValueError("page_table must be [n_seqs, max_pages] and seq_lens [n_seqs]")
+        if ref_count.numel() != free_list.numel() or free_count.numel() != 1:
+            raise ValueError("ref_count and free_list must be [n_pages] and free_count [1]")
+        page_size = int(page_size)
+        if page_size < 1:
+            raise ValueError("page_size must be >= 1")
+        put = super().__setattr__
+        for name, t in arrays.items():
+            put(name, t)
+        put("page_size", page_size)
+        put("device", page_table.device)
+        put("_c", _Pool(page_table.data_ptr(), seq_lens.data_ptr(), ref_count.data_ptr(),
+                        free_list.data_ptr(), free_count.data_ptr(), page_table.shape[0],
+                        page_table.shape[1], ref_count.numel(), page_size))
+
+    def __setattr__(self, name, value):
+        raise AttributeError("a KPoolPages keeps its tensors: make another one")
+
+    @property
+    def n_seqs(self) -> int:
+        return self._c.n_seqs
+
+    @property
+    def n_pages(self) -> int:
+        return self._c.n_pages
+
+
+def kpool_pages_new(n_seqs: int, n_pages: int, max_pages: int, page_size: int,
+                    device="cuda") -> KPoolPages:
+    """An empty pool: every page free (page 0 is taken first), no sequence
+    holding any."""
+    kw = dict(dtype=torch.int32, device=device)
+    return KPoolPages(torch.full((n_seqs, max_pages), -1, **kw), torch.zeros(n_seqs, **kw),
+                      torch.zeros(n_pages, **kw), torch.arange(n_pages - 1, -1, -1, **kw),
+                      torch.full((1,), n_pages, **kw), page_size)
+
+
+def _stores(stores, n_pages, device):
+    """(C array, count) of stores: tensors [layers, n_pages, rows, width] or
+    [n_pages, rows, width] whose pages are contiguous.  A strided view of either order
+    of layers and pages will do."""
+    if isinstance(stores, torch.Tensor):
+        stores = (stores,)
+    out = (_Store * max(1, len(stores)))()
+    for i, t in enumerate(stores):
+        if not t.is_cuda:
+            raise ValueError("a store must be a CUDA tensor")
+        if t.device != device:
+            raise ValueError("a store is on %s, not on %s" % (t.device, device))
+        dim = t.dim()
+        if dim not in (3, 4):
+            raise ValueError("a store is [layers, n_pages, rows, width] or [n_pages, rows, width]")
+        shape, stride = t.shape, t.stride()
+        rows, width = shape[-2], shape[-1]
+        if shape[-3] != n_pages:
+            raise ValueError("a store has %d pages, not %d" % (shape[-3], n_pages))
+        if (width > 1 and stride[-1] != 1) or (rows > 1 and stride[-2] != width):
+            raise ValueError("the rows of a store's page must be contiguous")
+        size = t.element_size()
+        s = out[i]
+        s.data = t.data_ptr()
+        s.n_layers = shape[0] if dim == 4 else 1
+        s.layer_stride = stride[0] * size if dim == 4 else 0
+        s.page_stride = stride[-3] * size
+        s.rows_per_page = rows
+        s.row_bytes = width * size
+    return out, len(stores)
+
+
+def kpool_pages_workspace_size(n: int, n_seqs: int, n_pages: int) -> int:
+    return int(_lib.kpool_pages_workspace_size(n, n_seqs, n_pages))
+
+
+def _pages_workspace(workspace, n, n_seqs, n_pages, device):
+    if workspace is None:
+        return torch.empty(max(256, _lib.kpool_pages_workspace_size(n, n_seqs, n_pages)),
+                           dtype=torch.uint8, device=device)
+    _need(workspace, "workspace", torch.uint8)
+    _same_device(device, workspace=workspace)
+    return workspace
+
+
+def _lists(device, n, **lists):
+    for name, t in lists.items():
+        _need(t, name, torch.int32)
+        if t.numel() != n:
+            raise ValueError("%s must have %d entries (got %d)" % (name, n, t.numel()))
+    _same_device(device, **lists)
+
+
+def kpool_pages_copy(src, dst, stores, workspace=None):
+    """Page dst[i] becomes a copy of page src[i] in every store and layer."""
+    if isinstance(stores, torch.Tensor):
+        stores = (stores,)
+    if not stores:
+        raise ValueError("a store is required")
+    dev, n, n_pages = src.device, src.numel(), stores[0].shape[-3]
+    _lists(dev, n, src=src, dst=dst)
+    st, n_stores = _stores(stores, n_pages, dev)
+    workspace = _pages_workspace(workspace, n, 0, n_pages, dev)
+    with _on(dev):
+        _check(_lib.kpool_pages_copy(_ptr(src), _ptr(dst), n, n_pages, st, n_stores,
+                                     _ptr(workspace), workspace.numel(), _stream(dev)),
+               "kpool_pages_copy")
+
+
+def kpool_pages_fork(pages: KPoolPages, parents, children, stores=(), workspace=None):
+    """Sequence children[i], which holds nothing, becomes a copy of sequence
+    parents[i]: whole pages are shared, a partial last page is copied."""
+    dev, n, c = pages.device, parents.numel(), pages._c
+    _lists(dev, n, parents=parents, children=children)
+    st, n_stores = _stores(stores, c.n_pages, dev)
+    workspace = _pages_workspace(workspace, n, c.n_seqs, c.n_pages, dev)
+    with _on(dev):
+        _check(_lib.kpool_pages_fork(ctypes.byref(c), _ptr(parents), _ptr(children), n, st,
+                                     n_stores, _ptr(workspace), workspace.numel(), _stream(dev)),
+               "kpool_pages_fork")
+
+
+def kpool_pages_extend(pages: KPoolPages, seqs, n_new, workspace=None, out=None):
+    """Sequence seqs[i] grows by n_new[i] tokens -> its length before, int32
+    [n] (-1 everywhere when the call is refused)."""
+    dev, n, c = pages.device, seqs.numel(), pages._c
+    begin = torch.empty(n, dtype=torch.int32, device=dev) if out is None else out
+    _lists(dev, n, seqs=seqs, n_new=n_new, out=begin)
+    workspace = _pages_workspace(workspace, n, c.n_seqs, c.n_pages, dev)
+    with _on(dev):
+        _check(_lib.kpool_pages_extend(ctypes.byref(c), _ptr(seqs), _ptr(n_new), n, _ptr(begin),
+                                       _ptr(workspace), workspace.numel(), _stream(dev)),
+               "kpool_pages_extend")
+    return begin
+
+
+def kpool_pages_write(pages: KPoolPages, seqs, begin, cu_rows, rows, store, workspace=None):
+    """Rows cu_rows[i] .. cu_rows[i+1] - 1 of `rows` ([layers, total, width], or
+    [total, width] for one layer) go to the rows begin[i], begin[i] + 1, ... of
+    sequence seqs[i] in `store`."""
+    dev, n, c = pages.device, seqs.numel(), pages._c
+    _lists(dev, n, seqs=seqs, begin=begin)
+    _lists(dev, n + 1, cu_rows=cu_rows)
+    _need(rows, "rows", store.dtype)
+    _same_device(dev, rows=rows)
+    st, _ = _stores((store,), c.n_pages, dev)
+    g = st[0]
+    total, width = rows.shape[-2], rows.shape[-1]
+    if rows.dim() not in (2, 3) or (rows.shape[0] if rows.dim() == 3 else 1) != g.n_layers:
+        raise ValueError("rows must be [layers, total, width] of the store's %d layers" % g.n_layers)
+    if width != store.shape[-1]:
+        raise ValueError("rows are %d wide, the store's %d" % (width, store.shape[-1]))
+    workspace = _pages_workspace(workspace, n, c.n_seqs, c.n_pages, dev)
+    with _on(dev):
+        _check(_lib.kpool_pages_write(ctypes.byref(c), _ptr(seqs), _ptr(begin), _ptr(cu_rows), n,
+                                      total, _ptr(rows), total * g.row_bytes, st,
+                                      _ptr(workspace), workspace.numel(), _stream(dev)),
+               "kpool_pages_write")
+
+
+def kpool_pages_free(pages: KPoolPages, seqs, workspace=None):
+    """The listed sequences give up their pages."""
+    dev, n, c = pages.device, seqs.numel(), pages._c
+    _lists(dev, n, seqs=seqs)
+    workspace = _pages_workspace(workspace, n, c.n_seqs, c.n_pages, dev)
+    with _on(dev):
+        _check(_lib.kpool_pages_free(ctypes.byref(c), _ptr(seqs), n, _ptr(workspace),
+                                     workspace.numel(), _stream(dev)), "kpool_pages_free")
+
+
+def kpool_pages_compact(pages: KPoolPages, stores=(), workspace=None):
+    """The k referenced pages move to the pages 0 .. k - 1, in every store."""
+    dev, c = pages.device, pages._c
+    st, n_stores = _stores(stores, c.n_pages, dev)
+    workspace = _pages_workspace(workspace, 0, c.n_seqs, c.n_pages, dev)
+    with _on(dev):
+        _check(_lib.kpool_pages_compact(ctypes.byref(c), st, n_stores, _ptr(workspace),
+                                        workspace.numel(), _stream(dev)), "kpool_pages_compact")
+
+
+def kpool_shared_prefix_mla_workspace_size(Tq: int, H: int, B: int, G: int) -> int:
+    return int(_lib.kpool_shared_prefix_mla_workspace_size(Tq, H, B, G))
+
+
+def kpool_shared_prefix_mla_fwd(q, kv, page_table, seq_lens, cu_seqlens_q, cu_groups, prefix_lens,
+                                softmax_scale: float, seq_ids=None, workspace=None, o=None,
+                                lse=None):
+    """Attention over a paged latent cache for groups of sequences that share
+    a prefix, read and multiplied once per group: q bf16 [Tq, H, 512], kv bf16
+    [n_pages, page_size, 512] (one layer of a store) -> (o bf16 [Tq, H, 512],
+    lse fp32 [Tq, H]).  A sequence's queries are its last tokens."""
+    dev = q.device
+    _need(q, "q", torch.bfloat16)
+    for t_, n_ in ((page_table, "page_table"), (seq_lens, "seq_lens"),
+                   (cu_seqlens_q, "cu_seqlens_q"), (cu_groups, "cu_groups"),
+                   (prefix_lens, "prefix_lens"), (seq_ids, "seq_ids")):
+        _need(t_, n_, torch.int32)
+    if kv.dtype != torch.bfloat16:
+        raise TypeError("kv must be %s (got %s)" % (torch.bfloat16, kv.dtype))
+    _same_device(dev, kv=kv, page_table=page_table, seq_lens=seq_lens, cu_seqlens_q=cu_seqlens_q,
+                 cu_groups=cu_groups, prefix_lens=prefix_lens, seq_ids=seq_ids, o=o, lse=lse,
+                 workspace=workspace)
+    n_pages, page_size, Dc = kv.shape
+    if kv.stride(2) != 1 or kv.stride(1) != Dc:
+        raise ValueError("the rows of a page of kv must be contiguous")
+    Tq, H, D = q.shape
+    if D != Dc:
+        raise ValueError("q is %d wide, kv %d" % (D, Dc))
+    if page_table.dim() != 2 or seq_lens.numel() != page_table.shape[0]:
+        raise ValueError("page_table must be [n_rows, max_pages] and seq_lens [n_rows]")
+    B, G = cu_seqlens_q.numel() - 1, cu_groups.numel() - 1
+    if prefix_lens.numel() != G or (seq_ids is not None and seq_ids.numel() != B):
+        raise ValueError("prefix_lens must have one entry per group and seq_ids one per sequence")
+    if o is None:
+        o = torch.empty(Tq, H, Dc, dtype=torch.bfloat16, device=dev)
+    else:
+        _need(o, "o", torch.bfloat16)
+    if lse is None:
+        lse = torch.empty(Tq, H, dtype=torch.float32, device=dev)
+    else:
+        _need(lse, "lse", torch.float32)
+    if o.shape != q.shape or lse.numel() != Tq * H:
+        raise ValueError("o must be shaped like q and lse [Tq, H]")
+    if workspace is None:
+        workspace = torch.empty(max(256, kpool_shared_prefix_mla_workspace_size(Tq, H, B, G)),
+                                dtype=torch.uint8, device=dev)
+    # (the stride of a single page says nothing)
+    stride = kv.stride(0) if n_pages > 1 else page_size * Dc
+    with _on(dev):
+        _check(_lib.kpool_shared_prefix_mla_fwd(
+            _ptr(q), _ptr(kv), stride, n_pages, page_size, _ptr(page_table), _ptr(seq_lens),
+            page_table.shape[0], page_table.shape[1], _ptr(seq_ids), _ptr(cu_seqlens_q), B,
+            _ptr(cu_groups), _ptr(prefix_lens), G, Tq, H, Dc, float(softmax_scale), _ptr(o),
+            _ptr(lse), _ptr(workspace), workspace.numel(), _stream(dev)),
+            "kpool_shared_prefix_mla_fwd")
+    return o, lse
+
+
 def _host_cu(cu_seqlens_host):
     if cu_seqlens_host is None:
         return None, 1
@@ -533,5 +835,5 @@ def kpool_indexer_forward(q, k, gate, ape, w, kpool: int, index_topk: int,
     return tok, idx, sc
 
 
-__all__ = [n for n in dir() if n.startswith("kpool_")] + ["KPoolError", "new_workspace",
-                                                           "LIB_PATH"]
+__all__ = [n for n in dir() if n.startswith("kpool_")] + ["KPoolError", "KPoolPages",
+                                                           "new_workspace", "LIB_PATH"]

@@ -3,6 +3,7 @@
 // contract of every entry point.
 #include <cstdarg>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <string>
 #include <vector>
@@ -101,6 +102,81 @@ int check_mla_args(const void *q, const void *kv, int64_t T, int64_t Tk, int H, 
     if (!workspace || workspace_bytes < sparse_mla_workspace_bytes() || !aligned(workspace, 256))
         return fail(KPOOL_ERR_WORKSPACE, "workspace of at least %zu bytes, 256-byte aligned, needed",
                     sparse_mla_workspace_bytes());
+    return KPOOL_OK;
+}
+
+// ---- paged cache -----------------------------------------------------------
+int check_pool(const kpool_page_pool *p)
+{
+    if (!p) return fail(KPOOL_ERR_INVALID_ARG, "pool is required");
+    if (p->n_seqs < 1 || p->n_pages < 1 || p->max_pages < 1 || p->page_size < 1)
+        return fail(KPOOL_ERR_INVALID_ARG, "n_seqs, n_pages, max_pages and page_size must be >= 1");
+    if ((static_cast<int64_t>(p->max_pages) + 1) * p->page_size > 0x7FFFFFFFLL || p->max_pages > (1 << 20))
+        return fail(KPOOL_ERR_INVALID_ARG, "max_pages must be <= 2^20 and (max_pages + 1) * page_size < 2^31");
+    if (p->n_pages > (1 << 28) || p->n_seqs > (1 << 28))
+        return fail(KPOOL_ERR_INVALID_ARG, "n_pages and n_seqs must be <= 2^28");
+    if (!p->page_table || !p->seq_lens || !p->ref_count || !p->free_list || !p->free_count)
+        return fail(KPOOL_ERR_INVALID_ARG, "the pool's five arrays are required");
+    if (!aligned(p->page_table, 4) || !aligned(p->seq_lens, 4) || !aligned(p->ref_count, 4) ||
+        !aligned(p->free_list, 4) || !aligned(p->free_count, 4))
+        return fail(KPOOL_ERR_INVALID_ARG, "the pool's arrays must be 4-byte aligned");
+    return KPOOL_OK;
+}
+
+// page_size 0: not known to the call.
+int check_stores(const kpool_page_store *st, int n, int n_pages, int page_size)
+{
+    if (n < 0 || n > KPOOL_MAX_STORES)
+        return fail(KPOOL_ERR_INVALID_ARG, "n_stores must be 0 .. %d", KPOOL_MAX_STORES);
+    if (n > 0 && !st) return fail(KPOOL_ERR_INVALID_ARG, "stores are required");
+    for (int i = 0; i < n; ++i) {
+        const kpool_page_store &g = st[i];
+        if (!g.data) return fail(KPOOL_ERR_INVALID_ARG, "store %d has no data", i);
+        if (g.n_layers < 1 || g.rows_per_page < 1 || g.row_bytes < 16)
+            return fail(KPOOL_ERR_INVALID_ARG, "store %d: n_layers, rows_per_page >= 1 and row_bytes >= 16 needed", i);
+        if (page_size > 0 && (g.rows_per_page > page_size || page_size % g.rows_per_page != 0))
+            return fail(KPOOL_ERR_INVALID_ARG, "store %d: rows_per_page must divide page_size", i);
+        if (!aligned(g.data, 16) || g.layer_stride % 16 != 0 || g.page_stride % 16 != 0 || g.row_bytes % 16 != 0)
+            return fail(KPOOL_ERR_INVALID_ARG, "store %d: address, strides and row_bytes must be multiples of 16", i);
+        const int64_t page = static_cast<int64_t>(g.rows_per_page) * g.row_bytes;
+        if (page > (int64_t(1) << 30) || g.n_layers > 4096)
+            return fail(KPOOL_ERR_INVALID_ARG, "store %d: pages of at most 2^30 bytes in at most 4096 layers", i);
+        if (g.layer_stride < 0 || g.page_stride < 0 || g.layer_stride > (int64_t(1) << 46) ||
+            g.page_stride > (int64_t(1) << 40))
+            return fail(KPOOL_ERR_INVALID_ARG, "store %d: strides out of range", i);
+        // pages within layers, or layers within pages; no two pages overlap
+        const bool pages_in = (n_pages == 1 || g.page_stride >= page) &&
+                              (g.n_layers == 1 || g.layer_stride >= (n_pages - 1) * g.page_stride + page);
+        const bool layers_in = (g.n_layers == 1 || g.layer_stride >= page) &&
+                               (n_pages == 1 || g.page_stride >= (g.n_layers - 1) * g.layer_stride + page);
+        if (!pages_in && !layers_in) return fail(KPOOL_ERR_INVALID_ARG, "store %d: its pages overlap", i);
+    }
+    return KPOOL_OK;
+}
+
+int check_pages_workspace(const void *ws, size_t bytes, int64_t n, int n_seqs, int n_pages)
+{
+    const size_t need = pages_workspace_bytes(n, n_seqs, n_pages);
+    if (!ws || bytes < need || !aligned(ws, 256))
+        return fail(KPOOL_ERR_WORKSPACE, "workspace of at least %zu bytes, 256-byte aligned, needed", need);
+    return KPOOL_OK;
+}
+
+// The list arguments of a call over n items, which are all int32 arrays.
+int check_items(int64_t n, std::initializer_list<const int32_t *> arrays)
+{
+    if (n < 0 || n > (1 << 28)) return fail(KPOOL_ERR_INVALID_ARG, "n out of range");
+    for (const int32_t *a : arrays) {
+        if (n > 0 && !a) return fail(KPOOL_ERR_INVALID_ARG, "a list of the call is missing");
+        if (!aligned(a, 4)) return fail(KPOOL_ERR_INVALID_ARG, "the lists must be 4-byte aligned");
+    }
+    return KPOOL_OK;
+}
+
+// A call without items: a clean status word and nothing else.
+int nothing_listed(void *ws, kpool_stream_t stream)
+{
+    KPOOL_CUDA_CHECK(cudaMemsetAsync(ws, 0, 16, reinterpret_cast<cudaStream_t>(stream)));
     return KPOOL_OK;
 }
 
@@ -693,6 +769,159 @@ int kpool_sparse_mla_fwd_pools_at(const void *q, const void *kv, const int32_t *
     a.kpool = kpool; a.Kp = index_topk / kpool; a.tail = always_select_tail ? 1 : 0;
     a.scale = softmax_scale; a.o = o_out; a.lse = lse_out; a.workspace = workspace;
     return run_sparse_mla(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t kpool_pages_workspace_size(int64_t n, int n_seqs, int n_pages)
+{
+    if (n < 0 || n > (1 << 28) || n_seqs < 0 || n_seqs > (1 << 28) || n_pages < 1 || n_pages > (1 << 28)) return 0;
+    return pages_workspace_bytes(n, n_seqs, n_pages);
+}
+
+int kpool_pages_copy(const int32_t *src, const int32_t *dst, int64_t n, int n_pages,
+                     const kpool_page_store *stores, int n_stores, void *workspace,
+                     size_t workspace_bytes, kpool_stream_t stream)
+{
+    clear_error();
+    KPOOL_NVTX_RANGE("kpool_pages_copy");
+    if (n_pages < 1 || n_pages > (1 << 28)) return fail(KPOOL_ERR_INVALID_ARG, "n_pages out of range");
+    int rc = check_items(n, {src, dst});
+    if (rc) return rc;
+    if ((rc = check_stores(stores, n_stores, n_pages, 0))) return rc;
+    if ((rc = check_pages_workspace(workspace, workspace_bytes, n, 0, n_pages))) return rc;
+    if (n == 0) return nothing_listed(workspace, stream);
+    return run_pages_copy(src, dst, static_cast<int>(n), n_pages, stores, n_stores, workspace,
+                          reinterpret_cast<cudaStream_t>(stream));
+}
+
+int kpool_pages_fork(const kpool_page_pool *pool, const int32_t *parents, const int32_t *children, int64_t n,
+                     const kpool_page_store *stores, int n_stores, void *workspace, size_t workspace_bytes,
+                     kpool_stream_t stream)
+{
+    clear_error();
+    KPOOL_NVTX_RANGE("kpool_pages_fork");
+    int rc = check_pool(pool);
+    if (rc) return rc;
+    if ((rc = check_items(n, {parents, children}))) return rc;
+    if ((rc = check_stores(stores, n_stores, pool->n_pages, pool->page_size))) return rc;
+    if ((rc = check_pages_workspace(workspace, workspace_bytes, n, pool->n_seqs, pool->n_pages))) return rc;
+    if (n == 0) return nothing_listed(workspace, stream);
+    return run_pages_fork(*pool, parents, children, static_cast<int>(n), stores, n_stores, workspace,
+                          reinterpret_cast<cudaStream_t>(stream));
+}
+
+int kpool_pages_extend(const kpool_page_pool *pool, const int32_t *seqs, const int32_t *n_new, int64_t n,
+                       int32_t *begin_out, void *workspace, size_t workspace_bytes, kpool_stream_t stream)
+{
+    clear_error();
+    KPOOL_NVTX_RANGE("kpool_pages_extend");
+    int rc = check_pool(pool);
+    if (rc) return rc;
+    if ((rc = check_items(n, {seqs, n_new, begin_out}))) return rc;
+    if ((rc = check_pages_workspace(workspace, workspace_bytes, n, pool->n_seqs, pool->n_pages))) return rc;
+    if (n == 0) return nothing_listed(workspace, stream);
+    return run_pages_extend(*pool, seqs, n_new, static_cast<int>(n), begin_out, workspace,
+                            reinterpret_cast<cudaStream_t>(stream));
+}
+
+int kpool_pages_write(const kpool_page_pool *pool, const int32_t *seqs, const int32_t *begin,
+                      const int32_t *cu_rows, int64_t n, int64_t total, const void *rows,
+                      int64_t rows_layer_stride, const kpool_page_store *store, void *workspace,
+                      size_t workspace_bytes, kpool_stream_t stream)
+{
+    clear_error();
+    KPOOL_NVTX_RANGE("kpool_pages_write");
+    int rc = check_pool(pool);
+    if (rc) return rc;
+    if ((rc = check_items(n, {seqs, begin, cu_rows}))) return rc;
+    if ((rc = check_stores(store, 1, pool->n_pages, pool->page_size))) return rc;
+    if (total < 0 || total > 0x7FFFFFFFLL) return fail(KPOOL_ERR_INVALID_ARG, "total out of range");
+    if (total > 0 && n == 0) return fail(KPOOL_ERR_INVALID_ARG, "rows without a sequence");
+    if (total > 0 && !rows) return fail(KPOOL_ERR_INVALID_ARG, "rows are required");
+    if (!aligned(rows, 16) || rows_layer_stride % 16 != 0)
+        return fail(KPOOL_ERR_INVALID_ARG, "rows must be 16-byte aligned in every layer");
+    if (rows_layer_stride < 0 || (store->n_layers > 1 && rows_layer_stride < total * store->row_bytes))
+        return fail(KPOOL_ERR_INVALID_ARG, "rows_layer_stride is less than a layer's rows");
+    if ((rc = check_pages_workspace(workspace, workspace_bytes, n, pool->n_seqs, pool->n_pages))) return rc;
+    return run_pages_write(*pool, seqs, begin, cu_rows, static_cast<int>(n), total, rows, rows_layer_stride, *store,
+                           workspace, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int kpool_pages_free(const kpool_page_pool *pool, const int32_t *seqs, int64_t n, void *workspace,
+                     size_t workspace_bytes, kpool_stream_t stream)
+{
+    clear_error();
+    KPOOL_NVTX_RANGE("kpool_pages_free");
+    int rc = check_pool(pool);
+    if (rc) return rc;
+    if ((rc = check_items(n, {seqs}))) return rc;
+    if ((rc = check_pages_workspace(workspace, workspace_bytes, n, pool->n_seqs, pool->n_pages))) return rc;
+    if (n == 0) return nothing_listed(workspace, stream);
+    return run_pages_free(*pool, seqs, static_cast<int>(n), workspace, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int kpool_pages_compact(const kpool_page_pool *pool, const kpool_page_store *stores, int n_stores, void *workspace,
+                        size_t workspace_bytes, kpool_stream_t stream)
+{
+    clear_error();
+    KPOOL_NVTX_RANGE("kpool_pages_compact");
+    int rc = check_pool(pool);
+    if (rc) return rc;
+    if ((rc = check_stores(stores, n_stores, pool->n_pages, pool->page_size))) return rc;
+    if ((rc = check_pages_workspace(workspace, workspace_bytes, 0, pool->n_seqs, pool->n_pages))) return rc;
+    return run_pages_compact(*pool, stores, n_stores, workspace, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t kpool_shared_prefix_mla_workspace_size(int64_t Tq, int H, int B, int G)
+{
+    if (Tq < 0 || H < 1 || H > 128 || Tq * H > 0x7FFFFFFFLL || B < 0 || B > (1 << 24) || G < 0 || G > (1 << 24))
+        return 0;
+    return prefix_mla_workspace_bytes(Tq, H, B, G);
+}
+
+int kpool_shared_prefix_mla_fwd(const void *q, const void *kv, int64_t kv_page_stride, int n_pages, int page_size,
+                                const int32_t *page_table, const int32_t *seq_lens, int n_rows, int max_pages,
+                                const int32_t *seq_ids, const int32_t *cu_seqlens_q, int B,
+                                const int32_t *cu_groups, const int32_t *prefix_lens, int G, int64_t Tq, int H,
+                                int Dc, float softmax_scale, void *o_out, float *lse_out, void *workspace,
+                                size_t workspace_bytes, kpool_stream_t stream)
+{
+    clear_error();
+    KPOOL_NVTX_RANGE("kpool_shared_prefix_mla_fwd");
+    if (H < 1 || H > 128 || Dc != 512)
+        return fail(KPOOL_ERR_UNSUPPORTED, "built for 1 <= H <= 128, Dc = 512 (got H = %d, Dc = %d)", H, Dc);
+    if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128)
+        return fail(KPOOL_ERR_UNSUPPORTED, "page_size must be 16, 32, 64 or 128 (got %d)", page_size);
+    if (Tq < 0 || Tq * H > 0x7FFFFFFFLL) return fail(KPOOL_ERR_INVALID_ARG, "Tq out of range");
+    if (B < 1 || B > (1 << 24) || G < 1 || G > (1 << 24))
+        return fail(KPOOL_ERR_INVALID_ARG, "B and G must be 1 .. 2^24");
+    if (n_rows < 1 || max_pages < 1 || max_pages > (1 << 20))
+        return fail(KPOOL_ERR_INVALID_ARG, "n_rows must be >= 1 and max_pages 1 .. 2^20");
+    if (!seq_ids && n_rows < B) return fail(KPOOL_ERR_INVALID_ARG, "without seq_ids, n_rows must be >= B");
+    if (n_pages < 1 || n_pages > (1 << 28)) return fail(KPOOL_ERR_INVALID_ARG, "n_pages out of range");
+    if (kv_page_stride < static_cast<int64_t>(page_size) * Dc || kv_page_stride % 8 != 0 ||
+        kv_page_stride >= (int64_t(1) << 39))
+        return fail(KPOOL_ERR_INVALID_ARG, "kv_page_stride must be a multiple of 8 of at least a page's elements");
+    if (!(softmax_scale > 0.f) || !std::isfinite(softmax_scale))
+        return fail(KPOOL_ERR_INVALID_ARG, "softmax_scale must be finite and > 0");
+    if (Tq > 0 && (!q || !o_out || !lse_out))
+        return fail(KPOOL_ERR_INVALID_ARG, "q, o_out and lse_out are required");
+    if (!kv || !page_table || !seq_lens || !cu_seqlens_q || !cu_groups || !prefix_lens)
+        return fail(KPOOL_ERR_INVALID_ARG,
+                    "kv, page_table, seq_lens, cu_seqlens_q, cu_groups and prefix_lens are required");
+    if (!aligned(q, 16) || !aligned(kv, 16) || !aligned(o_out, 16) || !aligned(lse_out, 4))
+        return fail(KPOOL_ERR_INVALID_ARG, "q, kv and o_out must be 16-byte aligned");
+    if (!aligned(page_table, 4) || !aligned(seq_lens, 4) || !aligned(seq_ids, 4) || !aligned(cu_seqlens_q, 4) ||
+        !aligned(cu_groups, 4) || !aligned(prefix_lens, 4))
+        return fail(KPOOL_ERR_INVALID_ARG, "index arrays must be 4-byte aligned");
+    const size_t need = prefix_mla_workspace_bytes(Tq, H, B, G);
+    if (!workspace || workspace_bytes < need || !aligned(workspace, 256))
+        return fail(KPOOL_ERR_WORKSPACE, "workspace of at least %zu bytes, 256-byte aligned, needed", need);
+    PrefixMlaArgs a{};
+    a.q = q; a.kv = kv; a.kv_page_stride = kv_page_stride; a.n_pages = n_pages; a.page_size = page_size;
+    a.page_table = page_table; a.seq_lens = seq_lens; a.n_rows = n_rows; a.max_pages = max_pages;
+    a.seq_ids = seq_ids; a.cu_q = cu_seqlens_q; a.B = B; a.cu_groups = cu_groups; a.prefix_lens = prefix_lens;
+    a.G = G; a.Tq = Tq; a.H = H; a.scale = softmax_scale; a.o = o_out; a.lse = lse_out; a.workspace = workspace;
+    return run_prefix_mla(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -144,6 +144,42 @@ struct SparseMlaArgs {
 size_t sparse_mla_workspace_bytes();
 int run_sparse_mla(const SparseMlaArgs &a, cudaStream_t s);
 
+// Paged cache (kpool_pages.cu); arguments are validated by the caller.
+size_t pages_workspace_bytes(int64_t n, int n_seqs, int n_pages);
+int run_pages_copy(const int32_t *src, const int32_t *dst, int n, int n_pages,
+                   const kpool_page_store *stores, int n_stores, void *ws, cudaStream_t s);
+int run_pages_fork(const kpool_page_pool &p, const int32_t *parents, const int32_t *children, int n,
+                   const kpool_page_store *stores, int n_stores, void *ws, cudaStream_t s);
+int run_pages_extend(const kpool_page_pool &p, const int32_t *seqs, const int32_t *n_new, int n,
+                     int32_t *begin, void *ws, cudaStream_t s);
+int run_pages_write(const kpool_page_pool &p, const int32_t *seqs, const int32_t *begin,
+                    const int32_t *cu_rows, int n, int64_t total, const void *rows,
+                    int64_t rows_layer_stride, const kpool_page_store &g, void *ws, cudaStream_t s);
+int run_pages_free(const kpool_page_pool &p, const int32_t *seqs, int n, void *ws, cudaStream_t s);
+int run_pages_compact(const kpool_page_pool &p, const kpool_page_store *stores, int n_stores, void *ws,
+                      cudaStream_t s);
+
+// Attention of a batch with shared prefixes over a paged cache (kpool_prefix_mla.cu).
+struct PrefixMlaArgs {
+    const void *q, *kv;                 // bf16 [Tq, H, 512], bf16 [n_pages, page_size, 512]
+    int64_t kv_page_stride;             // elements
+    int n_pages, page_size;
+    const int32_t *page_table, *seq_lens;
+    int n_rows, max_pages;
+    const int32_t *seq_ids, *cu_q;
+    int B;
+    const int32_t *cu_groups, *prefix_lens;
+    int G;
+    int64_t Tq;
+    int H;
+    float scale;
+    void *o;
+    float *lse;
+    void *workspace;
+};
+size_t prefix_mla_workspace_bytes(int64_t Tq, int H, int B, int G);
+int run_prefix_mla(const PrefixMlaArgs &a, cudaStream_t s);
+
 // Query tiles the fixed scratch of kpool_score_topk_noalloc can schedule.
 constexpr int kNoAllocMaxTiles = 131072;
 // Device address, size and tile capacity of the no-alloc scratch array of

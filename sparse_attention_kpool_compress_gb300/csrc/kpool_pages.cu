@@ -1,0 +1,679 @@
+// Upkeep of a paged cache: copying pages, forking, extending and freeing
+// sequences, writing rows, and compacting the pool.  include/kpool.h states
+// each call's contract.
+//
+// A page holds page_size tokens; a sequence's tokens lie in the pages that its
+// page-table row lists, and sequences forked from one parent list the same
+// whole pages (ref_count says how many do).  Free page ids form a stack
+// (free_list, free_count): allocation pops from its end, in the order of the
+// call's list, so equal inputs give equal tables.
+//
+// Every call that changes the pool is two kernels:
+//   plan    one block: validates the whole list, takes pages from or accounts
+//           for the pool, and writes what the second kernel has to do into the
+//           workspace.  A list with a bad entry, or one the free pages do not
+//           cover, changes nothing (its count of items becomes 0).
+//   apply   all SMs: page-table rows, reference counts and page contents.
+// The second kernel is launched with programmatic stream serialisation: its
+// blocks start while the plan runs and wait for its end, which hides the
+// launch.  No block waits for another one inside a kernel.
+//
+// Bound: contents by HBM (each byte read and written once, 16-byte accesses,
+// four in flight per thread); small calls by two launches and a handful of
+// dependent loads.
+#include <algorithm>
+#include <climits>
+
+#include "kpool_internal.h"
+
+namespace kpool {
+namespace {
+
+constexpr int kPlanThreads = 1024;
+constexpr int kApplyThreads = 256;
+constexpr int kChunk = 16 * 4 * kApplyThreads;   // bytes one block copies at a time
+constexpr int kPlanPages = 8;                    // pages per thread and round of the compaction scan
+constexpr uint32_t kFull = 0xFFFFFFFFu;
+
+// workspace header (ints)
+enum { W_TICKET = 0, W_STATUS = 1, W_COUNT = 2, W_LIVE = 3, W_HEADER = 64 };
+
+struct Stores {
+    kpool_page_store s[KPOOL_MAX_STORES];
+    int n;
+    int chunks[KPOOL_MAX_STORES];    // 16 KB pieces of a page
+    int per_item;                    // pieces of a page over all stores and layers
+};
+
+// Where the plan leaves its lists (ints in the workspace behind the header).
+struct Lists {
+    int *a, *b, *c;      // per item
+    int *mark;           // per sequence or per page
+};
+
+__device__ __forceinline__ void grid_dependency_wait()
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void grid_dependents_launch()
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// Exclusive prefix sum of v over the block (kPlanThreads); *total gets the sum.
+__device__ __forceinline__ int block_exclusive(int v, int *scratch, int *total)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(kFull, x, d);
+        if (lane >= d) x += y;
+    }
+    __syncthreads();                      // scratch of the previous call is read
+    if (lane == 31) scratch[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        int t = lane < warps ? scratch[lane] : 0;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int y = __shfl_up_sync(kFull, t, d);
+            if (lane >= d) t += y;
+        }
+        scratch[lane] = t;
+    }
+    __syncthreads();
+    *total = scratch[31];
+    return x - v + (warp > 0 ? scratch[warp - 1] : 0);
+}
+
+__device__ __forceinline__ bool in_range(int i, int n) { return i >= 0 && i < n; }
+
+// Block-wide: is any index of ids[0, n) out of [0, limit) or listed twice?
+// mark[id] ends as the first place that lists id.
+__device__ bool bad_or_twice(const int32_t *ids, int n, int limit, int *mark)
+{
+    bool bad = false;
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+        if (in_range(ids[i], limit)) mark[ids[i]] = INT_MAX;
+        else bad = true;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += blockDim.x)
+        if (in_range(ids[i], limit)) atomicMin(mark + ids[i], i);
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += blockDim.x)
+        if (in_range(ids[i], limit) && mark[ids[i]] != i) bad = true;
+    return __syncthreads_or(bad) != 0;
+}
+
+__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// One 16 KB piece of one page: the block's threads copy `bytes` (a multiple of
+// 16) from src to dst, all loads of a thread issued before its stores.
+__device__ __forceinline__ void copy_piece(const char *src, char *dst, int bytes)
+{
+    uint4 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int off = (k * kApplyThreads + threadIdx.x) * 16;
+        if (off < bytes) v[k] = *reinterpret_cast<const uint4 *>(src + off);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int off = (k * kApplyThreads + threadIdx.x) * 16;
+        if (off < bytes) *reinterpret_cast<uint4 *>(dst + off) = v[k];
+    }
+}
+
+// Contents of `count` page pairs, page src[i] to page dst[i] in every store and
+// layer: whole pages, or, given the sequences' lengths, the rows that a last
+// page of that length uses.
+__device__ void copy_pages(const Stores &st, const int *src, const int *dst, const int *lens,
+                           int count, int page_size, int n_pages)
+{
+    const int64_t tasks = static_cast<int64_t>(count) * st.per_item;
+    for (int64_t t = blockIdx.x; t < tasks; t += gridDim.x) {
+        const int item = static_cast<int>(t / st.per_item);
+        int r = static_cast<int>(t - static_cast<int64_t>(item) * st.per_item);
+        int s = 0;
+        while (r >= st.s[s].n_layers * st.chunks[s]) r -= st.s[s].n_layers * st.chunks[s], ++s;
+        const kpool_page_store &g = st.s[s];
+        const int layer = r / st.chunks[s], piece = r - layer * st.chunks[s];
+        const int a = src[item], b = dst[item];
+        if (!in_range(a, n_pages) || !in_range(b, n_pages)) continue;
+        const int tok = lens != nullptr ? lens[item] % page_size : page_size;
+        // the store's rows that hold those tokens, the last one whole
+        const int rows = static_cast<int>((static_cast<int64_t>(tok) * g.rows_per_page + page_size - 1) / page_size);
+        const int64_t bytes = static_cast<int64_t>(rows) * g.row_bytes - static_cast<int64_t>(piece) * kChunk;
+        if (bytes <= 0) continue;
+        const int64_t base = layer * g.layer_stride + static_cast<int64_t>(piece) * kChunk;
+        const char *p = static_cast<const char *>(g.data) + base;
+        char *q = static_cast<char *>(g.data) + base;
+        copy_piece(p + a * g.page_stride, q + b * g.page_stride, static_cast<int>(min(bytes, static_cast<int64_t>(kChunk))));
+    }
+}
+
+// ---- copy --------------------------------------------------------------------
+
+__global__ void __launch_bounds__(kPlanThreads) copy_plan(const int32_t *src, const int32_t *dst, int n,
+                                                          int n_pages, int *ws, Lists l)
+{
+    grid_dependents_launch();
+    bool bad = false;
+    // a source may be listed several times, a destination once, a page not as both
+    for (int i = threadIdx.x; i < n; i += blockDim.x)
+        if (in_range(src[i], n_pages)) l.mark[src[i]] = -1;
+    __syncthreads();
+    bad = bad_or_twice(dst, n, n_pages, l.mark);
+    for (int i = threadIdx.x; i < n; i += blockDim.x)
+        bad |= !in_range(src[i], n_pages) || l.mark[src[i]] != -1;
+    bad = __syncthreads_or(bad) != 0;
+    if (threadIdx.x == 0) {
+        ws[W_STATUS] = bad ? KPOOL_STATUS_BAD_PAGE : 0;
+        ws[W_COUNT] = bad ? 0 : n;
+    }
+}
+
+__global__ void __launch_bounds__(kApplyThreads) copy_apply(const __grid_constant__ Stores st, const int32_t *src,
+                                                            const int32_t *dst, int n_pages, const int *ws)
+{
+    grid_dependency_wait();
+    copy_pages(st, src, dst, nullptr, ws[W_COUNT], 1, n_pages);
+}
+
+// ---- fork --------------------------------------------------------------------
+// lists: a = source page of the partial page (or -1), b = its copy, c = length
+
+__global__ void __launch_bounds__(kPlanThreads) fork_plan(const kpool_page_pool p, const int32_t *parents,
+                                                          const int32_t *children, int n, int *ws, Lists l)
+{
+    __shared__ int scratch[32];
+    grid_dependents_launch();
+    const int ps = p.page_size;
+    const int64_t room = static_cast<int64_t>(p.max_pages) * ps;
+    bool bad = bad_or_twice(children, n, p.n_seqs, l.mark);
+    const int fc = *p.free_count;
+    if (!in_range(fc, p.n_pages + 1)) bad = true;
+    int need = 0;                          // pages taken by the items before this round
+    bool short_of = false;
+    for (int base = 0; base < n; base += blockDim.x) {
+        const int i = base + threadIdx.x;
+        int len = 0, last = -1, part = 0;
+        if (i < n) {
+            const int pa = parents[i], ch = children[i];
+            if (!in_range(pa, p.n_seqs) || !in_range(ch, p.n_seqs) || pa == ch || p.seq_lens[ch] != 0) bad = true;
+            else {
+                len = p.seq_lens[pa];
+                if (len < 0 || len > room) bad = true, len = 0;
+                part = len % ps;
+                if (part > 0) {
+                    last = p.page_table[static_cast<int64_t>(pa) * p.max_pages + len / ps];
+                    if (!in_range(last, p.n_pages)) bad = true;
+                }
+            }
+        }
+        int total;
+        const int rank = need + block_exclusive(part > 0, scratch, &total);
+        need += total;
+        if (i < n) {
+            int page = -1;
+            if (part > 0) {
+                if (rank >= fc) short_of = true;
+                else if (!bad) {
+                    page = p.free_list[fc - 1 - rank];
+                    if (!in_range(page, p.n_pages) || p.ref_count[page] != 0) bad = true;
+                }
+            }
+            l.a[i] = last;
+            l.b[i] = page;
+            l.c[i] = len;
+        }
+    }
+    bad = __syncthreads_or(bad) != 0;
+    short_of = __syncthreads_or(short_of) != 0;
+    const bool ok = !bad && !short_of;
+    if (ok)
+        for (int i = threadIdx.x; i < n; i += blockDim.x) {
+            p.seq_lens[children[i]] = l.c[i];
+            if (l.b[i] >= 0) p.ref_count[l.b[i]] = 1;
+        }
+    if (threadIdx.x == 0) {
+        if (ok) *p.free_count = fc - need;
+        ws[W_STATUS] = (bad ? KPOOL_STATUS_BAD_PAGE : 0) | (short_of && !bad ? KPOOL_STATUS_NO_PAGES : 0);
+        ws[W_COUNT] = ok ? n : 0;
+    }
+}
+
+__global__ void __launch_bounds__(kApplyThreads) fork_apply(const __grid_constant__ Stores st, const kpool_page_pool p,
+                                                            const int32_t *parents, const int32_t *children,
+                                                            int *ws, Lists l)
+{
+    grid_dependency_wait();
+    const int n = ws[W_COUNT];
+    const int cols = ceil_div(p.max_pages, kApplyThreads);
+    // the children's page-table rows, and one more reference on each whole page
+    const int64_t tasks = static_cast<int64_t>(n) * cols;
+    for (int64_t t = blockIdx.x; t < tasks; t += gridDim.x) {
+        const int i = static_cast<int>(t / cols);
+        const int j = static_cast<int>(t - static_cast<int64_t>(i) * cols) * kApplyThreads + threadIdx.x;
+        const int whole = l.c[i] / p.page_size;
+        if (j > whole || j >= p.max_pages) continue;
+        int32_t *row = p.page_table + static_cast<int64_t>(children[i]) * p.max_pages;
+        if (j == whole) {
+            if (l.b[i] >= 0) row[j] = l.b[i];
+            continue;
+        }
+        const int page = p.page_table[static_cast<int64_t>(parents[i]) * p.max_pages + j];
+        row[j] = page;
+        if (in_range(page, p.n_pages)) atomicAdd(p.ref_count + page, 1);
+        else atomicOr(ws + W_STATUS, KPOOL_STATUS_BAD_PAGE);
+    }
+    // the used rows of each partial page
+    copy_pages(st, l.a, l.b, l.c, n, p.page_size, p.n_pages);
+}
+
+// ---- extend ------------------------------------------------------------------
+// lists: a = pages taken before item i's, b = pages held, c = pages to take
+
+__global__ void __launch_bounds__(kPlanThreads) extend_kernel(const kpool_page_pool p, const int32_t *seqs,
+                                                              const int32_t *n_new, int n, int32_t *begin,
+                                                              int *ws, Lists l)
+{
+    __shared__ int scratch[32];
+    const int ps = p.page_size;
+    const int64_t room = static_cast<int64_t>(p.max_pages) * ps;
+    bool bad = bad_or_twice(seqs, n, p.n_seqs, l.mark);
+    const int fc = *p.free_count;
+    if (!in_range(fc, p.n_pages + 1)) bad = true;
+    int64_t need = 0;
+    for (int base = 0; base < n; base += blockDim.x) {
+        const int i = base + threadIdx.x;
+        int had = 0, take = 0, len = -1;
+        if (i < n && in_range(seqs[i], p.n_seqs)) {
+            const int s = seqs[i], add = n_new[i];
+            len = p.seq_lens[s];
+            if (len < 0 || add < 0 || static_cast<int64_t>(len) + add > room) bad = true;
+            else {
+                had = ceil_div(len, ps);
+                take = ceil_div(len + add, ps) - had;
+                if (add > 0 && len % ps != 0) {
+                    // the rows go on in the last page, which must be the sequence's own
+                    const int last = p.page_table[static_cast<int64_t>(s) * p.max_pages + had - 1];
+                    if (!in_range(last, p.n_pages) || p.ref_count[last] != 1) bad = true;
+                }
+            }
+        }
+        int total;
+        const int rank = block_exclusive(take, scratch, &total);
+        if (i < n) {
+            l.a[i] = static_cast<int>(min(need + rank, static_cast<int64_t>(INT_MAX)));
+            l.b[i] = had;
+            l.c[i] = take;
+            begin[i] = len;
+        }
+        need += total;
+    }
+    const bool short_of = need > fc;
+    bad = __syncthreads_or(bad) != 0;
+    bool ok = !bad && !short_of;
+    // the pages that will be popped must be free ones
+    if (ok)
+        for (int i = threadIdx.x; i < need; i += blockDim.x) {
+            const int page = p.free_list[fc - 1 - i];
+            if (!in_range(page, p.n_pages) || p.ref_count[page] != 0) bad = true;
+        }
+    bad = __syncthreads_or(bad) != 0;
+    ok = ok && !bad;
+    if (ok) {
+        const int lane = threadIdx.x & 31;
+        for (int i = threadIdx.x >> 5; i < n; i += blockDim.x >> 5) {
+            const int s = seqs[i], take = l.c[i];
+            int32_t *row = p.page_table + static_cast<int64_t>(s) * p.max_pages + l.b[i];
+            for (int j = lane; j < take; j += 32) {
+                const int page = p.free_list[fc - 1 - l.a[i] - j];
+                row[j] = page;
+                p.ref_count[page] = 1;
+            }
+            if (lane == 0) p.seq_lens[s] = begin[i] + n_new[i];
+        }
+    } else {
+        for (int i = threadIdx.x; i < n; i += blockDim.x) begin[i] = -1;
+    }
+    if (threadIdx.x == 0) {
+        if (ok) *p.free_count = fc - static_cast<int>(need);
+        ws[W_STATUS] = (bad ? KPOOL_STATUS_BAD_PAGE : 0) | (short_of && !bad ? KPOOL_STATUS_NO_PAGES : 0);
+    }
+}
+
+// ---- write -------------------------------------------------------------------
+
+// The last i with cu[i] <= r (n + 1 offsets), one warp probing 32 of them per round.
+__device__ __forceinline__ int segment_of(const int32_t *cu, int n, int r, int lane)
+{
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32;
+        const int at = lo + lane * step;
+        const unsigned m = __ballot_sync(kFull, at < hi && cu[at] <= r);
+        if (m == 0) return lo;             // offsets that do not begin at or before r
+        const int nlo = lo + (31 - __clz(m)) * step;
+        hi = min(hi, nlo + step);
+        lo = nlo;
+    }
+    return lo;
+}
+
+__global__ void __launch_bounds__(kApplyThreads) write_kernel(const kpool_page_pool p, const int32_t *seqs,
+                                                              const int32_t *begin, const int32_t *cu_rows, int n,
+                                                              int64_t total, const char *rows,
+                                                              int64_t rows_layer_stride, const kpool_page_store g,
+                                                              int *ws)
+{
+    const int lane = threadIdx.x & 31;
+    const int64_t warps = static_cast<int64_t>(gridDim.x) * (kApplyThreads / 32);
+    for (int64_t t = (static_cast<int64_t>(blockIdx.x) * kApplyThreads + threadIdx.x) >> 5;
+         t < total * g.n_layers; t += warps) {
+        const int layer = static_cast<int>(t / total);
+        const int r = static_cast<int>(t - layer * total);
+        const int i = segment_of(cu_rows, n, r, lane);
+        const int k = r - cu_rows[i];
+        bool ok = k >= 0 && r < cu_rows[i + 1] && in_range(seqs[i], p.n_seqs) && begin[i] >= 0;
+        int page = -1, row = 0;
+        if (ok) {
+            // tokens per row of this store: rows behind the sequence's length are not its own
+            const int64_t at = static_cast<int64_t>(begin[i]) + k;
+            const int64_t held = static_cast<int64_t>(p.seq_lens[seqs[i]]) * g.rows_per_page;
+            const int64_t col = at / g.rows_per_page;
+            row = static_cast<int>(at - col * g.rows_per_page);
+            ok = at * p.page_size < held && col < p.max_pages;
+            if (ok) page = p.page_table[static_cast<int64_t>(seqs[i]) * p.max_pages + col];
+            ok = ok && in_range(page, p.n_pages) && p.ref_count[page] == 1;
+        }
+        if (!ok) {
+            if (lane == 0) atomicOr(ws + W_STATUS, KPOOL_STATUS_BAD_PAGE);
+            continue;
+        }
+        const char *src = rows + layer * rows_layer_stride + static_cast<int64_t>(r) * g.row_bytes;
+        char *dst = static_cast<char *>(g.data) + layer * g.layer_stride + page * g.page_stride +
+                    static_cast<int64_t>(row) * g.row_bytes;
+        for (int off = lane * 16; off < g.row_bytes; off += 512)
+            *reinterpret_cast<uint4 *>(dst + off) = *reinterpret_cast<const uint4 *>(src + off);
+    }
+}
+
+// ---- free --------------------------------------------------------------------
+// lists: c = length of each listed sequence; mark = bit per page that lost its
+// last reference (after the per-sequence marks of the plan)
+
+__global__ void __launch_bounds__(kPlanThreads) free_plan(const kpool_page_pool p, const int32_t *seqs, int n,
+                                                          int *ws, Lists l, int *bits)
+{
+    grid_dependents_launch();
+    const int64_t room = static_cast<int64_t>(p.max_pages) * p.page_size;
+    bool bad = bad_or_twice(seqs, n, p.n_seqs, l.mark);
+    for (int i = threadIdx.x; i < n; i += blockDim.x)
+        if (in_range(seqs[i], p.n_seqs)) {
+            const int len = p.seq_lens[seqs[i]];
+            if (len < 0 || len > room) bad = true;
+            l.c[i] = len;
+        }
+    if (!in_range(*p.free_count, p.n_pages + 1)) bad = true;
+    for (int w = threadIdx.x; w < ceil_div(p.n_pages, 32); w += blockDim.x) bits[w] = 0;
+    bad = __syncthreads_or(bad) != 0;
+    if (!bad)
+        for (int i = threadIdx.x; i < n; i += blockDim.x) p.seq_lens[seqs[i]] = 0;
+    if (threadIdx.x == 0) {
+        ws[W_TICKET] = 0;
+        ws[W_STATUS] = bad ? KPOOL_STATUS_BAD_PAGE : 0;
+        ws[W_COUNT] = bad ? 0 : n;
+    }
+}
+
+__global__ void __launch_bounds__(kApplyThreads) free_apply(const kpool_page_pool p, const int32_t *seqs, int *ws,
+                                                            Lists l, int *bits)
+{
+    __shared__ int scratch[32];
+    __shared__ int ticket;
+    grid_dependency_wait();
+    const int n = ws[W_COUNT];
+    const int cols = ceil_div(p.max_pages, kApplyThreads);
+    for (int64_t t = blockIdx.x; t < static_cast<int64_t>(n) * cols; t += gridDim.x) {
+        const int i = static_cast<int>(t / cols);
+        const int j = static_cast<int>(t - static_cast<int64_t>(i) * cols) * kApplyThreads + threadIdx.x;
+        if (static_cast<int64_t>(j) * p.page_size >= l.c[i]) continue;
+        int32_t *at = p.page_table + static_cast<int64_t>(seqs[i]) * p.max_pages + j;
+        const int page = *at;
+        *at = -1;
+        int had = 0;
+        if (in_range(page, p.n_pages)) {
+            had = atomicSub(p.ref_count + page, 1);
+            if (had == 1) atomicOr(bits + (page >> 5), 1 << (page & 31));
+            if (had <= 0) atomicAdd(p.ref_count + page, 1);      // it had no reference to give back
+        }
+        if (had <= 0) atomicOr(ws + W_STATUS, KPOOL_STATUS_BAD_PAGE);
+    }
+    // the block that comes last pushes the freed pages, in ascending order
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) ticket = atomicAdd(ws + W_TICKET, 1);
+    __syncthreads();
+    if (ticket != static_cast<int>(gridDim.x) - 1) return;
+    __threadfence();
+    const int words = ceil_div(p.n_pages, 32);
+    int top = *p.free_count;
+    for (int base = 0; base < words; base += kApplyThreads) {
+        const int w = base + threadIdx.x;
+        uint32_t m = w < words ? static_cast<uint32_t>(__ldcg(bits + w)) : 0u;
+        int total;
+        int at = top + block_exclusive(__popc(m), scratch, &total);
+        for (; m != 0u; m &= m - 1u, ++at)
+            if (at < p.n_pages) p.free_list[at] = 32 * w + __ffs(m) - 1;
+        top += total;
+    }
+    if (threadIdx.x == 0) {
+        if (top > p.n_pages) atomicOr(ws + W_STATUS, KPOOL_STATUS_BAD_PAGE);
+        *p.free_count = min(top, p.n_pages);
+    }
+}
+
+// ---- compact -----------------------------------------------------------------
+// With k pages referenced, the i-th referenced page at or above k moves to the
+// i-th unreferenced page below k.  lists: a = sources, b = destinations,
+// mark = where each page at or above k goes (-1: nowhere)
+
+__global__ void __launch_bounds__(kPlanThreads) compact_plan(const kpool_page_pool p, int *ws, Lists l)
+{
+    __shared__ int scratch[32];
+    grid_dependents_launch();
+    const int n = p.n_pages;
+    int mine = 0;
+    for (int i = threadIdx.x; i < n; i += blockDim.x) mine += p.ref_count[i] > 0;
+    int k;
+    block_exclusive(mine, scratch, &k);
+    int from = 0, to = 0;                  // movers and holes before this round
+    for (int base = 0; base < n; base += kPlanPages * blockDim.x) {
+        const int p0 = base + kPlanPages * threadIdx.x;
+        // bit q: page p0 + q moves, or is a hole; a round's eight pages lie on
+        // both sides of k at most once, so both kinds are counted apart
+        uint32_t mv = 0, ho = 0;
+#pragma unroll
+        for (int q = 0; q < kPlanPages; ++q) {
+            const int page = p0 + q;
+            if (page >= n) break;
+            const bool live = p.ref_count[page] > 0;
+            if (page >= k) l.mark[page] = -1;
+            if (live && page >= k) mv |= 1u << q;
+            if (!live && page < k) ho |= 1u << q;
+        }
+        int tm, th;
+        int am = from + block_exclusive(__popc(mv), scratch, &tm);
+        int ah = to + block_exclusive(__popc(ho), scratch, &th);
+        for (; mv != 0u; mv &= mv - 1u) l.a[am++] = p0 + __ffs(mv) - 1;
+        for (; ho != 0u; ho &= ho - 1u) l.b[ah++] = p0 + __ffs(ho) - 1;
+        from += tm;
+        to += th;
+    }
+    __syncthreads();
+    // as many pages move as there are holes: both are k less the referenced pages below k
+    for (int i = threadIdx.x; i < from; i += blockDim.x) {
+        const int s = l.a[i], d = l.b[i];
+        l.mark[s] = d;
+        p.ref_count[d] = p.ref_count[s];
+        p.ref_count[s] = 0;
+    }
+    for (int i = threadIdx.x; i < n - k; i += blockDim.x) p.free_list[i] = n - 1 - i;
+    if (threadIdx.x == 0) {
+        *p.free_count = n - k;
+        ws[W_STATUS] = 0;
+        ws[W_COUNT] = from;
+        ws[W_LIVE] = k;
+    }
+}
+
+__global__ void __launch_bounds__(kApplyThreads) compact_apply(const __grid_constant__ Stores st,
+                                                               const kpool_page_pool p, int *ws, Lists l)
+{
+    grid_dependency_wait();
+    const int k = ws[W_LIVE];
+    const int cols = ceil_div(p.max_pages, kApplyThreads);
+    for (int64_t t = blockIdx.x; t < static_cast<int64_t>(p.n_seqs) * cols; t += gridDim.x) {
+        const int s = static_cast<int>(t / cols);
+        const int j = static_cast<int>(t - static_cast<int64_t>(s) * cols) * kApplyThreads + threadIdx.x;
+        if (j >= p.max_pages || static_cast<int64_t>(j) * p.page_size >= p.seq_lens[s]) continue;
+        int32_t *at = p.page_table + static_cast<int64_t>(s) * p.max_pages + j;
+        const int page = *at;
+        const int now = !in_range(page, p.n_pages) ? -1 : page < k ? page : l.mark[page];
+        if (now < 0) atomicOr(ws + W_STATUS, KPOOL_STATUS_BAD_PAGE);
+        else if (now != page) *at = now;
+    }
+    copy_pages(st, l.a, l.b, nullptr, ws[W_COUNT], 1, p.n_pages);
+}
+
+// ---- host --------------------------------------------------------------------
+
+Lists lists(void *ws, int64_t n)
+{
+    int *base = static_cast<int *>(ws) + W_HEADER;
+    return Lists{base, base + n, base + 2 * n, base + 3 * n};
+}
+
+Stores pack(const kpool_page_store *stores, int n_stores)
+{
+    Stores st{};
+    st.n = n_stores;
+    for (int i = 0; i < n_stores; ++i) {
+        st.s[i] = stores[i];
+        st.chunks[i] = static_cast<int>((static_cast<int64_t>(stores[i].rows_per_page) * stores[i].row_bytes + kChunk - 1) / kChunk);
+        st.per_item += st.chunks[i] * stores[i].n_layers;
+    }
+    return st;
+}
+
+// Blocks for `tasks` block-sized pieces of work: at most eight per SM, which
+// keep the copies' loads in flight (2048 threads).
+int grid_for(int64_t tasks)
+{
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(tasks, 8LL * num_sms())));
+}
+
+template <typename... P, typename... A>
+cudaError_t launch_after_plan(void (*kernel)(P...), int grid, cudaStream_t s, A... args)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kApplyThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
+}  // namespace
+
+size_t pages_workspace_bytes(int64_t n, int n_seqs, int n_pages)
+{
+    // three lists of the call's items (or of the pages, when compacting), the
+    // marks, and a bit per page
+    const int64_t items = std::max<int64_t>(n, n_pages);
+    return static_cast<size_t>(4 * (W_HEADER + 3 * items + std::max(n_seqs, n_pages) + (n_pages + 31) / 32 + 64));
+}
+
+int run_pages_copy(const int32_t *src, const int32_t *dst, int n, int n_pages, const kpool_page_store *stores,
+                   int n_stores, void *ws, cudaStream_t s)
+{
+    const Stores st = pack(stores, n_stores);
+    int *w = static_cast<int *>(ws);
+    copy_plan<<<1, kPlanThreads, 0, s>>>(src, dst, n, n_pages, w, lists(ws, n));
+    KPOOL_CUDA_CHECK(cudaGetLastError());
+    KPOOL_CUDA_CHECK(launch_after_plan(copy_apply, grid_for(static_cast<int64_t>(n) * st.per_item), s, st, src, dst,
+                                       n_pages, static_cast<const int *>(w)));
+    return KPOOL_OK;
+}
+
+int run_pages_fork(const kpool_page_pool &p, const int32_t *parents, const int32_t *children, int n,
+                   const kpool_page_store *stores, int n_stores, void *ws, cudaStream_t s)
+{
+    const Stores st = pack(stores, n_stores);
+    const Lists l = lists(ws, n);
+    int *w = static_cast<int *>(ws);
+    fork_plan<<<1, kPlanThreads, 0, s>>>(p, parents, children, n, w, l);
+    KPOOL_CUDA_CHECK(cudaGetLastError());
+    const int64_t cols = (p.max_pages + kApplyThreads - 1) / kApplyThreads;
+    KPOOL_CUDA_CHECK(launch_after_plan(fork_apply, grid_for(n * std::max<int64_t>(cols, st.per_item)), s, st, p,
+                                       parents, children, w, l));
+    return KPOOL_OK;
+}
+
+int run_pages_extend(const kpool_page_pool &p, const int32_t *seqs, const int32_t *n_new, int n, int32_t *begin,
+                     void *ws, cudaStream_t s)
+{
+    extend_kernel<<<1, kPlanThreads, 0, s>>>(p, seqs, n_new, n, begin, static_cast<int *>(ws), lists(ws, n));
+    KPOOL_CUDA_CHECK(cudaGetLastError());
+    return KPOOL_OK;
+}
+
+int run_pages_write(const kpool_page_pool &p, const int32_t *seqs, const int32_t *begin, const int32_t *cu_rows,
+                    int n, int64_t total, const void *rows, int64_t rows_layer_stride, const kpool_page_store &g,
+                    void *ws, cudaStream_t s)
+{
+    KPOOL_CUDA_CHECK(cudaMemsetAsync(ws, 0, 16, s));
+    if (total == 0 || n == 0) return KPOOL_OK;
+    const int64_t warps = total * g.n_layers;
+    write_kernel<<<grid_for((warps + kApplyThreads / 32 - 1) / (kApplyThreads / 32)), kApplyThreads, 0, s>>>(
+        p, seqs, begin, cu_rows, n, total, static_cast<const char *>(rows), rows_layer_stride, g,
+        static_cast<int *>(ws));
+    KPOOL_CUDA_CHECK(cudaGetLastError());
+    return KPOOL_OK;
+}
+
+int run_pages_free(const kpool_page_pool &p, const int32_t *seqs, int n, void *ws, cudaStream_t s)
+{
+    const Lists l = lists(ws, n);
+    int *w = static_cast<int *>(ws), *bits = l.mark + std::max(p.n_seqs, p.n_pages);
+    free_plan<<<1, kPlanThreads, 0, s>>>(p, seqs, n, w, l, bits);
+    KPOOL_CUDA_CHECK(cudaGetLastError());
+    const int64_t cols = (p.max_pages + kApplyThreads - 1) / kApplyThreads;
+    KPOOL_CUDA_CHECK(launch_after_plan(free_apply, grid_for(n * cols), s, p, seqs, w, l, bits));
+    return KPOOL_OK;
+}
+
+int run_pages_compact(const kpool_page_pool &p, const kpool_page_store *stores, int n_stores, void *ws,
+                      cudaStream_t s)
+{
+    const Stores st = pack(stores, n_stores);
+    const Lists l = lists(ws, p.n_pages);
+    int *w = static_cast<int *>(ws);
+    compact_plan<<<1, kPlanThreads, 0, s>>>(p, w, l);
+    KPOOL_CUDA_CHECK(cudaGetLastError());
+    const int64_t cols = (p.max_pages + kApplyThreads - 1) / kApplyThreads;
+    KPOOL_CUDA_CHECK(launch_after_plan(
+        compact_apply, grid_for(std::max<int64_t>(p.n_seqs * cols, static_cast<int64_t>(p.n_pages) / 2 * st.per_item)),
+        s, st, p, w, l));
+    return KPOOL_OK;
+}
+
+}  // namespace kpool

@@ -1,0 +1,123 @@
+"""Refusals of the paged-cache and shared-prefix calls, all on the host: no
+argument here reaches a device."""
+import ctypes
+
+import pytest
+import torch
+
+P = ctypes.c_void_p
+
+
+@pytest.fixture(scope="module")
+def b():
+    from sparse_attention_kpool_compress_gb300 import build as B
+    B.build()
+    from sparse_attention_kpool_compress_gb300 import binding
+    return binding
+
+
+def _fake(n=1 << 20):
+    buf = ctypes.create_string_buffer(n + 512)
+    return buf, (ctypes.addressof(buf) + 255) & ~255
+
+
+def _pool(b, a, **kw):
+    f = dict(page_table=a, seq_lens=a, ref_count=a, free_list=a, free_count=a, n_seqs=4, max_pages=8, n_pages=32,
+             page_size=16)
+    f.update(kw)
+    return ctypes.byref(b._Pool(**f))
+
+
+def _store(b, a, **kw):
+    f = dict(data=a, layer_stride=32 * 16 * 1024, page_stride=16 * 1024, n_layers=2, rows_per_page=16,
+             row_bytes=1024)
+    f.update(kw)
+    return ctypes.byref((b._Store * 1)(b._Store(**f)))
+
+
+def test_pools_and_stores_are_checked(b):
+    L = b._lib
+    keep, a = _fake()
+    p, mis = P(a), P(a + 2)
+    ws = L.kpool_pages_workspace_size(4, 4, 32)
+    good = _store(b, a)
+
+    def fork(pool=None, par=p, ch=p, n=4, st=good, n_st=1, w=p, wb=ws):
+        return L.kpool_pages_fork(_pool(b, a) if pool is None else pool, par, ch, n, st, n_st, w, wb, None)
+
+    bad = [
+        (fork(pool=P(None)), -1),
+        *[(fork(pool=_pool(b, a, **{k: 0})), -1) for k in ("n_seqs", "max_pages", "n_pages", "page_size")],
+        *[(fork(pool=_pool(b, a, **{k: None})), -1) for k in ("page_table", "seq_lens", "ref_count", "free_list",
+                                                             "free_count")],
+        (fork(pool=_pool(b, a, seq_lens=a + 2)), -1),
+        (fork(pool=_pool(b, a, max_pages=1 << 20, page_size=1 << 12)), -1),
+        (fork(par=P(None)), -1), (fork(ch=mis), -1), (fork(n=-1), -1), (fork(n_st=9), -1), (fork(st=P(None)), -1),
+        (fork(w=P(None)), -4), (fork(w=mis), -4), (fork(wb=ws - 1), -4),
+        *[(fork(st=_store(b, a, **kw)), -1) for kw in (
+            dict(data=None), dict(data=a + 8), dict(n_layers=0), dict(rows_per_page=0), dict(rows_per_page=5),
+            dict(rows_per_page=32), dict(row_bytes=1000), dict(row_bytes=0), dict(page_stride=16 * 1024 + 8),
+            dict(layer_stride=8), dict(page_stride=1024), dict(layer_stride=1024),
+            dict(page_stride=-16 * 1024), dict(n_layers=5000))],
+        (L.kpool_pages_extend(_pool(b, a), p, p, 4, P(None), p, ws, None), -1),
+        (L.kpool_pages_extend(_pool(b, a), p, p, 4, p, p, 16, None), -4),
+        (L.kpool_pages_free(_pool(b, a), P(None), 4, p, ws, None), -1),
+        (L.kpool_pages_free(_pool(b, a), p, 1 << 30, p, ws, None), -1),
+        (L.kpool_pages_compact(_pool(b, a), good, -1, p, ws, None), -1),
+        (L.kpool_pages_copy(p, p, 4, 0, good, 1, p, ws, None), -1),
+        (L.kpool_pages_copy(p, P(None), 4, 32, good, 1, p, ws, None), -1),
+        (L.kpool_pages_write(_pool(b, a), p, p, p, 4, 8, P(None), 8192, good, p, ws, None), -1),
+        (L.kpool_pages_write(_pool(b, a), p, p, p, 4, 8, mis, 8192, good, p, ws, None), -1),
+        (L.kpool_pages_write(_pool(b, a), p, p, p, 4, 8, p, 4096, good, p, ws, None), -1),
+        (L.kpool_pages_write(_pool(b, a), p, p, p, 4, -1, p, 8192, good, p, ws, None), -1),
+        (L.kpool_pages_write(_pool(b, a), p, p, p, 0, 8, p, 8192, good, p, ws, None), -1),
+    ]
+    for k, (rc, code) in enumerate(bad):
+        assert rc == code, (k, rc, L.kpool_last_error())
+    assert L.kpool_last_error()
+    assert L.kpool_pages_workspace_size(-1, 4, 32) == 0 and L.kpool_pages_workspace_size(4, 4, 0) == 0
+    del keep
+
+
+def test_shared_prefix_arguments_are_checked(b):
+    L = b._lib
+    keep, a = _fake()
+    p, mis = P(a), P(a + 2)
+    names = ("q", "kv", "stride", "n_pages", "page_size", "table", "lens", "n_rows", "max_pages", "seq_ids", "cu_q",
+             "B", "cu_g", "prefix", "G", "Tq", "H", "Dc", "scale", "o", "lse", "ws", "ws_bytes", "stream")
+    need = L.kpool_shared_prefix_mla_workspace_size(8, 64, 4, 2)
+    assert need >= 256
+    base = dict(zip(names, (p, p, 64 * 512, 32, 64, p, p, 4, 8, None, p, 4, p, p, 2, 8, 64, 512, 0.1, p, p, p, need,
+                            None)))
+    for change, code in (
+            (dict(H=0), -2), (dict(H=129), -2), (dict(Dc=576), -2), (dict(page_size=8), -2), (dict(page_size=48), -2),
+            (dict(page_size=256), -2), (dict(Tq=-1), -1), (dict(Tq=1 << 30), -1), (dict(B=0), -1), (dict(G=0), -1),
+            (dict(n_rows=0), -1), (dict(n_rows=3), -1), (dict(max_pages=0), -1), (dict(max_pages=1 << 26), -1),
+            (dict(n_pages=0), -1), (dict(stride=64 * 512 - 8), -1), (dict(stride=64 * 512 + 4), -1),
+            (dict(scale=0.0), -1), (dict(scale=float("nan")), -1), (dict(scale=float("inf")), -1),
+            (dict(q=None), -1), (dict(kv=None), -1), (dict(table=None), -1), (dict(lens=None), -1),
+            (dict(cu_q=None), -1), (dict(cu_g=None), -1), (dict(prefix=None), -1), (dict(o=None), -1),
+            (dict(lse=None), -1), (dict(q=mis), -1), (dict(kv=mis), -1), (dict(o=mis), -1), (dict(lse=mis), -1),
+            (dict(table=mis), -1), (dict(seq_ids=mis), -1), (dict(ws=None), -4), (dict(ws=mis), -4),
+            (dict(ws_bytes=need - 1), -4)):
+        args = {**base, **change}
+        rc = L.kpool_shared_prefix_mla_fwd(*(args[n] for n in names))
+        assert rc == code, (change, rc, L.kpool_last_error())
+    for bad in ((-1, 64, 4, 2), (8, 0, 4, 2), (8, 129, 4, 2), (1 << 31, 64, 4, 2), (8, 64, -1, 2)):
+        assert L.kpool_shared_prefix_mla_workspace_size(*bad) == 0
+    del keep
+
+
+def test_tensors_are_checked(b):
+    """The binding's own checks: types, shapes, strides and where a tensor lives."""
+    i32 = torch.zeros(4, dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA"):
+        b.KPoolPages(i32.view(2, 2), i32, i32, i32, i32, 16)
+    with pytest.raises(TypeError):
+        b.KPoolPages(i32.view(2, 2).long(), i32, i32, i32, i32, 16)
+    with pytest.raises(ValueError, match="contiguous"):
+        b.KPoolPages(torch.zeros(4, 4, dtype=torch.int32).t()[:2], i32, i32, i32, i32, 16)
+    with pytest.raises(ValueError):
+        b.kpool_pages_copy(i32, i32, ())
+    with pytest.raises(ValueError, match="CUDA"):
+        b.kpool_pages_copy(i32, i32, [torch.zeros(2, 8, 16, 8)])

@@ -1,0 +1,427 @@
+"""The paged cache's upkeep (kpool_pages_*) against a loop-by-loop restatement
+of include/kpool.h on the host.  Everything here is whole numbers or copied
+bytes, so every comparison is exact: tables, lengths, reference counts, the
+free list in its order, and each byte of each store, those that no call should
+touch among them."""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+BAD, SHORT = 4, 8            # KPOOL_STATUS_BAD_PAGE, KPOOL_STATUS_NO_PAGES
+
+
+@pytest.fixture(scope="module")
+def K():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import sparse_attention_kpool_compress_gb300 as K
+    return K
+
+
+class Host:
+    """The pool and its stores in numpy; each call returns the status word."""
+
+    def __init__(self, n_seqs, n_pages, max_pages, page_size, stores):
+        self.ps, self.n_pages, self.max = page_size, n_pages, max_pages
+        self.table = np.full((n_seqs, max_pages), -1, np.int64)
+        self.lens = np.zeros(n_seqs, np.int64)
+        self.refs = np.zeros(n_pages, np.int64)
+        self.free = list(range(n_pages - 1, -1, -1))
+        self.stores = stores                       # uint8 [layers, n_pages, rows, row_bytes]
+
+    def pages_of(self, n):
+        return -(-n // self.ps)
+
+    def _bad_list(self, ids, limit):
+        return any(not 0 <= i < limit for i in ids) or len(set(ids)) < len(ids)
+
+    def copy(self, src, dst):
+        if self._bad_list(dst, self.n_pages) or any(not 0 <= s < self.n_pages for s in src) or set(src) & set(dst):
+            return BAD
+        for st in self.stores:
+            st[:, dst] = st[:, src]
+        return 0
+
+    def fork(self, parents, children):
+        n = len(self.lens)
+        if self._bad_list(children, n) or any(not 0 <= p < n for p in parents):
+            return BAD
+        if any(p == c or self.lens[c] for p, c in zip(parents, children)):
+            return BAD
+        length = [int(self.lens[p]) for p in parents]
+        if sum(l % self.ps > 0 for l in length) > len(self.free):
+            return SHORT
+        for p, c, l in zip(parents, children, length):
+            whole, part = divmod(l, self.ps)
+            self.table[c, :whole] = self.table[p, :whole]
+            self.refs[self.table[c, :whole]] += 1
+            if part:
+                page = self.free.pop()
+                self.table[c, whole] = page
+                self.refs[page] = 1
+                for st in self.stores:
+                    rows = -(-part * st.shape[2] // self.ps)
+                    st[:, page, :rows] = st[:, self.table[p, whole], :rows]
+            self.lens[c] = l
+        return 0
+
+    def extend(self, seqs, more):
+        n = len(self.lens)
+        if self._bad_list(seqs, n) or any(m < 0 for m in more):
+            return BAD, [-1] * len(seqs)
+        need = 0
+        for s, m in zip(seqs, more):
+            l = int(self.lens[s])
+            if l + m > self.max * self.ps or (m and l % self.ps and self.refs[self.table[s, l // self.ps]] != 1):
+                return BAD, [-1] * len(seqs)
+            need += self.pages_of(l + m) - self.pages_of(l)
+        if need > len(self.free):
+            return SHORT, [-1] * len(seqs)
+        begin = [int(self.lens[s]) for s in seqs]
+        for s, m, l in zip(seqs, more, begin):
+            for j in range(self.pages_of(l), self.pages_of(l + m)):
+                self.table[s, j] = self.free.pop()
+                self.refs[self.table[s, j]] = 1
+            self.lens[s] = l + m
+        return 0, begin
+
+    def write(self, seqs, begin, cu, rows, k):
+        st, status = self.stores[k], 0
+        rpp = st.shape[2]
+        taken = set()
+        for i, s in enumerate(seqs):
+            for r in range(cu[i], cu[i + 1]):
+                at = begin[i] + r - cu[i]
+                col, row = divmod(at, rpp)
+                ok = 0 <= s < len(self.lens) and begin[i] >= 0 and at * self.ps < self.lens[s] * rpp and col < self.max
+                page = self.table[s, col] if ok else -1
+                if not ok or not 0 <= page < self.n_pages or self.refs[page] != 1:
+                    status = BAD
+                    continue
+                st[:, page, row] = rows[:, r]
+                taken.add(r)
+        return status if len(taken) == rows.shape[1] else BAD
+
+    def release(self, seqs):
+        if self._bad_list(seqs, len(self.lens)):
+            return BAD
+        gone = []
+        for s in seqs:
+            for j in range(self.pages_of(int(self.lens[s]))):
+                p = self.table[s, j]
+                self.refs[p] -= 1
+                if self.refs[p] == 0:
+                    gone.append(int(p))
+                self.table[s, j] = -1
+            self.lens[s] = 0
+        self.free += sorted(gone)
+        return 0
+
+    def compact(self):
+        k = int((self.refs > 0).sum())
+        src = [p for p in range(k, self.n_pages) if self.refs[p] > 0]
+        dst = [p for p in range(k) if self.refs[p] == 0]
+        to = dict(zip(src, dst))
+        for a, b in to.items():
+            for st in self.stores:
+                st[:, b] = st[:, a]
+            self.refs[b], self.refs[a] = self.refs[a], 0
+        for s, l in enumerate(self.lens):
+            for j in range(self.pages_of(int(l))):
+                self.table[s, j] = to.get(int(self.table[s, j]), self.table[s, j])
+        self.free = list(range(self.n_pages - 1, k - 1, -1))
+        return 0
+
+
+class Both:
+    """The same pool on the host and on the GPU."""
+
+    def __init__(self, K, n_seqs=7, n_pages=40, max_pages=6, page_size=16, layers=2, seed=0, inner_layers=False):
+        self.K, g = K, np.random.RandomState(seed)
+        rows = [page_size] + ([page_size // 4] if page_size % 4 == 0 else [])
+        widths = [48, 16]                          # bytes: three and one 16-byte pieces
+        host = [g.randint(0, 256, (layers, n_pages, r, w)).astype(np.uint8) for r, w in zip(rows, widths)]
+        if inner_layers:                           # layers within pages: [n_pages, layers, rows, width]
+            self.stores = [torch.from_numpy(h).cuda().transpose(0, 1).contiguous().transpose(0, 1) for h in host]
+        else:
+            self.stores = [torch.from_numpy(h).cuda() for h in host]
+        self.host = Host(n_seqs, n_pages, max_pages, page_size, [h.copy() for h in host])
+        self.gpu = K.kpool_pages_new(n_seqs, n_pages, max_pages, page_size)
+        self.ws = torch.empty(max(256, K.kpool_pages_workspace_size(1000, n_seqs, n_pages)), dtype=torch.uint8,
+                              device="cuda")
+        self.rng = g
+
+    def i32(self, a):
+        return torch.tensor(a, dtype=torch.int32, device="cuda")
+
+    def check(self, want, note=""):
+        assert self.K.kpool_read_status(self.ws) == want, note
+        h, p = self.host, self.gpu
+        assert p.free_count.item() == len(h.free), note
+        assert p.free_list.cpu().tolist()[:len(h.free)] == h.free, note
+        assert p.seq_lens.cpu().tolist() == h.lens.tolist(), note
+        assert p.ref_count.cpu().tolist() == h.refs.tolist(), note
+        table = p.page_table.cpu().numpy()
+        for s, l in enumerate(h.lens):
+            n = h.pages_of(int(l))
+            assert table[s, :n].tolist() == h.table[s, :n].tolist(), (note, s)
+        for a, b in zip(self.stores, h.stores):
+            assert np.array_equal(a.cpu().numpy(), b), note
+
+    def extend(self, seqs, more, want=0):
+        got = self.K.kpool_pages_extend(self.gpu, self.i32(seqs), self.i32(more), workspace=self.ws)
+        st, begin = self.host.extend(seqs, more)
+        assert st == want
+        assert got.cpu().tolist() == begin
+        self.check(want, ("extend", seqs, more))
+        return begin
+
+    def write(self, seqs, begin, cu, k=0, want=0):
+        st = self.host.stores[k]
+        rows = self.rng.randint(0, 256, (st.shape[0], cu[-1], st.shape[3])).astype(np.uint8)
+        self.K.kpool_pages_write(self.gpu, self.i32(seqs), self.i32(begin), self.i32(cu),
+                                 torch.from_numpy(rows).cuda(), self.stores[k], workspace=self.ws)
+        assert self.host.write(seqs, begin, cu, rows, k) == want
+        self.check(want, ("write", seqs, begin, cu, k))
+
+    def grow(self, seqs, more):
+        begin = self.extend(seqs, more)
+        self.write(seqs, begin, np.concatenate([[0], np.cumsum(more)]).tolist())
+
+    def fork(self, parents, children, want=0):
+        self.K.kpool_pages_fork(self.gpu, self.i32(parents), self.i32(children), self.stores, workspace=self.ws)
+        assert self.host.fork(parents, children) == want
+        self.check(want, ("fork", parents, children))
+
+    def free(self, seqs, want=0):
+        self.K.kpool_pages_free(self.gpu, self.i32(seqs), workspace=self.ws)
+        assert self.host.release(seqs) == want
+        self.check(want, ("free", seqs))
+
+    def compact(self, want=0):
+        self.K.kpool_pages_compact(self.gpu, self.stores, workspace=self.ws)
+        assert self.host.compact() == want
+        self.check(want, "compact")
+
+    def copy(self, src, dst, want=0):
+        self.K.kpool_pages_copy(self.i32(src), self.i32(dst), self.stores, workspace=self.ws)
+        assert self.host.copy(src, dst) == want
+        self.check(want, ("copy", src, dst))
+
+
+@pytest.mark.parametrize("page_size", [1, 4, 5, 16, 64])
+@pytest.mark.parametrize("inner_layers", [False, True])
+def test_a_rollout(K, page_size, inner_layers):
+    """Prompts filled, forked, grown, retired and packed, checked after every call."""
+    b = Both(K, n_seqs=9, n_pages=60, max_pages=8, page_size=page_size, seed=page_size, inner_layers=inner_layers)
+    ps = page_size
+    b.grow([0, 5], [3 * ps + (1 if ps > 1 else 0), 2 * ps])       # one ends inside a page, one at its end
+    b.fork([0, 0, 5, 0], [1, 2, 6, 4])
+    b.grow([4, 1, 0, 6], [1, ps, 2 * ps - 1, 0])
+    b.free([2, 0])
+    b.compact()
+    b.grow([1, 4], [1, 3])
+    b.fork([1], [0])
+    b.free([0, 1, 4, 5, 6])
+    b.compact()
+    assert b.gpu.free_count.item() == 60
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_random_calls(K, seed):
+    """Calls drawn at random, refused ones among them."""
+    rng = np.random.RandomState(100 + seed)
+    ps = int(rng.choice([3, 8, 16]))
+    b = Both(K, n_seqs=12, n_pages=50, max_pages=9, page_size=ps, layers=1 + seed % 3, seed=seed)
+    statuses = set()
+    for _ in range(60):
+        h = b.host
+        op = rng.randint(6)
+        live, empty = np.flatnonzero(h.lens > 0).tolist(), np.flatnonzero(h.lens == 0).tolist()
+        if op <= 1:
+            seqs = rng.permutation(12)[:rng.randint(1, 6)].tolist()
+            more = rng.randint(0, 3 * ps, len(seqs)).tolist()
+            import copy
+            st, _ = copy.deepcopy(h).extend(seqs, more)
+            statuses.add(st)
+            if st == 0:
+                b.grow(seqs, more)
+            else:
+                b.extend(seqs, more, st)
+        elif op == 2 and live and empty:
+            n = rng.randint(1, len(empty) + 1)
+            parents = rng.choice(live, n).tolist()
+            children = rng.permutation(empty)[:n].tolist()
+            if rng.rand() < 0.2:
+                children[-1] = live[0]
+            import copy
+            st = copy.deepcopy(h).fork(parents, children)
+            statuses.add(st)
+            b.fork(parents, children, st)
+        elif op == 3 and live:
+            b.free(rng.permutation(12)[:rng.randint(1, 5)].tolist())
+        elif op == 4:
+            b.compact()
+        elif op == 5:
+            at = rng.permutation(50)[:2 * rng.randint(1, 12)].tolist()
+            b.copy(at[::2], at[1::2])
+    assert 0 in statuses
+
+
+def test_lists_that_are_refused(K):
+    b = Both(K, n_seqs=5, n_pages=6, max_pages=4, page_size=8)
+    b.grow([0, 1], [13, 8])                       # three pages taken, three free
+    for parents, children in (([0], [5]), ([0], [-1]), ([7], [2]), ([-2], [2]), ([0, 0], [2, 2]), ([0], [1]),
+                              ([2], [2]), ([0, 1, 9], [2, 3, 4])):
+        b.fork(parents, children, BAD)
+    for seqs, more in (([0, 0], [1, 1]), ([5], [1]), ([-1], [0]), ([0], [-1]), ([0], [20]), ([2], [33])):
+        b.extend(seqs, more, BAD)
+    b.extend([2, 3], [17, 8], SHORT)              # four pages needed
+    b.extend([2], [2 ** 31 - 1], BAD)
+    for seqs in ([0, 0], [5], [-1], [1, 2, 1]):
+        b.free(seqs, BAD)
+    for src, dst in (([0], [6]), ([6], [0]), ([0], [-1]), ([-1], [0]), ([0, 1], [2, 2]), ([0, 1], [1, 2]), ([3], [3])):
+        b.copy(src, dst, BAD)
+    b.copy([0, 0, 1], [3, 4, 5])                  # a source twice
+    b.grow([2], [24])
+    b.fork([0], [3], SHORT)                       # its partial page has nowhere to go
+    b.fork([1, 2], [3, 4])                        # whole pages need none
+
+
+def test_writes_that_are_left_out(K):
+    b = Both(K, n_seqs=4, n_pages=12, max_pages=4, page_size=8)
+    b.grow([0], [12])
+    b.fork([0], [1])
+    b.write([0], [0], [0, 3], want=BAD)           # a shared page
+    b.write([0, 1], [8, 8], [0, 4, 8])            # each sequence's own
+    b.write([1], [10], [0, 5], want=BAD)          # the last three lie behind the length
+    b.write([1, 4], [11, 0], [0, 1, 2], want=BAD)
+    b.write([1, -1, 0], [11, 0, 9], [0, 1, 1, 2])  # no row goes to the unknown sequence
+    b.write([1], [-1], [0, 2], want=BAD)          # what a refused extension returned
+    b.write([2], [0], [0, 1], want=BAD)           # an empty sequence
+    b.write([0, 1], [2, 2], [0, 1, 2], k=1)       # pooled rows: two per page
+    b.write([1], [2 ** 31 - 1], [0, 1], want=BAD)
+
+
+def test_nothing_listed(K):
+    b = Both(K, n_seqs=3, n_pages=4, max_pages=2, page_size=8)
+    b.extend([], [])
+    b.fork([], [])
+    b.free([])
+    b.copy([], [])
+    b.compact()
+    b.extend([0, 1, 2], [0, 0, 0])
+    b.fork([0], [1])                              # an empty parent
+    b.free([0, 1, 2])                             # sequences that hold nothing
+
+
+def test_a_shared_partial_page_is_not_extended(K):
+    """A table made by hand, whose last partial page two sequences hold."""
+    b = Both(K, n_seqs=3, n_pages=6, max_pages=3, page_size=8)
+    b.grow([0], [5])
+    b.gpu.page_table[1, 0] = b.host.table[1, 0] = b.host.table[0, 0]
+    b.gpu.seq_lens[1] = 5
+    b.host.lens[1] = 5
+    b.gpu.ref_count[int(b.host.table[0, 0])] = 2
+    b.host.refs[b.host.table[0, 0]] = 2
+    b.extend([1], [1], BAD)
+    b.extend([1], [0])
+    b.free([1])
+    b.grow([0], [1])
+
+
+@pytest.mark.parametrize("what", ["id_high", "id_negative", "count_high", "count_negative", "list", "length"])
+def test_a_broken_pool_is_not_followed(K, what):
+    """Ids, counts and lengths outside their arrays set the status; no call goes where they point."""
+    b = Both(K, n_seqs=4, n_pages=8, max_pages=3, page_size=8)
+    b.grow([0, 1], [20, 3])
+    p, i = b.gpu, b.i32
+    calls = [lambda: K.kpool_pages_fork(p, i([0]), i([2]), b.stores, workspace=b.ws),
+             lambda: K.kpool_pages_extend(p, i([0, 1]), i([3, 9]), workspace=b.ws),
+             lambda: K.kpool_pages_free(p, i([0]), workspace=b.ws)]
+    if what.startswith("id"):
+        p.page_table[0, 2] = 1 << 20 if what == "id_high" else -7
+    elif what.startswith("count"):
+        p.free_count.fill_(9 if what == "count_high" else -1)
+    elif what == "list":
+        p.free_list.fill_(99)
+        calls = calls[:2]
+    else:
+        p.seq_lens[0] = 25
+    before = [s.clone() for s in b.stores]
+    for call in calls:
+        call()
+        assert K.kpool_read_status(b.ws) & BAD
+    if what != "length":
+        K.kpool_pages_compact(p, b.stores, workspace=b.ws)
+        torch.cuda.synchronize()
+    assert all(s.shape == t.shape for s, t in zip(before, b.stores))
+
+
+@pytest.mark.parametrize("n_seqs,n_pages,page_size", [(1500, 9000, 1), (1100, 40000, 4)])
+def test_many_sequences_and_pages(K, n_seqs, n_pages, page_size):
+    """More items than a plan block has threads, more pages than one round of its scan."""
+    rng = np.random.RandomState(n_seqs)
+    b = Both(K, n_seqs=n_seqs, n_pages=n_pages, max_pages=300, page_size=page_size, layers=1, seed=3)
+    b.ws = torch.empty(K.kpool_pages_workspace_size(n_seqs, n_seqs, n_pages), dtype=torch.uint8, device="cuda")
+    half = n_seqs // 2
+    seqs = rng.permutation(half).tolist()
+    b.grow(seqs, rng.randint(0, 5 * page_size, half).tolist())
+    b.extend([0], [257 * page_size])               # a table row longer than a block
+    b.fork(rng.randint(0, half, n_seqs - half).tolist(), (half + rng.permutation(n_seqs - half)).tolist())
+    b.free(rng.permutation(n_seqs)[:n_seqs - 40].tolist())
+    b.compact()
+
+
+def test_pages_larger_than_a_piece(K):
+    """Pages of more than one 16 KB piece, with an odd rest, in three layers."""
+    ps, width = 33, 624                            # 20592 bytes a page
+    b = Both(K, n_seqs=4, n_pages=9, max_pages=3, page_size=ps, layers=3)
+    g = np.random.RandomState(4)
+    h = g.randint(0, 256, (3, 9, ps, width)).astype(np.uint8)
+    b.stores, b.host.stores = [torch.from_numpy(h).cuda()], [h.copy()]
+    b.grow([0], [ps + 30])
+    b.fork([0, 0], [1, 2])
+    b.copy([0, 1], [7, 8])
+    b.free([0])
+    b.compact()
+
+
+def test_captured_and_replayed(K):
+    """A decode step's upkeep captured once and replayed: each replay goes on from the pool as it is."""
+    b = Both(K, n_seqs=4, n_pages=30, max_pages=8, page_size=8, layers=1)
+    b.grow([0, 1], [10, 16])
+    seqs, more, cu = b.i32([1, 0]), b.i32([1, 1]), b.i32([0, 1, 2])
+    rows = torch.from_numpy(b.rng.randint(0, 256, (1, 2, 48)).astype(np.uint8)).cuda()
+    child, parent = b.i32([2]), b.i32([0])
+
+    def step():
+        begin = K.kpool_pages_extend(b.gpu, seqs, more, workspace=b.ws)
+        K.kpool_pages_write(b.gpu, seqs, begin, cu, rows, b.stores[0], workspace=b.ws)
+        K.kpool_pages_fork(b.gpu, parent, child, b.stores, workspace=b.ws)
+        K.kpool_pages_free(b.gpu, child, workspace=b.ws)
+        K.kpool_pages_compact(b.gpu, b.stores, workspace=b.ws)
+
+    def host_step():
+        _, begin = b.host.extend([1, 0], [1, 1])
+        b.host.write([1, 0], begin, [0, 1, 2], rows.cpu().numpy(), 0)
+        b.host.fork([0], [2])
+        b.host.release([2])
+        b.host.compact()
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):                  # another stream than the default one
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    host_step()
+    b.check(0, "eager on a side stream")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for k in range(5):
+        graph.replay()
+        host_step()
+        b.check(0, ("replay", k))
