@@ -125,6 +125,10 @@ int run_pipeline(const PipelineArgs &a, cudaStream_t stream);
 // columns (128 bytes, 128-byte swizzle) x box_rows rows (kpool_project.cu).
 int encode_bf16_tmap(CUtensorMap *m, const void *base, uint64_t cols, uint64_t rows,
                      uint32_t box_rows);
+// The same of pages [pages, rows, cols] that lie page_stride elements apart:
+// boxes of 64 columns x box_rows rows of one page.
+int encode_bf16_pages_tmap(CUtensorMap *m, const void *base, uint64_t cols, uint64_t rows, uint64_t pages,
+                           uint64_t page_stride, uint32_t box_rows);
 
 // Sparse attention over the selection (kpool_mla.cu): tok_idx mode when
 // tok_idx is given, else pool mode (the expansion of pool_idx fused in).

@@ -25,6 +25,7 @@
 #include <climits>
 
 #include "kpool_internal.h"
+#include "kpool_ptx.cuh"
 
 namespace kpool {
 namespace {
@@ -50,15 +51,6 @@ struct Lists {
     int *a, *b, *c;      // per item
     int *mark;           // per sequence or per page
 };
-
-__device__ __forceinline__ void grid_dependency_wait()
-{
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-__device__ __forceinline__ void grid_dependents_launch()
-{
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
 
 // Exclusive prefix sum of v over the block (kPlanThreads); *total gets the sum.
 __device__ __forceinline__ int block_exclusive(int v, int *scratch, int *total)
@@ -159,7 +151,7 @@ __device__ void copy_pages(const Stores &st, const int *src, const int *dst, con
 __global__ void __launch_bounds__(kPlanThreads) copy_plan(const int32_t *src, const int32_t *dst, int n,
                                                           int n_pages, int *ws, Lists l)
 {
-    grid_dependents_launch();
+    ptx::grid_dependents_launch();
     bool bad = false;
     // a source may be listed several times, a destination once, a page not as both
     for (int i = threadIdx.x; i < n; i += blockDim.x)
@@ -178,7 +170,7 @@ __global__ void __launch_bounds__(kPlanThreads) copy_plan(const int32_t *src, co
 __global__ void __launch_bounds__(kApplyThreads) copy_apply(const __grid_constant__ Stores st, const int32_t *src,
                                                             const int32_t *dst, int n_pages, const int *ws)
 {
-    grid_dependency_wait();
+    ptx::grid_dependency_wait();
     copy_pages(st, src, dst, nullptr, ws[W_COUNT], 1, n_pages);
 }
 
@@ -189,7 +181,7 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan(const kpool_page_pool 
                                                           const int32_t *children, int n, int *ws, Lists l)
 {
     __shared__ int scratch[32];
-    grid_dependents_launch();
+    ptx::grid_dependents_launch();
     const int ps = p.page_size;
     const int64_t room = static_cast<int64_t>(p.max_pages) * ps;
     bool bad = bad_or_twice(children, n, p.n_seqs, l.mark);
@@ -249,7 +241,7 @@ __global__ void __launch_bounds__(kApplyThreads) fork_apply(const __grid_constan
                                                             const int32_t *parents, const int32_t *children,
                                                             int *ws, Lists l)
 {
-    grid_dependency_wait();
+    ptx::grid_dependency_wait();
     const int n = ws[W_COUNT];
     const int cols = ceil_div(p.max_pages, kApplyThreads);
     // the children's page-table rows, and one more reference on each whole page
@@ -409,7 +401,7 @@ __global__ void __launch_bounds__(kApplyThreads) write_kernel(const kpool_page_p
 __global__ void __launch_bounds__(kPlanThreads) free_plan(const kpool_page_pool p, const int32_t *seqs, int n,
                                                           int *ws, Lists l, int *bits)
 {
-    grid_dependents_launch();
+    ptx::grid_dependents_launch();
     const int64_t room = static_cast<int64_t>(p.max_pages) * p.page_size;
     bool bad = bad_or_twice(seqs, n, p.n_seqs, l.mark);
     for (int i = threadIdx.x; i < n; i += blockDim.x)
@@ -435,7 +427,7 @@ __global__ void __launch_bounds__(kApplyThreads) free_apply(const kpool_page_poo
 {
     __shared__ int scratch[32];
     __shared__ int ticket;
-    grid_dependency_wait();
+    ptx::grid_dependency_wait();
     const int n = ws[W_COUNT];
     const int cols = ceil_div(p.max_pages, kApplyThreads);
     for (int64_t t = blockIdx.x; t < static_cast<int64_t>(n) * cols; t += gridDim.x) {
@@ -485,7 +477,7 @@ __global__ void __launch_bounds__(kApplyThreads) free_apply(const kpool_page_poo
 __global__ void __launch_bounds__(kPlanThreads) compact_plan(const kpool_page_pool p, int *ws, Lists l)
 {
     __shared__ int scratch[32];
-    grid_dependents_launch();
+    ptx::grid_dependents_launch();
     const int n = p.n_pages;
     int mine = 0;
     for (int i = threadIdx.x; i < n; i += blockDim.x) mine += p.ref_count[i] > 0;
@@ -534,7 +526,7 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan(const kpool_page_po
 __global__ void __launch_bounds__(kApplyThreads) compact_apply(const __grid_constant__ Stores st,
                                                                const kpool_page_pool p, int *ws, Lists l)
 {
-    grid_dependency_wait();
+    ptx::grid_dependency_wait();
     const int k = ws[W_LIVE];
     const int cols = ceil_div(p.max_pages, kApplyThreads);
     for (int64_t t = blockIdx.x; t < static_cast<int64_t>(p.n_seqs) * cols; t += gridDim.x) {

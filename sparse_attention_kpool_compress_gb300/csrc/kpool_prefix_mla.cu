@@ -6,9 +6,40 @@
 //   s_j = scale * q[t, h, :] . c_b[j, :]
 //   o[t, h, :] = sum_j softmax_j(s) c_b[j, :],   lse[t, h] = ln sum_j exp(s_j)
 //
-// One warp per row: a lane holds 16 of the 512 columns, the scores are warp
-// sums, and the softmax runs on a reference maximum that follows the largest
-// score seen.
+// The (query, head) rows of a group are one flat matrix, and so are those of a
+// sequence.  A unit is 128 such rows against a span of tokens: a group's rows
+// against its shared tokens, read once for all of them, or a sequence's rows
+// against its own.  Three kernels:
+//   plan      one block: lengths, units, and an even cut of all units' tiles
+//             (256 tokens each) over the CTA pairs.  A cut may fall inside a
+//             unit, so a long prefix under few rows still fills the GPU.
+//   attend    one CTA pair per piece of a unit, persistent: unnormalised
+//             softmax with a running maximum, FP32 partial rows and their
+//             log-sum-exp to the workspace.
+//   combine   one warp per row joins its pieces, the shared ones and its own.
+//
+// attend, per CTA pair.  The output of 128 rows x 512 columns fills all of one
+// SM's tensor memory, so two SMs share it: tcgen05.mma with cta_group::2,
+// M = 128, gives each CTA 64 rows, as 2 x 64 lanes (lanes 0-63 the first half of
+// the N columns, lanes 64-127 the second).  Each CTA then holds
+//   O  [64 x 512]  256 columns of tensor memory, and
+//   S  [64 x 256]  128 columns, twice, so that the scores of the next tile run
+//                  while the softmax works on this one.
+// Both products take N = 256, at which the pair form runs at full rate (66.7
+// cycles per 128 x 256 x 16 MMA measured, M = 128 N = 256; N = 128 takes the
+// same time).  Operand B is split: for the scores each CTA brings 128 of the
+// tile's 256 tokens (K-major), for the output 256 of the 512 latent columns of
+// all its tokens (MN-major).  Both come through one ring of eight 16 KB chunks,
+// each feeding four MMAs.  (Keeping the quarter of a tile that both products use
+// would need 64 KB that the 64 KB of queries, the 32 KB of P and the ring leave
+// no room for.)
+//   warps 0, 3   TMA producers, chunks in turn (one warp alone issues too slowly)
+//   warp 1       MMA issuer (CTA 0)
+//   warp 2       relay: clears what lies outside the span in a chunk of values,
+//                so that nothing there, NaN included, meets a weight of 0, and
+//                passes the chunk on to the issuer
+//   warps 4-11   softmax and output: thread (lane, half of the columns) has 64
+//                of a row's 256 scores
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -20,9 +51,78 @@ namespace kpool {
 namespace {
 
 constexpr int kDc = 512;
+constexpr int kRows = 128;               // rows of a unit
+constexpr int kCtaRows = 64;             // of them in each CTA
+constexpr int kTile = 256;               // tokens of a tile
+constexpr int kOverhead = 2;             // a piece's start and end, in tiles (for the even cut)
+constexpr int kThreads = 384;
+constexpr int kSmWarps = 8;
+constexpr int kPlanThreads = 1024;
+constexpr float kRescale = 8.f;          // headroom of the reference maximum (log2)
+constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr uint32_t kFull = 0xFFFFFFFFu;
+constexpr int kTmemCols = 512;           // O: 0..255, S: 256..383 and 384..511
+constexpr int kTmemS = 256;
+
+// shared memory (from a 1024-byte aligned base)
+constexpr int kChunk = 16384;
+constexpr int kSlots = 8;
+constexpr int kOffQ = 0;                           // 8 x [64 rows x 64 columns]
+constexpr int kOffP = kOffQ + 8 * 8192;            // 4 x [64 rows x 64 tokens]
+constexpr int kOffRing = kOffP + 4 * 8192;
+constexpr int kOffRed = kOffRing + kSlots * kChunk;  // [4][64] floats
+constexpr int kOffWord = kOffRed + 4 * kCtaRows * 4; // agreement words [2 groups][2][4]
+constexpr int kOffBar = kOffWord + 64;
+enum {
+    B_FULL = 0, B_READY = B_FULL + kSlots, B_EMPTY = B_READY + kSlots, B_QFULL = B_EMPTY + kSlots, B_QREADY,
+    B_QEMPTY, B_SFULL, B_PFULL = B_SFULL + 2, B_PV, B_DRAIN, N_BARS
+};
+constexpr int kOffMisc = kOffBar + N_BARS * 8;     // [0] tmem base, [1] abort flag
+constexpr int kSmemBytes = kOffMisc + 16 + 1024;   // and alignment slack
+static_assert(kSmemBytes <= 232448, "shared memory over the per-block limit");
+
+// workspace header (ints)
+enum { H_STATUS = 1, H_OK = 2, H_UNITS = 3, H_INTS = 64 };
+
+struct Unit {
+    int row0, nrows;         // flat (query, head) rows
+    int table_row;           // page-table row its tokens are read through
+    int t0, t1, tiles;       // tokens t0 .. t1 - 1, in tiles from t0's box on
+    int64_t w0;              // first position of the unit in the cut work
+    int64_t out0;            // first partial row
+};
+static_assert(sizeof(Unit) == 40, "Unit");
+
+struct Token {               // per query
+    int vis;                 // tokens it sees
+    int pu, prow0;           // its group's first unit, and that unit's first row
+    int su, srow0;           // its sequence's
+};
+
+struct Work {
+    int *head;               // header; 64-bit words 8.. : [0] work per cluster
+    Token *tok;              // [Tq]
+    int *unit0;              // [G + B] first unit of each group and sequence
+    int *len;                // [B] tokens, [B..2B) shared tokens of its group
+    int *first;              // [clusters] first unit of each cluster
+    Unit *unit;
+    float *lse;              // [partial rows], base 2
+    float *o;                // [partial rows, 512]
+};
+
+struct Params {
+    PrefixMlaArgs a;
+    Work w;
+    int clusters;
+    int box;                 // rows of a TMA box
+    float c_scale;           // softmax scale * log2(e)
+    uint64_t wait_limit_ns;
+};
 
 __device__ __forceinline__ bool in_range(int i, int n) { return i >= 0 && i < n; }
+__device__ __forceinline__ int64_t *work_per_cluster(const Work &w) { return reinterpret_cast<int64_t *>(w.head + 8); }
+
+// ---- plan --------------------------------------------------------------------
 
 // The last i in [0, n) with cu[i] <= r.
 __device__ int segment_of(const int32_t *cu, int n, int r)
@@ -36,114 +136,827 @@ __device__ int segment_of(const int32_t *cu, int n, int r)
     return lo;
 }
 
-__global__ void __launch_bounds__(1024) check_kernel(const PrefixMlaArgs a, int *ws)
+// Exclusive prefix sum over the block; *total gets the sum.
+__device__ int64_t block_exclusive(int64_t v, int64_t *scratch, int64_t *total)
 {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t x = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t y = __shfl_up_sync(kFull, x, d);
+        if (lane >= d) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) scratch[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        int64_t t = scratch[lane];
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t y = __shfl_up_sync(kFull, t, d);
+            if (lane >= d) t += y;
+        }
+        scratch[lane] = t;
+    }
+    __syncthreads();
+    *total = scratch[31];
+    return x - v + (warp > 0 ? scratch[warp - 1] : 0);
+}
+
+// Pieces of a unit: the clusters whose share of the work touches its tiles.
+__device__ __forceinline__ void pieces_of(const Unit &u, int64_t share, int64_t *c0, int *n)
+{
+    *c0 = (u.w0 + kOverhead) / share;
+    *n = u.tiles > 0 ? static_cast<int>((u.w0 + kOverhead + u.tiles - 1) / share - *c0) + 1 : 0;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p)
+{
+    __shared__ int64_t scratch[32];
+    __shared__ int status;
+    const PrefixMlaArgs &a = p.a;
+    const Work &w = p.w;
+    ptx::grid_dependents_launch();
+    if (threadIdx.x == 0) status = 0;
     bool bad = false;
     for (int i = threadIdx.x; i <= a.B; i += blockDim.x)
         bad |= i == 0 ? a.cu_q[0] != 0 : a.cu_q[i] < a.cu_q[i - 1];
     for (int i = threadIdx.x; i <= a.G; i += blockDim.x)
         bad |= i == 0 ? a.cu_groups[0] != 0 : a.cu_groups[i] < a.cu_groups[i - 1];
     bad |= a.cu_q[a.B] != a.Tq || a.cu_groups[a.G] != a.B;
-    bad = __syncthreads_or(bad) != 0;
-    if (threadIdx.x == 0) ws[1] = bad ? KPOOL_STATUS_BAD_SEQLENS : 0;
-}
-
-__device__ __forceinline__ void load16(const uint16_t *row, int lane, float (&v)[16])
-{
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const uint4 x = *reinterpret_cast<const uint4 *>(row + 256 * k + 8 * lane);
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[8 * k + 2 * i] = __uint_as_float(w[i] << 16);
-            v[8 * k + 2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    if (__syncthreads_or(bad)) {
+        if (threadIdx.x == 0) {
+            w.head[H_STATUS] = KPOOL_STATUS_BAD_SEQLENS;
+            w.head[H_OK] = 0;
+            w.head[H_UNITS] = 0;
         }
+        return;
     }
-}
-
-__global__ void __launch_bounds__(256) rows_kernel(const PrefixMlaArgs a, int *ws)
-{
-    if (ws[1] & KPOOL_STATUS_BAD_SEQLENS) return;
-    const int lane = threadIdx.x & 31;
-    const int64_t row = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 5;
-    if (row >= a.Tq * a.H) return;
-    const int t = static_cast<int>(row / a.H);
-    const int b = segment_of(a.cu_q, a.B, t), g = segment_of(a.cu_groups, a.G, b);
-    auto table_row = [&](int seq) { return a.seq_ids != nullptr ? a.seq_ids[seq] : seq; };
-    auto length = [&](int r) {
-        const int64_t n = in_range(r, a.n_rows) ? a.seq_lens[r] : -1;
-        const int64_t room = static_cast<int64_t>(a.max_pages) * a.page_size;
+    const int64_t room = static_cast<int64_t>(a.max_pages) * a.page_size;
+    // a sequence's length, cut to what its table row holds
+    auto length_of = [&](int b, int *row) {
+        *row = a.seq_ids != nullptr ? a.seq_ids[b] : b;
+        int64_t n = -1;
+        if (in_range(*row, a.n_rows)) n = a.seq_lens[*row];
+        else *row = 0;
         if (n < 0 || n > room) {
-            if (lane == 0) atomicOr(ws + 1, KPOOL_STATUS_BAD_PAGE);
-            return static_cast<int>(n < 0 ? 0 : room);
+            atomicOr(&status, KPOOL_STATUS_BAD_PAGE);
+            n = n < 0 ? 0 : room;
         }
         return static_cast<int>(n);
     };
-    const int first = table_row(a.cu_groups[g]), own = table_row(b);
-    const int len = length(own);
-    const int shared = min(max(a.prefix_lens[g], 0), length(first));
-    const int vis = min(len, max(0, len - (a.cu_q[b + 1] - 1 - t)));
-    const uint16_t *kv = static_cast<const uint16_t *>(a.kv);
-    float q[16], acc[16], v[16];
-    load16(static_cast<const uint16_t *>(a.q) + row * kDc, lane, q);
+    for (int b = threadIdx.x; b < a.B; b += blockDim.x) {
+        const int g = segment_of(a.cu_groups, a.G, b);
+        int row;
+        w.len[b] = length_of(b, &row);
+        w.len[a.B + b] = min(max(a.prefix_lens[g], 0), length_of(a.cu_groups[g], &row));
+    }
+    __syncthreads();
+    // units of every group, then of every sequence
+    const int entities = a.G + a.B;
+    int64_t units = 0;
+    for (int base = 0; base < entities; base += blockDim.x) {
+        const int e = base + threadIdx.x;
+        int n = 0;
+        if (e < entities) {
+            const int b0 = e < a.G ? a.cu_groups[e] : e - a.G;
+            const int b1 = e < a.G ? a.cu_groups[e + 1] : b0 + 1;
+            n = static_cast<int>((static_cast<int64_t>(a.cu_q[b1] - a.cu_q[b0]) * a.H + kRows - 1) / kRows);
+        }
+        int64_t total;
+        const int64_t at = units + block_exclusive(n, scratch, &total);
+        if (e < entities) w.unit0[e] = static_cast<int>(at);
+        units += total;
+    }
+    __syncthreads();
+    for (int e = threadIdx.x >> 5; e < entities; e += blockDim.x >> 5) {
+        const int lane = threadIdx.x & 31;
+        const int b0 = e < a.G ? a.cu_groups[e] : e - a.G;
+        const int b1 = e < a.G ? a.cu_groups[e + 1] : b0 + 1;
+        const int row0 = a.cu_q[b0] * a.H, rows = a.cu_q[b1] * a.H - row0;
+        if (rows == 0) continue;
+        const int first = a.seq_ids != nullptr ? a.seq_ids[b0] : b0;
+        const int shared = w.len[a.B + b0], len = w.len[b0];
+        for (int k = lane; k * kRows < rows; k += 32) {
+            Unit u{};
+            u.row0 = row0 + k * kRows;
+            u.nrows = min(kRows, rows - k * kRows);
+            u.table_row = in_range(first, a.n_rows) ? first : 0;
+            if (e < a.G) {
+                u.t1 = shared;
+            } else {
+                // up to what the last of the rows' queries sees
+                const int last = (u.row0 + u.nrows - 1) / a.H;
+                u.t0 = shared;
+                u.t1 = len - (a.cu_q[b1] - 1 - last);
+            }
+            const int from = u.t0 / p.box * p.box;
+            u.tiles = u.t1 > u.t0 ? (u.t1 - from + kTile - 1) / kTile : 0;
+            w.unit[w.unit0[e] + k] = u;
+        }
+    }
+    // queries
+    for (int t = threadIdx.x; t < a.Tq; t += blockDim.x) {
+        const int b = segment_of(a.cu_q, a.B, t), g = segment_of(a.cu_groups, a.G, b);
+        Token x;
+        x.vis = max(0, w.len[b] - (a.cu_q[b + 1] - 1 - t));
+        x.pu = w.unit0[g];
+        x.prow0 = a.cu_q[a.cu_groups[g]] * a.H;
+        x.su = w.unit0[a.G + b];
+        x.srow0 = a.cu_q[b] * a.H;
+        w.tok[t] = x;
+    }
+    __syncthreads();
+    // the units' places in the work, and the even cut
+    int64_t work = 0;
+    for (int64_t base = 0; base < units; base += blockDim.x) {
+        const int64_t u = base + threadIdx.x;
+        const int n = u < units ? w.unit[u].tiles : 0;
+        int64_t total;
+        const int64_t at = work + block_exclusive(n > 0 ? n + kOverhead : 0, scratch, &total);
+        if (u < units) w.unit[u].w0 = at;
+        work += total;
+    }
+    const int64_t share = max(static_cast<int64_t>(1), (work + p.clusters - 1) / p.clusters);
+    for (int c = threadIdx.x; c < p.clusters; c += blockDim.x)
+        if (c * share >= work) w.first[c] = static_cast<int>(units);
+    __syncthreads();
+    int64_t rows = 0;
+    for (int64_t base = 0; base < units; base += blockDim.x) {
+        const int64_t u = base + threadIdx.x;
+        Unit x{};
+        int64_t c0 = 0;
+        int n = 0;
+        if (u < units) {
+            x = w.unit[u];
+            pieces_of(x, share, &c0, &n);
+            // the clusters whose share begins in this unit
+            if (x.tiles > 0)
+                for (int64_t c = (x.w0 + share - 1) / share; c * share < x.w0 + x.tiles + kOverhead; ++c)
+                    w.first[c] = static_cast<int>(u);
+        }
+        int64_t total;
+        const int64_t at = rows + block_exclusive(static_cast<int64_t>(n) * x.nrows, scratch, &total);
+        if (u < units) w.unit[u].out0 = at;
+        rows += total;
+    }
+    if (threadIdx.x == 0) {
+        *work_per_cluster(w) = share;
+        w.head[H_STATUS] = status;
+        w.head[H_OK] = 1;
+        w.head[H_UNITS] = static_cast<int>(units);
+    }
+}
+
+// ---- attend ------------------------------------------------------------------
+
+struct Sync {
+    volatile uint32_t *abort_flag;
+    int *status;
+    uint64_t limit_ns;
+};
+
+// Bounded mbarrier wait: completion, then the CTA abort flag, then a timer that
+// raises the flag and KPOOL_STATUS_TIMEOUT.
+template <bool kCluster>
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const Sync &sy)
+{
+    auto done = [&] { return kCluster ? ptx::mbar_try_wait_cluster(bar, parity) : ptx::mbar_try_wait(bar, parity); };
+    if (done()) return true;
+    const uint64_t t0 = ptx::globaltimer();
+    while (true) {
+#pragma unroll 1
+        for (int i = 0; i < 32; ++i)
+            if (done()) return true;
+        if (*sy.abort_flag) return false;
+        if (ptx::globaltimer() - t0 > sy.limit_ns) {
+            *sy.abort_flag = 1u;
+            atomicOr(sy.status, KPOOL_STATUS_TIMEOUT);
+            return false;
+        }
+    }
+}
+
+// All lanes wait; false when any of them gave up.
+__device__ __forceinline__ bool wait_bar_warp(uint32_t bar, uint32_t parity, const Sync &sy)
+{
+    const bool ok = wait_bar<false>(bar, parity, sy);
+    return __all_sync(kFull, ok);
+}
+
+// A wait for work in flight before the CTA ends: blind to the abort flag, and bounded.
+__device__ __forceinline__ void wait_landed(uint32_t bar, uint32_t parity)
+{
+    const uint64_t t0 = ptx::globaltimer();
+    while (!ptx::mbar_try_wait(bar, parity))
+        if (ptx::globaltimer() - t0 > kTimeoutNs) break;
+}
+
+// One cluster's share of a unit.
+struct Piece {
+    int row0, nrows, table_row, t0, t1;
+    int base, tiles;         // token at which its first tile begins; tiles
+    int64_t out;             // first partial row
+};
+
+struct Walk {
+    const Unit *unit;
+    int units, u, box;
+    int64_t cluster, share;
+
+    __device__ Walk(const Params &p, int c)
+        : unit(p.w.unit), units(p.w.head[H_UNITS]), box(p.box), cluster(c), share(0)
+    {
+        u = units > 0 ? p.w.first[c] : 0;
+        if (units > 0) share = *work_per_cluster(p.w);
+    }
+    __device__ bool next(Piece *q)
+    {
+        for (; u < units; ++u) {
+            const Unit x = unit[u];
+            if (x.tiles == 0) continue;
+            if (x.w0 >= (cluster + 1) * share) return false;
+            const int64_t begin = x.w0 + kOverhead;
+            const int64_t lo = max(begin, cluster * share), hi = min(begin + x.tiles, (cluster + 1) * share);
+            if (lo >= hi) continue;
+            q->row0 = x.row0;
+            q->nrows = x.nrows;
+            q->table_row = x.table_row;
+            q->t0 = x.t0;
+            q->t1 = x.t1;
+            q->base = x.t0 / box * box + static_cast<int>(lo - begin) * kTile;
+            q->tiles = static_cast<int>(hi - lo);
+            q->out = x.out0 + (cluster - begin / share) * x.nrows;
+            ++u;
+            return true;
+        }
+        return false;
+    }
+};
+
+// Tokens of the tile that begins at `base`, of those before t1.
+__device__ __forceinline__ int tile_tokens(const Piece &q, int base) { return min(kTile, q.t1 - base); }
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
+                  const __grid_constant__ Params p)
+{
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
+    const uint32_t sbase = ptx::smem_u32(smem);
+    const uint32_t sQ = sbase + kOffQ, sP = sbase + kOffP, sRing = sbase + kOffRing;
+    auto bar = [&](int i) { return sbase + kOffBar + 8 * i; };
+    uint32_t *misc = reinterpret_cast<uint32_t *>(smem + kOffMisc);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = ptx::cluster_ctarank();
+    const int cluster = blockIdx.x >> 1;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kSlots; ++i) {
+            ptx::mbar_init(bar(B_FULL + i), 1);
+            ptx::mbar_init(bar(B_READY + i), 2);             // a relay of each CTA
+            ptx::mbar_init(bar(B_EMPTY + i), 1);
+        }
+        ptx::mbar_init(bar(B_QFULL), 1);
+        ptx::mbar_init(bar(B_QREADY), 2);
+        ptx::mbar_init(bar(B_QEMPTY), 1);
+        ptx::mbar_init(bar(B_SFULL), 1);
+        ptx::mbar_init(bar(B_SFULL + 1), 1);
+        ptx::mbar_init(bar(B_PFULL), 2 * kSmWarps);          // the softmax warps of both CTAs
+        ptx::mbar_init(bar(B_PV), 1);
+        ptx::mbar_init(bar(B_DRAIN), 1);
+        misc[1] = 0u;
+        ptx::fence_mbar_init();
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc_pair(ptx::smem_u32(&misc[0]), kTmemCols);
+        ptx::tmem_relinquish_pair();
+        ptx::tc_fence_before();
+    }
+    __syncthreads();
+    ptx::cluster_sync();                 // no remote arrival before the peer's barriers exist
+    ptx::tc_fence_after();
+    const uint32_t tmem = misc[0];
+    const Sync sy{reinterpret_cast<volatile uint32_t *>(&misc[1]), p.w.head + H_STATUS, p.wait_limit_ns};
+    ptx::grid_dependents_launch();
+    ptx::grid_dependency_wait();         // the plan
+
+    if (warp == 0 || warp == 3) {
+        // ---------------- producers ----------------
+        const uint32_t odd = warp == 3;
+        const int box = p.box, ps = p.a.page_size;
+        if (lane == 0) {
+            ptx::tma_prefetch_desc(&tm_q);
+            ptx::tma_prefetch_desc(&tm_kv);
+        }
+        bool ok = true;
+        uint32_t g = 0;                  // chunks so far
+        uint32_t issued = 0;             // this lane 0's slots with a load: bit s, and its parity at bit 16 + s
+        uint32_t q_par = 0;
+        bool q_issued = false;
+        Walk walk(p, cluster);
+        Piece pc;
+        // page of each of a tile's boxes, lane j that of box j
+        auto pages_at = [&](int base) {
+            int page = 0;
+            if (lane * box < tile_tokens(pc, base)) {
+                page = __ldg(p.a.page_table + static_cast<int64_t>(pc.table_row) * p.a.max_pages + (base + lane * box) / ps);
+                if (!in_range(page, p.a.n_pages)) {
+                    atomicOr(sy.status, KPOOL_STATUS_BAD_PAGE);
+                    page = p.a.n_pages;  // out of the map's bounds: reads as zeros
+                }
+            }
+            return page;
+        };
+        // takes the next chunk's slot and announces `bytes` for it; the slot, or -1 for the other warp's chunk
+        auto take = [&](int bytes) {
+            const uint32_t s = g % kSlots, ph = (g / kSlots) & 1u;
+            const bool mine = (g & 1u) == odd;
+            ++g;
+            if (!mine || !ok) return -1;
+            ok = wait_bar_warp(bar(B_EMPTY + s), ph ^ 1u, sy);
+            if (!ok) return -1;
+            if (lane == 0) {
+                ptx::mbar_arrive_expect_tx(bar(B_FULL + s), bytes);
+                issued = (issued & ~(1u << (16 + s))) | 1u << s | ph << (16 + s);
+            }
+            __syncwarp();
+            return static_cast<int>(s);
+        };
+        auto scores_chunks = [&](int base, int page) {
+            // this CTA's 128 tokens, 64 columns at a time
+            const int n = max(0, min(128, tile_tokens(pc, base) - 128 * static_cast<int>(rank)));
+            const int boxes = (n + box - 1) / box;
+            const int at = 128 * static_cast<int>(rank) / box + lane;        // box of this lane
+            const int pg = __shfl_sync(kFull, page, at & 31);
+            const int y = (base + at * box) % ps;
+            for (int k = 0; k < 8 && ok; ++k) {
+                const int s = take(boxes * box * 128);
+                if (s >= 0 && lane < boxes)
+                    ptx::tma_load_3d(sRing + s * kChunk + lane * box * 128, &tm_kv, bar(B_FULL + s), 64 * k, y, pg);
+            }
+        };
+        auto values_chunks = [&](int base, int page) {
+            // 64 tokens x 128 of this CTA's 256 columns: lanes 2j and 2j + 1 bring
+            // the two 64-column halves of box j
+            const int n = tile_tokens(pc, base);
+            for (int kb = 0; 64 * kb < n && ok; ++kb) {
+                const int boxes = (min(64, n - 64 * kb) + box - 1) / box;
+                const int at = 64 * kb / box + (lane >> 1);
+                const int pg = __shfl_sync(kFull, page, at & 31);
+                const int y = (base + at * box) % ps;
+                for (int j = 0; j < 2 && ok; ++j) {
+                    const int s = take(2 * boxes * box * 128);
+                    if (s >= 0 && lane < 2 * boxes)
+                        ptx::tma_load_3d(sRing + s * kChunk + (lane & 1) * 8192 + (lane >> 1) * box * 128, &tm_kv,
+                                         bar(B_FULL + s), 256 * static_cast<int>(rank) + 128 * j + 64 * (lane & 1), y, pg);
+                }
+            }
+        };
+        uint32_t np = 0;                 // pieces so far
+        while (ok && walk.next(&pc)) {
+            int page = pages_at(pc.base);
+            if (!odd) {
+                ok = wait_bar_warp(bar(B_QEMPTY), (np & 1u) ^ 1u, sy);
+                if (!ok) break;
+                if (lane == 0) {
+                    ptx::mbar_arrive_expect_tx(bar(B_QFULL), 8 * 8192);
+                    q_issued = true;
+                    q_par = np & 1u;
+                }
+                __syncwarp();
+                if (lane < 8)
+                    ptx::tma_load_2d(sQ + lane * 8192, &tm_q, bar(B_QFULL), 64 * lane,
+                                     pc.row0 + kCtaRows * static_cast<int>(rank));
+            }
+            ++np;
+            scores_chunks(pc.base, page);
+            for (int i = 0; i < pc.tiles && ok; ++i) {
+                const int base = pc.base + i * kTile;
+                int next = 0;
+                if (i + 1 < pc.tiles) {
+                    next = pages_at(base + kTile);
+                    scores_chunks(base + kTile, next);
+                }
+                values_chunks(base, page);
+                page = next;
+            }
+        }
+        // no load may still be in flight when the CTA ends
+        if (lane == 0) {
+            for (int s = 0; s < kSlots; ++s)
+                if (issued >> s & 1u) wait_landed(bar(B_FULL + s), issued >> (16 + s) & 1u);
+            if (q_issued) wait_landed(bar(B_QFULL), q_par);
+        }
+    } else if (warp == 2) {
+        // ---------------- relay ----------------
+        bool ok = true;
+        uint32_t g = 0, np = 0;
+        Walk walk(p, cluster);
+        Piece pc;
+        auto pass = [&](int ready) {
+            if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(bar(ready), 0));
+        };
+        auto scores_chunks = [&]() {
+            for (int k = 0; k < 8 && ok; ++k, ++g) {
+                const uint32_t s = g % kSlots;
+                ok = wait_bar_warp(bar(B_FULL + s), (g / kSlots) & 1u, sy);
+                if (ok) pass(B_READY + s);
+            }
+        };
+        auto values_chunks = [&](int base) {
+            const int n = tile_tokens(pc, base), lo = pc.t0 - base;
+            for (int c = 0; 32 * (c & ~1) < n && ok; ++c, ++g) {
+                const uint32_t s = g % kSlots;
+                ok = wait_bar_warp(bar(B_FULL + s), (g / kSlots) & 1u, sy);
+                if (!ok) break;
+                // rows of the chunk outside the span, up to the last 16 that the MMAs read
+                const int first = 64 * (c >> 1);
+                const int cut0 = min(64, lo - first), cut1 = n - first;
+                if (cut0 > 0 || cut1 < 64) {
+                    const int end = (min(64, cut1) + 15) & ~15;
+                    for (int r = lane >> 4; r < end; r += 2)
+                        if (r < cut0 || r >= cut1)
+                            ptx::st_shared_v4(sRing + s * kChunk + (lane >> 3 & 1) * 8192 + r * 128 + (lane & 7) * 16, 0u,
+                                              0u, 0u, 0u);
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                pass(B_READY + s);
+            }
+        };
+        while (ok && walk.next(&pc)) {
+            ok = wait_bar_warp(bar(B_QFULL), np & 1u, sy);
+            if (!ok) break;
+            pass(B_QREADY);
+            ++np;
+            scores_chunks();
+            for (int i = 0; i < pc.tiles && ok; ++i) {
+                if (i + 1 < pc.tiles) scores_chunks();
+                if (ok) values_chunks(pc.base + i * kTile);
+            }
+        }
+    } else if (warp == 1) {
+        // ---------------- MMA issuer ----------------
+        if (rank == 0 && lane == 0) {
+            constexpr uint32_t idesc_s = ptx::make_idesc(1u, kRows, kTile);
+            constexpr uint32_t idesc_o = idesc_s | ptx::kIdescBMajorMN;
+            bool ok = true, any = false;
+            uint32_t g = 0, np = 0;
+            uint32_t gs = 0, gp = 0;     // score tiles and output tiles so far
+            Walk walk(p, cluster);
+            Piece pc;
+            auto scores = [&](bool last) {
+                for (int k = 0; k < 8; ++k, ++g) {
+                    const uint32_t s = g % kSlots;
+                    ok = wait_bar<true>(bar(B_READY + s), (g / kSlots) & 1u, sy);
+                    if (!ok) return;
+                    ptx::tc_fence_after();
+                    const uint64_t ad = ptx::smem_desc_sw128(sQ + k * 8192);
+                    const uint64_t bd = ptx::smem_desc_sw128(sRing + s * kChunk);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        ptx::mma_bf16_pair(tmem + kTmemS + (gs & 1u) * 128, ad + 2 * kk, bd + 2 * kk, idesc_s,
+                                           (k | kk) != 0);
+                    any = true;
+                    ptx::mma_commit_pair(bar(B_EMPTY + s));
+                }
+                ptx::mma_commit_pair(bar(B_SFULL + (gs & 1u)));
+                if (last) ptx::mma_commit_pair(bar(B_QEMPTY));
+                ++gs;
+            };
+            auto output = [&](int n, bool first) {
+                ok = wait_bar<true>(bar(B_PFULL), gp & 1u, sy);
+                if (!ok) return;
+                ptx::tc_fence_after();
+                for (int c = 0; 32 * (c & ~1) < n; ++c, ++g) {
+                    const uint32_t s = g % kSlots;
+                    ok = wait_bar<true>(bar(B_READY + s), (g / kSlots) & 1u, sy);
+                    if (!ok) return;
+                    ptx::tc_fence_after();
+                    const int kb = c >> 1, steps = min(4, (n - 64 * kb + 15) / 16);
+                    const uint64_t ad = ptx::smem_desc_sw128(sP + kb * 8192);
+                    const uint64_t bd = ptx::smem_desc_mn_sw128(sRing + s * kChunk, 8192);
+                    for (int kk = 0; kk < steps; ++kk)
+                        ptx::mma_bf16_pair(tmem + (c & 1) * 128, ad + 2 * kk, bd + 128 * kk, idesc_o,
+                                           !first || kb > 0 || kk > 0);
+                    ptx::mma_commit_pair(bar(B_EMPTY + s));
+                }
+                ptx::mma_commit_pair(bar(B_PV));
+                ++gp;
+            };
+            while (ok && walk.next(&pc)) {
+                ok = wait_bar<true>(bar(B_QREADY), np & 1u, sy);
+                if (!ok) break;
+                ++np;
+                scores(pc.tiles == 1);
+                for (int i = 0; i < pc.tiles && ok; ++i) {
+                    if (i + 1 < pc.tiles) scores(i + 2 == pc.tiles);
+                    if (ok) output(tile_tokens(pc, pc.base + i * kTile), i == 0);
+                }
+            }
+            if (any) {
+                // to this CTA alone: nothing of the pair's MMAs is in flight once it arrives
+                ptx::mma_commit_pair(bar(B_DRAIN));
+                wait_landed(bar(B_DRAIN), 0);
+            }
+        }
+    } else {
+        // ---------------- softmax and output ----------------
+        const int sw = warp - 4;
+        const int quarter = warp & 3;                 // lanes 32 * quarter .. of tensor memory
+        const int half = quarter >> 1;                // tokens 128 * half .. of the tile, columns 256 * half .. of the output
+        const int part = sw >> 2;                     // 64 of those tokens, 128 of those columns
+        const int r = 32 * (quarter & 1) + lane;      // row of this CTA
+        const int x0 = 128 * half + 64 * part;        // first of this thread's tokens
+        const int group = quarter & 1;                // the four warps that share rows
+        const int member = 2 * part + half;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
+        float *red = reinterpret_cast<float *>(smem + kOffRed);
+        volatile uint32_t *words = reinterpret_cast<volatile uint32_t *>(smem + kOffWord) + 8 * group;
+        const uint32_t prow = sP + (2 * half + part) * 8192 + r * 128;
+        const uint32_t p_full = ptx::map_to_rank(bar(B_PFULL), 0);
+        const float c = p.c_scale;
+        bool ok = true;
+        uint32_t gt = 0, rounds = 0;
+        // the four warps pass each agreement together: 0 in the common round,
+        // else all of their words
+        auto agree = [&](uint32_t word) {
+            if (!ptx::named_bar_or(1 + group, 128, word != 0u)) return 0u;
+            volatile uint32_t *f = words + 4 * (rounds & 1u);
+            ++rounds;
+            if (lane == 0) f[member] = word;
+            ptx::named_bar_sync(3 + group, 128);
+            return f[0] | f[1] | f[2] | f[3];
+        };
+        Walk walk(p, cluster);
+        Piece pc;
+        bool stop = false;
+        while (!stop && walk.next(&pc)) {
+            const int row = kCtaRows * static_cast<int>(rank) + r;        // of the unit
+            const int vis = row < pc.nrows ? p.w.tok[(pc.row0 + row) / p.a.H].vis : 0;
+            const int end = min(pc.t1, vis);
+            float m = -INFINITY, l = 0.f;
+            for (int i = 0; i < pc.tiles; ++i, ++gt) {
+                const int base = pc.base + i * kTile;
+                ok = ok && wait_bar_warp(bar(B_SFULL + (gt & 1u)), (gt >> 1) & 1u, sy);
+                ptx::tc_fence_after();
+                float v[64];
+                {
+                    uint32_t a0[32], a1[32];
+                    const uint32_t at = lanes + kTmemS + (gt & 1u) * 128 + 64 * part;
+                    ptx::tmem_ld32(at, a0);
+                    ptx::tmem_ld32(at + 32, a1);
+                    ptx::tmem_ld_wait2(a0, a1);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        v[k] = __uint_as_float(a0[k]);
+                        v[32 + k] = __uint_as_float(a1[k]);
+                    }
+                }
+                // tokens lo .. hi - 1 of this thread's 64 count
+                const int lo = pc.t0 - base - x0, hi = end - base - x0;
+                if (__any_sync(kFull, lo > 0 || hi < 64)) {
+#pragma unroll
+                    for (int k = 0; k < 64; ++k) v[k] = (k >= lo && k < hi) ? v[k] : -INFINITY;
+                }
+                float top = fmaxf(v[0], v[1]);
+#pragma unroll
+                for (int k = 2; k < 64; ++k) top = fmaxf(top, v[k]);
+                const bool need = top * c > m + kRescale;
+                const uint32_t all = agree((ok ? 0u : 1u) | (__any_sync(kFull, need) ? 2u : 0u));
+                if (all & 1u) {
+                    stop = true;
+                    break;
+                }
+                if (all & 2u) {
+                    // the row's exact maximum so far becomes the reference
+                    red[member * kCtaRows + r] = top;
+                    ptx::named_bar_sync(3 + group, 128);
+                    const float t4 = fmaxf(fmaxf(red[r], red[kCtaRows + r]),
+                                           fmaxf(red[2 * kCtaRows + r], red[3 * kCtaRows + r]));
+                    const float mn = fmaxf(m, t4 * c);
+                    const float f = mn == -INFINITY ? 1.f : ptx::ex2_approx(m - mn);
+                    m = mn;
+                    l *= f;
+                    if (i > 0) {
+                        // the output so far, once its MMAs are done
+                        ok = wait_bar_warp(bar(B_PV), (gt - 1u) & 1u, sy);
+                        ptx::tc_fence_after();
+                        if (__any_sync(kFull, f != 1.f)) {
+#pragma unroll 1
+                            for (int k = 0; k < 4; ++k) {
+                                uint32_t o[32];
+                                const uint32_t at = lanes + 128 * part + 32 * k;
+                                ptx::tmem_ld32(at, o);
+                                ptx::tmem_ld_wait(o);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                ptx::tmem_st32(at, o);
+                            }
+                            ptx::tmem_st_wait();
+                        }
+                    }
+                    ptx::named_bar_sync(3 + group, 128);      // red is read
+                }
+                const float ref = m == -INFINITY ? 0.f : m;
+                float sum = 0.f;
+#pragma unroll
+                for (int k = 0; k < 64; ++k) {
+                    v[k] = ptx::ex2_approx(fmaf(v[k], c, -ref));
+                    sum += v[k];
+                }
+                l += sum;
+                // P is free once the previous tile's output MMAs are done
+                if (gt > 0) ok = wait_bar_warp(bar(B_PV), (gt - 1u) & 1u, sy) && ok;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    uint32_t w4[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const __nv_bfloat162 b2 = __floats2bfloat162_rn(v[8 * k + 2 * e], v[8 * k + 2 * e + 1]);
+                        w4[e] = *reinterpret_cast<const uint32_t *>(&b2);
+                    }
+                    ptx::st_shared_v4(prow + ((k ^ (r & 7)) << 4), w4[0], w4[1], w4[2], w4[3]);
+                }
+                ptx::fence_proxy_async_smem();
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive_cluster(p_full);
+            }
+            if (stop) break;
+            // the piece's rows: sum over the four threads of each, then the output
+            red[member * kCtaRows + r] = l;
+            ok = wait_bar_warp(bar(B_PV), (gt - 1u) & 1u, sy) && ok;
+            ptx::named_bar_sync(3 + group, 128);
+            l = (red[r] + red[kCtaRows + r]) + (red[2 * kCtaRows + r] + red[3 * kCtaRows + r]);
+            ptx::named_bar_sync(3 + group, 128);
+            ptx::tc_fence_after();
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+            float *out = p.w.o + (pc.out + row) * kDc + 256 * half + 128 * part;
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k) {
+                uint32_t o[32];
+                ptx::tmem_ld32(lanes + 128 * part + 32 * k, o);
+                ptx::tmem_ld_wait(o);
+                if (row < pc.nrows) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        *reinterpret_cast<float4 *>(out + 32 * k + e) =
+                            make_float4(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv,
+                                        __uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+                }
+            }
+            if (member == 0 && row < pc.nrows) p.w.lse[pc.out + row] = l > 0.f ? m + log2f(l) : -INFINITY;
+            ptx::tc_fence_before();
+        }
+    }
+
+    // neither CTA ends while the other may still signal it or read its memory
+    __syncthreads();
+    __syncwarp();
+    ptx::cluster_sync();
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc_pair(tmem, kTmemCols);
+    }
+    ptx::cluster_sync();
+}
+
+// ---- combine -----------------------------------------------------------------
+
+__global__ void __launch_bounds__(256) combine_kernel(const Params p)
+{
+    ptx::grid_dependency_wait();
+    if (!p.w.head[H_OK]) return;
+    const int lane = threadIdx.x & 31;
+    const int64_t row = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 5;
+    if (row >= p.a.Tq * p.a.H) return;
+    const Token x = p.w.tok[row / p.a.H];
+    const int64_t share = *work_per_cluster(p.w);
+    float m = -INFINITY, l = 0.f;
+    float acc[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-    float m = -INFINITY, l = 0.f;
-    const float c = a.scale * 1.44269504088896341f;
-    for (int j = 0; j < vis; ++j) {
-        const int r = j < shared ? first : own;
-        const int page = a.page_table[static_cast<int64_t>(r) * a.max_pages + j / a.page_size];
-        if (!in_range(page, a.n_pages)) {
-            if (lane == 0) atomicOr(ws + 1, KPOOL_STATUS_BAD_PAGE);
-            continue;
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+        const int k = static_cast<int>(row - (side ? x.srow0 : x.prow0));
+        const Unit u = p.w.unit[(side ? x.su : x.pu) + k / kRows];
+        int64_t c0;
+        int n;
+        pieces_of(u, share, &c0, &n);
+        for (int i = 0; i < n; ++i) {
+            const int64_t at = u.out0 + static_cast<int64_t>(i) * u.nrows + k % kRows;
+            const float s = p.w.lse[at];
+            if (s == -INFINITY) continue;
+            const float mn = fmaxf(m, s);
+            const float f = ptx::ex2_approx(m - mn), g = ptx::ex2_approx(s - mn);
+            m = mn;
+            l = l * f + g;
+            const float4 *o = reinterpret_cast<const float4 *>(p.w.o + at * kDc);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float4 y = __ldcg(o + 32 * q + lane);
+                acc[4 * q] = acc[4 * q] * f + y.x * g;
+                acc[4 * q + 1] = acc[4 * q + 1] * f + y.y * g;
+                acc[4 * q + 2] = acc[4 * q + 2] * f + y.z * g;
+                acc[4 * q + 3] = acc[4 * q + 3] * f + y.w * g;
+            }
         }
-        load16(kv + page * a.kv_page_stride + (j % a.page_size) * kDc, lane, v);
-        float s = 0.f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s = fmaf(q[i], v[i], s);
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(kFull, s, d);
-        s *= c;
-        if (s > m) {
-            const float f = ptx::ex2_approx(m - s);
-            l *= f;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) acc[i] *= f;
-            m = s;
-        }
-        const float p = ptx::ex2_approx(s - m);
-        l += p;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[i] = fmaf(p, v[i], acc[i]);
     }
     const float inv = l > 0.f ? 1.f / l : 0.f;
-    uint16_t *o = static_cast<uint16_t *>(a.o) + row * kDc;
+    uint2 *out = reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.a.o) + row * kDc);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 x = __floats2bfloat162_rn(acc[8 * k + 2 * i] * inv, acc[8 * k + 2 * i + 1] * inv);
-            w[i] = *reinterpret_cast<const uint32_t *>(&x);
-        }
-        *reinterpret_cast<uint4 *>(o + 256 * k + 8 * lane) = make_uint4(w[0], w[1], w[2], w[3]);
+    for (int q = 0; q < 4; ++q) {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(acc[4 * q] * inv, acc[4 * q + 1] * inv);
+        const __nv_bfloat162 b = __floats2bfloat162_rn(acc[4 * q + 2] * inv, acc[4 * q + 3] * inv);
+        out[32 * q + lane] = make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
     }
-    if (lane == 0) a.lse[row] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+    if (lane == 0) p.a.lse[row] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
+
+// ---- host --------------------------------------------------------------------
+
+int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+
+// Lays the workspace out from `base` (NULL to size it); the bytes it takes.
+size_t lay_out(Work *w, uint8_t *base, int64_t Tq, int H, int B, int G, int clusters)
+{
+    const int64_t rows = Tq * H;
+    const int64_t units = 2 * (rows / kRows) + std::min<int64_t>(G, Tq) + std::min<int64_t>(B, Tq);
+    // every row in one piece of its shared and one of its own tokens, and at
+    // most one more piece per cluster
+    const int64_t partial = 2 * rows + static_cast<int64_t>(clusters) * kRows;
+    int64_t at = 0;
+    auto take = [&](int64_t bytes) {
+        uint8_t *q = base + at;
+        at += round_up(bytes, 256);
+        return q;
+    };
+    w->head = reinterpret_cast<int *>(take(4 * H_INTS));
+    w->tok = reinterpret_cast<Token *>(take(Tq * static_cast<int64_t>(sizeof(Token))));
+    w->unit0 = reinterpret_cast<int *>(take(4 * (static_cast<int64_t>(G) + B)));
+    w->len = reinterpret_cast<int *>(take(8 * static_cast<int64_t>(B)));
+    w->first = reinterpret_cast<int *>(take(4 * clusters));
+    w->unit = reinterpret_cast<Unit *>(take(units * static_cast<int64_t>(sizeof(Unit))));
+    w->lse = reinterpret_cast<float *>(take(4 * partial));
+    w->o = reinterpret_cast<float *>(take(4 * kDc * partial));
+    return static_cast<size_t>(at);
+}
+
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), int grid, int threads, int smem, cudaStream_t s, const A &...args)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// CTA pairs: one per two SMs.  (The size must not depend on the device that a
+// caller sizes its workspace on, so it is bounded rather than exact there.)
+constexpr int kMaxClusters = 80;
+int clusters() { return std::max(1, std::min(kMaxClusters, num_sms() / 2)); }
 
 }  // namespace
 
-size_t prefix_mla_workspace_bytes(int64_t, int, int, int) { return 256; }
+size_t prefix_mla_workspace_bytes(int64_t Tq, int H, int B, int G)
+{
+    Work w;
+    return lay_out(&w, nullptr, Tq, H, B, G, kMaxClusters);
+}
 
 int run_prefix_mla(const PrefixMlaArgs &a, cudaStream_t s)
 {
-    int *ws = static_cast<int *>(a.workspace);
-    check_kernel<<<1, 1024, 0, s>>>(a, ws);
-    KPOOL_CUDA_CHECK(cudaGetLastError());
+    Params p{};
+    p.a = a;
+    p.clusters = clusters();
+    lay_out(&p.w, static_cast<uint8_t *>(a.workspace), a.Tq, a.H, a.B, a.G, kMaxClusters);
+    p.box = std::min(a.page_size, 64);
+    p.c_scale = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
+    p.wait_limit_ns = get_wait_limit_ns();
     const int64_t rows = a.Tq * a.H;
-    if (rows > 0) rows_kernel<<<static_cast<unsigned>((rows + 7) / 8), 256, 0, s>>>(a, ws);
+    CUtensorMap mq, mkv;
+    if (rows > 0) {
+        int rc = encode_bf16_tmap(&mq, a.q, kDc, static_cast<uint64_t>(rows), kCtaRows);
+        if (rc) return rc;
+        rc = encode_bf16_pages_tmap(&mkv, a.kv, kDc, a.page_size, a.n_pages, a.kv_page_stride, p.box);
+        if (rc) return rc;
+        KPOOL_CUDA_CHECK(
+            cudaFuncSetAttribute(attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes));
+    }
+    plan_kernel<<<1, kPlanThreads, 0, s>>>(p);
     KPOOL_CUDA_CHECK(cudaGetLastError());
+    if (rows == 0) return KPOOL_OK;
+    KPOOL_CUDA_CHECK(launch_after(attend_kernel, 2 * p.clusters, kThreads, kSmemBytes, s, mq, mkv, p));
+    KPOOL_CUDA_CHECK(launch_after(combine_kernel, static_cast<int>((rows + 7) / 8), 256, 0, s, p));
     return KPOOL_OK;
 }
 

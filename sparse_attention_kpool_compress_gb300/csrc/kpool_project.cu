@@ -411,6 +411,23 @@ int encode_bf16_tmap(CUtensorMap *m, const void *base, uint64_t cols, uint64_t r
     return encode_bf16_2d(m, base, cols, rows, box_rows);
 }
 
+int encode_bf16_pages_tmap(CUtensorMap *m, const void *base, uint64_t cols, uint64_t rows, uint64_t pages,
+                           uint64_t page_stride, uint32_t box_rows)
+{
+    EncodeTiledFnP enc = get_encode_p();
+    if (!enc) return fail(KPOOL_ERR_CUDA, "cuTensorMapEncodeTiled entry point unavailable");
+    const cuuint64_t gdim[3] = {cols, rows, pages};
+    const cuuint64_t gstride[2] = {cols * 2, page_stride * 2};
+    const cuuint32_t box[3] = {64, box_rows, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), gdim,
+                           gstride, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(KPOOL_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+    return KPOOL_OK;
+}
+
 int run_project_compress(const ProjectArgs &a, cudaStream_t s)
 {
     KPOOL_CUDA_CHECK(cudaMemsetAsync(a.status, 0, sizeof(int), s));
