@@ -35,9 +35,10 @@
 // no room for.)
 //   warps 0, 3   TMA producers, chunks in turn (one warp alone issues too slowly)
 //   warp 1       MMA issuer (CTA 0)
-//   warp 2       relay: clears what lies outside the span in a chunk of values,
-//                so that nothing there, NaN included, meets a weight of 0, and
-//                passes the chunk on to the issuer
+//   warp 2       relay: in a chunk of values that reaches outside the span, clears
+//                those rows, so that nothing there, NaN included, meets a weight
+//                of 0, and passes it on to the issuer (all other loads complete
+//                on CTA 0's barriers directly)
 //   warps 4-11   softmax and output: thread (lane, half of the columns) has 64
 //                of a row's 256 scores
 #include <cuda_bf16.h>
@@ -60,6 +61,7 @@ constexpr int kSmWarps = 8;
 constexpr int kPlanThreads = 1024;
 constexpr float kRescale = 8.f;          // headroom of the reference maximum (log2)
 constexpr uint64_t kTimeoutNs = 2000000000ull;
+constexpr uint64_t kLandNs = 2000000ull;
 constexpr uint32_t kFull = 0xFFFFFFFFu;
 constexpr int kTmemCols = 512;           // O: 0..255, S: 256..383 and 384..511
 constexpr int kTmemS = 256;
@@ -74,7 +76,7 @@ constexpr int kOffRed = kOffRing + kSlots * kChunk;  // [4][64] floats
 constexpr int kOffWord = kOffRed + 4 * kCtaRows * 4; // agreement words [2 groups][2][4]
 constexpr int kOffBar = kOffWord + 64;
 enum {
-    B_FULL = 0, B_READY = B_FULL + kSlots, B_EMPTY = B_READY + kSlots, B_QFULL = B_EMPTY + kSlots, B_QREADY,
+    B_FULL = 0, B_EDGE = B_FULL + kSlots, B_EMPTY = B_EDGE + kSlots, B_QFULL = B_EMPTY + kSlots,
     B_QEMPTY, B_SFULL, B_PFULL = B_SFULL + 2, B_PV, B_DRAIN, N_BARS
 };
 constexpr int kOffMisc = kOffBar + N_BARS * 8;     // [0] tmem base, [1] abort flag
@@ -114,8 +116,10 @@ struct Params {
     PrefixMlaArgs a;
     Work w;
     int clusters;
-    int box;                 // rows of a TMA box
+    int box, box_log;        // rows of a TMA box, and its logarithm
+    int page_log;
     float c_scale;           // softmax scale * log2(e)
+    int wait_tries;
     uint64_t wait_limit_ns;
 };
 
@@ -313,6 +317,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p)
 struct Sync {
     volatile uint32_t *abort_flag;
     int *status;
+    int tries;               // before the timer is read
     uint64_t limit_ns;
 };
 
@@ -322,12 +327,13 @@ template <bool kCluster>
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const Sync &sy)
 {
     auto done = [&] { return kCluster ? ptx::mbar_try_wait_cluster(bar, parity) : ptx::mbar_try_wait(bar, parity); };
-    if (done()) return true;
+    // (the timer is slow to read: it would add its latency to each hop of the pipeline)
+#pragma unroll 1
+    for (int i = 0; i < sy.tries; ++i)
+        if (done()) return true;
     const uint64_t t0 = ptx::globaltimer();
     while (true) {
-#pragma unroll 1
-        for (int i = 0; i < 32; ++i)
-            if (done()) return true;
+        if (done()) return true;
         if (*sy.abort_flag) return false;
         if (ptx::globaltimer() - t0 > sy.limit_ns) {
             *sy.abort_flag = 1u;
@@ -338,9 +344,10 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const Sy
 }
 
 // All lanes wait; false when any of them gave up.
+template <bool kCluster = false>
 __device__ __forceinline__ bool wait_bar_warp(uint32_t bar, uint32_t parity, const Sync &sy)
 {
-    const bool ok = wait_bar<false>(bar, parity, sy);
+    const bool ok = wait_bar<kCluster>(bar, parity, sy);
     return __all_sync(kFull, ok);
 }
 
@@ -357,6 +364,15 @@ struct Piece {
     int row0, nrows, table_row, t0, t1;
     int base, tiles;         // token at which its first tile begins; tiles
     int64_t out;             // first partial row
+
+    // what the MMA issuer reads, broadcast to be the same in all lanes
+    __device__ void uniform()
+    {
+        t0 = __shfl_sync(kFull, t0, 0);
+        t1 = __shfl_sync(kFull, t1, 0);
+        base = __shfl_sync(kFull, base, 0);
+        tiles = __shfl_sync(kFull, tiles, 0);
+    }
 };
 
 struct Walk {
@@ -384,7 +400,7 @@ struct Walk {
             q->table_row = x.table_row;
             q->t0 = x.t0;
             q->t1 = x.t1;
-            q->base = x.t0 / box * box + static_cast<int>(lo - begin) * kTile;
+            q->base = (x.t0 & -box) + static_cast<int>(lo - begin) * kTile;
             q->tiles = static_cast<int>(hi - lo);
             q->out = x.out0 + (cluster - begin / share) * x.nrows;
             ++u;
@@ -397,6 +413,13 @@ struct Walk {
 // Tokens of the tile that begins at `base`, of those before t1.
 __device__ __forceinline__ int tile_tokens(const Piece &q, int base) { return min(kTile, q.t1 - base); }
 
+// Does the chunk of values that holds tokens 64 kb .. of the tile at `base` have
+// rows outside the span?
+__device__ __forceinline__ bool has_edge(const Piece &q, int base, int kb)
+{
+    return q.t0 - base > 64 * kb || tile_tokens(q, base) < 64 * kb + 64;
+}
+
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
                   const __grid_constant__ Params p)
@@ -407,22 +430,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t sQ = sbase + kOffQ, sP = sbase + kOffP, sRing = sbase + kOffRing;
     auto bar = [&](int i) { return sbase + kOffBar + 8 * i; };
     uint32_t *misc = reinterpret_cast<uint32_t *>(smem + kOffMisc);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = ptx::cluster_ctarank();
+    // (a broadcast, so that the compiler sees that a warp takes one role together)
+    const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const uint32_t rank = blockIdx.x & 1u;             // of the CTA in its pair
     const int cluster = blockIdx.x >> 1;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kSlots; ++i) {
-            ptx::mbar_init(bar(B_FULL + i), 1);
-            ptx::mbar_init(bar(B_READY + i), 2);             // a relay of each CTA
+            ptx::mbar_init(bar(B_FULL + i), 2);              // CTA 0's: a producer or relay of each CTA
+            ptx::mbar_init(bar(B_EDGE + i), 1);
             ptx::mbar_init(bar(B_EMPTY + i), 1);
         }
-        ptx::mbar_init(bar(B_QFULL), 1);
-        ptx::mbar_init(bar(B_QREADY), 2);
+        ptx::mbar_init(bar(B_QFULL), 2);                     // CTA 0's
         ptx::mbar_init(bar(B_QEMPTY), 1);
         ptx::mbar_init(bar(B_SFULL), 1);
         ptx::mbar_init(bar(B_SFULL + 1), 1);
-        ptx::mbar_init(bar(B_PFULL), 2 * kSmWarps);          // the softmax warps of both CTAs
+        ptx::mbar_init(bar(B_PFULL), 2 * kSmWarps);          // CTA 0's: the softmax warps of both
         ptx::mbar_init(bar(B_PV), 1);
         ptx::mbar_init(bar(B_DRAIN), 1);
         misc[1] = 0u;
@@ -436,31 +459,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncthreads();
     ptx::cluster_sync();                 // no remote arrival before the peer's barriers exist
     ptx::tc_fence_after();
-    const uint32_t tmem = misc[0];
-    const Sync sy{reinterpret_cast<volatile uint32_t *>(&misc[1]), p.w.head + H_STATUS, p.wait_limit_ns};
+    const uint32_t tmem = __shfl_sync(kFull, misc[0], 0);
+    const Sync sy{reinterpret_cast<volatile uint32_t *>(&misc[1]), p.w.head + H_STATUS, p.wait_tries, p.wait_limit_ns};
     ptx::grid_dependents_launch();
     ptx::grid_dependency_wait();         // the plan
 
     if (warp == 0 || warp == 3) {
         // ---------------- producers ----------------
         const uint32_t odd = warp == 3;
-        const int box = p.box, ps = p.a.page_size;
+        const int box = p.box, bl = p.box_log, pl = p.page_log, in_page = p.a.page_size - 1;
         if (lane == 0) {
             ptx::tma_prefetch_desc(&tm_q);
             ptx::tma_prefetch_desc(&tm_kv);
         }
         bool ok = true;
         uint32_t g = 0;                  // chunks so far
-        uint32_t issued = 0;             // this lane 0's slots with a load: bit s, and its parity at bit 16 + s
-        uint32_t q_par = 0;
-        bool q_issued = false;
         Walk walk(p, cluster);
         Piece pc;
         // page of each of a tile's boxes, lane j that of box j
         auto pages_at = [&](int base) {
             int page = 0;
             if (lane * box < tile_tokens(pc, base)) {
-                page = __ldg(p.a.page_table + static_cast<int64_t>(pc.table_row) * p.a.max_pages + (base + lane * box) / ps);
+                page = __ldg(p.a.page_table + static_cast<int64_t>(pc.table_row) * p.a.max_pages + ((base + lane * box) >> pl));
                 if (!in_range(page, p.a.n_pages)) {
                     atomicOr(sy.status, KPOOL_STATUS_BAD_PAGE);
                     page = p.a.n_pages;  // out of the map's bounds: reads as zeros
@@ -468,32 +488,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             return page;
         };
-        // takes the next chunk's slot and announces `bytes` for it; the slot, or -1 for the other warp's chunk
-        auto take = [&](int bytes) {
+        // takes the next chunk's slot and announces `bytes` for it, to CTA 0 or, for
+        // a chunk with rows to clear, to this CTA's relay; the slot, or -1 for the
+        // other warp's chunk
+        uint32_t to = 0;
+        auto take = [&](int bytes, bool edge) {
             const uint32_t s = g % kSlots, ph = (g / kSlots) & 1u;
             const bool mine = (g & 1u) == odd;
             ++g;
             if (!mine || !ok) return -1;
             ok = wait_bar_warp(bar(B_EMPTY + s), ph ^ 1u, sy);
             if (!ok) return -1;
-            if (lane == 0) {
-                ptx::mbar_arrive_expect_tx(bar(B_FULL + s), bytes);
-                issued = (issued & ~(1u << (16 + s))) | 1u << s | ph << (16 + s);
-            }
+            to = edge ? ptx::map_to_rank(bar(B_EDGE + s), rank) : ptx::map_to_rank(bar(B_FULL + s), 0);
+            if (lane == 0) ptx::mbar_arrive_expect_tx_cluster(to, bytes);
             __syncwarp();
             return static_cast<int>(s);
         };
         auto scores_chunks = [&](int base, int page) {
             // this CTA's 128 tokens, 64 columns at a time
             const int n = max(0, min(128, tile_tokens(pc, base) - 128 * static_cast<int>(rank)));
-            const int boxes = (n + box - 1) / box;
-            const int at = 128 * static_cast<int>(rank) / box + lane;        // box of this lane
+            const int boxes = (n + box - 1) >> bl;
+            const int at = (128 * static_cast<int>(rank) >> bl) + lane;        // box of this lane
             const int pg = __shfl_sync(kFull, page, at & 31);
-            const int y = (base + at * box) % ps;
+            const int y = (base + at * box) & in_page;
             for (int k = 0; k < 8 && ok; ++k) {
-                const int s = take(boxes * box * 128);
+                const int s = take(boxes * box * 128, false);
                 if (s >= 0 && lane < boxes)
-                    ptx::tma_load_3d(sRing + s * kChunk + lane * box * 128, &tm_kv, bar(B_FULL + s), 64 * k, y, pg);
+                    ptx::tma_load_3d_pair(sRing + s * kChunk + lane * box * 128, &tm_kv, to, 64 * k, y, pg);
             }
         };
         auto values_chunks = [&](int base, int page) {
@@ -501,15 +522,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // the two 64-column halves of box j
             const int n = tile_tokens(pc, base);
             for (int kb = 0; 64 * kb < n && ok; ++kb) {
-                const int boxes = (min(64, n - 64 * kb) + box - 1) / box;
-                const int at = 64 * kb / box + (lane >> 1);
+                const int boxes = (min(64, n - 64 * kb) + box - 1) >> bl;
+                const bool edge = has_edge(pc, base, kb);
+                const int at = (64 * kb >> bl) + (lane >> 1);
                 const int pg = __shfl_sync(kFull, page, at & 31);
-                const int y = (base + at * box) % ps;
+                const int y = (base + at * box) & in_page;
                 for (int j = 0; j < 2 && ok; ++j) {
-                    const int s = take(2 * boxes * box * 128);
+                    const int s = take(2 * boxes * box * 128, edge);
                     if (s >= 0 && lane < 2 * boxes)
-                        ptx::tma_load_3d(sRing + s * kChunk + (lane & 1) * 8192 + (lane >> 1) * box * 128, &tm_kv,
-                                         bar(B_FULL + s), 256 * static_cast<int>(rank) + 128 * j + 64 * (lane & 1), y, pg);
+                        ptx::tma_load_3d_pair(sRing + s * kChunk + (lane & 1) * 8192 + (lane >> 1) * box * 128, &tm_kv, to,
+                                              256 * static_cast<int>(rank) + 128 * j + 64 * (lane & 1), y, pg);
                 }
             }
         };
@@ -519,15 +541,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (!odd) {
                 ok = wait_bar_warp(bar(B_QEMPTY), (np & 1u) ^ 1u, sy);
                 if (!ok) break;
-                if (lane == 0) {
-                    ptx::mbar_arrive_expect_tx(bar(B_QFULL), 8 * 8192);
-                    q_issued = true;
-                    q_par = np & 1u;
-                }
+                const uint32_t qbar = ptx::map_to_rank(bar(B_QFULL), 0);
+                if (lane == 0) ptx::mbar_arrive_expect_tx_cluster(qbar, 8 * 8192);
                 __syncwarp();
                 if (lane < 8)
-                    ptx::tma_load_2d(sQ + lane * 8192, &tm_q, bar(B_QFULL), 64 * lane,
-                                     pc.row0 + kCtaRows * static_cast<int>(rank));
+                    ptx::tma_load_2d_pair(sQ + lane * 8192, &tm_q, qbar, 64 * lane,
+                                          pc.row0 + kCtaRows * static_cast<int>(rank));
             }
             ++np;
             scores_chunks(pc.base, page);
@@ -542,38 +561,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 page = next;
             }
         }
-        // no load may still be in flight when the CTA ends
-        if (lane == 0) {
-            for (int s = 0; s < kSlots; ++s)
-                if (issued >> s & 1u) wait_landed(bar(B_FULL + s), issued >> (16 + s) & 1u);
-            if (q_issued) wait_landed(bar(B_QFULL), q_par);
-        }
     } else if (warp == 2) {
         // ---------------- relay ----------------
         bool ok = true;
-        uint32_t g = 0, np = 0;
+        uint32_t g = 0, par = 0;         // chunks so far; parity of each slot's edge barrier
         Walk walk(p, cluster);
         Piece pc;
-        auto pass = [&](int ready) {
-            if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(bar(ready), 0));
-        };
-        auto scores_chunks = [&]() {
-            for (int k = 0; k < 8 && ok; ++k, ++g) {
-                const uint32_t s = g % kSlots;
-                ok = wait_bar_warp(bar(B_FULL + s), (g / kSlots) & 1u, sy);
-                if (ok) pass(B_READY + s);
-            }
-        };
-        auto values_chunks = [&](int base) {
-            const int n = tile_tokens(pc, base), lo = pc.t0 - base;
-            for (int c = 0; 32 * (c & ~1) < n && ok; ++c, ++g) {
-                const uint32_t s = g % kSlots;
-                ok = wait_bar_warp(bar(B_FULL + s), (g / kSlots) & 1u, sy);
-                if (!ok) break;
-                // rows of the chunk outside the span, up to the last 16 that the MMAs read
-                const int first = 64 * (c >> 1);
-                const int cut0 = min(64, lo - first), cut1 = n - first;
-                if (cut0 > 0 || cut1 < 64) {
+        while (ok && walk.next(&pc)) {
+            g += 8;
+            for (int i = 0; i < pc.tiles && ok; ++i) {
+                if (i + 1 < pc.tiles) g += 8;
+                const int base = pc.base + i * kTile;
+                const int n = tile_tokens(pc, base), lo = pc.t0 - base;
+                for (int c = 0; 32 * (c & ~1) < n && ok; ++c, ++g) {
+                    if (!has_edge(pc, base, c >> 1)) continue;
+                    const uint32_t s = g % kSlots;
+                    ok = wait_bar_warp(bar(B_EDGE + s), par >> s & 1u, sy);
+                    if (!ok) break;
+                    par ^= 1u << s;
+                    // rows outside the span, up to the last 16 that the MMAs read
+                    const int first = 64 * (c >> 1), cut0 = lo - first, cut1 = n - first;
                     const int end = (min(64, cut1) + 15) & ~15;
                     for (int r = lane >> 4; r < end; r += 2)
                         if (r < cut0 || r >= cut1)
@@ -581,83 +588,92 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                               0u, 0u, 0u);
                     ptx::fence_proxy_async_smem();
                     __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(bar(B_FULL + s), 0));
                 }
-                pass(B_READY + s);
-            }
-        };
-        while (ok && walk.next(&pc)) {
-            ok = wait_bar_warp(bar(B_QFULL), np & 1u, sy);
-            if (!ok) break;
-            pass(B_QREADY);
-            ++np;
-            scores_chunks();
-            for (int i = 0; i < pc.tiles && ok; ++i) {
-                if (i + 1 < pc.tiles) scores_chunks();
-                if (ok) values_chunks(pc.base + i * kTile);
             }
         }
     } else if (warp == 1) {
         // ---------------- MMA issuer ----------------
-        if (rank == 0 && lane == 0) {
+        // The whole warp runs the loop and one lane issues: operands that are the
+        // same in all lanes stay in uniform registers, which the MMAs take them
+        // from (a lone thread's loop moves each one over first: 120 cycles an MMA).
+        if (rank == 0) {
             constexpr uint32_t idesc_s = ptx::make_idesc(1u, kRows, kTile);
             constexpr uint32_t idesc_o = idesc_s | ptx::kIdescBMajorMN;
             bool ok = true, any = false;
             uint32_t g = 0, np = 0;
             uint32_t gs = 0, gp = 0;     // score tiles and output tiles so far
+            const bool one = ptx::elect_one();
             Walk walk(p, cluster);
             Piece pc;
             auto scores = [&](bool last) {
+                const uint32_t d = tmem + kTmemS + (gs & 1u) * 128;
                 for (int k = 0; k < 8; ++k, ++g) {
                     const uint32_t s = g % kSlots;
-                    ok = wait_bar<true>(bar(B_READY + s), (g / kSlots) & 1u, sy);
+                    ok = wait_bar_warp(bar(B_FULL + s), (g / kSlots) & 1u, sy);
                     if (!ok) return;
                     ptx::tc_fence_after();
                     const uint64_t ad = ptx::smem_desc_sw128(sQ + k * 8192);
                     const uint64_t bd = ptx::smem_desc_sw128(sRing + s * kChunk);
+                    if (one) {
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        ptx::mma_bf16_pair(tmem + kTmemS + (gs & 1u) * 128, ad + 2 * kk, bd + 2 * kk, idesc_s,
-                                           (k | kk) != 0);
+                        for (int kk = 0; kk < 4; ++kk)
+                            ptx::mma_bf16_pair(d, ad + 2 * kk, bd + 2 * kk, idesc_s, (k | kk) != 0);
+                        ptx::mma_commit_pair(bar(B_EMPTY + s));
+                    }
                     any = true;
-                    ptx::mma_commit_pair(bar(B_EMPTY + s));
                 }
-                ptx::mma_commit_pair(bar(B_SFULL + (gs & 1u)));
-                if (last) ptx::mma_commit_pair(bar(B_QEMPTY));
+                if (one) {
+                    ptx::mma_commit_pair(bar(B_SFULL + (gs & 1u)));
+                    if (last) ptx::mma_commit_pair(bar(B_QEMPTY));
+                }
                 ++gs;
             };
-            auto output = [&](int n, bool first) {
-                ok = wait_bar<true>(bar(B_PFULL), gp & 1u, sy);
+            auto output = [&](int base, bool first) {
+                const int n = tile_tokens(pc, base);
+                ok = wait_bar_warp<true>(bar(B_PFULL), gp & 1u, sy);
                 if (!ok) return;
                 ptx::tc_fence_after();
                 for (int c = 0; 32 * (c & ~1) < n; ++c, ++g) {
                     const uint32_t s = g % kSlots;
-                    ok = wait_bar<true>(bar(B_READY + s), (g / kSlots) & 1u, sy);
+                    const bool edge = has_edge(pc, base, c >> 1);      // cleared by other threads' stores
+                    ok = edge ? wait_bar_warp<true>(bar(B_FULL + s), (g / kSlots) & 1u, sy)
+                              : wait_bar_warp(bar(B_FULL + s), (g / kSlots) & 1u, sy);
                     if (!ok) return;
                     ptx::tc_fence_after();
                     const int kb = c >> 1, steps = min(4, (n - 64 * kb + 15) / 16);
                     const uint64_t ad = ptx::smem_desc_sw128(sP + kb * 8192);
                     const uint64_t bd = ptx::smem_desc_mn_sw128(sRing + s * kChunk, 8192);
-                    for (int kk = 0; kk < steps; ++kk)
-                        ptx::mma_bf16_pair(tmem + (c & 1) * 128, ad + 2 * kk, bd + 128 * kk, idesc_o,
-                                           !first || kb > 0 || kk > 0);
-                    ptx::mma_commit_pair(bar(B_EMPTY + s));
+                    const uint32_t d = tmem + (c & 1) * 128;
+                    if (one) {
+                        if (steps == 4) {
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                ptx::mma_bf16_pair(d, ad + 2 * kk, bd + 128 * kk, idesc_o, !first || kb > 0 || kk > 0);
+                        } else {
+                            for (int kk = 0; kk < steps; ++kk)
+                                ptx::mma_bf16_pair(d, ad + 2 * kk, bd + 128 * kk, idesc_o, !first || kb > 0 || kk > 0);
+                        }
+                        ptx::mma_commit_pair(bar(B_EMPTY + s));
+                    }
                 }
-                ptx::mma_commit_pair(bar(B_PV));
+                if (one) ptx::mma_commit_pair(bar(B_PV));
                 ++gp;
             };
             while (ok && walk.next(&pc)) {
-                ok = wait_bar<true>(bar(B_QREADY), np & 1u, sy);
+                pc.uniform();
+                ok = wait_bar_warp(bar(B_QFULL), np & 1u, sy);
                 if (!ok) break;
                 ++np;
                 scores(pc.tiles == 1);
                 for (int i = 0; i < pc.tiles && ok; ++i) {
                     if (i + 1 < pc.tiles) scores(i + 2 == pc.tiles);
-                    if (ok) output(tile_tokens(pc, pc.base + i * kTile), i == 0);
+                    if (ok) output(pc.base + i * kTile, i == 0);
                 }
             }
             if (any) {
-                // to this CTA alone: nothing of the pair's MMAs is in flight once it arrives
-                ptx::mma_commit_pair(bar(B_DRAIN));
+                // nothing of the pair's MMAs is in flight once this has arrived
+                if (one) ptx::mma_commit_pair(bar(B_DRAIN));
                 wait_landed(bar(B_DRAIN), 0);
             }
         }
@@ -812,8 +828,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     }
 
-    // neither CTA ends while the other may still signal it or read its memory
+    // Neither CTA ends while the other may still signal it or read its memory, nor
+    // with a load in flight: all have landed when the last tile's MMAs are done,
+    // except after an expired wait.  CTA 1's loads complete on CTA 0's barriers,
+    // where it cannot wait for them, so it then lets far more time pass than a
+    // load takes.
     __syncthreads();
+    if (*sy.abort_flag != 0u && threadIdx.x == 0) {
+        const uint64_t t0 = ptx::globaltimer();
+        while (ptx::globaltimer() - t0 < kLandNs) __nanosleep(1000);
+    }
     __syncwarp();
     ptx::cluster_sync();
     if (warp == 1) {
@@ -940,8 +964,11 @@ int run_prefix_mla(const PrefixMlaArgs &a, cudaStream_t s)
     p.clusters = clusters();
     lay_out(&p.w, static_cast<uint8_t *>(a.workspace), a.Tq, a.H, a.B, a.G, kMaxClusters);
     p.box = std::min(a.page_size, 64);
+    while (1 << p.box_log < p.box) ++p.box_log;
+    while (1 << p.page_log < a.page_size) ++p.page_log;
     p.c_scale = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
     p.wait_limit_ns = get_wait_limit_ns();
+    p.wait_tries = p.wait_limit_ns >= 1000000u ? 4096 : 1;
     const int64_t rows = a.Tq * a.H;
     CUtensorMap mq, mkv;
     if (rows > 0) {

@@ -364,13 +364,6 @@ __device__ __forceinline__ float ex2_approx(float x)
 }
 
 // ---- thread-block clusters and CTA pairs -------------------------------------
-__device__ __forceinline__ uint32_t cluster_ctarank()
-{
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-
 // All threads of all CTAs of the cluster; orders shared-memory accesses.
 __device__ __forceinline__ void cluster_sync()
 {
@@ -406,13 +399,34 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t par
     return ok != 0;
 }
 
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *desc, uint32_t bar, int32_t x,
-                                            int32_t y, int32_t z)
+// Arrive on an mbarrier of the cluster and announce `bytes` of loads; orders
+// nothing else (the loads order themselves).
+__device__ __forceinline__ void mbar_arrive_expect_tx_cluster(uint32_t cluster_bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_bar),
+                 "r"(bytes)
+                 : "memory");
+}
+
+// TMA loads into this CTA that complete on an mbarrier of either CTA of a pair
+// (an address from map_to_rank).
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void *desc, uint32_t cluster_bar, int32_t x,
+                                                 int32_t y)
 {
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(desc), "r"(cluster_bar), "r"(x), "r"(y)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void *desc, uint32_t cluster_bar, int32_t x,
+                                                 int32_t y, int32_t z)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
         " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
-        "l"(desc), "r"(bar), "r"(x), "r"(y), "r"(z)
+        "l"(desc), "r"(cluster_bar), "r"(x), "r"(y), "r"(z)
         : "memory");
 }
 
@@ -455,6 +469,18 @@ __device__ __forceinline__ void mma_commit_pair(uint32_t bar)
         "[%0], %1;" ::"r"(bar),
         "h"(static_cast<uint16_t>(3))
         : "memory");
+}
+
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
 }
 
 // ---- programmatic dependent launch ------------------------------------------
