@@ -15,7 +15,9 @@ indexer"; xtuner PR "GLM-5.3-Flash F5: NoPE DSA + KPool indexer".
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
 
 import torch
 
@@ -463,34 +465,61 @@ class _Pool(ctypes.Structure):
                 ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32)]
 
 
-class _Store(ctypes.Structure):
-    _fields_ = [("data", _P), ("layer_stride", _L), ("page_stride", _L),
-                ("n_layers", ctypes.c_int32), ("rows_per_page", ctypes.c_int32),
-                ("row_bytes", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+# The calls below are short on the GPU, so the host's part is kept short as well:
+# one combined test per tensor (the messages are made only when it fails), raw
+# pointers and streams, structures packed in one go.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_pack_store = struct.Struct("@Pqqiiii").pack
+_I32 = torch.int32
 
 
-class _on(object):
-    """Makes a device the current one for a call, when it is not already."""
-
-    def __init__(self, device):
-        self.index = device.index
-        self.before = None
-
-    def __enter__(self):
-        now = torch.cuda.current_device()
-        if self.index is not None and now != self.index:
-            self.before = now
-            torch.cuda.set_device(self.index)
-
-    def __exit__(self, *exc):
-        if self.before is not None:
-            torch.cuda.set_device(self.before)
-
-
-def _same_device(device, **tensors):
+def _same_device(index, **tensors):
     for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError("%s is on %s, not on %s" % (name, t.device, device))
+        if t is not None and t.get_device() != index:
+            raise ValueError("%s is on %s, not on cuda:%d" % (name, t.device, index))
+
+
+def _ints(t, name, n, index):
+    """Address of a contiguous int32 tensor of n entries on CUDA device `index`."""
+    if not (t.dtype is _I32 and t.is_cuda and t.get_device() == index and t.numel() == n
+            and t.is_contiguous()):
+        _need(t, name, _I32)
+        _same_device(index, **{name: t})
+        raise ValueError("%s must have %d entries (got %d)" % (name, n, t.numel()))
+    return t.data_ptr()
+
+
+def _device_of(t, name):
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    return t.get_device()
+
+
+def _call(index, name, fn, *args):
+    """fn(*args, stream) on device `index` and its current stream."""
+    if torch._C._cuda_getDevice() == index:
+        rc = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, _raw_stream(index))
+    if rc:
+        raise KPoolError(rc, name)
+
+
+@functools.lru_cache(maxsize=None)
+def _devices(index):
+    return torch.device("cuda", index)
+
+
+def _bytes(workspace, size, index):
+    """(tensor, address, size) of a call's workspace: the caller's, or a new one."""
+    if workspace is None:
+        workspace = torch.empty(max(256, size), dtype=torch.uint8, device=_devices(index))
+    elif not (workspace.is_cuda and workspace.get_device() == index
+              and workspace.dtype is torch.uint8 and workspace.is_contiguous()):
+        _need(workspace, "workspace", torch.uint8)
+        _same_device(index, workspace=workspace)
+    return workspace, workspace.data_ptr(), workspace.numel()
 
 
 class KPoolPages:
@@ -501,14 +530,14 @@ class KPoolPages:
     kpool_page_pool).  kpool_pages_new makes an empty one."""
 
     __slots__ = ("page_table", "seq_lens", "ref_count", "free_list", "free_count", "page_size",
-                 "device", "_c")
+                 "n_seqs", "n_pages", "_index", "_c", "_at")
 
     def __init__(self, page_table, seq_lens, ref_count, free_list, free_count, page_size: int):
         arrays = dict(page_table=page_table, seq_lens=seq_lens, ref_count=ref_count,
                       free_list=free_list, free_count=free_count)
         for name, t in arrays.items():
             _need(t, name, torch.int32)
-        _same_device(page_table.device, **arrays)
+        _same_device(page_table.get_device(), **arrays)
         if page_table.dim() != 2 or seq_lens.numel() != page_table.shape[0]:
             raise ValueError("page_table must be [n_seqs, max_pages] and seq_lens [n_seqs]")
         if ref_count.numel() != free_list.numel() or free_count.numel() != 1:
@@ -520,21 +549,16 @@ class KPoolPages:
         for name, t in arrays.items():
             put(name, t)
         put("page_size", page_size)
-        put("device", page_table.device)
+        put("n_seqs", page_table.shape[0])
+        put("n_pages", ref_count.numel())
+        put("_index", page_table.get_device())
         put("_c", _Pool(page_table.data_ptr(), seq_lens.data_ptr(), ref_count.data_ptr(),
                         free_list.data_ptr(), free_count.data_ptr(), page_table.shape[0],
                         page_table.shape[1], ref_count.numel(), page_size))
+        put("_at", ctypes.addressof(self._c))
 
     def __setattr__(self, name, value):
         raise AttributeError("a KPoolPages keeps its tensors: make another one")
-
-    @property
-    def n_seqs(self) -> int:
-        return self._c.n_seqs
-
-    @property
-    def n_pages(self) -> int:
-        return self._c.n_pages
 
 
 def kpool_pages_new(n_seqs: int, n_pages: int, max_pages: int, page_size: int,
@@ -547,144 +571,120 @@ def kpool_pages_new(n_seqs: int, n_pages: int, max_pages: int, page_size: int,
                       torch.full((1,), n_pages, **kw), page_size)
 
 
-def _stores(stores, n_pages, device):
-    """(C array, count) of stores: tensors [layers, n_pages, rows, width] or
-    [n_pages, rows, width] whose pages are contiguous.  A strided view of either order
-    of layers and pages will do."""
+def _store(t, n_pages, index):
+    """A kpool_page_store, packed."""
+    shape, stride = t.shape, t.stride()
+    dim = len(shape)
+    if dim != 3 and dim != 4:
+        raise ValueError("a store is [layers, n_pages, rows, width] or [n_pages, rows, width]")
+    rows, width = shape[-2], shape[-1]
+    if not t.is_cuda:
+        raise ValueError("a store must be a CUDA tensor")
+    if t.get_device() != index:
+        raise ValueError("a store is on %s, not on cuda:%d" % (t.device, index))
+    if shape[-3] != n_pages:
+        raise ValueError("a store has %d pages, not %d" % (shape[-3], n_pages))
+    if (width > 1 and stride[-1] != 1) or (rows > 1 and stride[-2] != width):
+        raise ValueError("the rows of a store's page must be contiguous")
+    size = t.element_size()
+    return _pack_store(t.data_ptr(), stride[0] * size if dim == 4 else 0, stride[-3] * size,
+                       shape[0] if dim == 4 else 1, rows, width * size, 0)
+
+
+def _stores(stores, n_pages, index):
+    """(packed array, count) of stores: tensors [layers, n_pages, rows, width] or
+    [n_pages, rows, width] whose pages are contiguous, with layers and pages in
+    either order of memory."""
     if isinstance(stores, torch.Tensor):
-        stores = (stores,)
-    out = (_Store * max(1, len(stores)))()
-    for i, t in enumerate(stores):
-        if not t.is_cuda:
-            raise ValueError("a store must be a CUDA tensor")
-        if t.device != device:
-            raise ValueError("a store is on %s, not on %s" % (t.device, device))
-        dim = t.dim()
-        if dim not in (3, 4):
-            raise ValueError("a store is [layers, n_pages, rows, width] or [n_pages, rows, width]")
-        shape, stride = t.shape, t.stride()
-        rows, width = shape[-2], shape[-1]
-        if shape[-3] != n_pages:
-            raise ValueError("a store has %d pages, not %d" % (shape[-3], n_pages))
-        if (width > 1 and stride[-1] != 1) or (rows > 1 and stride[-2] != width):
-            raise ValueError("the rows of a store's page must be contiguous")
-        size = t.element_size()
-        s = out[i]
-        s.data = t.data_ptr()
-        s.n_layers = shape[0] if dim == 4 else 1
-        s.layer_stride = stride[0] * size if dim == 4 else 0
-        s.page_stride = stride[-3] * size
-        s.rows_per_page = rows
-        s.row_bytes = width * size
-    return out, len(stores)
+        return _store(stores, n_pages, index), 1
+    return b"".join([_store(t, n_pages, index) for t in stores]), len(stores)
 
 
 def kpool_pages_workspace_size(n: int, n_seqs: int, n_pages: int) -> int:
     return int(_lib.kpool_pages_workspace_size(n, n_seqs, n_pages))
 
 
-def _pages_workspace(workspace, n, n_seqs, n_pages, device):
-    if workspace is None:
-        return torch.empty(max(256, _lib.kpool_pages_workspace_size(n, n_seqs, n_pages)),
-                           dtype=torch.uint8, device=device)
-    _need(workspace, "workspace", torch.uint8)
-    _same_device(device, workspace=workspace)
-    return workspace
-
-
-def _lists(device, n, **lists):
-    for name, t in lists.items():
-        _need(t, name, torch.int32)
-        if t.numel() != n:
-            raise ValueError("%s must have %d entries (got %d)" % (name, n, t.numel()))
-    _same_device(device, **lists)
-
-
 def kpool_pages_copy(src, dst, stores, workspace=None):
     """Page dst[i] becomes a copy of page src[i] in every store and layer."""
-    if isinstance(stores, torch.Tensor):
-        stores = (stores,)
-    if not stores:
+    first = stores if isinstance(stores, torch.Tensor) else stores[0] if len(stores) else None
+    if first is None:
         raise ValueError("a store is required")
-    dev, n, n_pages = src.device, src.numel(), stores[0].shape[-3]
-    _lists(dev, n, src=src, dst=dst)
-    st, n_stores = _stores(stores, n_pages, dev)
-    workspace = _pages_workspace(workspace, n, 0, n_pages, dev)
-    with _on(dev):
-        _check(_lib.kpool_pages_copy(_ptr(src), _ptr(dst), n, n_pages, st, n_stores,
-                                     _ptr(workspace), workspace.numel(), _stream(dev)),
-               "kpool_pages_copy")
+    index, n, n_pages = _device_of(src, "src"), src.numel(), first.shape[-3]
+    a, b = _ints(src, "src", n, index), _ints(dst, "dst", n, index)
+    st, n_stores = _stores(stores, n_pages, index)
+    keep, ws, size = _bytes(workspace, 0 if workspace is not None else
+                            _lib.kpool_pages_workspace_size(n, 0, n_pages), index)
+    _call(index, "kpool_pages_copy", _lib.kpool_pages_copy, a, b, n, n_pages, st, n_stores, ws,
+          size)
+
+
+def _pool_workspace(workspace, n, pages):
+    return _bytes(workspace, 0 if workspace is not None else
+                  _lib.kpool_pages_workspace_size(n, pages.n_seqs, pages.n_pages), pages._index)
 
 
 def kpool_pages_fork(pages: KPoolPages, parents, children, stores=(), workspace=None):
     """Sequence children[i], which holds nothing, becomes a copy of sequence
     parents[i]: whole pages are shared, a partial last page is copied."""
-    dev, n, c = pages.device, parents.numel(), pages._c
-    _lists(dev, n, parents=parents, children=children)
-    st, n_stores = _stores(stores, c.n_pages, dev)
-    workspace = _pages_workspace(workspace, n, c.n_seqs, c.n_pages, dev)
-    with _on(dev):
-        _check(_lib.kpool_pages_fork(ctypes.byref(c), _ptr(parents), _ptr(children), n, st,
-                                     n_stores, _ptr(workspace), workspace.numel(), _stream(dev)),
-               "kpool_pages_fork")
+    index, n = pages._index, parents.numel()
+    a, b = _ints(parents, "parents", n, index), _ints(children, "children", n, index)
+    st, n_stores = _stores(stores, pages.n_pages, index)
+    keep, ws, size = _pool_workspace(workspace, n, pages)
+    _call(index, "kpool_pages_fork", _lib.kpool_pages_fork, pages._at, a, b, n, st, n_stores, ws,
+          size)
 
 
 def kpool_pages_extend(pages: KPoolPages, seqs, n_new, workspace=None, out=None):
     """Sequence seqs[i] grows by n_new[i] tokens -> its length before, int32
     [n] (-1 everywhere when the call is refused)."""
-    dev, n, c = pages.device, seqs.numel(), pages._c
-    begin = torch.empty(n, dtype=torch.int32, device=dev) if out is None else out
-    _lists(dev, n, seqs=seqs, n_new=n_new, out=begin)
-    workspace = _pages_workspace(workspace, n, c.n_seqs, c.n_pages, dev)
-    with _on(dev):
-        _check(_lib.kpool_pages_extend(ctypes.byref(c), _ptr(seqs), _ptr(n_new), n, _ptr(begin),
-                                       _ptr(workspace), workspace.numel(), _stream(dev)),
-               "kpool_pages_extend")
-    return begin
+    index, n = pages._index, seqs.numel()
+    a, b = _ints(seqs, "seqs", n, index), _ints(n_new, "n_new", n, index)
+    if out is None:
+        out = torch.empty(n, dtype=_I32, device=_devices(index))
+    c = _ints(out, "out", n, index)
+    keep, ws, size = _pool_workspace(workspace, n, pages)
+    _call(index, "kpool_pages_extend", _lib.kpool_pages_extend, pages._at, a, b, n, c, ws, size)
+    return out
 
 
 def kpool_pages_write(pages: KPoolPages, seqs, begin, cu_rows, rows, store, workspace=None):
     """Rows cu_rows[i] .. cu_rows[i+1] - 1 of `rows` ([layers, total, width], or
     [total, width] for one layer) go to the rows begin[i], begin[i] + 1, ... of
     sequence seqs[i] in `store`."""
-    dev, n, c = pages.device, seqs.numel(), pages._c
-    _lists(dev, n, seqs=seqs, begin=begin)
-    _lists(dev, n + 1, cu_rows=cu_rows)
-    _need(rows, "rows", store.dtype)
-    _same_device(dev, rows=rows)
-    st, _ = _stores((store,), c.n_pages, dev)
-    g = st[0]
-    total, width = rows.shape[-2], rows.shape[-1]
-    if rows.dim() not in (2, 3) or (rows.shape[0] if rows.dim() == 3 else 1) != g.n_layers:
-        raise ValueError("rows must be [layers, total, width] of the store's %d layers" % g.n_layers)
-    if width != store.shape[-1]:
-        raise ValueError("rows are %d wide, the store's %d" % (width, store.shape[-1]))
-    workspace = _pages_workspace(workspace, n, c.n_seqs, c.n_pages, dev)
-    with _on(dev):
-        _check(_lib.kpool_pages_write(ctypes.byref(c), _ptr(seqs), _ptr(begin), _ptr(cu_rows), n,
-                                      total, _ptr(rows), total * g.row_bytes, st,
-                                      _ptr(workspace), workspace.numel(), _stream(dev)),
-               "kpool_pages_write")
+    index, n = pages._index, seqs.numel()
+    a, b = _ints(seqs, "seqs", n, index), _ints(begin, "begin", n, index)
+    c = _ints(cu_rows, "cu_rows", n + 1, index)
+    if not (rows.dtype is store.dtype and rows.is_contiguous() and rows.get_device() == index):
+        _need(rows, "rows", store.dtype)
+        _same_device(index, rows=rows)
+    st = _store(store, pages.n_pages, index)
+    layers, width = store.shape[0] if store.dim() == 4 else 1, store.shape[-1]
+    shape = rows.shape
+    if len(shape) not in (2, 3) or (shape[0] if len(shape) == 3 else 1) != layers:
+        raise ValueError("rows must be [layers, total, width] of the store's %d layers" % layers)
+    if shape[-1] != width:
+        raise ValueError("rows are %d wide, the store's %d" % (shape[-1], width))
+    total = shape[-2]
+    keep, ws, size = _pool_workspace(workspace, n, pages)
+    _call(index, "kpool_pages_write", _lib.kpool_pages_write, pages._at, a, b, c, n, total,
+          rows.data_ptr(), total * width * rows.element_size(), st, ws, size)
 
 
 def kpool_pages_free(pages: KPoolPages, seqs, workspace=None):
     """The listed sequences give up their pages."""
-    dev, n, c = pages.device, seqs.numel(), pages._c
-    _lists(dev, n, seqs=seqs)
-    workspace = _pages_workspace(workspace, n, c.n_seqs, c.n_pages, dev)
-    with _on(dev):
-        _check(_lib.kpool_pages_free(ctypes.byref(c), _ptr(seqs), n, _ptr(workspace),
-                                     workspace.numel(), _stream(dev)), "kpool_pages_free")
+    index, n = pages._index, seqs.numel()
+    a = _ints(seqs, "seqs", n, index)
+    keep, ws, size = _pool_workspace(workspace, n, pages)
+    _call(index, "kpool_pages_free", _lib.kpool_pages_free, pages._at, a, n, ws, size)
 
 
 def kpool_pages_compact(pages: KPoolPages, stores=(), workspace=None):
     """The k referenced pages move to the pages 0 .. k - 1, in every store."""
-    dev, c = pages.device, pages._c
-    st, n_stores = _stores(stores, c.n_pages, dev)
-    workspace = _pages_workspace(workspace, 0, c.n_seqs, c.n_pages, dev)
-    with _on(dev):
-        _check(_lib.kpool_pages_compact(ctypes.byref(c), st, n_stores, _ptr(workspace),
-                                        workspace.numel(), _stream(dev)), "kpool_pages_compact")
+    index = pages._index
+    st, n_stores = _stores(stores, pages.n_pages, index)
+    keep, ws, size = _pool_workspace(workspace, 0, pages)
+    _call(index, "kpool_pages_compact", _lib.kpool_pages_compact, pages._at, st, n_stores, ws,
+          size)
 
 
 def kpool_shared_prefix_mla_workspace_size(Tq: int, H: int, B: int, G: int) -> int:
@@ -698,50 +698,49 @@ def kpool_shared_prefix_mla_fwd(q, kv, page_table, seq_lens, cu_seqlens_q, cu_gr
     a prefix, read and multiplied once per group: q bf16 [Tq, H, 512], kv bf16
     [n_pages, page_size, 512] (one layer of a store) -> (o bf16 [Tq, H, 512],
     lse fp32 [Tq, H]).  A sequence's queries are its last tokens."""
-    dev = q.device
-    _need(q, "q", torch.bfloat16)
-    for t_, n_ in ((page_table, "page_table"), (seq_lens, "seq_lens"),
-                   (cu_seqlens_q, "cu_seqlens_q"), (cu_groups, "cu_groups"),
-                   (prefix_lens, "prefix_lens"), (seq_ids, "seq_ids")):
-        _need(t_, n_, torch.int32)
-    if kv.dtype != torch.bfloat16:
-        raise TypeError("kv must be %s (got %s)" % (torch.bfloat16, kv.dtype))
-    _same_device(dev, kv=kv, page_table=page_table, seq_lens=seq_lens, cu_seqlens_q=cu_seqlens_q,
-                 cu_groups=cu_groups, prefix_lens=prefix_lens, seq_ids=seq_ids, o=o, lse=lse,
-                 workspace=workspace)
+    index, bf16 = _device_of(q, "q"), torch.bfloat16
+    if not (q.dtype is bf16 and q.is_contiguous()):
+        _need(q, "q", bf16)
+    if kv.dtype is not bf16:
+        raise TypeError("kv must be %s (got %s)" % (bf16, kv.dtype))
     n_pages, page_size, Dc = kv.shape
-    if kv.stride(2) != 1 or kv.stride(1) != Dc:
+    stride = kv.stride()
+    if kv.get_device() != index or stride[2] != 1 or stride[1] != Dc:
+        _same_device(index, kv=kv)
         raise ValueError("the rows of a page of kv must be contiguous")
     Tq, H, D = q.shape
     if D != Dc:
         raise ValueError("q is %d wide, kv %d" % (D, Dc))
-    if page_table.dim() != 2 or seq_lens.numel() != page_table.shape[0]:
-        raise ValueError("page_table must be [n_rows, max_pages] and seq_lens [n_rows]")
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [n_rows, max_pages]")
+    n_rows, max_pages = page_table.shape
     B, G = cu_seqlens_q.numel() - 1, cu_groups.numel() - 1
-    if prefix_lens.numel() != G or (seq_ids is not None and seq_ids.numel() != B):
-        raise ValueError("prefix_lens must have one entry per group and seq_ids one per sequence")
+    lists = (_ints(page_table, "page_table", n_rows * max_pages, index),
+             _ints(seq_lens, "seq_lens", n_rows, index), n_rows, max_pages,
+             None if seq_ids is None else _ints(seq_ids, "seq_ids", B, index),
+             _ints(cu_seqlens_q, "cu_seqlens_q", B + 1, index), B,
+             _ints(cu_groups, "cu_groups", G + 1, index),
+             _ints(prefix_lens, "prefix_lens", G, index), G)
     if o is None:
-        o = torch.empty(Tq, H, Dc, dtype=torch.bfloat16, device=dev)
-    else:
-        _need(o, "o", torch.bfloat16)
+        o = torch.empty_like(q)
+    elif (o.shape != q.shape or o.dtype is not bf16 or not o.is_contiguous()
+          or o.get_device() != index):
+        _need(o, "o", bf16)
+        _same_device(index, o=o)
+        raise ValueError("o must be shaped like q")
     if lse is None:
-        lse = torch.empty(Tq, H, dtype=torch.float32, device=dev)
-    else:
+        lse = torch.empty(Tq, H, dtype=torch.float32, device=_devices(index))
+    elif (lse.numel() != Tq * H or lse.dtype is not torch.float32 or not lse.is_contiguous()
+          or lse.get_device() != index):
         _need(lse, "lse", torch.float32)
-    if o.shape != q.shape or lse.numel() != Tq * H:
-        raise ValueError("o must be shaped like q and lse [Tq, H]")
-    if workspace is None:
-        workspace = torch.empty(max(256, kpool_shared_prefix_mla_workspace_size(Tq, H, B, G)),
-                                dtype=torch.uint8, device=dev)
+        _same_device(index, lse=lse)
+        raise ValueError("lse must be [Tq, H]")
+    keep, ws, size = _bytes(workspace, 0 if workspace is not None else
+                            _lib.kpool_shared_prefix_mla_workspace_size(Tq, H, B, G), index)
     # (the stride of a single page says nothing)
-    stride = kv.stride(0) if n_pages > 1 else page_size * Dc
-    with _on(dev):
-        _check(_lib.kpool_shared_prefix_mla_fwd(
-            _ptr(q), _ptr(kv), stride, n_pages, page_size, _ptr(page_table), _ptr(seq_lens),
-            page_table.shape[0], page_table.shape[1], _ptr(seq_ids), _ptr(cu_seqlens_q), B,
-            _ptr(cu_groups), _ptr(prefix_lens), G, Tq, H, Dc, float(softmax_scale), _ptr(o),
-            _ptr(lse), _ptr(workspace), workspace.numel(), _stream(dev)),
-            "kpool_shared_prefix_mla_fwd")
+    _call(index, "kpool_shared_prefix_mla_fwd", _lib.kpool_shared_prefix_mla_fwd, q.data_ptr(),
+          kv.data_ptr(), stride[0] if n_pages > 1 else page_size * Dc, n_pages, page_size, *lists,
+          Tq, H, Dc, float(softmax_scale), o.data_ptr(), lse.data_ptr(), ws, size)
     return o, lse
 
 

@@ -59,6 +59,8 @@ constexpr int kOverhead = 2;             // a piece's start and end, in tiles (f
 constexpr int kThreads = 384;
 constexpr int kSmWarps = 8;
 constexpr int kPlanThreads = 1024;
+constexpr int kPlanLists = 1024;         // sequences, groups and units that the plan keeps in shared memory
+constexpr int kPlanUnits = 1024;
 constexpr float kRescale = 8.f;          // headroom of the reference maximum (log2)
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr uint64_t kLandNs = 2000000ull;
@@ -84,7 +86,7 @@ constexpr int kSmemBytes = kOffMisc + 16 + 1024;   // and alignment slack
 static_assert(kSmemBytes <= 232448, "shared memory over the per-block limit");
 
 // workspace header (ints)
-enum { H_STATUS = 1, H_OK = 2, H_UNITS = 3, H_INTS = 64 };
+enum { H_STATUS = 1, H_OK = 2, H_INTS = 64 };
 
 struct Unit {
     int row0, nrows;         // flat (query, head) rows
@@ -101,16 +103,24 @@ struct Token {               // per query
     int su, srow0;           // its sequence's
 };
 
+// Where a cluster begins: all that it reads before its first loads, in one place.
+struct __align__(16) Start {
+    int u, units;            // its first unit; number of units
+    int64_t share;           // work of each cluster
+    Unit first;
+};
+
 struct Work {
-    int *head;               // header; 64-bit words 8.. : [0] work per cluster
+    int *head;               // header
     Token *tok;              // [Tq]
-    int *unit0;              // [G + B] first unit of each group and sequence
-    int *len;                // [B] tokens, [B..2B) shared tokens of its group
-    int *first;              // [clusters] first unit of each cluster
+    int *lists;              // [3 B + 2 G]: the plan's, when they do not fit shared memory
+    Start *start;            // [clusters]
     Unit *unit;
     float *lse;              // [partial rows], base 2
     float *o;                // [partial rows, 512]
 };
+
+constexpr int kPlanSmem = kPlanUnits * static_cast<int>(sizeof(Unit)) + (5 * kPlanLists + 2 * (kPlanLists + 1)) * 4;
 
 struct Params {
     PrefixMlaArgs a;
@@ -124,7 +134,6 @@ struct Params {
 };
 
 __device__ __forceinline__ bool in_range(int i, int n) { return i >= 0 && i < n; }
-__device__ __forceinline__ int64_t *work_per_cluster(const Work &w) { return reinterpret_cast<int64_t *>(w.head + 8); }
 
 // ---- plan --------------------------------------------------------------------
 
@@ -174,141 +183,141 @@ __device__ __forceinline__ void pieces_of(const Unit &u, int64_t share, int64_t 
     *n = u.tiles > 0 ? static_cast<int>((u.w0 + kOverhead + u.tiles - 1) / share - *c0) + 1 : 0;
 }
 
+// Reads its lists once, into shared memory where they fit (any realistic
+// batch), so that the searches and scans behind it do not wait for the L2.
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p)
 {
+    extern __shared__ __align__(16) uint8_t plan_smem[];
     __shared__ int64_t scratch[32];
     __shared__ int status;
     const PrefixMlaArgs &a = p.a;
     const Work &w = p.w;
     ptx::grid_dependents_launch();
     if (threadIdx.x == 0) status = 0;
-    bool bad = false;
-    for (int i = threadIdx.x; i <= a.B; i += blockDim.x)
-        bad |= i == 0 ? a.cu_q[0] != 0 : a.cu_q[i] < a.cu_q[i - 1];
-    for (int i = threadIdx.x; i <= a.G; i += blockDim.x)
-        bad |= i == 0 ? a.cu_groups[0] != 0 : a.cu_groups[i] < a.cu_groups[i - 1];
-    bad |= a.cu_q[a.B] != a.Tq || a.cu_groups[a.G] != a.B;
-    if (__syncthreads_or(bad)) {
-        if (threadIdx.x == 0) {
-            w.head[H_STATUS] = KPOOL_STATUS_BAD_SEQLENS;
-            w.head[H_OK] = 0;
-            w.head[H_UNITS] = 0;
-        }
-        return;
+    const int entities = a.G + a.B;          // groups, then sequences
+    const bool small = a.B <= kPlanLists && a.G <= kPlanLists;
+    int *lists = small ? reinterpret_cast<int *>(plan_smem + kPlanUnits * sizeof(Unit)) : w.lists;
+    int *len = lists, *shared = len + a.B, *row = shared + a.G, *unit0 = row + a.B;
+    const int32_t *cu_q = a.cu_q, *cu_g = a.cu_groups;
+    if (small) {
+        int *q = unit0 + entities, *g = q + a.B + 1;
+        for (int i = threadIdx.x; i <= a.B; i += blockDim.x) q[i] = a.cu_q[i];
+        for (int i = threadIdx.x; i <= a.G; i += blockDim.x) g[i] = a.cu_groups[i];
+        cu_q = q;
+        cu_g = g;
     }
     const int64_t room = static_cast<int64_t>(a.max_pages) * a.page_size;
+    __syncthreads();
     // a sequence's length, cut to what its table row holds
-    auto length_of = [&](int b, int *row) {
-        *row = a.seq_ids != nullptr ? a.seq_ids[b] : b;
+    for (int b = threadIdx.x; b < a.B; b += blockDim.x) {
+        int r = a.seq_ids != nullptr ? a.seq_ids[b] : b;
         int64_t n = -1;
-        if (in_range(*row, a.n_rows)) n = a.seq_lens[*row];
-        else *row = 0;
+        if (in_range(r, a.n_rows)) n = a.seq_lens[r];
+        else r = 0;
         if (n < 0 || n > room) {
             atomicOr(&status, KPOOL_STATUS_BAD_PAGE);
             n = n < 0 ? 0 : room;
         }
-        return static_cast<int>(n);
-    };
-    for (int b = threadIdx.x; b < a.B; b += blockDim.x) {
-        const int g = segment_of(a.cu_groups, a.G, b);
-        int row;
-        w.len[b] = length_of(b, &row);
-        w.len[a.B + b] = min(max(a.prefix_lens[g], 0), length_of(a.cu_groups[g], &row));
+        row[b] = r;
+        len[b] = static_cast<int>(n);
     }
-    __syncthreads();
+    bool bad = false;
+    for (int i = threadIdx.x; i <= a.B; i += blockDim.x) bad |= i == 0 ? cu_q[0] != 0 : cu_q[i] < cu_q[i - 1];
+    for (int i = threadIdx.x; i <= a.G; i += blockDim.x) bad |= i == 0 ? cu_g[0] != 0 : cu_g[i] < cu_g[i - 1];
+    bad |= cu_q[a.B] != a.Tq || cu_g[a.G] != a.B;
+    if (__syncthreads_or(bad)) {
+        if (threadIdx.x == 0) {
+            w.head[H_STATUS] = KPOOL_STATUS_BAD_SEQLENS;
+            w.head[H_OK] = 0;
+        }
+        for (int c = threadIdx.x; c < p.clusters; c += blockDim.x) w.start[c] = Start{};
+        return;
+    }
     // units of every group, then of every sequence
-    const int entities = a.G + a.B;
     int64_t units = 0;
     for (int base = 0; base < entities; base += blockDim.x) {
         const int e = base + threadIdx.x;
         int n = 0;
         if (e < entities) {
-            const int b0 = e < a.G ? a.cu_groups[e] : e - a.G;
-            const int b1 = e < a.G ? a.cu_groups[e + 1] : b0 + 1;
-            n = static_cast<int>((static_cast<int64_t>(a.cu_q[b1] - a.cu_q[b0]) * a.H + kRows - 1) / kRows);
+            const int b0 = e < a.G ? cu_g[e] : e - a.G;
+            const int b1 = e < a.G ? cu_g[e + 1] : b0 + 1;
+            n = static_cast<int>((static_cast<int64_t>(cu_q[b1] - cu_q[b0]) * a.H + kRows - 1) / kRows);
+            // shared tokens are read through the group's first sequence
+            if (e < a.G) shared[e] = b1 > b0 ? min(max(a.prefix_lens[e], 0), len[b0]) : 0;
         }
         int64_t total;
         const int64_t at = units + block_exclusive(n, scratch, &total);
-        if (e < entities) w.unit0[e] = static_cast<int>(at);
+        if (e < entities) unit0[e] = static_cast<int>(at);
         units += total;
     }
     __syncthreads();
-    for (int e = threadIdx.x >> 5; e < entities; e += blockDim.x >> 5) {
-        const int lane = threadIdx.x & 31;
-        const int b0 = e < a.G ? a.cu_groups[e] : e - a.G;
-        const int b1 = e < a.G ? a.cu_groups[e + 1] : b0 + 1;
-        const int row0 = a.cu_q[b0] * a.H, rows = a.cu_q[b1] * a.H - row0;
-        if (rows == 0) continue;
-        const int first = a.seq_ids != nullptr ? a.seq_ids[b0] : b0;
-        const int shared = w.len[a.B + b0], len = w.len[b0];
-        for (int k = lane; k * kRows < rows; k += 32) {
-            Unit u{};
-            u.row0 = row0 + k * kRows;
-            u.nrows = min(kRows, rows - k * kRows);
-            u.table_row = in_range(first, a.n_rows) ? first : 0;
+    // each unit's span, and its place in the work
+    Unit *unit = units <= kPlanUnits ? reinterpret_cast<Unit *>(plan_smem) : w.unit;
+    int64_t work = 0;
+    for (int64_t base = 0; base < units; base += blockDim.x) {
+        const int64_t k = base + threadIdx.x;
+        Unit u{};
+        if (k < units) {
+            const int e = segment_of(unit0, entities, static_cast<int>(k));
+            const int b0 = e < a.G ? cu_g[e] : e - a.G;
+            const int b1 = e < a.G ? cu_g[e + 1] : b0 + 1;
+            const int r0 = cu_q[b0] * a.H, rows = cu_q[b1] * a.H - r0, at = (static_cast<int>(k) - unit0[e]) * kRows;
+            u.row0 = r0 + at;
+            u.nrows = min(kRows, rows - at);
+            u.table_row = row[b0];
             if (e < a.G) {
-                u.t1 = shared;
+                u.t1 = shared[e];
             } else {
                 // up to what the last of the rows' queries sees
                 const int last = (u.row0 + u.nrows - 1) / a.H;
-                u.t0 = shared;
-                u.t1 = len - (a.cu_q[b1] - 1 - last);
+                u.t0 = shared[segment_of(cu_g, a.G, b0)];
+                u.t1 = len[b0] - (cu_q[b1] - 1 - last);
             }
-            const int from = u.t0 / p.box * p.box;
-            u.tiles = u.t1 > u.t0 ? (u.t1 - from + kTile - 1) / kTile : 0;
-            w.unit[w.unit0[e] + k] = u;
+            u.tiles = u.t1 > u.t0 ? (u.t1 - (u.t0 & -p.box) + kTile - 1) / kTile : 0;
         }
+        int64_t total;
+        u.w0 = work + block_exclusive(u.tiles > 0 ? u.tiles + kOverhead : 0, scratch, &total);
+        if (k < units) unit[k] = u;
+        work += total;
     }
     // queries
     for (int t = threadIdx.x; t < a.Tq; t += blockDim.x) {
-        const int b = segment_of(a.cu_q, a.B, t), g = segment_of(a.cu_groups, a.G, b);
+        const int b = segment_of(cu_q, a.B, t), g = segment_of(cu_g, a.G, b);
         Token x;
-        x.vis = max(0, w.len[b] - (a.cu_q[b + 1] - 1 - t));
-        x.pu = w.unit0[g];
-        x.prow0 = a.cu_q[a.cu_groups[g]] * a.H;
-        x.su = w.unit0[a.G + b];
-        x.srow0 = a.cu_q[b] * a.H;
+        x.vis = max(0, len[b] - (cu_q[b + 1] - 1 - t));
+        x.pu = unit0[g];
+        x.prow0 = cu_q[cu_g[g]] * a.H;
+        x.su = unit0[a.G + b];
+        x.srow0 = cu_q[b] * a.H;
         w.tok[t] = x;
     }
-    __syncthreads();
-    // the units' places in the work, and the even cut
-    int64_t work = 0;
-    for (int64_t base = 0; base < units; base += blockDim.x) {
-        const int64_t u = base + threadIdx.x;
-        const int n = u < units ? w.unit[u].tiles : 0;
-        int64_t total;
-        const int64_t at = work + block_exclusive(n > 0 ? n + kOverhead : 0, scratch, &total);
-        if (u < units) w.unit[u].w0 = at;
-        work += total;
-    }
+    // the even cut: where each cluster begins, and each unit's partial rows
     const int64_t share = max(static_cast<int64_t>(1), (work + p.clusters - 1) / p.clusters);
     for (int c = threadIdx.x; c < p.clusters; c += blockDim.x)
-        if (c * share >= work) w.first[c] = static_cast<int>(units);
-    __syncthreads();
+        if (c * share >= work) w.start[c] = Start{static_cast<int>(units), static_cast<int>(units), share, Unit{}};
     int64_t rows = 0;
     for (int64_t base = 0; base < units; base += blockDim.x) {
-        const int64_t u = base + threadIdx.x;
-        Unit x{};
+        const int64_t k = base + threadIdx.x;
+        Unit u{};
         int64_t c0 = 0;
         int n = 0;
-        if (u < units) {
-            x = w.unit[u];
-            pieces_of(x, share, &c0, &n);
-            // the clusters whose share begins in this unit
-            if (x.tiles > 0)
-                for (int64_t c = (x.w0 + share - 1) / share; c * share < x.w0 + x.tiles + kOverhead; ++c)
-                    w.first[c] = static_cast<int>(u);
+        if (k < units) {
+            u = unit[k];
+            pieces_of(u, share, &c0, &n);
         }
         int64_t total;
-        const int64_t at = rows + block_exclusive(static_cast<int64_t>(n) * x.nrows, scratch, &total);
-        if (u < units) w.unit[u].out0 = at;
+        u.out0 = rows + block_exclusive(static_cast<int64_t>(n) * u.nrows, scratch, &total);
+        if (k < units) {
+            w.unit[k] = u;
+            if (u.tiles > 0)
+                for (int64_t c = (u.w0 + share - 1) / share; c * share < u.w0 + u.tiles + kOverhead; ++c)
+                    w.start[c] = Start{static_cast<int>(k), static_cast<int>(units), share, u};
+        }
         rows += total;
     }
     if (threadIdx.x == 0) {
-        *work_per_cluster(w) = share;
         w.head[H_STATUS] = status;
         w.head[H_OK] = 1;
-        w.head[H_UNITS] = static_cast<int>(units);
     }
 }
 
@@ -377,34 +386,39 @@ struct Piece {
 
 struct Walk {
     const Unit *unit;
-    int units, u, box;
+    Unit x;                  // unit u
+    int u, units, box;
     int64_t cluster, share;
 
-    __device__ Walk(const Params &p, int c)
-        : unit(p.w.unit), units(p.w.head[H_UNITS]), box(p.box), cluster(c), share(0)
+    __device__ Walk(const Params &p, int c) : unit(p.w.unit), box(p.box), cluster(c)
     {
-        u = units > 0 ? p.w.first[c] : 0;
-        if (units > 0) share = *work_per_cluster(p.w);
+        const Start s = p.w.start[c];
+        u = s.u;
+        units = s.units;
+        share = s.share;
+        x = s.first;
     }
     __device__ bool next(Piece *q)
     {
-        for (; u < units; ++u) {
-            const Unit x = unit[u];
-            if (x.tiles == 0) continue;
-            if (x.w0 >= (cluster + 1) * share) return false;
-            const int64_t begin = x.w0 + kOverhead;
-            const int64_t lo = max(begin, cluster * share), hi = min(begin + x.tiles, (cluster + 1) * share);
-            if (lo >= hi) continue;
-            q->row0 = x.row0;
-            q->nrows = x.nrows;
-            q->table_row = x.table_row;
-            q->t0 = x.t0;
-            q->t1 = x.t1;
-            q->base = (x.t0 & -box) + static_cast<int>(lo - begin) * kTile;
-            q->tiles = static_cast<int>(hi - lo);
-            q->out = x.out0 + (cluster - begin / share) * x.nrows;
-            ++u;
-            return true;
+        while (u < units) {
+            if (x.tiles > 0) {
+                if (x.w0 >= (cluster + 1) * share) return false;
+                const int64_t begin = x.w0 + kOverhead;
+                const int64_t lo = max(begin, cluster * share), hi = min(begin + x.tiles, (cluster + 1) * share);
+                if (lo < hi) {
+                    q->row0 = x.row0;
+                    q->nrows = x.nrows;
+                    q->table_row = x.table_row;
+                    q->t0 = x.t0;
+                    q->t1 = x.t1;
+                    q->base = (x.t0 & -box) + static_cast<int>(lo - begin) * kTile;
+                    q->tiles = static_cast<int>(hi - lo);
+                    q->out = x.out0 + (cluster - begin / share) * x.nrows;
+                    if (++u < units) x = unit[u];
+                    return true;
+                }
+            }
+            if (++u < units) x = unit[u];
         }
         return false;
     }
@@ -817,10 +831,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 ptx::tmem_ld_wait(o);
                 if (row < pc.nrows) {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4)
-                        *reinterpret_cast<float4 *>(out + 32 * k + e) =
-                            make_float4(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv,
-                                        __uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) ptx::st_global_v8(out + 32 * k + e, &o[e]);
                 }
             }
             if (member == 0 && row < pc.nrows) p.w.lse[pc.out + row] = l > 0.f ? m + log2f(l) : -INFINITY;
@@ -849,54 +862,58 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 // ---- combine -----------------------------------------------------------------
 
+// Four warps per row, a float4 of a lane each: short rows of many pieces want
+// more loads in flight than one warp has.
 __global__ void __launch_bounds__(256) combine_kernel(const Params p)
 {
     ptx::grid_dependency_wait();
     if (!p.w.head[H_OK]) return;
     const int lane = threadIdx.x & 31;
-    const int64_t row = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 5;
+    const int64_t w = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 5;
+    const int64_t row = w >> 2;
     if (row >= p.a.Tq * p.a.H) return;
+    const int64_t share = p.w.start[0].share;
     const Token x = p.w.tok[row / p.a.H];
-    const int64_t share = *work_per_cluster(p.w);
-    float m = -INFINITY, l = 0.f;
-    float acc[16];
+    const int ks = static_cast<int>(row - x.prow0), ko = static_cast<int>(row - x.srow0);
+    const Unit us = p.w.unit[x.pu + ks / kRows], uo = p.w.unit[x.su + ko / kRows];
+    int64_t c0;
+    int ns, no;
+    pieces_of(us, share, &c0, &ns);
+    pieces_of(uo, share, &c0, &no);
+    // partial row of piece i: the shared ones, then the sequence's own
+    auto at = [&](int i) {
+        return i < ns ? us.out0 + static_cast<int64_t>(i) * us.nrows + ks % kRows
+                      : uo.out0 + static_cast<int64_t>(i - ns) * uo.nrows + ko % kRows;
+    };
+    const int n = ns + no;
+    float m = -INFINITY;
+    for (int i = lane; i < n; i += 32) m = fmaxf(m, p.w.lse[at(i)]);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-#pragma unroll
-    for (int side = 0; side < 2; ++side) {
-        const int k = static_cast<int>(row - (side ? x.srow0 : x.prow0));
-        const Unit u = p.w.unit[(side ? x.su : x.pu) + k / kRows];
-        int64_t c0;
-        int n;
-        pieces_of(u, share, &c0, &n);
-        for (int i = 0; i < n; ++i) {
-            const int64_t at = u.out0 + static_cast<int64_t>(i) * u.nrows + k % kRows;
-            const float s = p.w.lse[at];
-            if (s == -INFINITY) continue;
-            const float mn = fmaxf(m, s);
-            const float f = ptx::ex2_approx(m - mn), g = ptx::ex2_approx(s - mn);
-            m = mn;
-            l = l * f + g;
-            const float4 *o = reinterpret_cast<const float4 *>(p.w.o + at * kDc);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const float4 y = __ldcg(o + 32 * q + lane);
-                acc[4 * q] = acc[4 * q] * f + y.x * g;
-                acc[4 * q + 1] = acc[4 * q + 1] * f + y.y * g;
-                acc[4 * q + 2] = acc[4 * q + 2] * f + y.z * g;
-                acc[4 * q + 3] = acc[4 * q + 3] * f + y.w * g;
-            }
+    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
+    const float ref = m == -INFINITY ? 0.f : m;
+    const float4 *o = reinterpret_cast<const float4 *>(p.w.o) + (w & 3) * 32 + lane;
+    float l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int base = 0; base < n; base += 32) {
+        const float mine = base + lane < n ? ptx::ex2_approx(p.w.lse[at(base + lane)] - ref) : 0.f;
+        const int here = min(32, n - base);
+#pragma unroll 4
+        for (int i = 0; i < here; ++i) {
+            const float f = __shfl_sync(kFull, mine, i);
+            const float4 y = __ldcg(o + at(base + i) * (kDc / 4));
+            l += f;
+            acc.x = fmaf(y.x, f, acc.x);
+            acc.y = fmaf(y.y, f, acc.y);
+            acc.z = fmaf(y.z, f, acc.z);
+            acc.w = fmaf(y.w, f, acc.w);
         }
     }
     const float inv = l > 0.f ? 1.f / l : 0.f;
-    uint2 *out = reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.a.o) + row * kDc);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const __nv_bfloat162 a = __floats2bfloat162_rn(acc[4 * q] * inv, acc[4 * q + 1] * inv);
-        const __nv_bfloat162 b = __floats2bfloat162_rn(acc[4 * q + 2] * inv, acc[4 * q + 3] * inv);
-        out[32 * q + lane] = make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
-    }
-    if (lane == 0) p.a.lse[row] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+    const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+    uint2 *out = reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.a.o) + row * kDc) + (w & 3) * 32 + lane;
+    *out = make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+    if ((w & 3) == 0 && lane == 0) p.a.lse[row] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
 // ---- host --------------------------------------------------------------------
@@ -919,9 +936,8 @@ size_t lay_out(Work *w, uint8_t *base, int64_t Tq, int H, int B, int G, int clus
     };
     w->head = reinterpret_cast<int *>(take(4 * H_INTS));
     w->tok = reinterpret_cast<Token *>(take(Tq * static_cast<int64_t>(sizeof(Token))));
-    w->unit0 = reinterpret_cast<int *>(take(4 * (static_cast<int64_t>(G) + B)));
-    w->len = reinterpret_cast<int *>(take(8 * static_cast<int64_t>(B)));
-    w->first = reinterpret_cast<int *>(take(4 * clusters));
+    w->lists = reinterpret_cast<int *>(take(4 * (3 * static_cast<int64_t>(B) + 2 * static_cast<int64_t>(G))));
+    w->start = reinterpret_cast<Start *>(take(clusters * static_cast<int64_t>(sizeof(Start))));
     w->unit = reinterpret_cast<Unit *>(take(units * static_cast<int64_t>(sizeof(Unit))));
     w->lse = reinterpret_cast<float *>(take(4 * partial));
     w->o = reinterpret_cast<float *>(take(4 * kDc * partial));
@@ -979,11 +995,12 @@ int run_prefix_mla(const PrefixMlaArgs &a, cudaStream_t s)
         KPOOL_CUDA_CHECK(
             cudaFuncSetAttribute(attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes));
     }
-    plan_kernel<<<1, kPlanThreads, 0, s>>>(p);
+    KPOOL_CUDA_CHECK(cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPlanSmem));
+    plan_kernel<<<1, kPlanThreads, kPlanSmem, s>>>(p);
     KPOOL_CUDA_CHECK(cudaGetLastError());
     if (rows == 0) return KPOOL_OK;
     KPOOL_CUDA_CHECK(launch_after(attend_kernel, 2 * p.clusters, kThreads, kSmemBytes, s, mq, mkv, p));
-    KPOOL_CUDA_CHECK(launch_after(combine_kernel, static_cast<int>((rows + 7) / 8), 256, 0, s, p));
+    KPOOL_CUDA_CHECK(launch_after(combine_kernel, static_cast<int>((rows + 1) / 2), 256, 0, s, p));
     return KPOOL_OK;
 }
 

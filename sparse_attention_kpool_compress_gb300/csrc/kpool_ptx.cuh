@@ -471,6 +471,14 @@ __device__ __forceinline__ void mma_commit_pair(uint32_t bar)
         : "memory");
 }
 
+// 32-byte global store (a whole sector).
+__device__ __forceinline__ void st_global_v8(void *p, const uint32_t *v)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]),
+                 "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
 // True in one lane of the (converged) warp.
 __device__ __forceinline__ bool elect_one()
 {

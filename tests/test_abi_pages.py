@@ -32,7 +32,8 @@ def _store(b, a, **kw):
     f = dict(data=a, layer_stride=32 * 16 * 1024, page_stride=16 * 1024, n_layers=2, rows_per_page=16,
              row_bytes=1024)
     f.update(kw)
-    return ctypes.byref((b._Store * 1)(b._Store(**f)))
+    order = ("data", "layer_stride", "page_stride", "n_layers", "rows_per_page", "row_bytes")
+    return b._pack_store(*(f[k] or 0 for k in order), 0)
 
 
 def test_pools_and_stores_are_checked(b):
