@@ -29,18 +29,25 @@
 // cycles per 128 x 256 x 16 MMA measured, M = 128 N = 256; N = 128 takes the
 // same time).  Operand B is split: for the scores each CTA brings 128 of the
 // tile's 256 tokens (K-major), for the output 256 of the 512 latent columns of
-// all its tokens (MN-major).  Both come through one ring of eight 16 KB chunks,
-// each feeding four MMAs.  (Keeping the quarter of a tile that both products use
-// would need 64 KB that the 64 KB of queries, the 32 KB of P and the ring leave
-// no room for.)
-//   warps 0, 3   TMA producers, chunks in turn (one warp alone issues too slowly)
-//   warp 1       MMA issuer (CTA 0)
-//   warp 2       relay: in a chunk of values that reaches outside the span, clears
-//                those rows, so that nothing there, NaN included, meets a weight
-//                of 0, and passes it on to the issuer (all other loads complete
-//                on CTA 0's barriers directly)
+// all its tokens (MN-major).  Each product has a ring of four 16 KB chunks, each
+// feeding four MMAs.  (Keeping the quarter of a tile that both products use would
+// need 64 KB that the 64 KB of queries, the 32 KB of P and the rings leave no
+// room for.)
+//   warp 0       TMA producer of queries and scores chunks
+//   warp 1       issuer of the scores' MMAs (CTA 0)
+//   warp 2       issuer of the output's MMAs (CTA 0).  Two issuers, because one
+//                that waits and commits for every four MMAs reaches 98 cycles
+//                an MMA, two together the pipe's 64 (measured).  In both CTAs
+//                it also clears the rows of a chunk of values that lie outside
+//                the span, so that nothing there, NaN included, meets a weight
+//                of 0
+//   warp 3       TMA producer of values chunks
 //   warps 4-11   softmax and output: thread (lane, half of the columns) has 64
 //                of a row's 256 scores
+// All loads and arrivals meet on CTA 0's barriers, where the issuers wait.  P
+// passes in four parts of 64 tokens, so that the output of a tile's first part
+// begins while the last one is exponentiated, and the next tile's P is written
+// behind the parts that are still being read.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -70,16 +77,18 @@ constexpr int kTmemS = 256;
 
 // shared memory (from a 1024-byte aligned base)
 constexpr int kChunk = 16384;
-constexpr int kSlots = 8;
+constexpr int kRing = 4;                 // chunks of each ring
 constexpr int kOffQ = 0;                           // 8 x [64 rows x 64 columns]
 constexpr int kOffP = kOffQ + 8 * 8192;            // 4 x [64 rows x 64 tokens]
-constexpr int kOffRing = kOffP + 4 * 8192;
-constexpr int kOffRed = kOffRing + kSlots * kChunk;  // [4][64] floats
+constexpr int kOffK = kOffP + 4 * 8192;            // scores chunks
+constexpr int kOffV = kOffK + kRing * kChunk;      // values chunks
+constexpr int kOffRed = kOffV + kRing * kChunk;    // [4][64] floats
 constexpr int kOffWord = kOffRed + 4 * kCtaRows * 4; // agreement words [2 groups][2][4]
 constexpr int kOffBar = kOffWord + 64;
 enum {
-    B_FULL = 0, B_EDGE = B_FULL + kSlots, B_EMPTY = B_EDGE + kSlots, B_QFULL = B_EMPTY + kSlots,
-    B_QEMPTY, B_SFULL, B_PFULL = B_SFULL + 2, B_PV, B_DRAIN, N_BARS
+    B_KFULL = 0, B_KEMPTY = B_KFULL + kRing, B_VFULL = B_KEMPTY + kRing, B_VEMPTY = B_VFULL + kRing,
+    B_VEDGE = B_VEMPTY + kRing, B_PFULL = B_VEDGE + kRing, B_PFREE = B_PFULL + 4, B_SFULL = B_PFREE + 4,
+    B_SFREE = B_SFULL + 2, B_QFULL = B_SFREE + 2, B_QEMPTY, B_PV, B_DRAIN, N_BARS = B_DRAIN + 2
 };
 constexpr int kOffMisc = kOffBar + N_BARS * 8;     // [0] tmem base, [1] abort flag
 constexpr int kSmemBytes = kOffMisc + 16 + 1024;   // and alignment slack
@@ -332,17 +341,15 @@ struct Sync {
 
 // Bounded mbarrier wait: completion, then the CTA abort flag, then a timer that
 // raises the flag and KPOOL_STATUS_TIMEOUT.
-template <bool kCluster>
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const Sync &sy)
 {
-    auto done = [&] { return kCluster ? ptx::mbar_try_wait_cluster(bar, parity) : ptx::mbar_try_wait(bar, parity); };
     // (the timer is slow to read: it would add its latency to each hop of the pipeline)
 #pragma unroll 1
-    for (int i = 0; i < sy.tries; ++i)
-        if (done()) return true;
+    for (int i = 0; i <= sy.tries; ++i)
+        if (ptx::mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = ptx::globaltimer();
     while (true) {
-        if (done()) return true;
+        if (ptx::mbar_try_wait(bar, parity)) return true;
         if (*sy.abort_flag) return false;
         if (ptx::globaltimer() - t0 > sy.limit_ns) {
             *sy.abort_flag = 1u;
@@ -353,10 +360,9 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const Sy
 }
 
 // All lanes wait; false when any of them gave up.
-template <bool kCluster = false>
 __device__ __forceinline__ bool wait_bar_warp(uint32_t bar, uint32_t parity, const Sync &sy)
 {
-    const bool ok = wait_bar<kCluster>(bar, parity, sy);
+    const bool ok = wait_bar(bar, parity, sy);
     return __all_sync(kFull, ok);
 }
 
@@ -441,7 +447,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t sbase = ptx::smem_u32(smem);
-    const uint32_t sQ = sbase + kOffQ, sP = sbase + kOffP, sRing = sbase + kOffRing;
+    const uint32_t sQ = sbase + kOffQ, sP = sbase + kOffP, sK = sbase + kOffK, sV = sbase + kOffV;
     auto bar = [&](int i) { return sbase + kOffBar + 8 * i; };
     uint32_t *misc = reinterpret_cast<uint32_t *>(smem + kOffMisc);
     // (a broadcast, so that the compiler sees that a warp takes one role together)
@@ -450,18 +456,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int cluster = blockIdx.x >> 1;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kSlots; ++i) {
-            ptx::mbar_init(bar(B_FULL + i), 2);              // CTA 0's: a producer or relay of each CTA
-            ptx::mbar_init(bar(B_EDGE + i), 1);
-            ptx::mbar_init(bar(B_EMPTY + i), 1);
+        // (CTA 0's of the "full" barriers are the ones in use)
+        for (int i = 0; i < kRing; ++i) {
+            ptx::mbar_init(bar(B_KFULL + i), 2);             // a producer of each CTA
+            ptx::mbar_init(bar(B_KEMPTY + i), 1);
+            ptx::mbar_init(bar(B_VFULL + i), 2);             // a producer, or the clearing warp, of each
+            ptx::mbar_init(bar(B_VEMPTY + i), 1);
+            ptx::mbar_init(bar(B_VEDGE + i), 1);
         }
-        ptx::mbar_init(bar(B_QFULL), 2);                     // CTA 0's
+        for (int i = 0; i < 4; ++i) {
+            ptx::mbar_init(bar(B_PFULL + i), 4);             // two softmax warps of each CTA
+            ptx::mbar_init(bar(B_PFREE + i), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(bar(B_SFULL + i), 1);
+            ptx::mbar_init(bar(B_SFREE + i), 2 * kSmWarps);  // the softmax warps of both CTAs
+            ptx::mbar_init(bar(B_DRAIN + i), 1);
+        }
+        ptx::mbar_init(bar(B_QFULL), 2);
         ptx::mbar_init(bar(B_QEMPTY), 1);
-        ptx::mbar_init(bar(B_SFULL), 1);
-        ptx::mbar_init(bar(B_SFULL + 1), 1);
-        ptx::mbar_init(bar(B_PFULL), 2 * kSmWarps);          // CTA 0's: the softmax warps of both
         ptx::mbar_init(bar(B_PV), 1);
-        ptx::mbar_init(bar(B_DRAIN), 1);
         misc[1] = 0u;
         ptx::fence_mbar_init();
     }
@@ -480,14 +494,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
     if (warp == 0 || warp == 3) {
         // ---------------- producers ----------------
-        const uint32_t odd = warp == 3;
         const int box = p.box, bl = p.box_log, pl = p.page_log, in_page = p.a.page_size - 1;
         if (lane == 0) {
             ptx::tma_prefetch_desc(&tm_q);
             ptx::tma_prefetch_desc(&tm_kv);
         }
         bool ok = true;
-        uint32_t g = 0;                  // chunks so far
+        uint32_t g = 0, np = 0;          // chunks and pieces so far
         Walk walk(p, cluster);
         Piece pc;
         // page of each of a tile's boxes, lane j that of box j
@@ -502,57 +515,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             return page;
         };
-        // takes the next chunk's slot and announces `bytes` for it, to CTA 0 or, for
-        // a chunk with rows to clear, to this CTA's relay; the slot, or -1 for the
-        // other warp's chunk
-        uint32_t to = 0;
-        auto take = [&](int bytes, bool edge) {
-            const uint32_t s = g % kSlots, ph = (g / kSlots) & 1u;
-            const bool mine = (g & 1u) == odd;
-            ++g;
-            if (!mine || !ok) return -1;
-            ok = wait_bar_warp(bar(B_EMPTY + s), ph ^ 1u, sy);
-            if (!ok) return -1;
-            to = edge ? ptx::map_to_rank(bar(B_EDGE + s), rank) : ptx::map_to_rank(bar(B_FULL + s), 0);
-            if (lane == 0) ptx::mbar_arrive_expect_tx_cluster(to, bytes);
+        // waits for the next slot of the ring and announces `bytes` for it
+        auto take = [&](int empty, uint32_t to, uint32_t s, int bytes) {
+            ok = wait_bar_warp(bar(empty + s), ((g / kRing) & 1u) ^ 1u, sy);
+            if (ok && lane == 0) ptx::mbar_arrive_expect_tx_cluster(to, bytes);
             __syncwarp();
-            return static_cast<int>(s);
+            ++g;
         };
-        auto scores_chunks = [&](int base, int page) {
-            // this CTA's 128 tokens, 64 columns at a time
-            const int n = max(0, min(128, tile_tokens(pc, base) - 128 * static_cast<int>(rank)));
-            const int boxes = (n + box - 1) >> bl;
-            const int at = (128 * static_cast<int>(rank) >> bl) + lane;        // box of this lane
-            const int pg = __shfl_sync(kFull, page, at & 31);
-            const int y = (base + at * box) & in_page;
-            for (int k = 0; k < 8 && ok; ++k) {
-                const int s = take(boxes * box * 128, false);
-                if (s >= 0 && lane < boxes)
-                    ptx::tma_load_3d_pair(sRing + s * kChunk + lane * box * 128, &tm_kv, to, 64 * k, y, pg);
-            }
-        };
-        auto values_chunks = [&](int base, int page) {
-            // 64 tokens x 128 of this CTA's 256 columns: lanes 2j and 2j + 1 bring
-            // the two 64-column halves of box j
-            const int n = tile_tokens(pc, base);
-            for (int kb = 0; 64 * kb < n && ok; ++kb) {
-                const int boxes = (min(64, n - 64 * kb) + box - 1) >> bl;
-                const bool edge = has_edge(pc, base, kb);
-                const int at = (64 * kb >> bl) + (lane >> 1);
-                const int pg = __shfl_sync(kFull, page, at & 31);
-                const int y = (base + at * box) & in_page;
-                for (int j = 0; j < 2 && ok; ++j) {
-                    const int s = take(2 * boxes * box * 128, edge);
-                    if (s >= 0 && lane < 2 * boxes)
-                        ptx::tma_load_3d_pair(sRing + s * kChunk + (lane & 1) * 8192 + (lane >> 1) * box * 128, &tm_kv, to,
-                                              256 * static_cast<int>(rank) + 128 * j + 64 * (lane & 1), y, pg);
-                }
-            }
-        };
-        uint32_t np = 0;                 // pieces so far
         while (ok && walk.next(&pc)) {
-            int page = pages_at(pc.base);
-            if (!odd) {
+            if (warp == 0) {
+                int page = pages_at(pc.base);
                 ok = wait_bar_warp(bar(B_QEMPTY), (np & 1u) ^ 1u, sy);
                 if (!ok) break;
                 const uint32_t qbar = ptx::map_to_rank(bar(B_QFULL), 0);
@@ -561,135 +533,171 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (lane < 8)
                     ptx::tma_load_2d_pair(sQ + lane * 8192, &tm_q, qbar, 64 * lane,
                                           pc.row0 + kCtaRows * static_cast<int>(rank));
-            }
-            ++np;
-            scores_chunks(pc.base, page);
-            for (int i = 0; i < pc.tiles && ok; ++i) {
-                const int base = pc.base + i * kTile;
-                int next = 0;
-                if (i + 1 < pc.tiles) {
-                    next = pages_at(base + kTile);
-                    scores_chunks(base + kTile, next);
+                ++np;
+                for (int i = 0; i < pc.tiles && ok; ++i) {
+                    // this CTA's 128 tokens, 64 columns at a time
+                    const int base = pc.base + i * kTile;
+                    const int next = i + 1 < pc.tiles ? pages_at(base + kTile) : 0;
+                    const int n = max(0, min(128, tile_tokens(pc, base) - 128 * static_cast<int>(rank)));
+                    const int boxes = (n + box - 1) >> bl;
+                    const int at = (128 * static_cast<int>(rank) >> bl) + lane;        // box of this lane
+                    const int pg = __shfl_sync(kFull, page, at & 31);
+                    const int y = (base + at * box) & in_page;
+                    for (int k = 0; k < 8 && ok; ++k) {
+                        const uint32_t s = g % kRing, to = ptx::map_to_rank(bar(B_KFULL + s), 0);
+                        take(B_KEMPTY, to, s, boxes * box * 128);
+                        if (ok && lane < boxes)
+                            ptx::tma_load_3d_pair(sK + s * kChunk + lane * box * 128, &tm_kv, to, 64 * k, y, pg);
+                    }
+                    page = next;
                 }
-                values_chunks(base, page);
-                page = next;
-            }
-        }
-    } else if (warp == 2) {
-        // ---------------- relay ----------------
-        bool ok = true;
-        uint32_t g = 0, par = 0;         // chunks so far; parity of each slot's edge barrier
-        Walk walk(p, cluster);
-        Piece pc;
-        while (ok && walk.next(&pc)) {
-            g += 8;
-            for (int i = 0; i < pc.tiles && ok; ++i) {
-                if (i + 1 < pc.tiles) g += 8;
-                const int base = pc.base + i * kTile;
-                const int n = tile_tokens(pc, base), lo = pc.t0 - base;
-                for (int c = 0; 32 * (c & ~1) < n && ok; ++c, ++g) {
-                    if (!has_edge(pc, base, c >> 1)) continue;
-                    const uint32_t s = g % kSlots;
-                    ok = wait_bar_warp(bar(B_EDGE + s), par >> s & 1u, sy);
-                    if (!ok) break;
-                    par ^= 1u << s;
-                    // rows outside the span, up to the last 16 that the MMAs read
-                    const int first = 64 * (c >> 1), cut0 = lo - first, cut1 = n - first;
-                    const int end = (min(64, cut1) + 15) & ~15;
-                    for (int r = lane >> 4; r < end; r += 2)
-                        if (r < cut0 || r >= cut1)
-                            ptx::st_shared_v4(sRing + s * kChunk + (lane >> 3 & 1) * 8192 + r * 128 + (lane & 7) * 16, 0u,
-                                              0u, 0u, 0u);
-                    ptx::fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(bar(B_FULL + s), 0));
+            } else {
+                int page = pages_at(pc.base);
+                for (int i = 0; i < pc.tiles && ok; ++i) {
+                    // 64 tokens x 128 of this CTA's 256 columns: lanes 2j and 2j + 1 bring
+                    // the two 64-column halves of box j
+                    const int base = pc.base + i * kTile;
+                    const int next = i + 1 < pc.tiles ? pages_at(base + kTile) : 0;
+                    const int n = tile_tokens(pc, base);
+                    for (int kb = 0; 64 * kb < n && ok; ++kb) {
+                        const int boxes = (min(64, n - 64 * kb) + box - 1) >> bl;
+                        const bool edge = has_edge(pc, base, kb);
+                        const int at = (64 * kb >> bl) + (lane >> 1);
+                        const int pg = __shfl_sync(kFull, page, at & 31);
+                        const int y = (base + at * box) & in_page;
+                        for (int j = 0; j < 2 && ok; ++j) {
+                            const uint32_t s = g % kRing;
+                            const uint32_t to = edge ? ptx::map_to_rank(bar(B_VEDGE + s), rank)
+                                                     : ptx::map_to_rank(bar(B_VFULL + s), 0);
+                            take(B_VEMPTY, to, s, 2 * boxes * box * 128);
+                            if (ok && lane < 2 * boxes)
+                                ptx::tma_load_3d_pair(sV + s * kChunk + (lane & 1) * 8192 + (lane >> 1) * box * 128, &tm_kv,
+                                                      to, 256 * static_cast<int>(rank) + 128 * j + 64 * (lane & 1), y, pg);
+                        }
+                    }
+                    page = next;
                 }
             }
         }
     } else if (warp == 1) {
-        // ---------------- MMA issuer ----------------
+        // ---------------- issuer of the scores ----------------
         // The whole warp runs the loop and one lane issues: operands that are the
         // same in all lanes stay in uniform registers, which the MMAs take them
         // from (a lone thread's loop moves each one over first: 120 cycles an MMA).
         if (rank == 0) {
-            constexpr uint32_t idesc_s = ptx::make_idesc(1u, kRows, kTile);
-            constexpr uint32_t idesc_o = idesc_s | ptx::kIdescBMajorMN;
+            constexpr uint32_t idesc = ptx::make_idesc(1u, kRows, kTile);
             bool ok = true, any = false;
-            uint32_t g = 0, np = 0;
-            uint32_t gs = 0, gp = 0;     // score tiles and output tiles so far
+            uint32_t g = 0, np = 0, gs = 0;          // chunks, pieces and tiles so far
             const bool one = ptx::elect_one();
             Walk walk(p, cluster);
             Piece pc;
-            auto scores = [&](bool last) {
-                const uint32_t d = tmem + kTmemS + (gs & 1u) * 128;
-                for (int k = 0; k < 8; ++k, ++g) {
-                    const uint32_t s = g % kSlots;
-                    ok = wait_bar_warp(bar(B_FULL + s), (g / kSlots) & 1u, sy);
-                    if (!ok) return;
-                    ptx::tc_fence_after();
-                    const uint64_t ad = ptx::smem_desc_sw128(sQ + k * 8192);
-                    const uint64_t bd = ptx::smem_desc_sw128(sRing + s * kChunk);
-                    if (one) {
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            ptx::mma_bf16_pair(d, ad + 2 * kk, bd + 2 * kk, idesc_s, (k | kk) != 0);
-                        ptx::mma_commit_pair(bar(B_EMPTY + s));
-                    }
-                    any = true;
-                }
-                if (one) {
-                    ptx::mma_commit_pair(bar(B_SFULL + (gs & 1u)));
-                    if (last) ptx::mma_commit_pair(bar(B_QEMPTY));
-                }
-                ++gs;
-            };
-            auto output = [&](int base, bool first) {
-                const int n = tile_tokens(pc, base);
-                ok = wait_bar_warp<true>(bar(B_PFULL), gp & 1u, sy);
-                if (!ok) return;
-                ptx::tc_fence_after();
-                for (int c = 0; 32 * (c & ~1) < n; ++c, ++g) {
-                    const uint32_t s = g % kSlots;
-                    const bool edge = has_edge(pc, base, c >> 1);      // cleared by other threads' stores
-                    ok = edge ? wait_bar_warp<true>(bar(B_FULL + s), (g / kSlots) & 1u, sy)
-                              : wait_bar_warp(bar(B_FULL + s), (g / kSlots) & 1u, sy);
-                    if (!ok) return;
-                    ptx::tc_fence_after();
-                    const int kb = c >> 1, steps = min(4, (n - 64 * kb + 15) / 16);
-                    const uint64_t ad = ptx::smem_desc_sw128(sP + kb * 8192);
-                    const uint64_t bd = ptx::smem_desc_mn_sw128(sRing + s * kChunk, 8192);
-                    const uint32_t d = tmem + (c & 1) * 128;
-                    if (one) {
-                        if (steps == 4) {
-#pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-                                ptx::mma_bf16_pair(d, ad + 2 * kk, bd + 128 * kk, idesc_o, !first || kb > 0 || kk > 0);
-                        } else {
-                            for (int kk = 0; kk < steps; ++kk)
-                                ptx::mma_bf16_pair(d, ad + 2 * kk, bd + 128 * kk, idesc_o, !first || kb > 0 || kk > 0);
-                        }
-                        ptx::mma_commit_pair(bar(B_EMPTY + s));
-                    }
-                }
-                if (one) ptx::mma_commit_pair(bar(B_PV));
-                ++gp;
-            };
             while (ok && walk.next(&pc)) {
                 pc.uniform();
                 ok = wait_bar_warp(bar(B_QFULL), np & 1u, sy);
-                if (!ok) break;
                 ++np;
-                scores(pc.tiles == 1);
-                for (int i = 0; i < pc.tiles && ok; ++i) {
-                    if (i + 1 < pc.tiles) scores(i + 2 == pc.tiles);
-                    if (ok) output(pc.base + i * kTile, i == 0);
+                for (int i = 0; i < pc.tiles && ok; ++i, ++gs) {
+                    // the tile before the last has been read
+                    ok = wait_bar_warp(bar(B_SFREE + (gs & 1u)), ((gs >> 1) & 1u) ^ 1u, sy);
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    const uint32_t d = tmem + kTmemS + (gs & 1u) * 128;
+                    for (int k = 0; k < 8; ++k, ++g) {
+                        const uint32_t s = g % kRing;
+                        ok = wait_bar_warp(bar(B_KFULL + s), (g / kRing) & 1u, sy);
+                        if (!ok) break;
+                        const uint64_t ad = ptx::smem_desc_sw128(sQ + k * 8192);
+                        const uint64_t bd = ptx::smem_desc_sw128(sK + s * kChunk);
+                        if (one) {
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                ptx::mma_bf16_pair(d, ad + 2 * kk, bd + 2 * kk, idesc, (k | kk) != 0);
+                            ptx::mma_commit_pair(bar(B_KEMPTY + s));
+                        }
+                        any = true;
+                    }
+                    if (ok && one) {
+                        ptx::mma_commit_pair(bar(B_SFULL + (gs & 1u)));
+                        if (i + 1 == pc.tiles) ptx::mma_commit_pair(bar(B_QEMPTY));
+                    }
                 }
             }
             if (any) {
-                // nothing of the pair's MMAs is in flight once this has arrived
+                // none of these MMAs is in flight once this has arrived
                 if (one) ptx::mma_commit_pair(bar(B_DRAIN));
                 wait_landed(bar(B_DRAIN), 0);
             }
+        }
+    } else if (warp == 2) {
+        // ---------------- issuer of the output; clearing ----------------
+        constexpr uint32_t idesc = ptx::make_idesc(1u, kRows, kTile) | ptx::kIdescBMajorMN;
+        bool ok = true, any = false;
+        uint32_t g = 0, gp = 0, par = 0;             // chunks and tiles so far; parity of each slot's edge barrier
+        const bool one = ptx::elect_one();
+        Walk walk(p, cluster);
+        Piece pc;
+        while (ok && walk.next(&pc)) {
+            pc.uniform();
+            for (int i = 0; i < pc.tiles && ok; ++i, ++gp) {
+                const int base = pc.base + i * kTile;
+                const int n = tile_tokens(pc, base), lo = pc.t0 - base;
+                for (int kb = 0; 64 * kb < n && ok; ++kb) {
+                    const bool edge = has_edge(pc, base, kb);
+                    if (rank == 0) {
+                        ok = wait_bar_warp(bar(B_PFULL + kb), gp & 1u, sy);
+                        if (!ok) break;
+                        ptx::tc_fence_after();
+                    }
+                    const int steps = min(4, (n - 64 * kb + 15) / 16);
+                    for (int j = 0; j < 2; ++j, ++g) {
+                        const uint32_t s = g % kRing;
+                        if (edge) {
+                            ok = wait_bar_warp(bar(B_VEDGE + s), par >> s & 1u, sy);
+                            if (!ok) break;
+                            par ^= 1u << s;
+                            // rows outside the span, up to the last 16 that the MMAs read
+                            const int cut0 = lo - 64 * kb, cut1 = n - 64 * kb;
+                            for (int r = lane >> 4; r < 16 * steps; r += 2)
+                                if (r < cut0 || r >= cut1)
+                                    ptx::st_shared_v4(sV + s * kChunk + (lane >> 3 & 1) * 8192 + r * 128 + (lane & 7) * 16,
+                                                      0u, 0u, 0u, 0u);
+                            ptx::fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(bar(B_VFULL + s), 0));
+                            __syncwarp();
+                        }
+                        if (rank == 0) {
+                            ok = wait_bar_warp(bar(B_VFULL + s), (g / kRing) & 1u, sy);
+                            if (!ok) break;
+                            const uint64_t ad = ptx::smem_desc_sw128(sP + kb * 8192);
+                            const uint64_t bd = ptx::smem_desc_mn_sw128(sV + s * kChunk, 8192);
+                            const uint32_t d = tmem + j * 128;
+                            const bool more = i > 0 || kb > 0;
+                            if (one) {
+                                if (steps == 4) {
+#pragma unroll
+                                    for (int kk = 0; kk < 4; ++kk)
+                                        ptx::mma_bf16_pair(d, ad + 2 * kk, bd + 128 * kk, idesc, more || kk > 0);
+                                } else {
+                                    for (int kk = 0; kk < steps; ++kk)
+                                        ptx::mma_bf16_pair(d, ad + 2 * kk, bd + 128 * kk, idesc, more || kk > 0);
+                                }
+                                ptx::mma_commit_pair(bar(B_VEMPTY + s));
+                                if (j == 1) ptx::mma_commit_pair(bar(B_PFREE + kb));
+                            }
+                            any = true;
+                        }
+                    }
+                }
+                if (ok && rank == 0 && one) {
+                    // parts without a token are free as well
+                    for (int kb = (n + 63) / 64; kb < 4; ++kb) ptx::mma_commit_pair(bar(B_PFREE + kb));
+                    ptx::mma_commit_pair(bar(B_PV));
+                }
+            }
+        }
+        if (any) {
+            if (one) ptx::mma_commit_pair(bar(B_DRAIN + 1));
+            wait_landed(bar(B_DRAIN + 1), 0);
         }
     } else {
         // ---------------- softmax and output ----------------
@@ -704,8 +712,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
         float *red = reinterpret_cast<float *>(smem + kOffRed);
         volatile uint32_t *words = reinterpret_cast<volatile uint32_t *>(smem + kOffWord) + 8 * group;
-        const uint32_t prow = sP + (2 * half + part) * 8192 + r * 128;
-        const uint32_t p_full = ptx::map_to_rank(bar(B_PFULL), 0);
+        const int kb = 2 * half + part;               // part of P that holds them
+        const uint32_t prow = sP + kb * 8192 + r * 128;
+        const uint32_t p_full = ptx::map_to_rank(bar(B_PFULL + kb), 0);
         const float c = p.c_scale;
         bool ok = true;
         uint32_t gt = 0, rounds = 0;
@@ -744,6 +753,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         v[32 + k] = __uint_as_float(a1[k]);
                     }
                 }
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(bar(B_SFREE + (gt & 1u)), 0));
                 // tokens lo .. hi - 1 of this thread's 64 count
                 const int lo = pc.t0 - base - x0, hi = end - base - x0;
                 if (__any_sync(kFull, lo > 0 || hi < 64)) {
@@ -787,7 +799,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             ptx::tmem_st_wait();
                         }
                     }
-                    ptx::named_bar_sync(3 + group, 128);      // red is read
+                    // red is read, and all of the rows' output rescaled before any
+                    // part of the new P lets its MMAs begin
+                    ptx::tc_fence_before();
+                    ptx::named_bar_sync(3 + group, 128);
+                    ptx::tc_fence_after();
                 }
                 const float ref = m == -INFINITY ? 0.f : m;
                 float sum = 0.f;
@@ -797,8 +813,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     sum += v[k];
                 }
                 l += sum;
-                // P is free once the previous tile's output MMAs are done
-                if (gt > 0) ok = wait_bar_warp(bar(B_PV), (gt - 1u) & 1u, sy) && ok;
+                // this part of P is free once the previous tile's MMAs have read it
+                if (gt > 0) ok = wait_bar_warp(bar(B_PFREE + kb), (gt - 1u) & 1u, sy) && ok;
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
                     uint32_t w4[4];

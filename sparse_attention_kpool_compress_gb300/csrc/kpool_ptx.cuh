@@ -378,25 +378,13 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t saddr, uint32_t rank)
     return r;
 }
 
-// Arrive on an mbarrier of the cluster (an address from map_to_rank).
+// Arrive on an mbarrier of the cluster (an address from map_to_rank).  What the
+// arrival hands over lies in this CTA's own memory and is read there by MMAs, so
+// the writer's fence.proxy.async (shared memory) or tcgen05 fence (tensor
+// memory) orders it, and no cluster-wide release is paid for.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar)
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
-                 : "memory");
-}
-
-// mbar_try_wait whose success also makes the other CTAs' writes visible.
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 
 // Arrive on an mbarrier of the cluster and announce `bytes` of loads; orders
