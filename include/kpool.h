@@ -634,8 +634,9 @@ KPOOL_API int kpool_read_status(const void *workspace, int *status_out);
 /*
  * kpool_debug_set_wait_limit_ns -- test entry: the time limit of each wait
  * inside the scoring kernel (kpool_score_topk, _at, _noalloc, _dense and the
- * host-buffer pass) and the sparse attention (kpool_sparse_mla_*) for
- * launches made after this call, process-wide; ns = 0
+ * host-buffer pass), the sparse attention (kpool_sparse_mla_*) and the
+ * shared-prefix attention (kpool_shared_prefix_mla_fwd) for launches made
+ * after this call, process-wide; ns = 0
  * restores the default of 2 s.  Returns the previous limit.  A wait that
  * runs out sets KPOOL_STATUS_TIMEOUT in the call's status word and raises an
  * abort flag in its CTA: the CTA's roles stop waiting, let their in-flight

@@ -15,5 +15,6 @@ def __getattr__(name):
                                              "LIB_PATH", "STATUS_TIMEOUT", "STATUS_BAD_SEQLENS",
                                              "STATUS_BAD_PAGE", "STATUS_NO_PAGES"):
         mod = importlib.import_module(".binding", __name__)
-        return getattr(mod, name)
+        value = globals()[name] = getattr(mod, name)      # found at once from now on
+        return value
     raise AttributeError(name)

@@ -527,10 +527,13 @@ class KPoolPages:
     [n_seqs, max_pages], seq_lens [n_seqs], ref_count [n_pages], free_list
     [n_pages] and free_count [1], CUDA tensors of one device that the
     kpool_pages_* calls read and change in place (include/kpool.h,
-    kpool_page_pool).  kpool_pages_new makes an empty one."""
+    kpool_page_pool).  kpool_pages_new makes an empty one.  `workspace` is the
+    one that calls on this pool use unless they are given another (calls on a
+    pool are ordered anyway); kpool_read_status(pages.workspace) tells how the
+    last of them went."""
 
     __slots__ = ("page_table", "seq_lens", "ref_count", "free_list", "free_count", "page_size",
-                 "n_seqs", "n_pages", "_index", "_c", "_at")
+                 "n_seqs", "n_pages", "workspace", "_index", "_c", "_at", "_ws")
 
     def __init__(self, page_table, seq_lens, ref_count, free_list, free_count, page_size: int):
         arrays = dict(page_table=page_table, seq_lens=seq_lens, ref_count=ref_count,
@@ -556,6 +559,11 @@ class KPoolPages:
                         free_list.data_ptr(), free_count.data_ptr(), page_table.shape[0],
                         page_table.shape[1], ref_count.numel(), page_size))
         put("_at", ctypes.addressof(self._c))
+        # (enough for every list of at most n_pages items)
+        put("workspace", torch.zeros(
+            max(256, _lib.kpool_pages_workspace_size(self.n_pages, self.n_seqs, self.n_pages)),
+            dtype=torch.uint8, device=page_table.device))
+        put("_ws", (self.workspace, self.workspace.data_ptr(), self.workspace.numel()))
 
     def __setattr__(self, name, value):
         raise AttributeError("a KPoolPages keeps its tensors: make another one")
@@ -619,6 +627,8 @@ def kpool_pages_copy(src, dst, stores, workspace=None):
 
 
 def _pool_workspace(workspace, n, pages):
+    if workspace is None and n <= pages.n_pages:
+        return pages._ws
     return _bytes(workspace, 0 if workspace is not None else
                   _lib.kpool_pages_workspace_size(n, pages.n_seqs, pages.n_pages), pages._index)
 

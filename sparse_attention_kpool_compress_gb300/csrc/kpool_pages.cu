@@ -360,37 +360,39 @@ __global__ void __launch_bounds__(kApplyThreads) write_kernel(const kpool_page_p
                                                               const int32_t *begin, const int32_t *cu_rows, int n,
                                                               int64_t total, const char *rows,
                                                               int64_t rows_layer_stride, const kpool_page_store g,
-                                                              int *ws)
+                                                              int split, int *ws)
 {
+    // One warp per row and `split`-th of the layers.
     const int lane = threadIdx.x & 31;
     const int64_t warps = static_cast<int64_t>(gridDim.x) * (kApplyThreads / 32);
-    for (int64_t t = (static_cast<int64_t>(blockIdx.x) * kApplyThreads + threadIdx.x) >> 5;
-         t < total * g.n_layers; t += warps) {
-        const int layer = static_cast<int>(t / total);
-        const int r = static_cast<int>(t - layer * total);
+    for (int64_t t = (static_cast<int64_t>(blockIdx.x) * kApplyThreads + threadIdx.x) >> 5; t < total * split;
+         t += warps) {
+        const int first = static_cast<int>(t / total);
+        const int r = static_cast<int>(t - first * total);
         const int i = segment_of(cu_rows, n, r, lane);
-        const int k = r - cu_rows[i];
-        bool ok = k >= 0 && r < cu_rows[i + 1] && in_range(seqs[i], p.n_seqs) && begin[i] >= 0;
+        const int k = r - cu_rows[i], seq = seqs[i], from = begin[i];
+        bool ok = k >= 0 && r < cu_rows[i + 1] && in_range(seq, p.n_seqs) && from >= 0;
         int page = -1, row = 0;
         if (ok) {
-            // tokens per row of this store: rows behind the sequence's length are not its own
-            const int64_t at = static_cast<int64_t>(begin[i]) + k;
-            const int64_t held = static_cast<int64_t>(p.seq_lens[seqs[i]]) * g.rows_per_page;
+            // rows behind the sequence's length (rows_per_page of every page_size tokens) are not its own
+            const int64_t at = static_cast<int64_t>(from) + k;
+            const int64_t held = static_cast<int64_t>(p.seq_lens[seq]) * g.rows_per_page;
             const int64_t col = at / g.rows_per_page;
             row = static_cast<int>(at - col * g.rows_per_page);
             ok = at * p.page_size < held && col < p.max_pages;
-            if (ok) page = p.page_table[static_cast<int64_t>(seqs[i]) * p.max_pages + col];
+            if (ok) page = p.page_table[static_cast<int64_t>(seq) * p.max_pages + col];
             ok = ok && in_range(page, p.n_pages) && p.ref_count[page] == 1;
         }
         if (!ok) {
             if (lane == 0) atomicOr(ws + W_STATUS, KPOOL_STATUS_BAD_PAGE);
             continue;
         }
-        const char *src = rows + layer * rows_layer_stride + static_cast<int64_t>(r) * g.row_bytes;
-        char *dst = static_cast<char *>(g.data) + layer * g.layer_stride + page * g.page_stride +
-                    static_cast<int64_t>(row) * g.row_bytes;
-        for (int off = lane * 16; off < g.row_bytes; off += 512)
-            *reinterpret_cast<uint4 *>(dst + off) = *reinterpret_cast<const uint4 *>(src + off);
+        const char *src = rows + static_cast<int64_t>(r) * g.row_bytes;
+        char *dst = static_cast<char *>(g.data) + page * g.page_stride + static_cast<int64_t>(row) * g.row_bytes;
+        for (int layer = first; layer < g.n_layers; layer += split)
+            for (int off = lane * 16; off < g.row_bytes; off += 512)
+                *reinterpret_cast<uint4 *>(dst + layer * g.layer_stride + off) =
+                    __ldcs(reinterpret_cast<const uint4 *>(src + layer * rows_layer_stride + off));
     }
 }
 
@@ -634,9 +636,11 @@ int run_pages_write(const kpool_page_pool &p, const int32_t *seqs, const int32_t
 {
     KPOOL_CUDA_CHECK(cudaMemsetAsync(ws, 0, 16, s));
     if (total == 0 || n == 0) return KPOOL_OK;
-    const int64_t warps = total * g.n_layers;
-    write_kernel<<<grid_for((warps + kApplyThreads / 32 - 1) / (kApplyThreads / 32)), kApplyThreads, 0, s>>>(
-        p, seqs, begin, cu_rows, n, total, static_cast<const char *>(rows), rows_layer_stride, g,
+    // a row's place is looked up once for all its layers where the rows alone fill the
+    // GPU, once per layer where they do not
+    const int split = total >= 32 * static_cast<int64_t>(num_sms()) ? 1 : g.n_layers;
+    write_kernel<<<grid_for((total * split + kApplyThreads / 32 - 1) / (kApplyThreads / 32)), kApplyThreads, 0, s>>>(
+        p, seqs, begin, cu_rows, n, total, static_cast<const char *>(rows), rows_layer_stride, g, split,
         static_cast<int *>(ws));
     KPOOL_CUDA_CHECK(cudaGetLastError());
     return KPOOL_OK;

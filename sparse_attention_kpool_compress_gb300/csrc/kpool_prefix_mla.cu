@@ -62,12 +62,13 @@ constexpr int kDc = 512;
 constexpr int kRows = 128;               // rows of a unit
 constexpr int kCtaRows = 64;             // of them in each CTA
 constexpr int kTile = 256;               // tokens of a tile
-constexpr int kOverhead = 2;             // a piece's start and end, in tiles (for the even cut)
+constexpr int kOverhead = 3;             // a piece's start and end, in tiles (for the even cut; 2 and 4 measured slower)
 constexpr int kThreads = 384;
 constexpr int kSmWarps = 8;
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanLists = 1024;         // sequences, groups and units that the plan keeps in shared memory
 constexpr int kPlanUnits = 1024;
+static_assert(kPlanLists <= kPlanThreads, "a thread per entry");
 constexpr float kRescale = 8.f;          // headroom of the reference maximum (log2)
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr uint64_t kLandNs = 2000000ull;
@@ -138,7 +139,8 @@ struct Params {
     int box, box_log;        // rows of a TMA box, and its logarithm
     int page_log;
     float c_scale;           // softmax scale * log2(e)
-    int wait_tries;
+    int wait_tries;          // see Sync
+    uint32_t wait_nap_ns;
     uint64_t wait_limit_ns;
 };
 
@@ -203,20 +205,23 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p)
     const Work &w = p.w;
     ptx::grid_dependents_launch();
     if (threadIdx.x == 0) status = 0;
+    __syncthreads();
     const int entities = a.G + a.B;          // groups, then sequences
     const bool small = a.B <= kPlanLists && a.G <= kPlanLists;
     int *lists = small ? reinterpret_cast<int *>(plan_smem + kPlanUnits * sizeof(Unit)) : w.lists;
     int *len = lists, *shared = len + a.B, *row = shared + a.G, *unit0 = row + a.B;
     const int32_t *cu_q = a.cu_q, *cu_g = a.cu_groups;
+    // (at most one entry of each list per thread then: all loads are in flight at once)
+    int my_q = 0, my_g = 0;
     if (small) {
-        int *q = unit0 + entities, *g = q + a.B + 1;
-        for (int i = threadIdx.x; i <= a.B; i += blockDim.x) q[i] = a.cu_q[i];
-        for (int i = threadIdx.x; i <= a.G; i += blockDim.x) g[i] = a.cu_groups[i];
-        cu_q = q;
-        cu_g = g;
+        const int i = threadIdx.x;
+        if (i < a.B) my_q = a.cu_q[i];
+        if (i < a.G) my_g = a.cu_groups[i], shared[i] = a.prefix_lens[i];
+    } else {
+        for (int i = threadIdx.x; i < a.G; i += blockDim.x) shared[i] = a.prefix_lens[i];
     }
+    const int last_q = a.cu_q[a.B], last_g = a.cu_groups[a.G];
     const int64_t room = static_cast<int64_t>(a.max_pages) * a.page_size;
-    __syncthreads();
     // a sequence's length, cut to what its table row holds
     for (int b = threadIdx.x; b < a.B; b += blockDim.x) {
         int r = a.seq_ids != nullptr ? a.seq_ids[b] : b;
@@ -230,10 +235,20 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p)
         row[b] = r;
         len[b] = static_cast<int>(n);
     }
+    if (small) {
+        int *q = unit0 + entities, *g = q + a.B + 1;
+        const int i = threadIdx.x;
+        if (i < a.B) q[i] = my_q;
+        if (i < a.G) g[i] = my_g;
+        if (i == 0) q[a.B] = last_q, g[a.G] = last_g;
+        cu_q = q;
+        cu_g = g;
+    }
+    __syncthreads();
     bool bad = false;
     for (int i = threadIdx.x; i <= a.B; i += blockDim.x) bad |= i == 0 ? cu_q[0] != 0 : cu_q[i] < cu_q[i - 1];
     for (int i = threadIdx.x; i <= a.G; i += blockDim.x) bad |= i == 0 ? cu_g[0] != 0 : cu_g[i] < cu_g[i - 1];
-    bad |= cu_q[a.B] != a.Tq || cu_g[a.G] != a.B;
+    bad |= last_q != a.Tq || last_g != a.B;
     if (__syncthreads_or(bad)) {
         if (threadIdx.x == 0) {
             w.head[H_STATUS] = KPOOL_STATUS_BAD_SEQLENS;
@@ -252,7 +267,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p)
             const int b1 = e < a.G ? cu_g[e + 1] : b0 + 1;
             n = static_cast<int>((static_cast<int64_t>(cu_q[b1] - cu_q[b0]) * a.H + kRows - 1) / kRows);
             // shared tokens are read through the group's first sequence
-            if (e < a.G) shared[e] = b1 > b0 ? min(max(a.prefix_lens[e], 0), len[b0]) : 0;
+            if (e < a.G) shared[e] = b1 > b0 ? min(max(shared[e], 0), len[b0]) : 0;
         }
         int64_t total;
         const int64_t at = units + block_exclusive(n, scratch, &total);
@@ -336,6 +351,7 @@ struct Sync {
     volatile uint32_t *abort_flag;
     int *status;
     int tries;               // before the timer is read
+    uint32_t nap_ns;         // one try's suspension
     uint64_t limit_ns;
 };
 
@@ -345,11 +361,11 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const Sy
 {
     // (the timer is slow to read: it would add its latency to each hop of the pipeline)
 #pragma unroll 1
-    for (int i = 0; i <= sy.tries; ++i)
-        if (ptx::mbar_try_wait(bar, parity)) return true;
+    for (int i = 0; i < sy.tries; ++i)
+        if (ptx::mbar_try_wait_ns(bar, parity, sy.nap_ns)) return true;
     const uint64_t t0 = ptx::globaltimer();
     while (true) {
-        if (ptx::mbar_try_wait(bar, parity)) return true;
+        if (ptx::mbar_try_wait_ns(bar, parity, sy.nap_ns)) return true;
         if (*sy.abort_flag) return false;
         if (ptx::globaltimer() - t0 > sy.limit_ns) {
             *sy.abort_flag = 1u;
@@ -488,7 +504,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     ptx::cluster_sync();                 // no remote arrival before the peer's barriers exist
     ptx::tc_fence_after();
     const uint32_t tmem = __shfl_sync(kFull, misc[0], 0);
-    const Sync sy{reinterpret_cast<volatile uint32_t *>(&misc[1]), p.w.head + H_STATUS, p.wait_tries, p.wait_limit_ns};
+    const Sync sy{reinterpret_cast<volatile uint32_t *>(&misc[1]), p.w.head + H_STATUS, p.wait_tries, p.wait_nap_ns, p.wait_limit_ns};
     ptx::grid_dependents_launch();
     ptx::grid_dependency_wait();         // the plan
 
@@ -839,19 +855,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             ptx::named_bar_sync(3 + group, 128);
             ptx::tc_fence_after();
             const float inv = l > 0.f ? 1.f / l : 0.f;
-            float *out = p.w.o + (pc.out + row) * kDc + 256 * half + 128 * part;
+            // 32 columns at a time through this warp's own part of P (which no MMA
+            // reads any more), so that a store covers whole lines of four rows: straight
+            // from the registers, one row a lane, the stores take twice as long
+            const uint32_t stage = prow - lane * 128;
+            const int row0 = row - lane;
+            float *out = p.w.o + (pc.out + row0) * kDc + 256 * half + 128 * part + 4 * (lane & 7);
 #pragma unroll 1
             for (int k = 0; k < 4; ++k) {
                 uint32_t o[32];
                 ptx::tmem_ld32(lanes + 128 * part + 32 * k, o);
                 ptx::tmem_ld_wait(o);
-                if (row < pc.nrows) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
+                __syncwarp();
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8) ptx::st_global_v8(out + 32 * k + e, &o[e]);
+                for (int e = 0; e < 8; ++e)
+                    ptx::st_shared_v4(prow + ((e ^ (lane & 7)) << 4), o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                __syncwarp();
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int rr = 4 * e + (lane >> 3);
+                    const float4 y = ptx::ld_shared_v4(stage + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
+                    if (row0 + rr < pc.nrows) *reinterpret_cast<float4 *>(out + rr * kDc + 32 * k) = y;
                 }
             }
+            __syncwarp();
             if (member == 0 && row < pc.nrows) p.w.lse[pc.out + row] = l > 0.f ? m + log2f(l) : -INFINITY;
             ptx::tc_fence_before();
         }
@@ -878,15 +907,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 // ---- combine -----------------------------------------------------------------
 
-// Four warps per row, a float4 of a lane each: short rows of many pieces want
-// more loads in flight than one warp has.
+// kWarps warps per row, 4 / kWarps float4 of a lane each.  Four when all rows'
+// warps fit the GPU at once (a few long rows of many pieces want more loads in
+// flight than one warp has), one otherwise.
+template <int kWarps>
 __global__ void __launch_bounds__(256) combine_kernel(const Params p)
 {
+    constexpr int kVec = 4 / kWarps;
     ptx::grid_dependency_wait();
     if (!p.w.head[H_OK]) return;
     const int lane = threadIdx.x & 31;
     const int64_t w = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 5;
-    const int64_t row = w >> 2;
+    const int64_t row = w / kWarps;
+    const int quarter = static_cast<int>(w % kWarps) * kVec;       // first 128 columns of this warp
     if (row >= p.a.Tq * p.a.H) return;
     const int64_t share = p.w.start[0].share;
     const Token x = p.w.tok[row / p.a.H];
@@ -907,29 +940,38 @@ __global__ void __launch_bounds__(256) combine_kernel(const Params p)
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
     const float ref = m == -INFINITY ? 0.f : m;
-    const float4 *o = reinterpret_cast<const float4 *>(p.w.o) + (w & 3) * 32 + lane;
+    const float4 *o = reinterpret_cast<const float4 *>(p.w.o) + quarter * 32 + lane;
     float l = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 acc[kVec];
+#pragma unroll
+    for (int v = 0; v < kVec; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int base = 0; base < n; base += 32) {
         const float mine = base + lane < n ? ptx::ex2_approx(p.w.lse[at(base + lane)] - ref) : 0.f;
         const int here = min(32, n - base);
 #pragma unroll 4
         for (int i = 0; i < here; ++i) {
             const float f = __shfl_sync(kFull, mine, i);
-            const float4 y = __ldcg(o + at(base + i) * (kDc / 4));
+            const float4 *from = o + at(base + i) * (kDc / 4);
             l += f;
-            acc.x = fmaf(y.x, f, acc.x);
-            acc.y = fmaf(y.y, f, acc.y);
-            acc.z = fmaf(y.z, f, acc.z);
-            acc.w = fmaf(y.w, f, acc.w);
+#pragma unroll
+            for (int v = 0; v < kVec; ++v) {
+                const float4 y = __ldcg(from + 32 * v);
+                acc[v].x = fmaf(y.x, f, acc[v].x);
+                acc[v].y = fmaf(y.y, f, acc[v].y);
+                acc[v].z = fmaf(y.z, f, acc[v].z);
+                acc[v].w = fmaf(y.w, f, acc[v].w);
+            }
         }
     }
     const float inv = l > 0.f ? 1.f / l : 0.f;
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
-    const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-    uint2 *out = reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.a.o) + row * kDc) + (w & 3) * 32 + lane;
-    *out = make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
-    if ((w & 3) == 0 && lane == 0) p.a.lse[row] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+    uint2 *out = reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.a.o) + row * kDc) + quarter * 32 + lane;
+#pragma unroll
+    for (int v = 0; v < kVec; ++v) {
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(acc[v].x * inv, acc[v].y * inv);
+        const __nv_bfloat162 hi = __floats2bfloat162_rn(acc[v].z * inv, acc[v].w * inv);
+        out[32 * v] = make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+    }
+    if (quarter == 0 && lane == 0) p.a.lse[row] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
 // ---- host --------------------------------------------------------------------
@@ -1000,7 +1042,8 @@ int run_prefix_mla(const PrefixMlaArgs &a, cudaStream_t s)
     while (1 << p.page_log < a.page_size) ++p.page_log;
     p.c_scale = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
     p.wait_limit_ns = get_wait_limit_ns();
-    p.wait_tries = p.wait_limit_ns >= 1000000u ? 4096 : 1;
+    p.wait_tries = p.wait_limit_ns >= 10000000u ? 1000 : 0;
+    p.wait_nap_ns = static_cast<uint32_t>(std::min<uint64_t>(p.wait_limit_ns, 1000));
     const int64_t rows = a.Tq * a.H;
     CUtensorMap mq, mkv;
     if (rows > 0) {
@@ -1016,7 +1059,10 @@ int run_prefix_mla(const PrefixMlaArgs &a, cudaStream_t s)
     KPOOL_CUDA_CHECK(cudaGetLastError());
     if (rows == 0) return KPOOL_OK;
     KPOOL_CUDA_CHECK(launch_after(attend_kernel, 2 * p.clusters, kThreads, kSmemBytes, s, mq, mkv, p));
-    KPOOL_CUDA_CHECK(launch_after(combine_kernel, static_cast<int>((rows + 1) / 2), 256, 0, s, p));
+    if (4 * rows <= 64 * static_cast<int64_t>(num_sms()))
+        KPOOL_CUDA_CHECK(launch_after(combine_kernel<4>, static_cast<int>((rows + 1) / 2), 256, 0, s, p));
+    else
+        KPOOL_CUDA_CHECK(launch_after(combine_kernel<1>, static_cast<int>((rows + 7) / 8), 256, 0, s, p));
     return KPOOL_OK;
 }
 

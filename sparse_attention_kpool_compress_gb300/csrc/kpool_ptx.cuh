@@ -66,6 +66,20 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity)
     return ok != 0;
 }
 
+// The same, suspended for at most about `ns` when the phase is not complete.
+__device__ __forceinline__ bool mbar_try_wait_ns(uint32_t bar, uint32_t parity, uint32_t ns)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(ns)
+        : "memory");
+    return ok != 0;
+}
+
 // ---- TMA -----------------------------------------------------------------
 __device__ __forceinline__ void tma_prefetch_desc(const void *desc)
 {
@@ -459,12 +473,15 @@ __device__ __forceinline__ void mma_commit_pair(uint32_t bar)
         : "memory");
 }
 
-// 32-byte global store (a whole sector).
-__device__ __forceinline__ void st_global_v8(void *p, const uint32_t *v)
+// 16-byte shared-memory load.
+__device__ __forceinline__ float4 ld_shared_v4(uint32_t saddr)
 {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]),
-                 "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(saddr)
                  : "memory");
+    return v;
 }
 
 // True in one lane of the (converged) warp.

@@ -331,6 +331,26 @@ def test_streams_and_graphs(K):
         c.check(o, lse, note=k)
 
 
+@pytest.mark.parametrize("limit", [1, 3000])
+def test_expired_waits(K, limit):
+    """Waits that run out at once, or part way through, end the call with KPOOL_STATUS_TIMEOUT (never with a hang), and
+    the next call is whole."""
+    c = Case([(3000, [(3001, 1), (3300, 1), (3010, 2)])], H=64, page=64, seed=17)
+    args = c.args()
+    ws = torch.empty(K.kpool_shared_prefix_mla_workspace_size(4, 64, 3, 1), dtype=torch.uint8, device="cuda")
+    before = K.kpool_debug_set_wait_limit_ns(limit)
+    try:
+        for _ in range(3):
+            K.kpool_shared_prefix_mla_fwd(*args, workspace=ws)
+            status = K.kpool_read_status(ws)
+            assert status in (0, 1) and (limit > 1 or status == 1)
+    finally:
+        K.kpool_debug_set_wait_limit_ns(before)
+    o, lse = K.kpool_shared_prefix_mla_fwd(*args, workspace=ws)
+    assert K.kpool_read_status(ws) == 0
+    c.check(o, lse)
+
+
 def test_a_rollout_from_pages_to_attention(K):
     """The calls together, as a rollout makes them: a prompt's rows written, forked for three samples, each grown by its
     own tokens step by step, attended through the pool's own table, one sample retired, the pool packed."""
