@@ -360,15 +360,22 @@ __global__ void __launch_bounds__(kApplyThreads) write_kernel(const kpool_page_p
                                                               const int32_t *begin, const int32_t *cu_rows, int n,
                                                               int64_t total, const char *rows,
                                                               int64_t rows_layer_stride, const kpool_page_store g,
-                                                              int split, int *ws)
+                                                              int *ws)
 {
-    // One warp per row and `split`-th of the layers.
+    // One warp per row and layer (one per row for all layers measured slower: 11.8
+    // against 9.4 us for 8200 rows in two layers).
     const int lane = threadIdx.x & 31;
     const int64_t warps = static_cast<int64_t>(gridDim.x) * (kApplyThreads / 32);
-    for (int64_t t = (static_cast<int64_t>(blockIdx.x) * kApplyThreads + threadIdx.x) >> 5; t < total * split;
-         t += warps) {
-        const int first = static_cast<int>(t / total);
-        const int r = static_cast<int>(t - first * total);
+    for (int64_t t = (static_cast<int64_t>(blockIdx.x) * kApplyThreads + threadIdx.x) >> 5;
+         t < total * g.n_layers; t += warps) {
+        const int layer = static_cast<int>(t / total);
+        const int r = static_cast<int>(t - layer * total);
+        const char *src = rows + layer * rows_layer_stride + static_cast<int64_t>(r) * g.row_bytes;
+        // the row's first 2 KB, on their way while its place is looked up
+        uint4 v[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            if (lane * 16 + 512 * q < g.row_bytes) v[q] = __ldcs(reinterpret_cast<const uint4 *>(src + lane * 16 + 512 * q));
         const int i = segment_of(cu_rows, n, r, lane);
         const int k = r - cu_rows[i], seq = seqs[i], from = begin[i];
         bool ok = k >= 0 && r < cu_rows[i + 1] && in_range(seq, p.n_seqs) && from >= 0;
@@ -387,12 +394,13 @@ __global__ void __launch_bounds__(kApplyThreads) write_kernel(const kpool_page_p
             if (lane == 0) atomicOr(ws + W_STATUS, KPOOL_STATUS_BAD_PAGE);
             continue;
         }
-        const char *src = rows + static_cast<int64_t>(r) * g.row_bytes;
-        char *dst = static_cast<char *>(g.data) + page * g.page_stride + static_cast<int64_t>(row) * g.row_bytes;
-        for (int layer = first; layer < g.n_layers; layer += split)
-            for (int off = lane * 16; off < g.row_bytes; off += 512)
-                *reinterpret_cast<uint4 *>(dst + layer * g.layer_stride + off) =
-                    __ldcs(reinterpret_cast<const uint4 *>(src + layer * rows_layer_stride + off));
+        char *dst = static_cast<char *>(g.data) + layer * g.layer_stride + page * g.page_stride +
+                    static_cast<int64_t>(row) * g.row_bytes;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            if (lane * 16 + 512 * q < g.row_bytes) *reinterpret_cast<uint4 *>(dst + lane * 16 + 512 * q) = v[q];
+        for (int off = 2048 + lane * 16; off < g.row_bytes; off += 512)
+            *reinterpret_cast<uint4 *>(dst + off) = __ldcs(reinterpret_cast<const uint4 *>(src + off));
     }
 }
 
@@ -571,6 +579,9 @@ int grid_for(int64_t tasks)
     return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(tasks, 8LL * num_sms())));
 }
 
+// A plan's block: short lists take a small one, whose barriers and scans are shorter.
+int plan_threads(int n) { return n <= 256 ? 256 : kPlanThreads; }
+
 template <typename... P, typename... A>
 cudaError_t launch_after_plan(void (*kernel)(P...), int grid, cudaStream_t s, A... args)
 {
@@ -601,7 +612,7 @@ int run_pages_copy(const int32_t *src, const int32_t *dst, int n, int n_pages, c
 {
     const Stores st = pack(stores, n_stores);
     int *w = static_cast<int *>(ws);
-    copy_plan<<<1, kPlanThreads, 0, s>>>(src, dst, n, n_pages, w, lists(ws, n));
+    copy_plan<<<1, plan_threads(n), 0, s>>>(src, dst, n, n_pages, w, lists(ws, n));
     KPOOL_CUDA_CHECK(cudaGetLastError());
     KPOOL_CUDA_CHECK(launch_after_plan(copy_apply, grid_for(static_cast<int64_t>(n) * st.per_item), s, st, src, dst,
                                        n_pages, static_cast<const int *>(w)));
@@ -614,7 +625,7 @@ int run_pages_fork(const kpool_page_pool &p, const int32_t *parents, const int32
     const Stores st = pack(stores, n_stores);
     const Lists l = lists(ws, n);
     int *w = static_cast<int *>(ws);
-    fork_plan<<<1, kPlanThreads, 0, s>>>(p, parents, children, n, w, l);
+    fork_plan<<<1, plan_threads(n), 0, s>>>(p, parents, children, n, w, l);
     KPOOL_CUDA_CHECK(cudaGetLastError());
     const int64_t cols = (p.max_pages + kApplyThreads - 1) / kApplyThreads;
     KPOOL_CUDA_CHECK(launch_after_plan(fork_apply, grid_for(n * std::max<int64_t>(cols, st.per_item)), s, st, p,
@@ -625,7 +636,7 @@ int run_pages_fork(const kpool_page_pool &p, const int32_t *parents, const int32
 int run_pages_extend(const kpool_page_pool &p, const int32_t *seqs, const int32_t *n_new, int n, int32_t *begin,
                      void *ws, cudaStream_t s)
 {
-    extend_kernel<<<1, kPlanThreads, 0, s>>>(p, seqs, n_new, n, begin, static_cast<int *>(ws), lists(ws, n));
+    extend_kernel<<<1, plan_threads(n), 0, s>>>(p, seqs, n_new, n, begin, static_cast<int *>(ws), lists(ws, n));
     KPOOL_CUDA_CHECK(cudaGetLastError());
     return KPOOL_OK;
 }
@@ -636,11 +647,10 @@ int run_pages_write(const kpool_page_pool &p, const int32_t *seqs, const int32_t
 {
     KPOOL_CUDA_CHECK(cudaMemsetAsync(ws, 0, 16, s));
     if (total == 0 || n == 0) return KPOOL_OK;
-    // a row's place is looked up once for all its layers where the rows alone fill the
-    // GPU, once per layer where they do not
-    const int split = total >= 32 * static_cast<int64_t>(num_sms()) ? 1 : g.n_layers;
-    write_kernel<<<grid_for((total * split + kApplyThreads / 32 - 1) / (kApplyThreads / 32)), kApplyThreads, 0, s>>>(
-        p, seqs, begin, cu_rows, n, total, static_cast<const char *>(rows), rows_layer_stride, g, split,
+    // (more blocks than fit at once: a warp has one row's chain of lookups to wait for)
+    const int64_t blocks = (total * g.n_layers + kApplyThreads / 32 - 1) / (kApplyThreads / 32);
+    write_kernel<<<static_cast<int>(std::min<int64_t>(blocks, 1 << 20)), kApplyThreads, 0, s>>>(
+        p, seqs, begin, cu_rows, n, total, static_cast<const char *>(rows), rows_layer_stride, g,
         static_cast<int *>(ws));
     KPOOL_CUDA_CHECK(cudaGetLastError());
     return KPOOL_OK;
@@ -650,7 +660,7 @@ int run_pages_free(const kpool_page_pool &p, const int32_t *seqs, int n, void *w
 {
     const Lists l = lists(ws, n);
     int *w = static_cast<int *>(ws), *bits = l.mark + std::max(p.n_seqs, p.n_pages);
-    free_plan<<<1, kPlanThreads, 0, s>>>(p, seqs, n, w, l, bits);
+    free_plan<<<1, plan_threads(n), 0, s>>>(p, seqs, n, w, l, bits);
     KPOOL_CUDA_CHECK(cudaGetLastError());
     const int64_t cols = (p.max_pages + kApplyThreads - 1) / kApplyThreads;
     KPOOL_CUDA_CHECK(launch_after_plan(free_apply, grid_for(n * cols), s, p, seqs, w, l, bits));

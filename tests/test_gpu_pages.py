@@ -389,6 +389,15 @@ def test_pages_larger_than_a_piece(K):
     b.compact()
 
 
+def test_rows_wider_than_a_warp_loads_at_once(K):
+    """Rows of 2 KB and a little, and of 5 KB."""
+    for width in (2064, 5120):
+        b = Both(K, n_seqs=3, n_pages=6, max_pages=2, page_size=4, layers=2)
+        h = np.random.RandomState(width).randint(0, 256, (2, 6, 4, width)).astype(np.uint8)
+        b.stores, b.host.stores = [torch.from_numpy(h).cuda()], [h.copy()]
+        b.grow([1, 0], [5, 3])
+
+
 def test_captured_and_replayed(K):
     """A decode step's upkeep captured once and replayed: each replay goes on from the pool as it is."""
     b = Both(K, n_seqs=4, n_pages=30, max_pages=8, page_size=8, layers=1)
