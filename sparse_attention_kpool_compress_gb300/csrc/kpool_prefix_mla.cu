@@ -87,7 +87,7 @@ constexpr int kOffBar = kOffWord + 64;
 enum {
     B_KFULL = 0, B_KEMPTY = B_KFULL + kRing, B_VFULL = B_KEMPTY + kRing, B_VEMPTY = B_VFULL + kRing,
     B_VEDGE = B_VEMPTY + kRing, B_PFULL = B_VEDGE + kRing, B_PFREE = B_PFULL + 4, B_SFULL = B_PFREE + 4,
-    B_SFREE = B_SFULL + 2, B_QFULL = B_SFREE + 2, B_QEMPTY, B_PV, B_DRAIN, N_BARS = B_DRAIN + 2
+    B_SFREE = B_SFULL + 2, B_QFULL = B_SFREE + 2, B_QEMPTY, B_DRAIN, N_BARS = B_DRAIN + 2
 };
 constexpr int kOffMisc = kOffBar + N_BARS * 8;     // [0] tmem base, [1] abort flag
 constexpr int kSmemBytes = kOffMisc + 16 + 1024;   // and alignment slack
@@ -489,7 +489,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         ptx::mbar_init(bar(B_QFULL), 2);
         ptx::mbar_init(bar(B_QEMPTY), 1);
-        ptx::mbar_init(bar(B_PV), 1);
         misc[1] = 0u;
         ptx::fence_mbar_init();
     }
@@ -702,10 +701,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
-                if (ok && rank == 0 && one) {
-                    // parts without a token are free as well
-                    for (int kb = (n + 63) / 64; kb < 4; ++kb) ptx::mma_commit_pair(bar(B_PFREE + kb));
-                    ptx::mma_commit_pair(bar(B_PV));
+                // parts without a token pass as well
+                for (int kb = (n + 63) / 64; rank == 0 && kb < 4 && ok; ++kb) {
+                    ok = wait_bar_warp(bar(B_PFULL + kb), gp & 1u, sy);
+                    if (ok && one) ptx::mma_commit_pair(bar(B_PFREE + kb));
                 }
             }
         }
@@ -796,8 +795,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     m = mn;
                     l *= f;
                     if (i > 0) {
-                        // the output so far, once its MMAs are done
-                        ok = wait_bar_warp(bar(B_PV), (gt - 1u) & 1u, sy);
+                        // the output so far, once its MMAs are done (the four warps have
+                        // met since each waited for its part of the tile before the last,
+                        // so these parities mean the last one)
+                        for (int k = 0; k < 4; ++k) ok = wait_bar_warp(bar(B_PFREE + k), (gt - 1u) & 1u, sy) && ok;
                         ptx::tc_fence_after();
                         if (__any_sync(kFull, f != 1.f)) {
 #pragma unroll 1
@@ -847,8 +848,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (stop) break;
             // the piece's rows: sum over the four threads of each, then the output
             red[member * kCtaRows + r] = l;
-            ok = wait_bar_warp(bar(B_PV), (gt - 1u) & 1u, sy) && ok;
             ptx::named_bar_sync(3 + group, 128);
+            for (int k = 0; k < 4; ++k) ok = wait_bar_warp(bar(B_PFREE + k), (gt - 1u) & 1u, sy) && ok;
             l = (red[r] + red[kCtaRows + r]) + (red[2 * kCtaRows + r] + red[3 * kCtaRows + r]);
             ptx::named_bar_sync(3 + group, 128);
             ptx::tc_fence_after();
