@@ -16,7 +16,8 @@
 //   attend    one CTA pair per piece of a unit, persistent: unnormalised
 //             softmax with a running maximum, FP32 partial rows and their
 //             log-sum-exp to the workspace.
-//   combine   one warp per row joins its pieces, the shared ones and its own.
+//   combine   one or four warps per row join its pieces, the shared ones and its
+//             own.
 //
 // attend, per CTA pair.  The output of 128 rows x 512 columns fills all of one
 // SM's tensor memory, so two SMs share it: tcgen05.mma with cta_group::2,
