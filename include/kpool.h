@@ -486,9 +486,10 @@ KPOOL_API int kpool_sparse_mla_fwd_pools_at(const void *q, const void *kv, const
  * the device first.  A sequence or page id out of range or listed twice, a
  * negative count, a length that the table has no room for, or free_count
  * outside 0..n_pages sets KPOOL_STATUS_BAD_PAGE; too few free pages set
- * KPOOL_STATUS_NO_PAGES.  Either way the call changes nothing.  Page ids out of
- * range inside the used part of a page-table row are skipped, with
- * KPOOL_STATUS_BAD_PAGE.  No id is followed out of its array.  Calls on one
+ * KPOOL_STATUS_NO_PAGES.  Either way the call changes nothing.  The same goes
+ * for the last, partial page of a sequence that a call forks or extends; other
+ * page ids out of range inside the used part of a page-table row are skipped,
+ * with KPOOL_STATUS_BAD_PAGE.  No id is followed out of its array.  Calls on one
  * pool are ordered by the caller (one stream, or events).
  * workspace: kpool_pages_workspace_size(n, n_seqs, n_pages) bytes, n the
  * listed items (0 for kpool_pages_compact), 256-byte aligned; its status word
@@ -534,8 +535,8 @@ KPOOL_API int kpool_pages_fork(const kpool_page_pool *pool, const int32_t *paren
 /*
  * kpool_pages_extend -- sequence seqs[i] grows by n_new[i] >= 0 tokens; the
  * pages that it lacks are popped from the free pages in list order.
- * begin_out[i] (int32 [n]) gets its length before the call, or -1 everywhere
- * when the call is refused.  A sequence whose last, partial page is held by
+ * begin_out[i] (int32 [n], apart from the lists) gets its length before the
+ * call, or -1 everywhere when the call is refused.  A sequence whose last, partial page is held by
  * others as well is refused (KPOOL_STATUS_BAD_PAGE): fork copies such pages.
  */
 KPOOL_API int kpool_pages_extend(const kpool_page_pool *pool, const int32_t *seqs,
@@ -551,8 +552,8 @@ KPOOL_API int kpool_pages_extend(const kpool_page_pool *pool, const int32_t *seq
  *   cu_rows  int32 [n + 1]
  * A row outside its sequence's length (rows_per_page of every page_size
  * tokens), in a page that other sequences hold too, or with no sequence to go
- * to is left out, with KPOOL_STATUS_BAD_PAGE.  Rows that go to one place twice
- * leave either.
+ * to is left out, with KPOOL_STATUS_BAD_PAGE.  Two rows that go to one place
+ * leave a mixture of both.
  */
 KPOOL_API int kpool_pages_write(const kpool_page_pool *pool, const int32_t *seqs,
                                 const int32_t *begin, const int32_t *cu_rows, int64_t n,
@@ -614,7 +615,8 @@ KPOOL_API int kpool_pages_compact(const kpool_page_pool *pool, const kpool_page_
  * is out of range (results of the rows that use it are not valid; a length is
  * cut to its table's room); KPOOL_STATUS_TIMEOUT as for the sparse attention.
  * Supported: 1 <= H <= 128, Dc = 512, page_size 16, 32, 64 or 128
- * (UNSUPPORTED otherwise); softmax_scale finite and > 0.
+ * (UNSUPPORTED otherwise); softmax_scale finite and > 0; B and G up to 2^24.
+ * Calls that may overlap need workspaces of their own.
  */
 KPOOL_API size_t kpool_shared_prefix_mla_workspace_size(int64_t Tq, int H, int B, int G);
 KPOOL_API int kpool_shared_prefix_mla_fwd(

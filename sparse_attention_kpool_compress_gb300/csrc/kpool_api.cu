@@ -817,6 +817,8 @@ int kpool_pages_extend(const kpool_page_pool *pool, const int32_t *seqs, const i
     int rc = check_pool(pool);
     if (rc) return rc;
     if ((rc = check_items(n, {seqs, n_new, begin_out}))) return rc;
+    if ((begin_out < seqs + n && seqs < begin_out + n) || (begin_out < n_new + n && n_new < begin_out + n))
+        return fail(KPOOL_ERR_INVALID_ARG, "begin_out overlaps a list of the call");
     if ((rc = check_pages_workspace(workspace, workspace_bytes, n, pool->n_seqs, pool->n_pages))) return rc;
     if (n == 0) return nothing_listed(workspace, stream);
     return run_pages_extend(*pool, seqs, n_new, static_cast<int>(n), begin_out, workspace,

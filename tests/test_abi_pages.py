@@ -61,7 +61,9 @@ def test_pools_and_stores_are_checked(b):
             dict(layer_stride=8), dict(page_stride=1024), dict(layer_stride=1024),
             dict(page_stride=-16 * 1024), dict(n_layers=5000))],
         (L.kpool_pages_extend(_pool(b, a), p, p, 4, P(None), p, ws, None), -1),
-        (L.kpool_pages_extend(_pool(b, a), p, p, 4, p, p, 16, None), -4),
+        (L.kpool_pages_extend(_pool(b, a), p, p, 4, P(a + 64), p, 16, None), -4),
+        (L.kpool_pages_extend(_pool(b, a), p, P(a + 64), 4, P(a + 12), p, ws, None), -1),
+        (L.kpool_pages_extend(_pool(b, a), P(a + 64), p, 4, p, p, ws, None), -1),
         (L.kpool_pages_free(_pool(b, a), P(None), 4, p, ws, None), -1),
         (L.kpool_pages_free(_pool(b, a), p, 1 << 30, p, ws, None), -1),
         (L.kpool_pages_compact(_pool(b, a), good, -1, p, ws, None), -1),

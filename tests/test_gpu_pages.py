@@ -389,6 +389,33 @@ def test_pages_larger_than_a_piece(K):
     b.compact()
 
 
+def test_a_store_of_more_than_4_gb(K):
+    """Pages and layers whose byte offsets pass 32 bits."""
+    n, ps, width = 3000, 32, 49152                 # 1.5 MB a page, 4.7 GB a layer
+    store = torch.zeros(2, n, ps, width, dtype=torch.uint8, device="cuda")
+    pages = K.kpool_pages_new(4, n, 4, ps)
+    i = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    pages.free_list.copy_(pages.free_list.flip(0))  # the last page is taken first
+    g = torch.Generator("cuda")
+    g.manual_seed(1)
+    rows = torch.randint(0, 256, (2, 40, width), dtype=torch.uint8, device="cuda", generator=g)
+    begin = K.kpool_pages_extend(pages, i([2]), i([40]))
+    K.kpool_pages_write(pages, i([2]), begin, i([0, 40]), rows, store)
+    K.kpool_pages_fork(pages, i([2]), i([0]), store)
+    assert pages.page_table[2, :2].tolist() == [n - 1, n - 2]
+    assert pages.page_table[0, :2].tolist() == [n - 1, n - 3]
+    K.kpool_pages_copy(i([n - 1]), i([1500]), store)
+    assert K.kpool_read_status(pages.workspace) == 0
+    assert torch.equal(store[:, n - 1], rows[:, :32]) and torch.equal(store[:, 1500], rows[:, :32])
+    assert torch.equal(store[:, n - 2, :8], rows[:, 32:]) and torch.equal(store[:, n - 3, :8], rows[:, 32:])
+    K.kpool_pages_free(pages, i([2]))
+    K.kpool_pages_compact(pages, store)
+    assert K.kpool_read_status(pages.workspace) == 0
+    # the two pages still held, n - 3 and n - 1, move to 0 and 1 in their order
+    assert pages.page_table[0, :2].tolist() == [1, 0] and pages.free_count.item() == n - 2
+    assert torch.equal(store[:, 1], rows[:, :32]) and torch.equal(store[:, 0, :8], rows[:, 32:])
+
+
 def test_rows_wider_than_a_warp_loads_at_once(K):
     """Rows of 2 KB and a little, and of 5 KB."""
     for width in (2064, 5120):

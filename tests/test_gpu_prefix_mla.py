@@ -331,6 +331,21 @@ def test_streams_and_graphs(K):
         c.check(o, lse, note=k)
 
 
+def test_a_cache_of_more_than_4_gb(K):
+    """Pages whose byte offsets pass 32 bits, next to pages at the beginning."""
+    c = Case([(150, [(200, 1), (151, 2)]), (0, [(64, 1)])], H=16, page=64, seed=19)
+    n = 70000
+    big = torch.full((n, 64, W), float("nan"), dtype=torch.bfloat16, device="cuda")
+    to = torch.tensor([(n - 1 - 7 * k) if k % 2 else 5 * k for k in range(c.n_pages)])
+    big[to.cuda()] = c.kv.cuda()
+    args = c.args()
+    args[1] = big
+    table = torch.from_numpy(c.table).long()
+    args[2] = torch.where(table >= 0, to[table.clamp(min=0)], -1).to(torch.int32).cuda()
+    o, lse = K.kpool_shared_prefix_mla_fwd(*args)
+    c.check(o, lse)
+
+
 @pytest.mark.parametrize("limit", [1, 3000])
 def test_expired_waits(K, limit):
     """Waits that run out at once, or part way through, end the call with KPOOL_STATUS_TIMEOUT (never with a hang), and
