@@ -68,6 +68,8 @@ constexpr int kThreads = 384;
 constexpr int kSmWarps = 8;
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanUnits = 1024;         // units that the plan keeps in shared memory, with lists of a thread per entry
+constexpr int kMaxClusters = 80;         // CTA pairs that a workspace has room for
+constexpr int64_t kBlockRows = 512;      // rows up to which combine takes a block for each
 constexpr float kRescale = 8.f;          // headroom of the reference maximum (log2)
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr uint64_t kLandNs = 2000000ull;
@@ -907,17 +909,112 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 // ---- combine -----------------------------------------------------------------
 
-// kWarps warps per row, 4 / kWarps float4 of a lane each.  Four when all rows'
-// warps fit the GPU at once (a few long rows of many pieces want more loads in
-// flight than one warp has), one otherwise.
-template <int kWarps>
+// The pieces of one row: the shared ones, then the sequence's own.
+struct Pieces {
+    int64_t shared0, own0;   // partial row of the first of each
+    int shared_n, own_n, shared_rows, own_rows;
+
+    __device__ Pieces(const Params &p, int64_t row, const Token &x, int64_t share)
+    {
+        const int ks = static_cast<int>(row - x.prow0), ko = static_cast<int>(row - x.srow0);
+        const Unit us = p.w.unit[x.pu + ks / kRows], uo = p.w.unit[x.su + ko / kRows];
+        int64_t c0;
+        pieces_of(us, share, &c0, &shared_n);
+        pieces_of(uo, share, &c0, &own_n);
+        shared0 = us.out0 + ks % kRows;
+        own0 = uo.out0 + ko % kRows;
+        shared_rows = us.nrows;
+        own_rows = uo.nrows;
+    }
+    __device__ int count() const { return shared_n + own_n; }
+    __device__ int64_t at(int i) const
+    {
+        return i < shared_n ? shared0 + static_cast<int64_t>(i) * shared_rows
+                            : own0 + static_cast<int64_t>(i - shared_n) * own_rows;
+    }
+};
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    const __nv_bfloat162 x = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&x);
+}
+
+// A block per row, a piece per warp at a time, then a sum over the warps: for few
+// rows, whose pieces may be many and are then all on their way at once (one
+// sequence of 131072 tokens, 74 pieces a row: 78 -> 52 us in all; 256 rows of two
+// pieces: 20.8 -> 21.3; 1680 rows of four: 33 -> 37, so only up to kBlockRows).
+__global__ void __launch_bounds__(256) combine_block_kernel(const Params p)
+{
+    constexpr int kWarps = 8;
+    static_assert(2 * kMaxClusters <= 256, "a thread per piece");
+    __shared__ float weight[256], top[kWarps], sums[kWarps];
+    __shared__ float4 part[kWarps][kDc / 4];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t row = blockIdx.x;
+    const int query = static_cast<int>(row / p.a.H);
+    ptx::grid_dependency_wait();
+    const int ok = p.w.head[H_OK];
+    const int64_t share = p.w.start[0].share;
+    const Token x = p.w.tok[query];
+    if (!ok) return;
+    const Pieces pc(p, row, x, share);
+    const int n = pc.count();
+    const float s = static_cast<int>(threadIdx.x) < n ? p.w.lse[pc.at(threadIdx.x)] : -INFINITY;
+    float m = s;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
+    if (lane == 0) top[warp] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) m = fmaxf(m, top[i]);
+    const float f = m == -INFINITY ? 0.f : ptx::ex2_approx(s - m);
+    weight[threadIdx.x] = f;
+    float l = f;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(kFull, l, d);
+    if (lane == 0) sums[warp] = l;
+    __syncthreads();
+    l = 0.f;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) l += sums[i];
+    float4 acc[4];
+#pragma unroll
+    for (int v = 0; v < 4; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = warp; i < n; i += kWarps) {
+        const float4 *from = reinterpret_cast<const float4 *>(p.w.o) + pc.at(i) * (kDc / 4) + lane;
+        const float g = weight[i];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            const float4 y = __ldcg(from + 32 * v);
+            acc[v].x = fmaf(y.x, g, acc[v].x);
+            acc[v].y = fmaf(y.y, g, acc[v].y);
+            acc[v].z = fmaf(y.z, g, acc[v].z);
+            acc[v].w = fmaf(y.w, g, acc[v].w);
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < 4; ++v) part[warp][32 * v + lane] = acc[v];
+    __syncthreads();
+    // columns 2 threadIdx.x and the next
+    float2 y = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+        const float2 z = reinterpret_cast<const float2 *>(part[i])[threadIdx.x];
+        y.x += z.x;
+        y.y += z.y;
+    }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.a.o) + row * kDc)[threadIdx.x] = pack_bf16(y.x * inv, y.y * inv);
+    if (threadIdx.x == 0) p.a.lse[row] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+}
+
+// A warp per row, for more rows than the GPU holds blocks of the other form.
 __global__ void __launch_bounds__(256) combine_kernel(const Params p)
 {
-    constexpr int kVec = 4 / kWarps;
     const int lane = threadIdx.x & 31;
-    const int64_t w = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 5;
-    const int64_t row = w / kWarps;
-    const int quarter = static_cast<int>(w % kWarps) * kVec;       // first 128 columns of this warp
+    const int64_t row = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 5;
     if (row >= p.a.Tq * p.a.H) return;
     const int query = static_cast<int>(row / p.a.H);
     ptx::grid_dependency_wait();
@@ -925,38 +1022,27 @@ __global__ void __launch_bounds__(256) combine_kernel(const Params p)
     const int64_t share = p.w.start[0].share;
     const Token x = p.w.tok[query];
     if (!ok) return;
-    const int ks = static_cast<int>(row - x.prow0), ko = static_cast<int>(row - x.srow0);
-    const Unit us = p.w.unit[x.pu + ks / kRows], uo = p.w.unit[x.su + ko / kRows];
-    int64_t c0;
-    int ns, no;
-    pieces_of(us, share, &c0, &ns);
-    pieces_of(uo, share, &c0, &no);
-    // partial row of piece i: the shared ones, then the sequence's own
-    auto at = [&](int i) {
-        return i < ns ? us.out0 + static_cast<int64_t>(i) * us.nrows + ks % kRows
-                      : uo.out0 + static_cast<int64_t>(i - ns) * uo.nrows + ko % kRows;
-    };
-    const int n = ns + no;
+    const Pieces pc(p, row, x, share);
+    const int n = pc.count();
     float m = -INFINITY;
-    for (int i = lane; i < n; i += 32) m = fmaxf(m, p.w.lse[at(i)]);
+    for (int i = lane; i < n; i += 32) m = fmaxf(m, p.w.lse[pc.at(i)]);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
     const float ref = m == -INFINITY ? 0.f : m;
-    const float4 *o = reinterpret_cast<const float4 *>(p.w.o) + quarter * 32 + lane;
     float l = 0.f;
-    float4 acc[kVec];
+    float4 acc[4];
 #pragma unroll
-    for (int v = 0; v < kVec; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int v = 0; v < 4; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int base = 0; base < n; base += 32) {
-        const float mine = base + lane < n ? ptx::ex2_approx(p.w.lse[at(base + lane)] - ref) : 0.f;
+        const float mine = base + lane < n ? ptx::ex2_approx(p.w.lse[pc.at(base + lane)] - ref) : 0.f;
         const int here = min(32, n - base);
 #pragma unroll 4
         for (int i = 0; i < here; ++i) {
             const float f = __shfl_sync(kFull, mine, i);
-            const float4 *from = o + at(base + i) * (kDc / 4);
+            const float4 *from = reinterpret_cast<const float4 *>(p.w.o) + pc.at(base + i) * (kDc / 4) + lane;
             l += f;
 #pragma unroll
-            for (int v = 0; v < kVec; ++v) {
+            for (int v = 0; v < 4; ++v) {
                 const float4 y = __ldcg(from + 32 * v);
                 acc[v].x = fmaf(y.x, f, acc[v].x);
                 acc[v].y = fmaf(y.y, f, acc[v].y);
@@ -966,14 +1052,11 @@ __global__ void __launch_bounds__(256) combine_kernel(const Params p)
         }
     }
     const float inv = l > 0.f ? 1.f / l : 0.f;
-    uint2 *out = reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.a.o) + row * kDc) + quarter * 32 + lane;
+    uint2 *out = reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.a.o) + row * kDc) + lane;
 #pragma unroll
-    for (int v = 0; v < kVec; ++v) {
-        const __nv_bfloat162 lo = __floats2bfloat162_rn(acc[v].x * inv, acc[v].y * inv);
-        const __nv_bfloat162 hi = __floats2bfloat162_rn(acc[v].z * inv, acc[v].w * inv);
-        out[32 * v] = make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
-    }
-    if (quarter == 0 && lane == 0) p.a.lse[row] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+    for (int v = 0; v < 4; ++v)
+        out[32 * v] = make_uint2(pack_bf16(acc[v].x * inv, acc[v].y * inv), pack_bf16(acc[v].z * inv, acc[v].w * inv));
+    if (lane == 0) p.a.lse[row] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
 // ---- host --------------------------------------------------------------------
@@ -1022,7 +1105,6 @@ cudaError_t launch_after(void (*kernel)(P...), int grid, int threads, int smem, 
 
 // CTA pairs: one per two SMs.  (The size must not depend on the device that a
 // caller sizes its workspace on, so it is bounded rather than exact there.)
-constexpr int kMaxClusters = 80;
 int clusters() { return std::max(1, std::min(kMaxClusters, num_sms() / 2)); }
 
 }  // namespace
@@ -1063,10 +1145,10 @@ int run_prefix_mla(const PrefixMlaArgs &a, cudaStream_t s)
     KPOOL_CUDA_CHECK(cudaGetLastError());
     if (rows == 0) return KPOOL_OK;
     KPOOL_CUDA_CHECK(launch_after(attend_kernel, 2 * p.clusters, kThreads, kSmemBytes, s, mq, mkv, p));
-    if (4 * rows <= 64 * static_cast<int64_t>(num_sms()))
-        KPOOL_CUDA_CHECK(launch_after(combine_kernel<4>, static_cast<int>((rows + 1) / 2), 256, 0, s, p));
+    if (rows <= kBlockRows)
+        KPOOL_CUDA_CHECK(launch_after(combine_block_kernel, static_cast<int>(rows), 256, 0, s, p));
     else
-        KPOOL_CUDA_CHECK(launch_after(combine_kernel<1>, static_cast<int>((rows + 7) / 8), 256, 0, s, p));
+        KPOOL_CUDA_CHECK(launch_after(combine_kernel, static_cast<int>((rows + 7) / 8), 256, 0, s, p));
     return KPOOL_OK;
 }
 
