@@ -14,8 +14,8 @@
 //           workspace.  A list with a bad entry, or one the free pages do not
 //           cover, changes nothing (its count of items becomes 0).
 //   apply   all SMs: page-table rows, reference counts and page contents.
-// The second kernel is launched with programmatic stream serialisation: its
-// blocks start while the plan runs and wait for its end, which hides the
+// All are launched with programmatic stream serialisation: a kernel's blocks
+// start while the one in front of it runs and wait for its end, which hides the
 // launch.  No block waits for another one inside a kernel.
 //
 // Bound: contents by HBM (each byte read and written once, 16-byte accesses,
@@ -154,6 +154,7 @@ __global__ void __launch_bounds__(kPlanThreads) copy_plan(const int32_t *src, co
                                                           int n_pages, int *ws, Lists l)
 {
     ptx::grid_dependents_launch();
+    ptx::grid_dependency_wait();
     bool bad = false;
     // a source may be listed several times, a destination once, a page not as both
     for (int i = threadIdx.x; i < n; i += blockDim.x)
@@ -172,6 +173,7 @@ __global__ void __launch_bounds__(kPlanThreads) copy_plan(const int32_t *src, co
 __global__ void __launch_bounds__(kApplyThreads) copy_apply(const __grid_constant__ Stores st, const int32_t *src,
                                                             const int32_t *dst, int n_pages, const int *ws)
 {
+    ptx::grid_dependents_launch();
     ptx::grid_dependency_wait();
     copy_pages(st, src, dst, nullptr, ws[W_COUNT], 1, n_pages);
 }
@@ -184,6 +186,7 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan(const kpool_page_pool 
 {
     __shared__ int scratch[32];
     ptx::grid_dependents_launch();
+    ptx::grid_dependency_wait();
     const int ps = p.page_size;
     const int64_t room = static_cast<int64_t>(p.max_pages) * ps;
     bool bad = bad_or_twice(children, n, p.n_seqs, l.mark);
@@ -243,6 +246,7 @@ __global__ void __launch_bounds__(kApplyThreads) fork_apply(const __grid_constan
                                                             const int32_t *parents, const int32_t *children,
                                                             int *ws, Lists l)
 {
+    ptx::grid_dependents_launch();
     ptx::grid_dependency_wait();
     const int n = ws[W_COUNT];
     const int cols = ceil_div(p.max_pages, kApplyThreads);
@@ -275,6 +279,8 @@ __global__ void __launch_bounds__(kPlanThreads) extend_kernel(const kpool_page_p
                                                               int *ws, Lists l)
 {
     __shared__ int scratch[32];
+    ptx::grid_dependents_launch();
+    ptx::grid_dependency_wait();
     const int ps = p.page_size;
     const int64_t room = static_cast<int64_t>(p.max_pages) * ps;
     bool bad = bad_or_twice(seqs, n, p.n_seqs, l.mark);
@@ -414,6 +420,7 @@ __global__ void __launch_bounds__(kPlanThreads) free_plan(const kpool_page_pool 
                                                           int *ws, Lists l, int *bits)
 {
     ptx::grid_dependents_launch();
+    ptx::grid_dependency_wait();
     const int64_t room = static_cast<int64_t>(p.max_pages) * p.page_size;
     bool bad = bad_or_twice(seqs, n, p.n_seqs, l.mark);
     for (int i = threadIdx.x; i < n; i += blockDim.x)
@@ -439,6 +446,7 @@ __global__ void __launch_bounds__(kApplyThreads) free_apply(const kpool_page_poo
 {
     __shared__ int scratch[32];
     __shared__ int ticket;
+    ptx::grid_dependents_launch();
     ptx::grid_dependency_wait();
     const int n = ws[W_COUNT];
     const int cols = ceil_div(p.max_pages, kApplyThreads);
@@ -490,6 +498,7 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan(const kpool_page_po
 {
     __shared__ int scratch[32];
     ptx::grid_dependents_launch();
+    ptx::grid_dependency_wait();
     const int n = p.n_pages;
     int mine = 0;
     for (int i = threadIdx.x; i < n; i += blockDim.x) mine += p.ref_count[i] > 0;
@@ -538,6 +547,7 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan(const kpool_page_po
 __global__ void __launch_bounds__(kApplyThreads) compact_apply(const __grid_constant__ Stores st,
                                                                const kpool_page_pool p, int *ws, Lists l)
 {
+    ptx::grid_dependents_launch();
     ptx::grid_dependency_wait();
     const int k = ws[W_LIVE];
     const int cols = ceil_div(p.max_pages, kApplyThreads);
@@ -585,11 +595,11 @@ int grid_for(int64_t tasks)
 int plan_threads(int n) { return n <= 256 ? 256 : kPlanThreads; }
 
 template <typename... P, typename... A>
-cudaError_t launch_after_plan(void (*kernel)(P...), int grid, cudaStream_t s, A... args)
+cudaError_t launch_after(void (*kernel)(P...), int grid, int threads, cudaStream_t s, A... args)
 {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kApplyThreads);
+    cfg.blockDim = dim3(threads);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -614,9 +624,8 @@ int run_pages_copy(const int32_t *src, const int32_t *dst, int n, int n_pages, c
 {
     const Stores st = pack(stores, n_stores);
     int *w = static_cast<int *>(ws);
-    copy_plan<<<1, plan_threads(n), 0, s>>>(src, dst, n, n_pages, w, lists(ws, n));
-    KPOOL_CUDA_CHECK(cudaGetLastError());
-    KPOOL_CUDA_CHECK(launch_after_plan(copy_apply, grid_for(static_cast<int64_t>(n) * st.per_item), s, st, src, dst,
+    KPOOL_CUDA_CHECK(launch_after(copy_plan, 1, plan_threads(n), s, src, dst, n, n_pages, w, lists(ws, n)));
+    KPOOL_CUDA_CHECK(launch_after(copy_apply, grid_for(static_cast<int64_t>(n) * st.per_item), kApplyThreads, s, st, src, dst,
                                        n_pages, static_cast<const int *>(w)));
     return KPOOL_OK;
 }
@@ -627,10 +636,9 @@ int run_pages_fork(const kpool_page_pool &p, const int32_t *parents, const int32
     const Stores st = pack(stores, n_stores);
     const Lists l = lists(ws, n);
     int *w = static_cast<int *>(ws);
-    fork_plan<<<1, plan_threads(n), 0, s>>>(p, parents, children, n, w, l);
-    KPOOL_CUDA_CHECK(cudaGetLastError());
+    KPOOL_CUDA_CHECK(launch_after(fork_plan, 1, plan_threads(n), s, p, parents, children, n, w, l));
     const int64_t cols = (p.max_pages + kApplyThreads - 1) / kApplyThreads;
-    KPOOL_CUDA_CHECK(launch_after_plan(fork_apply, grid_for(n * std::max<int64_t>(cols, st.per_item)), s, st, p,
+    KPOOL_CUDA_CHECK(launch_after(fork_apply, grid_for(n * std::max<int64_t>(cols, st.per_item)), kApplyThreads, s, st, p,
                                        parents, children, w, l));
     return KPOOL_OK;
 }
@@ -638,8 +646,7 @@ int run_pages_fork(const kpool_page_pool &p, const int32_t *parents, const int32
 int run_pages_extend(const kpool_page_pool &p, const int32_t *seqs, const int32_t *n_new, int n, int32_t *begin,
                      void *ws, cudaStream_t s)
 {
-    extend_kernel<<<1, plan_threads(n), 0, s>>>(p, seqs, n_new, n, begin, static_cast<int *>(ws), lists(ws, n));
-    KPOOL_CUDA_CHECK(cudaGetLastError());
+    KPOOL_CUDA_CHECK(launch_after(extend_kernel, 1, plan_threads(n), s, p, seqs, n_new, n, begin, static_cast<int *>(ws), lists(ws, n)));
     return KPOOL_OK;
 }
 
@@ -662,10 +669,9 @@ int run_pages_free(const kpool_page_pool &p, const int32_t *seqs, int n, void *w
 {
     const Lists l = lists(ws, n);
     int *w = static_cast<int *>(ws), *bits = l.mark + std::max(p.n_seqs, p.n_pages);
-    free_plan<<<1, plan_threads(n), 0, s>>>(p, seqs, n, w, l, bits);
-    KPOOL_CUDA_CHECK(cudaGetLastError());
+    KPOOL_CUDA_CHECK(launch_after(free_plan, 1, plan_threads(n), s, p, seqs, n, w, l, bits));
     const int64_t cols = (p.max_pages + kApplyThreads - 1) / kApplyThreads;
-    KPOOL_CUDA_CHECK(launch_after_plan(free_apply, grid_for(n * cols), s, p, seqs, w, l, bits));
+    KPOOL_CUDA_CHECK(launch_after(free_apply, grid_for(n * cols), kApplyThreads, s, p, seqs, w, l, bits));
     return KPOOL_OK;
 }
 
@@ -675,12 +681,11 @@ int run_pages_compact(const kpool_page_pool &p, const kpool_page_store *stores, 
     const Stores st = pack(stores, n_stores);
     const Lists l = lists(ws, p.n_pages);
     int *w = static_cast<int *>(ws);
-    compact_plan<<<1, kPlanThreads, 0, s>>>(p, w, l);
-    KPOOL_CUDA_CHECK(cudaGetLastError());
+    KPOOL_CUDA_CHECK(launch_after(compact_plan, 1, kPlanThreads, s, p, w, l));
     const int64_t cols = (p.max_pages + kApplyThreads - 1) / kApplyThreads;
-    KPOOL_CUDA_CHECK(launch_after_plan(
+    KPOOL_CUDA_CHECK(launch_after(
         compact_apply, grid_for(std::max<int64_t>(p.n_seqs * cols, static_cast<int64_t>(p.n_pages) / 2 * st.per_item)),
-        s, st, p, w, l));
+        kApplyThreads, s, st, p, w, l));
     return KPOOL_OK;
 }
 

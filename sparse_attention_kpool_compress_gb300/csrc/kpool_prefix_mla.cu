@@ -205,6 +205,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p)
     const PrefixMlaArgs &a = p.a;
     const Work &w = p.w;
     ptx::grid_dependents_launch();
+    ptx::grid_dependency_wait();         // what came before in the stream
     if (threadIdx.x == 0) status = 0;
     __syncthreads();
     const int entities = a.G + a.B;          // groups, then sequences
@@ -965,6 +966,7 @@ __global__ void __launch_bounds__(256) combine_block_kernel(const Params p)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t row = blockIdx.x;
     const int query = static_cast<int>(row / p.a.H);
+    ptx::grid_dependents_launch();
     ptx::grid_dependency_wait();
     const int ok = p.w.head[H_OK];
     const int64_t share = p.w.start[0].share;
@@ -1029,6 +1031,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const Params p)
     const int64_t row = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 5;
     if (row >= p.a.Tq * p.a.H) return;
     const int query = static_cast<int>(row / p.a.H);
+    ptx::grid_dependents_launch();
     ptx::grid_dependency_wait();
     const int ok = p.w.head[H_OK];
     const int64_t share = p.w.start[0].share;
@@ -1153,8 +1156,7 @@ int run_prefix_mla(const PrefixMlaArgs &a, cudaStream_t s)
     KPOOL_CUDA_CHECK(cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPlanSmem));
     // a small batch takes a small block, whose barriers and scans are shorter (2 us of a 22 us call)
     const int plan_threads = std::max({static_cast<int64_t>(a.B), static_cast<int64_t>(a.G), a.Tq}) <= 256 ? 256 : kPlanThreads;
-    plan_kernel<<<1, plan_threads, kPlanSmem, s>>>(p);
-    KPOOL_CUDA_CHECK(cudaGetLastError());
+    KPOOL_CUDA_CHECK(launch_after(plan_kernel, 1, plan_threads, kPlanSmem, s, p));
     if (rows == 0) return KPOOL_OK;
     KPOOL_CUDA_CHECK(launch_after(attend_kernel, 2 * p.clusters, kThreads, kSmemBytes, s, mq, mkv, p));
     if (rows <= kBlockRows)
