@@ -103,10 +103,11 @@ struct Unit {
     int row0, nrows;         // flat (query, head) rows
     int table_row;           // page-table row its tokens are read through
     int t0, t1, tiles;       // tokens t0 .. t1 - 1, in tiles from t0's box on
+    int c0, pieces;          // cut into pieces, for the clusters c0, c0 + 1, ...
     int64_t w0;              // first position of the unit in the cut work
     int64_t out0;            // first partial row
 };
-static_assert(sizeof(Unit) == 40, "Unit");
+static_assert(sizeof(Unit) == 48, "Unit");
 
 struct Token {               // per query
     int vis;                 // tokens it sees
@@ -186,13 +187,6 @@ __device__ int64_t block_exclusive(int64_t v, int64_t *scratch, int64_t *total)
     __syncthreads();
     *total = scratch[31];
     return x - v + (warp > 0 ? scratch[warp - 1] : 0);
-}
-
-// Pieces of a unit: the clusters whose share of the work touches its tiles.
-__device__ __forceinline__ void pieces_of(const Unit &u, int64_t share, int64_t *c0, int *n)
-{
-    *c0 = (u.w0 + kOverhead) / share;
-    *n = u.tiles > 0 ? static_cast<int>((u.w0 + kOverhead + u.tiles - 1) / share - *c0) + 1 : 0;
 }
 
 // Reads its lists once, into shared memory where they fit (any realistic
@@ -325,14 +319,17 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p)
     for (int64_t base = 0; base < units; base += blockDim.x) {
         const int64_t k = base + threadIdx.x;
         Unit u{};
-        int64_t c0 = 0;
-        int n = 0;
         if (k < units) {
             u = unit[k];
-            pieces_of(u, share, &c0, &n);
+            if (u.tiles > 0) {
+                // the clusters whose share of the work touches its tiles
+                const int64_t c0 = (u.w0 + kOverhead) / share;
+                u.c0 = static_cast<int>(c0);
+                u.pieces = static_cast<int>((u.w0 + kOverhead + u.tiles - 1) / share - c0) + 1;
+            }
         }
         int64_t total;
-        u.out0 = rows + block_exclusive(static_cast<int64_t>(n) * u.nrows, scratch, &total);
+        u.out0 = rows + block_exclusive(static_cast<int64_t>(u.pieces) * u.nrows, scratch, &total);
         if (k < units) {
             w.unit[k] = u;
             if (u.tiles > 0)
@@ -438,7 +435,7 @@ struct Walk {
                     q->t1 = x.t1;
                     q->base = (x.t0 & -box) + static_cast<int>(lo - begin) * kTile;
                     q->tiles = static_cast<int>(hi - lo);
-                    q->out = x.out0 + (cluster - begin / share) * x.nrows;
+                    q->out = x.out0 + (cluster - x.c0) * x.nrows;
                     if (++u < units) x = unit[u];
                     return true;
                 }
@@ -524,7 +521,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // tokens: the values by one lane 194 us, this 189; the scores by lanes 189, but
         // 21.2 against 20.6 us on four short sequences.)
         const bool one = ptx::elect_one();
-        const int r128 = 128 * static_cast<int>(rank), r256 = 256 * static_cast<int>(rank);
+        const int r128 = 128 * static_cast<int>(rank);
         bool ok = true;
         uint32_t g = 0, np = 0;          // chunks and pieces so far
         Walk walk(p, cluster);
@@ -927,13 +924,12 @@ struct Pieces {
     int64_t shared0, own0;   // partial row of the first of each
     int shared_n, own_n, shared_rows, own_rows;
 
-    __device__ Pieces(const Params &p, int64_t row, const Token &x, int64_t share)
+    __device__ Pieces(const Params &p, int64_t row, const Token &x)
     {
         const int ks = static_cast<int>(row - x.prow0), ko = static_cast<int>(row - x.srow0);
         const Unit us = p.w.unit[x.pu + ks / kRows], uo = p.w.unit[x.su + ko / kRows];
-        int64_t c0;
-        pieces_of(us, share, &c0, &shared_n);
-        pieces_of(uo, share, &c0, &own_n);
+        shared_n = us.pieces;
+        own_n = uo.pieces;
         shared0 = us.out0 + ks % kRows;
         own0 = uo.out0 + ko % kRows;
         shared_rows = us.nrows;
@@ -969,10 +965,9 @@ __global__ void __launch_bounds__(256) combine_block_kernel(const Params p)
     ptx::grid_dependents_launch();
     ptx::grid_dependency_wait();
     const int ok = p.w.head[H_OK];
-    const int64_t share = p.w.start[0].share;
     const Token x = p.w.tok[query];
     if (!ok) return;
-    const Pieces pc(p, row, x, share);
+    const Pieces pc(p, row, x);
     const int n = pc.count();
     const float s = static_cast<int>(threadIdx.x) < n ? p.w.lse[pc.at(threadIdx.x)] : -INFINITY;
     float m = s;
@@ -1034,10 +1029,9 @@ __global__ void __launch_bounds__(256) combine_kernel(const Params p)
     ptx::grid_dependents_launch();
     ptx::grid_dependency_wait();
     const int ok = p.w.head[H_OK];
-    const int64_t share = p.w.start[0].share;
     const Token x = p.w.tok[query];
     if (!ok) return;
-    const Pieces pc(p, row, x, share);
+    const Pieces pc(p, row, x);
     const int n = pc.count();
     float m = -INFINITY;
     for (int i = lane; i < n; i += 32) m = fmaxf(m, p.w.lse[pc.at(i)]);
