@@ -513,7 +513,8 @@ KPOOL_API size_t kpool_pages_workspace_size(int64_t n, int n_seqs, int n_pages);
  * kpool_pages_copy -- page dst[i] becomes a copy of page src[i], in every store
  * and layer (contents only: no table or count changes).  A source may be
  * listed several times; a destination listed twice, or also as a source, is
- * refused (KPOOL_STATUS_BAD_PAGE, nothing copied).
+ * refused (KPOOL_STATUS_BAD_PAGE, nothing copied).  256 bytes of workspace are
+ * enough for up to 1024 pairs.
  */
 KPOOL_API int kpool_pages_copy(const int32_t *src, const int32_t *dst, int64_t n, int n_pages,
                                const kpool_page_store *stores, int n_stores, void *workspace,

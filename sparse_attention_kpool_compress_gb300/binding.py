@@ -620,10 +620,20 @@ def kpool_pages_copy(src, dst, stores, workspace=None):
     index, n, n_pages = _device_of(src, "src"), src.numel(), first.shape[-3]
     a, b = _ints(src, "src", n, index), _ints(dst, "dst", n, index)
     st, n_stores = _stores(stores, n_pages, index)
-    keep, ws, size = _bytes(workspace, 0 if workspace is not None else
-                            _lib.kpool_pages_workspace_size(n, 0, n_pages), index)
+    if workspace is None and n <= 1024:
+        keep, ws, size = _status_words(index)
+    else:
+        keep, ws, size = _bytes(workspace, 0 if workspace is not None else
+                                _lib.kpool_pages_workspace_size(n, 0, n_pages), index)
     _call(index, "kpool_pages_copy", _lib.kpool_pages_copy, a, b, n, n_pages, st, n_stores, ws,
           size)
+
+
+@functools.lru_cache(maxsize=None)
+def _status_words(index):
+    """Workspace of calls that write a status word only, which nobody reads."""
+    t = torch.zeros(256, dtype=torch.uint8, device=_devices(index))
+    return t, t.data_ptr(), 256
 
 
 def _pool_workspace(workspace, n, pages):

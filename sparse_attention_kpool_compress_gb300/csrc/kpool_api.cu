@@ -787,7 +787,12 @@ int kpool_pages_copy(const int32_t *src, const int32_t *dst, int64_t n, int n_pa
     int rc = check_items(n, {src, dst});
     if (rc) return rc;
     if ((rc = check_stores(stores, n_stores, n_pages, 0))) return rc;
-    if ((rc = check_pages_workspace(workspace, workspace_bytes, n, 0, n_pages))) return rc;
+    if (n <= kPagesFusedCopy) {
+        if (!workspace || workspace_bytes < 256 || !aligned(workspace, 256))
+            return fail(KPOOL_ERR_WORKSPACE, "workspace of at least 256 bytes, 256-byte aligned, needed");
+    } else if ((rc = check_pages_workspace(workspace, workspace_bytes, n, 0, n_pages))) {
+        return rc;
+    }
     if (n == 0) return nothing_listed(workspace, stream);
     return run_pages_copy(src, dst, static_cast<int>(n), n_pages, stores, n_stores, workspace,
                           reinterpret_cast<cudaStream_t>(stream));

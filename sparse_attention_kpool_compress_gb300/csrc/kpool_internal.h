@@ -148,7 +148,9 @@ struct SparseMlaArgs {
 size_t sparse_mla_workspace_bytes();
 int run_sparse_mla(const SparseMlaArgs &a, cudaStream_t s);
 
-// Paged cache (kpool_pages.cu); arguments are validated by the caller.
+// Paged cache (kpool_pages.cu); arguments are validated by the caller.  Copies of up
+// to kPagesFusedCopy pages need a status word of workspace only.
+constexpr int kPagesFusedCopy = 1024;
 size_t pages_workspace_bytes(int64_t n, int n_seqs, int n_pages);
 int run_pages_copy(const int32_t *src, const int32_t *dst, int n, int n_pages,
                    const kpool_page_store *stores, int n_stores, void *ws, cudaStream_t s);

@@ -290,6 +290,51 @@ def test_lists_that_are_refused(K):
     b.fork([1, 2], [3, 4])                        # whole pages need none
 
 
+@pytest.mark.parametrize("n", [1, 255, 257, 1023, 1024, 1025, 3000])
+def test_long_copies(K, n):
+    """Around the length up to which every block checks the list itself; a doubled destination, a page on both sides
+    and an id out of range at its far end."""
+    rng = np.random.RandomState(n)
+    b = Both(K, n_seqs=1, n_pages=2 * n + 5, max_pages=1, page_size=4, layers=2, seed=n)
+    b.ws = torch.empty(K.kpool_pages_workspace_size(n, 1, 2 * n + 5), dtype=torch.uint8, device="cuda")
+    at = rng.permutation(2 * n + 5)
+    dst = at[:n].tolist()
+    src = rng.choice(at[n:], n).tolist()
+    b.copy(src, dst)
+    if n > 1:
+        b.copy(src, dst[:-1] + [dst[0]], BAD)
+        b.copy(src[:-1] + [dst[0]], dst, BAD)
+        b.copy([dst[-1]] + src[1:], dst, BAD)
+    b.copy(src[:-1] + [2 * n + 5], dst, BAD)
+    b.copy(src, dst[:-1] + [-1], BAD)
+    b.copy(src[:-1] + [-2 ** 31], dst, BAD)
+
+
+def test_copies_without_a_workspace(K):
+    """On two streams at once, and captured: nothing but the status word is shared."""
+    b = Both(K, n_seqs=1, n_pages=40, max_pages=1, page_size=8)
+    lists = [([0, 1, 2], [10, 11, 12]), ([3, 4], [20, 21])]
+    torch.cuda.synchronize()
+    for src, dst in lists:
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            K.kpool_pages_copy(b.i32(src), b.i32(dst), b.stores)
+        b.host.copy(src, dst)
+    torch.cuda.synchronize()
+    for a, h in zip(b.stores, b.host.stores):
+        assert np.array_equal(a.cpu().numpy(), h)
+    src, dst = b.i32([5, 6]), b.i32([30, 31])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        K.kpool_pages_copy(src, dst, b.stores)
+    dst.copy_(b.i32([32, 33]))
+    g.replay()
+    torch.cuda.synchronize()
+    b.host.copy([5, 6], [32, 33])
+    for a, h in zip(b.stores, b.host.stores):
+        assert np.array_equal(a.cpu().numpy(), h)
+
+
 def test_writes_that_are_left_out(K):
     b = Both(K, n_seqs=4, n_pages=12, max_pages=4, page_size=8)
     b.grow([0], [12])
