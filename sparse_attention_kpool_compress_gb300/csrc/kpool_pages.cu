@@ -20,9 +20,9 @@
 //
 // Bound: contents by HBM (each byte read and written once, 16-byte accesses,
 // four in flight per thread: copying 300 pages of four layers moves its 167 MB in
-// 23 us, 7.1 TB/s with what the L2 holds); small calls by two launches and a
-// handful of dependent loads (copy 4 us, fork 6.5, extend 11 with the write, free
-// 6, compact 6, in a graph).
+// 23 us, 7.1 TB/s with what the L2 holds); small calls by their launches and a
+// handful of dependent loads (copy 2.4 us, fork 5.4, extend and write 10, free and
+// compact 11.6, in a graph).
 #include <algorithm>
 #include <climits>
 

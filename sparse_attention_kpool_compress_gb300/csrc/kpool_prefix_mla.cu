@@ -117,8 +117,8 @@ struct Token {               // per query
 
 // Where a cluster begins: all that it reads before its first loads, in one place.
 struct __align__(16) Start {
-    int u, units;            // its first unit; number of units
-    int64_t share;           // work of each cluster
+    int u, units;            // its first unit and the number of them, among those with tiles
+    int64_t from, to;        // its share of the work
     Unit first;
 };
 
@@ -127,7 +127,8 @@ struct Work {
     Token *tok;              // [Tq]
     int *lists;              // [3 B + 2 G]: the plan's, when they do not fit shared memory
     Start *start;            // [clusters]
-    Unit *unit;
+    Unit *unit;              // all, in the order of the rows
+    Unit *live;              // those with tiles
     float *lse;              // [partial rows], base 2
     float *o;                // [partial rows, 512]
 };
@@ -271,9 +272,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p)
         units += total;
     }
     __syncthreads();
-    // each unit's span, and its place in the work
+    // each unit's span, and its place in the work; how many have tiles (one scan for
+    // both: units are below 2^26)
+    constexpr int kLow = 26;
+    constexpr int64_t kLowMask = (int64_t(1) << kLow) - 1;
     Unit *unit = units <= kPlanUnits ? reinterpret_cast<Unit *>(plan_smem) : w.unit;
     int64_t work = 0;
+    int live = 0;
     for (int64_t base = 0; base < units; base += blockDim.x) {
         const int64_t k = base + threadIdx.x;
         Unit u{};
@@ -296,9 +301,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p)
             u.tiles = u.t1 > u.t0 ? (u.t1 - (u.t0 & -p.box) + kTile - 1) / kTile : 0;
         }
         int64_t total;
-        u.w0 = work + block_exclusive(u.tiles > 0 ? u.tiles + kOverhead : 0, scratch, &total);
+        u.w0 = work + (block_exclusive(u.tiles > 0 ? static_cast<int64_t>(u.tiles + kOverhead) << kLow | 1 : 0, scratch,
+                                       &total) >> kLow);
         if (k < units) unit[k] = u;
-        work += total;
+        work += total >> kLow;
+        live += static_cast<int>(total & kLowMask);
     }
     // queries
     for (int t = threadIdx.x; t < a.Tq; t += blockDim.x) {
@@ -314,8 +321,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p)
     // the even cut: where each cluster begins, and each unit's partial rows
     const int64_t share = max(static_cast<int64_t>(1), (work + p.clusters - 1) / p.clusters);
     for (int c = threadIdx.x; c < p.clusters; c += blockDim.x)
-        if (c * share >= work) w.start[c] = Start{static_cast<int>(units), static_cast<int>(units), share, Unit{}};
+        if (c * share >= work) w.start[c] = Start{};
     int64_t rows = 0;
+    int place = 0;
     for (int64_t base = 0; base < units; base += blockDim.x) {
         const int64_t k = base + threadIdx.x;
         Unit u{};
@@ -329,14 +337,21 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p)
             }
         }
         int64_t total;
-        u.out0 = rows + block_exclusive(static_cast<int64_t>(u.pieces) * u.nrows, scratch, &total);
+        // (partial rows, below 2^33, and units with tiles in one scan)
+        const int64_t before = block_exclusive(
+            u.tiles > 0 ? (static_cast<int64_t>(u.pieces) * u.nrows) << kLow | 1 : 0, scratch, &total);
+        u.out0 = rows + (before >> kLow);
         if (k < units) {
             w.unit[k] = u;
-            if (u.tiles > 0)
+            if (u.tiles > 0) {
+                const int j = place + static_cast<int>(before & kLowMask);
+                w.live[j] = u;
                 for (int64_t c = (u.w0 + share - 1) / share; c * share < u.w0 + u.tiles + kOverhead; ++c)
-                    w.start[c] = Start{static_cast<int>(k), static_cast<int>(units), share, u};
+                    w.start[c] = Start{j, live, c * share, (c + 1) * share, u};
+            }
         }
-        rows += total;
+        rows += total >> kLow;
+        place += static_cast<int>(total & kLowMask);
     }
     if (threadIdx.x == 0) {
         w.head[H_STATUS] = status;
@@ -407,40 +422,38 @@ struct Piece {
 };
 
 struct Walk {
-    const Unit *unit;
+    const Unit *live;
     Unit x;                  // unit u
-    int u, units, box;
-    int64_t cluster, share;
+    int u, units, box, cluster;
+    int64_t from, to;
 
-    __device__ Walk(const Params &p, int c) : unit(p.w.unit), box(p.box), cluster(c)
+    __device__ Walk(const Params &p, int c) : live(p.w.live), box(p.box), cluster(c)
     {
         const Start s = p.w.start[c];
         u = s.u;
         units = s.units;
-        share = s.share;
+        from = s.from;
+        to = s.to;
         x = s.first;
     }
     __device__ bool next(Piece *q)
     {
-        while (u < units) {
-            if (x.tiles > 0) {
-                if (x.w0 >= (cluster + 1) * share) return false;
-                const int64_t begin = x.w0 + kOverhead;
-                const int64_t lo = max(begin, cluster * share), hi = min(begin + x.tiles, (cluster + 1) * share);
-                if (lo < hi) {
-                    q->row0 = x.row0;
-                    q->nrows = x.nrows;
-                    q->table_row = x.table_row;
-                    q->t0 = x.t0;
-                    q->t1 = x.t1;
-                    q->base = (x.t0 & -box) + static_cast<int>(lo - begin) * kTile;
-                    q->tiles = static_cast<int>(hi - lo);
-                    q->out = x.out0 + (cluster - x.c0) * x.nrows;
-                    if (++u < units) x = unit[u];
-                    return true;
-                }
+        while (u < units && x.w0 < to) {
+            const int64_t begin = x.w0 + kOverhead;
+            const int64_t lo = max(begin, from), hi = min(begin + x.tiles, to);
+            const bool some = lo < hi;
+            if (some) {
+                q->row0 = x.row0;
+                q->nrows = x.nrows;
+                q->table_row = x.table_row;
+                q->t0 = x.t0;
+                q->t1 = x.t1;
+                q->base = (x.t0 & -box) + static_cast<int>(lo - begin) * kTile;
+                q->tiles = static_cast<int>(hi - lo);
+                q->out = x.out0 + static_cast<int64_t>(cluster - x.c0) * x.nrows;
             }
-            if (++u < units) x = unit[u];
+            if (++u < units) x = live[u];
+            if (some) return true;
         }
         return false;
     }
@@ -866,7 +879,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             l = (red[r] + red[kCtaRows + r]) + (red[2 * kCtaRows + r] + red[3 * kCtaRows + r]);
             ptx::named_bar_sync(3 + group, 128);
             ptx::tc_fence_after();
-            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const float inv = l != 0.f ? 1.f / l : 0.f;      // (0: no token; NaN goes on)
             // 32 columns at a time through this warp's own part of P (which no MMA
             // reads any more), so that a store covers whole lines of four rows: straight
             // from the registers, one row a lane, the stores take twice as long
@@ -893,7 +906,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
             }
             __syncwarp();
-            if (member == 0 && row < pc.nrows) p.w.lse[pc.out + row] = l > 0.f ? m + log2f(l) : -INFINITY;
+            if (member == 0 && row < pc.nrows) p.w.lse[pc.out + row] = l != 0.f ? m + log2f(l) : -INFINITY;
             ptx::tc_fence_before();
         }
     }
@@ -1014,9 +1027,9 @@ __global__ void __launch_bounds__(256) combine_block_kernel(const Params p)
         y.x += z.x;
         y.y += z.y;
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l != 0.f ? 1.f / l : 0.f;      // (0: no token; NaN goes on)
     reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.a.o) + row * kDc)[threadIdx.x] = pack_bf16(y.x * inv, y.y * inv);
-    if (threadIdx.x == 0) p.a.lse[row] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+    if (threadIdx.x == 0) p.a.lse[row] = l != 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
 // A warp per row, for more rows than the GPU holds blocks of the other form.
@@ -1060,12 +1073,12 @@ __global__ void __launch_bounds__(256) combine_kernel(const Params p)
             }
         }
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l != 0.f ? 1.f / l : 0.f;      // (0: no token; NaN goes on)
     uint2 *out = reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.a.o) + row * kDc) + lane;
 #pragma unroll
     for (int v = 0; v < 4; ++v)
         out[32 * v] = make_uint2(pack_bf16(acc[v].x * inv, acc[v].y * inv), pack_bf16(acc[v].z * inv, acc[v].w * inv));
-    if (lane == 0) p.a.lse[row] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+    if (lane == 0) p.a.lse[row] = l != 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
 // ---- host --------------------------------------------------------------------
@@ -1091,6 +1104,7 @@ size_t lay_out(Work *w, uint8_t *base, int64_t Tq, int H, int B, int G, int clus
     w->lists = reinterpret_cast<int *>(take(4 * (3 * static_cast<int64_t>(B) + 2 * static_cast<int64_t>(G))));
     w->start = reinterpret_cast<Start *>(take(clusters * static_cast<int64_t>(sizeof(Start))));
     w->unit = reinterpret_cast<Unit *>(take(units * static_cast<int64_t>(sizeof(Unit))));
+    w->live = reinterpret_cast<Unit *>(take(units * static_cast<int64_t>(sizeof(Unit))));
     w->lse = reinterpret_cast<float *>(take(4 * partial));
     w->o = reinterpret_cast<float *>(take(4 * kDc * partial));
     return static_cast<size_t>(at);

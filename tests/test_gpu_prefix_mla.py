@@ -182,6 +182,34 @@ def test_what_lies_behind_the_end_is_not_read_into_results(K, junk):
     c.check(o, lse)
 
 
+def test_nan_and_infinite_queries_stay_in_their_rows(K):
+    """A query head that is not finite gives NaN in its own row, and in no other of its tile."""
+    c = Case([(300, [(301, 1), (420, 2)]), (0, [(33, 1)])], H=16, page=32, seed=23)
+    sick = {(0, 3): float("nan"), (2, 0): float("inf"), (3, 15): float("nan")}
+    q = c.q.clone()
+    for (t, h), value in sick.items():
+        c.q[t, h, 7] = value
+    o, lse = run(K, c)
+    for t, h in sick:
+        assert torch.isnan(o[t, h]).all() and not torch.isfinite(lse[t, h])
+        o[t, h], lse[t, h] = 0, 0
+    c.q = q
+    want_o, want_l = run(K, c)
+    for t, h in sick:
+        want_o[t, h], want_l[t, h] = 0, 0
+    assert torch.equal(o, want_o) and torch.equal(lse, want_l)
+
+
+def test_units_without_tokens_in_between(K):
+    """Groups with and without shared tokens, sequences with and without their own, in turn."""
+    groups = []
+    for k in range(150):
+        p = 40 if k % 3 == 0 else 0
+        groups.append((p, [(p + (k % 5 == 0) * 20, 1), (p + (k % 7 == 1) * 300, k % 2)]))
+    c = Case(groups, H=8, page=16, seed=29)
+    c.check(*run(K, c))
+
+
 def test_sharp_and_flat_scores(K):
     """Scores hundreds apart (one weight takes all), equal scores, and scores that rise along the tokens."""
     for sharp, seed in ((60.0, 1), (0.0, 2)):
