@@ -35,6 +35,11 @@ namespace {
 constexpr int kPlanThreads = 1024;
 constexpr int kApplyThreads = 256;
 constexpr int kChunk = 16 * 4 * kApplyThreads;   // bytes one block copies at a time
+// Page-table entries that one block handles at a time.  A table is as wide as the
+// longest sequence may become, and most rows end early: with 256 at a time, 4096 rows
+// of 32768 entries that hold 8 pages each took compact 280 us and free 438; with 1024,
+// 131 and 231.  8 rows that are full take the same either way (109 and 175).
+constexpr int kSpan = 1024;
 constexpr int kPlanPages = 8;                    // pages per thread and round of the compaction scan
 constexpr uint32_t kFull = 0xFFFFFFFFu;
 
@@ -294,23 +299,20 @@ __global__ void __launch_bounds__(kApplyThreads) fork_apply(const __grid_constan
     ptx::grid_dependents_launch();
     ptx::grid_dependency_wait();
     const int n = ws[W_COUNT];
-    const int cols = ceil_div(p.max_pages, kApplyThreads);
+    const int spans = ceil_div(p.max_pages, kSpan);
     // the children's page-table rows, and one more reference on each whole page
-    const int64_t tasks = static_cast<int64_t>(n) * cols;
-    for (int64_t t = blockIdx.x; t < tasks; t += gridDim.x) {
-        const int i = static_cast<int>(t / cols);
-        const int j = static_cast<int>(t - static_cast<int64_t>(i) * cols) * kApplyThreads + threadIdx.x;
+    for (int64_t t = blockIdx.x; t < static_cast<int64_t>(n) * spans; t += gridDim.x) {
+        const int i = static_cast<int>(t / spans), first = static_cast<int>(t - static_cast<int64_t>(i) * spans) * kSpan;
         const int whole = l.c[i] / p.page_size;
-        if (j > whole || j >= p.max_pages) continue;
         int32_t *row = p.page_table + static_cast<int64_t>(children[i]) * p.max_pages;
-        if (j == whole) {
-            if (l.b[i] >= 0) row[j] = l.b[i];
-            continue;
+        const int32_t *from = p.page_table + static_cast<int64_t>(parents[i]) * p.max_pages;
+        if (first <= whole && whole < first + kSpan && threadIdx.x == 0 && l.b[i] >= 0) row[whole] = l.b[i];
+        for (int j = first + threadIdx.x; j < min(whole, first + kSpan); j += kApplyThreads) {
+            const int page = from[j];
+            row[j] = page;
+            if (in_range(page, p.n_pages)) atomicAdd(p.ref_count + page, 1);
+            else atomicOr(ws + W_STATUS, KPOOL_STATUS_BAD_PAGE);
         }
-        const int page = p.page_table[static_cast<int64_t>(parents[i]) * p.max_pages + j];
-        row[j] = page;
-        if (in_range(page, p.n_pages)) atomicAdd(p.ref_count + page, 1);
-        else atomicOr(ws + W_STATUS, KPOOL_STATUS_BAD_PAGE);
     }
     // the used rows of each partial page
     copy_pages(st, l.a, l.b, l.c, n, p.page_size, p.n_pages);
@@ -494,21 +496,22 @@ __global__ void __launch_bounds__(kApplyThreads) free_apply(const kpool_page_poo
     ptx::grid_dependents_launch();
     ptx::grid_dependency_wait();
     const int n = ws[W_COUNT];
-    const int cols = ceil_div(p.max_pages, kApplyThreads);
-    for (int64_t t = blockIdx.x; t < static_cast<int64_t>(n) * cols; t += gridDim.x) {
-        const int i = static_cast<int>(t / cols);
-        const int j = static_cast<int>(t - static_cast<int64_t>(i) * cols) * kApplyThreads + threadIdx.x;
-        if (static_cast<int64_t>(j) * p.page_size >= l.c[i]) continue;
-        int32_t *at = p.page_table + static_cast<int64_t>(seqs[i]) * p.max_pages + j;
-        const int page = *at;
-        *at = -1;
-        int had = 0;
-        if (in_range(page, p.n_pages)) {
-            had = atomicSub(p.ref_count + page, 1);
-            if (had == 1) atomicOr(bits + (page >> 5), 1 << (page & 31));
-            if (had <= 0) atomicAdd(p.ref_count + page, 1);      // it had no reference to give back
+    const int spans = ceil_div(p.max_pages, kSpan);
+    for (int64_t t = blockIdx.x; t < static_cast<int64_t>(n) * spans; t += gridDim.x) {
+        const int i = static_cast<int>(t / spans), first = static_cast<int>(t - static_cast<int64_t>(i) * spans) * kSpan;
+        const int held = ceil_div(l.c[i], p.page_size);
+        int32_t *row = p.page_table + static_cast<int64_t>(seqs[i]) * p.max_pages;
+        for (int j = first + threadIdx.x; j < min(held, first + kSpan); j += kApplyThreads) {
+            const int page = row[j];
+            row[j] = -1;
+            int had = 0;
+            if (in_range(page, p.n_pages)) {
+                had = atomicSub(p.ref_count + page, 1);
+                if (had == 1) atomicOr(bits + (page >> 5), 1 << (page & 31));
+                if (had <= 0) atomicAdd(p.ref_count + page, 1);  // it had no reference to give back
+            }
+            if (had <= 0) atomicOr(ws + W_STATUS, KPOOL_STATUS_BAD_PAGE);
         }
-        if (had <= 0) atomicOr(ws + W_STATUS, KPOOL_STATUS_BAD_PAGE);
     }
     // the block that comes last pushes the freed pages, in ascending order
     __threadfence();
@@ -595,16 +598,18 @@ __global__ void __launch_bounds__(kApplyThreads) compact_apply(const __grid_cons
     ptx::grid_dependents_launch();
     ptx::grid_dependency_wait();
     const int k = ws[W_LIVE];
-    const int cols = ceil_div(p.max_pages, kApplyThreads);
-    for (int64_t t = blockIdx.x; t < static_cast<int64_t>(p.n_seqs) * cols; t += gridDim.x) {
-        const int s = static_cast<int>(t / cols);
-        const int j = static_cast<int>(t - static_cast<int64_t>(s) * cols) * kApplyThreads + threadIdx.x;
-        if (j >= p.max_pages || static_cast<int64_t>(j) * p.page_size >= p.seq_lens[s]) continue;
-        int32_t *at = p.page_table + static_cast<int64_t>(s) * p.max_pages + j;
-        const int page = *at;
-        const int now = !in_range(page, p.n_pages) ? -1 : page < k ? page : l.mark[page];
-        if (now < 0) atomicOr(ws + W_STATUS, KPOOL_STATUS_BAD_PAGE);
-        else if (now != page) *at = now;
+    const int spans = ceil_div(p.max_pages, kSpan);
+    for (int64_t t = blockIdx.x; t < static_cast<int64_t>(p.n_seqs) * spans; t += gridDim.x) {
+        const int s = static_cast<int>(t / spans), first = static_cast<int>(t - static_cast<int64_t>(s) * spans) * kSpan;
+        const int64_t len = p.seq_lens[s];
+        const int held = static_cast<int>(min((len + p.page_size - 1) / p.page_size, static_cast<int64_t>(p.max_pages)));
+        int32_t *row = p.page_table + static_cast<int64_t>(s) * p.max_pages;
+        for (int j = first + threadIdx.x; j < min(held, first + kSpan); j += kApplyThreads) {
+            const int page = row[j];
+            const int now = !in_range(page, p.n_pages) ? -1 : page < k ? page : l.mark[page];
+            if (now < 0) atomicOr(ws + W_STATUS, KPOOL_STATUS_BAD_PAGE);
+            else if (now != page) row[j] = now;
+        }
     }
     copy_pages(st, l.a, l.b, nullptr, ws[W_COUNT], 1, p.n_pages);
 }
@@ -687,8 +692,8 @@ int run_pages_fork(const kpool_page_pool &p, const int32_t *parents, const int32
     const Lists l = lists(ws, n);
     int *w = static_cast<int *>(ws);
     KPOOL_CUDA_CHECK(launch_after(fork_plan, 1, plan_threads(n), s, p, parents, children, n, w, l));
-    const int64_t cols = (p.max_pages + kApplyThreads - 1) / kApplyThreads;
-    KPOOL_CUDA_CHECK(launch_after(fork_apply, grid_for(n * std::max<int64_t>(cols, st.per_item)), kApplyThreads, s, st, p,
+    const int64_t spans = (p.max_pages + kSpan - 1) / kSpan;
+    KPOOL_CUDA_CHECK(launch_after(fork_apply, grid_for(n * std::max<int64_t>(spans, st.per_item)), kApplyThreads, s, st, p,
                                        parents, children, w, l));
     return KPOOL_OK;
 }
@@ -720,8 +725,8 @@ int run_pages_free(const kpool_page_pool &p, const int32_t *seqs, int n, void *w
     const Lists l = lists(ws, n);
     int *w = static_cast<int *>(ws), *bits = l.mark + std::max(p.n_seqs, p.n_pages);
     KPOOL_CUDA_CHECK(launch_after(free_plan, 1, plan_threads(n), s, p, seqs, n, w, l, bits));
-    const int64_t cols = (p.max_pages + kApplyThreads - 1) / kApplyThreads;
-    KPOOL_CUDA_CHECK(launch_after(free_apply, grid_for(n * cols), kApplyThreads, s, p, seqs, w, l, bits));
+    const int64_t spans = (p.max_pages + kSpan - 1) / kSpan;
+    KPOOL_CUDA_CHECK(launch_after(free_apply, grid_for(n * spans), kApplyThreads, s, p, seqs, w, l, bits));
     return KPOOL_OK;
 }
 
@@ -732,9 +737,9 @@ int run_pages_compact(const kpool_page_pool &p, const kpool_page_store *stores, 
     const Lists l = lists(ws, p.n_pages);
     int *w = static_cast<int *>(ws);
     KPOOL_CUDA_CHECK(launch_after(compact_plan, 1, kPlanThreads, s, p, w, l));
-    const int64_t cols = (p.max_pages + kApplyThreads - 1) / kApplyThreads;
+    const int64_t spans = (p.max_pages + kSpan - 1) / kSpan;
     KPOOL_CUDA_CHECK(launch_after(
-        compact_apply, grid_for(std::max<int64_t>(p.n_seqs * cols, static_cast<int64_t>(p.n_pages) / 2 * st.per_item)),
+        compact_apply, grid_for(std::max<int64_t>(p.n_seqs * spans, static_cast<int64_t>(p.n_pages) / 2 * st.per_item)),
         kApplyThreads, s, st, p, w, l));
     return KPOOL_OK;
 }
