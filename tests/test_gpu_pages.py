@@ -350,6 +350,17 @@ def test_writes_that_are_left_out(K):
     b.write([1], [2 ** 31 - 1], [0, 1], want=BAD)
 
 
+@pytest.mark.parametrize("rows", [1, 63, 255, 256, 257, 1030])
+def test_a_status_is_of_its_own_call(K, rows):
+    """Rows of one cluster and of more, with one row too many and without."""
+    b = Both(K, n_seqs=2, n_pages=140, max_pages=130, page_size=8)
+    b.grow([1], [rows])
+    b.write([1], [0], [0, rows + 1], want=BAD)
+    b.write([1], [0], [0, rows])
+    b.write([0, 1], [0, 0], [0, 1, rows], want=BAD)
+    b.write([0, 1], [0, 0], [0, 0, rows])
+
+
 def test_nothing_listed(K):
     b = Both(K, n_seqs=3, n_pages=4, max_pages=2, page_size=8)
     b.extend([], [])
