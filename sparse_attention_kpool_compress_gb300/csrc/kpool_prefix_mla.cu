@@ -133,6 +133,7 @@ struct Work {
     float *o;                // [partial rows, 512]
 };
 
+constexpr int kFewStarts = 16;            // start entries that one thread writes
 constexpr int kPlanSmem = kPlanUnits * static_cast<int>(sizeof(Unit)) + (5 * kPlanThreads + 2 * (kPlanThreads + 1)) * 4;
 
 struct Params {
@@ -341,14 +342,30 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p)
         const int64_t before = block_exclusive(
             u.tiles > 0 ? (static_cast<int64_t>(u.pieces) * u.nrows) << kLow | 1 : 0, scratch, &total);
         u.out0 = rows + (before >> kLow);
+        const int j = place + static_cast<int>(before & kLowMask);
+        int c0 = 0, c1 = 0;                  // the clusters that begin in it
         if (k < units) {
             w.unit[k] = u;
             if (u.tiles > 0) {
-                const int j = place + static_cast<int>(before & kLowMask);
                 w.live[j] = u;
-                for (int64_t c = (u.w0 + share - 1) / share; c * share < u.w0 + u.tiles + kOverhead; ++c)
-                    w.start[c] = Start{j, live, c * share, (c + 1) * share, u};
+                c0 = static_cast<int>((u.w0 + share - 1) / share);
+                c1 = static_cast<int>((u.w0 + u.tiles + kOverhead + share - 1) / share);
             }
+        }
+        // a thread writes a few; the many of a long unit its whole warp (one sequence of
+        // 131072 tokens: 53 -> LONG us)
+        const bool many = c1 - c0 > kFewStarts;
+        for (int c = c0; c < c1 && !many; ++c) w.start[c] = Start{j, live, c * share, (c + 1) * share, u};
+        for (unsigned m = __ballot_sync(kFull, many); m != 0; m &= m - 1) {
+            const int from = __ffs(m) - 1;
+            Unit v;
+            const int *src = reinterpret_cast<const int *>(&u);
+            int *dst = reinterpret_cast<int *>(&v);
+#pragma unroll
+            for (int i = 0; i < static_cast<int>(sizeof(Unit) / 4); ++i) dst[i] = __shfl_sync(kFull, src[i], from);
+            const int vj = __shfl_sync(kFull, j, from), end = __shfl_sync(kFull, c1, from);
+            for (int c = __shfl_sync(kFull, c0, from) + static_cast<int>(threadIdx.x & 31); c < end; c += 32)
+                w.start[c] = Start{vj, live, c * share, (c + 1) * share, v};
         }
         rows += total >> kLow;
         place += static_cast<int>(total & kLowMask);
