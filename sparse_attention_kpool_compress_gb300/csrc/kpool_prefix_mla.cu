@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p)
             }
         }
         // a thread writes a few; the many of a long unit its whole warp (one sequence of
-        // 131072 tokens: 53 -> LONG us)
+        // 131072 tokens: 53 -> 48.4 us)
         const bool many = c1 - c0 > kFewStarts;
         for (int c = c0; c < c1 && !many; ++c) w.start[c] = Start{j, live, c * share, (c + 1) * share, u};
         for (unsigned m = __ballot_sync(kFull, many); m != 0; m &= m - 1) {
