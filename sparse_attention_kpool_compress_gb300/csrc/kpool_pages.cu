@@ -8,21 +8,24 @@
 // (free_list, free_count): allocation pops from its end, in the order of the
 // call's list, so equal inputs give equal tables.
 //
-// Every call that changes the pool is two kernels:
+// fork, free, compact, and a copy of more than 1024 pages, are two kernels:
 //   plan    one block: validates the whole list, takes pages from or accounts
 //           for the pool, and writes what the second kernel has to do into the
 //           workspace.  A list with a bad entry, or one the free pages do not
 //           cover, changes nothing (its count of items becomes 0).
 //   apply   all SMs: page-table rows, reference counts and page contents.
+// extend is a plan alone; a smaller copy and a write check what they read in the
+// blocks that move it.
 // All are launched with programmatic stream serialisation: a kernel's blocks
 // start while the one in front of it runs and wait for its end, which hides the
-// launch.  No block waits for another one inside a kernel.
+// launch.  No block waits for another one inside a kernel, but for the cluster
+// barrier of a small write.
 //
 // Bound: contents by HBM (each byte read and written once, 16-byte accesses,
 // four in flight per thread: copying 300 pages of four layers moves its 167 MB in
 // 23 us, 7.1 TB/s with what the L2 holds); small calls by their launches and a
-// handful of dependent loads (copy 2.4 us, fork 5.4, extend and write 10, free and
-// compact 11.6, in a graph).
+// handful of dependent loads (copy 2.4 us, fork 4.8, extend and write 6.6, free and
+// compact 11.2, in a graph).
 #include <algorithm>
 #include <climits>
 
