@@ -67,7 +67,11 @@ constexpr int kOverhead = 3;             // a piece's start and end, in tiles (f
 constexpr int kThreads = 384;
 constexpr int kSmWarps = 8;
 constexpr int kPlanThreads = 1024;
-constexpr int kPlanUnits = 1024;         // units that the plan keeps in shared memory, with lists of a thread per entry
+// What the plan keeps in shared memory: its lists up to about 6000 sequences, and the
+// units that fit beside them.  (With room for 1024 of each, 1000 sequences in 50 groups
+// planned in 22.7 us and 2000 in 43.6, now 19.7 and 34.4: what is left is the one block's
+// instructions, not its loads, divisions or searches alone.)
+constexpr int kPlanListBytes = 96 * 1024, kPlanSmem = 200 * 1024;
 constexpr int kMaxClusters = 80;         // CTA pairs that a workspace has room for
 constexpr int64_t kBlockRows = 512;      // rows up to which combine takes a block for each
 constexpr float kRescale = 8.f;          // headroom of the reference maximum (log2)
@@ -134,7 +138,6 @@ struct Work {
 };
 
 constexpr int kFewStarts = 16;            // start entries that one thread writes
-constexpr int kPlanSmem = kPlanUnits * static_cast<int>(sizeof(Unit)) + (5 * kPlanThreads + 2 * (kPlanThreads + 1)) * 4;
 
 struct Params {
     PrefixMlaArgs a;
@@ -146,6 +149,8 @@ struct Params {
     int wait_tries;          // see Sync
     uint32_t wait_nap_ns;
     uint64_t wait_limit_ns;
+    int plan_units;          // units that fit the plan's shared memory
+    bool plan_lists;         // do its lists?
 };
 
 __device__ __forceinline__ bool in_range(int i, int n) { return i >= 0 && i < n; }
@@ -205,19 +210,14 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p)
     if (threadIdx.x == 0) status = 0;
     __syncthreads();
     const int entities = a.G + a.B;          // groups, then sequences
-    const bool small = a.B <= static_cast<int>(blockDim.x) && a.G <= static_cast<int>(blockDim.x);
-    int *lists = small ? reinterpret_cast<int *>(plan_smem + kPlanUnits * sizeof(Unit)) : w.lists;
+    const bool small = p.plan_lists;
+    int *lists = small ? reinterpret_cast<int *>(plan_smem + p.plan_units * sizeof(Unit)) : w.lists;
     int *len = lists, *shared = len + a.B, *row = shared + a.G, *unit0 = row + a.B;
     const int32_t *cu_q = a.cu_q, *cu_g = a.cu_groups;
-    // (at most one entry of each list per thread then: all loads are in flight at once)
-    int my_q = 0, my_g = 0;
-    if (small) {
-        const int i = threadIdx.x;
-        if (i < a.B) my_q = a.cu_q[i];
-        if (i < a.G) my_g = a.cu_groups[i], shared[i] = a.prefix_lens[i];
-    } else {
-        for (int i = threadIdx.x; i < a.G; i += blockDim.x) shared[i] = a.prefix_lens[i];
-    }
+    // (the first entry of each list is held back, so that all loads are in flight at once)
+    int my_q = 0, my_g = 0, my_p = 0;
+    if (threadIdx.x < a.B) my_q = a.cu_q[threadIdx.x];
+    if (threadIdx.x < a.G) my_g = a.cu_groups[threadIdx.x], my_p = a.prefix_lens[threadIdx.x];
     const int last_q = a.cu_q[a.B], last_g = a.cu_groups[a.G];
     const int64_t room = static_cast<int64_t>(a.max_pages) * a.page_size;
     // a sequence's length, cut to what its table row holds
@@ -233,11 +233,15 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p)
         row[b] = r;
         len[b] = static_cast<int>(n);
     }
+    if (threadIdx.x < a.G) shared[threadIdx.x] = my_p;
+    for (int i = threadIdx.x + blockDim.x; i < a.G; i += blockDim.x) shared[i] = a.prefix_lens[i];
     if (small) {
         int *q = unit0 + entities, *g = q + a.B + 1;
         const int i = threadIdx.x;
         if (i < a.B) q[i] = my_q;
         if (i < a.G) g[i] = my_g;
+        for (int j = i + blockDim.x; j < a.B; j += blockDim.x) q[j] = a.cu_q[j];
+        for (int j = i + blockDim.x; j < a.G; j += blockDim.x) g[j] = a.cu_groups[j];
         if (i == 0) q[a.B] = last_q, g[a.G] = last_g;
         cu_q = q;
         cu_g = g;
@@ -277,7 +281,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p)
     // both: units are below 2^26)
     constexpr int kLow = 26;
     constexpr int64_t kLowMask = (int64_t(1) << kLow) - 1;
-    Unit *unit = units <= kPlanUnits ? reinterpret_cast<Unit *>(plan_smem) : w.unit;
+    Unit *unit = units <= p.plan_units ? reinterpret_cast<Unit *>(plan_smem) : w.unit;
     int64_t work = 0;
     int live = 0;
     for (int64_t base = 0; base < units; base += blockDim.x) {
@@ -1102,11 +1106,15 @@ __global__ void __launch_bounds__(256) combine_kernel(const Params p)
 
 int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
+int64_t most_units(int64_t Tq, int H, int B, int G)
+{
+    return 2 * (Tq * H / kRows) + std::min<int64_t>(G, Tq) + std::min<int64_t>(B, Tq);
+}
+
 // Lays the workspace out from `base` (NULL to size it); the bytes it takes.
 size_t lay_out(Work *w, uint8_t *base, int64_t Tq, int H, int B, int G, int clusters)
 {
-    const int64_t rows = Tq * H;
-    const int64_t units = 2 * (rows / kRows) + std::min<int64_t>(G, Tq) + std::min<int64_t>(B, Tq);
+    const int64_t rows = Tq * H, units = most_units(Tq, H, B, G);
     // every row in one piece of its shared and one of its own tokens, and at
     // most one more piece per cluster
     const int64_t partial = 2 * rows + static_cast<int64_t>(clusters) * kRows;
@@ -1181,7 +1189,13 @@ int run_prefix_mla(const PrefixMlaArgs &a, cudaStream_t s)
     KPOOL_CUDA_CHECK(cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPlanSmem));
     // a small batch takes a small block, whose barriers and scans are shorter (2 us of a 22 us call)
     const int plan_threads = std::max({static_cast<int64_t>(a.B), static_cast<int64_t>(a.G), a.Tq}) <= 256 ? 256 : kPlanThreads;
-    KPOOL_CUDA_CHECK(launch_after(plan_kernel, 1, plan_threads, kPlanSmem, s, p));
+    int64_t list_bytes = 4 * (4 * static_cast<int64_t>(a.B) + 3 * static_cast<int64_t>(a.G) + 2);
+    p.plan_lists = list_bytes <= kPlanListBytes;
+    if (!p.plan_lists) list_bytes = 0;
+    constexpr int64_t kUnitBytes = sizeof(Unit);
+    p.plan_units = static_cast<int>(std::min(most_units(a.Tq, a.H, a.B, a.G), (kPlanSmem - list_bytes) / kUnitBytes));
+    const int plan_smem = static_cast<int>(p.plan_units * kUnitBytes + list_bytes);
+    KPOOL_CUDA_CHECK(launch_after(plan_kernel, 1, plan_threads, plan_smem, s, p));
     if (rows == 0) return KPOOL_OK;
     KPOOL_CUDA_CHECK(launch_after(attend_kernel, 2 * p.clusters, kThreads, kSmemBytes, s, mq, mkv, p));
     if (rows <= kBlockRows)

@@ -284,6 +284,21 @@ def test_many_sequences(K):
     c.check(*run(K, c))
 
 
+@pytest.mark.parametrize("B, groups, queries, H", [(1024, 7, 1, 1), (1025, 1025, 1, 1), (4600, 30, 1, 1),
+                                                   (6143, 1, 1, 1), (6144, 5, 1, 2), (40, 4, 16, 128),
+                                                   (1, 1, 600, 128), (1500, 2, 1, 128)])
+def test_lists_that_the_plan_holds_on_chip_and_not(K, B, groups, queries, H):
+    """Lists and units on either side of what fits the plan's shared memory."""
+    rng = np.random.RandomState(B + H)
+    size = -(-B // groups)
+    lists = [(9, [(9 + queries + int(rng.randint(0, 20)), queries) for _ in range(min(size, B - g * size))])
+             for g in range(groups) if g * size < B]
+    c = Case(lists, H=H, page=16, seed=B)
+    o, lse = run(K, c)
+    rows = set(rng.choice(len(c.q), min(len(c.q), 300), replace=False).tolist()) | {0, len(c.q) - 1}
+    c.check(o, lse, rows=rows)
+
+
 def test_bad_offsets(K):
     c = Case([(10, [(20, 1), (21, 1)])], H=8, page=16)
     q, kv, table, lens, cu_q, cu_g, pre, scale = c.args()
