@@ -38,13 +38,16 @@
 //   warp 1       issuer of the scores' MMAs (CTA 0)
 //   warp 2       issuer of the output's MMAs (CTA 0).  Two issuers, because one
 //                that waits and commits for every four MMAs reaches 98 cycles
-//                an MMA, two together the pipe's 64 (measured).  In both CTAs
-//                it also clears the rows of a chunk of values that lie outside
-//                the span, so that nothing there, NaN included, meets a weight
-//                of 0
+//                an MMA, two together the pipe's 64 (measured)
 //   warp 3       TMA producer of values chunks
 //   warps 4-11   softmax and output: thread (lane, half of the columns) has 64
 //                of a row's 256 scores
+//   warp 12      clears the rows of a chunk of values that lie outside the span,
+//                so that nothing there, NaN included, meets a weight of 0.  (Ahead
+//                of the issuer, while the softmax works: in the issuer's own loop
+//                the first and last chunks of a short span took 2 us: 16 samples
+//                over 8191 shared tokens 34.0 -> 32.7 us a call, 64 queries each
+//                over 8192 of their own 195 -> 183.)
 // All loads and arrivals meet on CTA 0's barriers, where the issuers wait.  P
 // passes in four parts of 64 tokens, so that the output of a tile's first part
 // begins while the last one is exponentiated, and the next tile's P is written
@@ -64,8 +67,9 @@ constexpr int kRows = 128;               // rows of a unit
 constexpr int kCtaRows = 64;             // of them in each CTA
 constexpr int kTile = 256;               // tokens of a tile
 constexpr int kOverhead = 3;             // a piece's start and end, in tiles (for the even cut; 2 and 4 measured slower)
-constexpr int kThreads = 384;
+constexpr int kThreads = 416;
 constexpr int kSmWarps = 8;
+constexpr int kClearWarp = 4 + kSmWarps;
 constexpr int kPlanThreads = 1024;
 // What the plan keeps in shared memory: its lists up to about 6000 sequences, and the
 // units that fit beside them.  (With room for 1024 of each, 1000 sequences in 50 groups
@@ -688,44 +692,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
         }
     } else if (warp == 2) {
-        // ---------------- issuer of the output; clearing ----------------
-        constexpr uint32_t idesc = ptx::make_idesc(1u, kRows, kTile) | ptx::kIdescBMajorMN;
-        bool ok = true, any = false;
-        uint32_t g = 0, gp = 0, par = 0;             // chunks and tiles so far; parity of each slot's edge barrier
-        const bool one = ptx::elect_one();
-        Walk walk(p, cluster);
-        Piece pc;
-        while (ok && walk.next(&pc)) {
-            pc.uniform();
-            for (int i = 0; i < pc.tiles && ok; ++i, ++gp) {
-                const int base = pc.base + i * kTile;
-                const int n = tile_tokens(pc, base), lo = pc.t0 - base;
-                for (int kb = 0; 64 * kb < n && ok; ++kb) {
-                    const bool edge = has_edge(pc, base, kb);
-                    if (rank == 0) {
+        // ---------------- issuer of the output ----------------
+        if (rank == 0) {
+            constexpr uint32_t idesc = ptx::make_idesc(1u, kRows, kTile) | ptx::kIdescBMajorMN;
+            bool ok = true, any = false;
+            uint32_t g = 0, gp = 0;                      // chunks and tiles so far
+            const bool one = ptx::elect_one();
+            Walk walk(p, cluster);
+            Piece pc;
+            while (ok && walk.next(&pc)) {
+                pc.uniform();
+                for (int i = 0; i < pc.tiles && ok; ++i, ++gp) {
+                    const int n = tile_tokens(pc, pc.base + i * kTile);
+                    for (int kb = 0; 64 * kb < n && ok; ++kb) {
                         ok = wait_bar_warp(bar(B_PFULL + kb), gp & 1u, sy);
                         if (!ok) break;
                         ptx::tc_fence_after();
-                    }
-                    const int steps = min(4, (n - 64 * kb + 15) / 16);
-                    for (int j = 0; j < 2; ++j, ++g) {
-                        const uint32_t s = g % kRing;
-                        if (edge) {
-                            ok = wait_bar_warp(bar(B_VEDGE + s), par >> s & 1u, sy);
-                            if (!ok) break;
-                            par ^= 1u << s;
-                            // rows outside the span, up to the last 16 that the MMAs read
-                            const int cut0 = lo - 64 * kb, cut1 = n - 64 * kb;
-                            for (int r = lane >> 4; r < 16 * steps; r += 2)
-                                if (r < cut0 || r >= cut1)
-                                    ptx::st_shared_v4(sV + s * kChunk + (lane >> 3 & 1) * 8192 + r * 128 + (lane & 7) * 16,
-                                                      0u, 0u, 0u, 0u);
-                            ptx::fence_proxy_async_smem();
-                            __syncwarp();
-                            if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(bar(B_VFULL + s), 0));
-                            __syncwarp();
-                        }
-                        if (rank == 0) {
+                        const int steps = min(4, (n - 64 * kb + 15) / 16);
+                        for (int j = 0; j < 2; ++j, ++g) {
+                            const uint32_t s = g % kRing;
                             ok = wait_bar_warp(bar(B_VFULL + s), (g / kRing) & 1u, sy);
                             if (!ok) break;
                             const uint64_t ad = ptx::smem_desc_sw128(sP + kb * 8192);
@@ -747,17 +732,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             any = true;
                         }
                     }
-                }
-                // parts without a token pass as well
-                for (int kb = (n + 63) / 64; rank == 0 && kb < 4 && ok; ++kb) {
-                    ok = wait_bar_warp(bar(B_PFULL + kb), gp & 1u, sy);
-                    if (ok && one) ptx::mma_commit_pair(bar(B_PFREE + kb));
+                    // parts without a token pass as well
+                    for (int kb = (n + 63) / 64; kb < 4 && ok; ++kb) {
+                        ok = wait_bar_warp(bar(B_PFULL + kb), gp & 1u, sy);
+                        if (ok && one) ptx::mma_commit_pair(bar(B_PFREE + kb));
+                    }
                 }
             }
+            if (any) {
+                if (one) ptx::mma_commit_pair(bar(B_DRAIN + 1));
+                wait_landed(bar(B_DRAIN + 1), 0);
+            }
         }
-        if (any) {
-            if (one) ptx::mma_commit_pair(bar(B_DRAIN + 1));
-            wait_landed(bar(B_DRAIN + 1), 0);
+    } else if (warp == kClearWarp) {
+        // ---------------- clearing ----------------
+        bool ok = true;
+        uint32_t g = 0, par = 0;                     // chunks so far; parity of each slot's edge barrier
+        Walk walk(p, cluster);
+        Piece pc;
+        while (ok && walk.next(&pc)) {
+            pc.uniform();
+            for (int i = 0; i < pc.tiles && ok; ++i) {
+                const int base = pc.base + i * kTile;
+                const int n = tile_tokens(pc, base), lo = pc.t0 - base;
+                for (int kb = 0; 64 * kb < n && ok; ++kb) {
+                    if (!has_edge(pc, base, kb)) {
+                        g += 2;
+                        continue;
+                    }
+                    // rows outside the span, up to the last 16 that the MMAs read
+                    const int steps = min(4, (n - 64 * kb + 15) / 16);
+                    const int cut0 = lo - 64 * kb, cut1 = n - 64 * kb;
+                    for (int j = 0; j < 2; ++j, ++g) {
+                        const uint32_t s = g % kRing;
+                        ok = wait_bar_warp(bar(B_VEDGE + s), par >> s & 1u, sy);
+                        if (!ok) break;
+                        par ^= 1u << s;
+                        for (int r = lane >> 4; r < 16 * steps; r += 2)
+                            if (r < cut0 || r >= cut1)
+                                ptx::st_shared_v4(sV + s * kChunk + (lane >> 3 & 1) * 8192 + r * 128 + (lane & 7) * 16,
+                                                  0u, 0u, 0u, 0u);
+                        ptx::fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(bar(B_VFULL + s), 0));
+                        __syncwarp();
+                    }
+                }
+            }
         }
     } else {
         // ---------------- softmax and output ----------------
