@@ -421,6 +421,29 @@ __device__ __forceinline__ bool wait_bar_warp(uint32_t bar, uint32_t parity, con
     return __all_sync(kFull, ok);
 }
 
+// A wait that other tiles may pass in front of: `pace`, whose phase turns with each
+// of them, starts the limit anew.  (Polled much faster than tiles go by: a wait that
+// suspends may see every second one.  A counter that another warp writes costs
+// that warp 1% of a long call.)
+__device__ __forceinline__ bool wait_paced_warp(uint32_t bar, uint32_t parity, uint32_t pace, const Sync &sy)
+{
+    bool ok = ptx::mbar_test(bar, parity), turn = ptx::mbar_test(pace, 0);
+    for (uint64_t t0 = ptx::globaltimer(); !ok; ok = ptx::mbar_test(bar, parity)) {
+        if (*sy.abort_flag) break;
+        const bool now = ptx::mbar_test(pace, 0);
+        if (now != turn) {
+            turn = now;
+            t0 = ptx::globaltimer();
+        } else if (ptx::globaltimer() - t0 > sy.limit_ns) {
+            *sy.abort_flag = 1u;
+            atomicOr(sy.status, KPOOL_STATUS_TIMEOUT);
+            break;
+        }
+        __nanosleep(100);
+    }
+    return __all_sync(kFull, ok);
+}
+
 // A wait for work in flight before the CTA ends: blind to the abort flag, and bounded.
 __device__ __forceinline__ void wait_landed(uint32_t bar, uint32_t parity)
 {
@@ -765,7 +788,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     const int cut0 = lo - 64 * kb, cut1 = n - 64 * kb;
                     for (int j = 0; j < 2; ++j, ++g) {
                         const uint32_t s = g % kRing;
-                        ok = wait_bar_warp(bar(B_VEDGE + s), par >> s & 1u, sy);
+                        // (this warp goes past the chunks without an edge at once)
+                        ok = wait_paced_warp(bar(B_VEDGE + s), par >> s & 1u, bar(B_PFREE), sy);
                         if (!ok) break;
                         par ^= 1u << s;
                         for (int r = lane >> 4; r < 16 * steps; r += 2)

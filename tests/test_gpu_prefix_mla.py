@@ -409,6 +409,19 @@ def test_expired_waits(K, limit):
     c.check(o, lse)
 
 
+def test_a_limit_is_for_a_wait_not_for_a_piece(K):
+    """Work of half a millisecond per block, whose spans begin and end inside a chunk, under a limit of 0.15."""
+    c = Case([(32700, [(32790, 80)])], H=128, page=64, seed=23)
+    want = run(K, c)
+    before = K.kpool_debug_set_wait_limit_ns(150000)
+    try:
+        got = run(K, c)
+    finally:
+        K.kpool_debug_set_wait_limit_ns(before)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    c.check(*got, rows={0, 79})
+
+
 def test_a_rollout_from_pages_to_attention(K):
     """The calls together, as a rollout makes them: a prompt's rows written, forked for three samples, each grown by its
     own tokens step by step, attended through the pool's own table, one sample retired, the pool packed."""
