@@ -953,7 +953,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int row0 = row - lane;
             float *out = p.w.o + (pc.out + row0) * kDc + 256 * half + 128 * part + 4 * (lane & 7);
 #pragma unroll 1
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < 4 && row0 < pc.nrows; ++k) {
                 uint32_t o[32];
                 ptx::tmem_ld32(lanes + 128 * part + 32 * k, o);
                 ptx::tmem_ld_wait(o);
