@@ -66,15 +66,14 @@ constexpr int kDc = 512;
 constexpr int kRows = 128;               // rows of a unit
 constexpr int kCtaRows = 64;             // of them in each CTA
 constexpr int kTile = 256;               // tokens of a tile
-constexpr int kOverhead = 3;             // a piece's start and end, in tiles (for the even cut; 2 and 4 measured slower)
+constexpr int kOverhead = 3;             // a piece's start and end, in tiles (for the even cut: 2 takes 194 us where 3 takes 191, 64 samples over 32768 shared tokens)
 constexpr int kThreads = 416;
 constexpr int kSmWarps = 8;
 constexpr int kClearWarp = 4 + kSmWarps;
 constexpr int kPlanThreads = 1024;
 // What the plan keeps in shared memory: its lists up to about 6000 sequences, and the
 // units that fit beside them.  (With room for 1024 of each, 1000 sequences in 50 groups
-// planned in 22.7 us and 2000 in 43.6, now 19.7 and 34.4: what is left is the one block's
-// instructions, not its loads, divisions or searches alone.)
+// planned in 22.7 us and 2000 in 43.6, now in 19.7 and 34.4: one block plans them all.)
 constexpr int kPlanListBytes = 96 * 1024, kPlanSmem = 200 * 1024;
 constexpr int kMaxClusters = 80;         // CTA pairs that a workspace has room for
 constexpr int64_t kBlockRows = 512;      // rows up to which combine takes a block for each
