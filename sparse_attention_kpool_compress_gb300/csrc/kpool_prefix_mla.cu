@@ -1055,7 +1055,8 @@ __global__ void __launch_bounds__(256) combine_block_kernel(const Params p)
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kWarps; ++i) m = fmaxf(m, top[i]);
-    const float f = m == -INFINITY ? 0.f : ptx::ex2_approx(s - m);
+    const float ref = m == -INFINITY ? 0.f : m;      // (the maximum passes over NaN, the weights do not)
+    const float f = ptx::ex2_approx(s - ref);
     weight[threadIdx.x] = f;
     float l = f;
 #pragma unroll

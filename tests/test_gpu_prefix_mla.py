@@ -465,3 +465,22 @@ def test_a_rollout_from_pages_to_attention(K):
         grow([4, 1], [16, 1])
         attend([1, 4], 37)
     assert int((pages.ref_count > 0).sum()) == 40 - pages.free_count.item()
+
+
+@pytest.mark.parametrize("H", [1, 16, 128])
+def test_the_log_sum_of_a_nan_query_is_nan(K, H):
+    """In batches whose rows are joined by a block each (up to 512 rows) and by a warp each: -inf is a row without
+    tokens, and a merge by lse would drop a NaN row that had it."""
+    for n in (3, 512 // H + 1):
+        c = Case([(300, [(301 + k % 3, 1) for k in range(n)]), (0, [(0, 1), (40, 1)])], H=H, page=32, seed=H)
+        sick = {0: float("nan"), n - 1: float("inf"), n + 1: float("nan")}
+        for t, value in sick.items():
+            c.q[t, H - 1, 7] = value
+        o, lse = run(K, c)
+        for t in sick:
+            assert torch.isnan(o[t, H - 1]).all() and torch.isnan(lse[t, H - 1]), (n, t)
+        assert torch.all(o[n] == 0) and torch.isneginf(lse[n]).all()
+        whole = torch.ones(lse.shape, dtype=torch.bool)
+        whole[n] = False
+        whole[list(sick), H - 1] = False
+        assert torch.isfinite(lse.cpu()[whole]).all() and torch.isfinite(o.cpu()[whole]).all()
