@@ -590,7 +590,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         auto pages_at = [&](int base) {
             int page = 0;
             if (lane * box < tile_tokens(pc, base)) {
-                page = __ldg(p.a.page_table + static_cast<int64_t>(pc.table_row) * p.a.max_pages + ((base + lane * box) >> pl));
+                // (an ordinary load: the read-only path asks for data that stay as they are
+                // from the grid's start, and a call that changes the table may still run then)
+                page = p.a.page_table[static_cast<int64_t>(pc.table_row) * p.a.max_pages + ((base + lane * box) >> pl)];
                 if (!in_range(page, p.a.n_pages)) {
                     atomicOr(sy.status, KPOOL_STATUS_BAD_PAGE);
                     page = p.a.n_pages;  // out of the map's bounds: reads as zeros

@@ -484,3 +484,66 @@ def test_the_log_sum_of_a_nan_query_is_nan(K, H):
         whole[n] = False
         whole[list(sick), H - 1] = False
         assert torch.isfinite(lse.cpu()[whole]).all() and torch.isfinite(o.cpu()[whole]).all()
+
+
+def test_tables_that_change_in_front_of_the_attention(K):
+    """One captured chain of page calls with the attention right behind those that write the table, replayed: no two
+    calls in a row read the same entries, and rows share cache lines."""
+    page, H, prefix = 16, 16, 37
+    g = torch.Generator().manual_seed(31)
+    pages = K.kpool_pages_new(5, 64, 13, page)
+    store = torch.full((64, page, W), float("nan"), dtype=torch.bfloat16, device="cuda")
+    i = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    first = torch.randn(prefix, W, generator=g).to(torch.bfloat16)
+    begin = K.kpool_pages_extend(pages, i([0]), i([prefix]))
+    K.kpool_pages_write(pages, i([0]), begin, i([0, prefix]), first.cuda(), store)
+    K.kpool_pages_fork(pages, i([0]), i([2]), store)
+    parent, child, both = i([0]), (i([2]), i([3])), (i([2, 0]), i([3, 0]))
+    cu, more = i([0, 3, 4]), i([3, 1])
+    rows = torch.empty(2, 4, W, dtype=torch.bfloat16, device="cuda")
+    q = (2 * torch.randn(3, H, W, generator=g)).to(torch.bfloat16)
+    cu_q, cu_g, pre, qd = i([0, 2, 3]), i([0, 2]), i([prefix]), q.cuda()
+    tables = []
+
+    def attend(k):
+        out = K.kpool_shared_prefix_mla_fwd(qd, store, pages.page_table, pages.seq_lens, cu_q, cu_g, pre, W ** -0.5,
+                                            seq_ids=both[k])
+        tables.append(pages.page_table[2 + k].clone())
+        return out
+
+    def half(k):
+        """A new child of sequence 0 in place of the old one, each grown; attended before and after packing."""
+        K.kpool_pages_fork(pages, parent, child[k], store)
+        K.kpool_pages_free(pages, child[1 - k])
+        begin = K.kpool_pages_extend(pages, both[k], more)
+        K.kpool_pages_write(pages, both[k], begin, cu, rows[k], store)
+        a = attend(k)
+        K.kpool_pages_compact(pages, store)
+        return [a, attend(k)]
+
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = [half(1), half(0)]
+    mine, read = first, []
+    for k in range(24):
+        # another sequence's pages come and go in between
+        if k % 2 == 0:
+            K.kpool_pages_extend(pages, i([4]), i([16 * (1 + k % 5)]))
+        else:
+            K.kpool_pages_free(pages, i([4]))
+        new = torch.randn(2, 4, W, generator=g).to(torch.bfloat16)
+        rows.copy_(new)
+        graph.replay()
+        torch.cuda.synchronize()
+        for h in (1, 0):
+            c = Case.__new__(Case)
+            c.H, c.scale, c.q, c.cu_q, c.nq = H, W ** -0.5, q, np.array([0, 2, 3]), [2, 1]
+            held = [torch.cat([mine, new[h, :3]]).double(), torch.cat([mine, new[h, 3:]]).double()]
+            c.lens, c.tokens = [len(x) for x in held], lambda b: held[b]
+            a, b = outs[1 - h]
+            c.check(*a, note=(k, h))
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]), (k, h)
+            mine = torch.cat([mine, new[h, 3:]])
+        read += [tuple(t.tolist()) for t in tables]
+    assert len(set(read[::4])) > 15 and len(set(read[2::4])) > 15      # (the table did change)
+    assert K.kpool_read_status(pages.workspace) == 0
