@@ -569,6 +569,7 @@ __global__ void __launch_bounds__(kApplyThreads) free_apply(const kpool_page_poo
     ptx::grid_dependents_launch();
     ptx::grid_dependency_wait();
     const int n = ws[W_COUNT];
+    if (n == 0) return;                    // refused: the count stays too, whatever it is
     const int spans = ceil_div(p.max_pages, kSpan);
     for (int64_t t = blockIdx.x; t < static_cast<int64_t>(n) * spans; t += gridDim.x) {
         const int i = static_cast<int>(t / spans), first = static_cast<int>(t - static_cast<int64_t>(i) * spans) * kSpan;

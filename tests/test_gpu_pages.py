@@ -517,3 +517,73 @@ def test_captured_and_replayed(K):
         graph.replay()
         host_step()
         b.check(0, ("replay", k))
+
+
+ARRAYS = ("page_table", "seq_lens", "ref_count", "free_list", "free_count")
+
+
+def _state(b):
+    """Copies of the pool's five arrays and of the stores."""
+    return [getattr(b.gpu, a).clone() for a in ARRAYS] + [s.clone() for s in b.stores]
+
+
+def _broken(K, what):
+    """Sequences of 20 and 3 tokens in pages of 8, of at most 3 each, then one number out of its range."""
+    b = Both(K, n_seqs=4, n_pages=8, max_pages=3, page_size=8)
+    b.grow([0, 1], [20, 3])
+    p = b.gpu
+    if what == "id":
+        p.page_table[0, 2] = 1 << 20
+    elif what == "negative id":
+        p.page_table[0, 2] = -7
+    elif what == "count":
+        p.free_count.fill_(9)
+    elif what == "negative count":
+        p.free_count.fill_(-1)
+    elif what == "list":
+        p.free_list.fill_(99)
+    elif what == "length":
+        p.seq_lens[0] = 25
+    else:
+        p.seq_lens[0] = -1
+    return b
+
+
+BROKEN = ["id", "negative id", "count", "negative count", "list", "length", "negative length"]
+
+
+@pytest.mark.parametrize("what", BROKEN)
+def test_a_refused_call_changes_nothing(K, what):
+    """Every array of the pool and every byte of the stores, whatever is wrong with the pool."""
+    b = _broken(K, what)
+    p, i = b.gpu, b.i32
+    begin = i([7, 7])
+    calls = [lambda: K.kpool_pages_fork(p, i([0]), i([2]), b.stores, workspace=b.ws),
+             lambda: K.kpool_pages_extend(p, i([0, 1]), i([3, 9]), workspace=b.ws, out=begin)]
+    if "id" not in what and what != "list":
+        calls.append(lambda: K.kpool_pages_free(p, i([0]), workspace=b.ws))
+        calls.append(lambda: K.kpool_pages_free(p, i([1, 0]), workspace=b.ws))
+    before = _state(b)
+    for k, call in enumerate(calls):
+        call()
+        assert K.kpool_read_status(b.ws) == BAD, k
+        assert all(torch.equal(x, y) for x, y in zip(before, _state(b))), k
+    assert begin.tolist() == [-1, -1]
+
+
+@pytest.mark.parametrize("what", ["id", "negative id"])
+def test_a_freed_id_out_of_range_is_skipped(K, what):
+    """The other pages of the sequence are given back, and nothing else changes."""
+    b = _broken(K, what)
+    before = _state(b)
+    one, two = before[0][0, :2].tolist()
+    K.kpool_pages_free(b.gpu, b.i32([0]), workspace=b.ws)
+    assert K.kpool_read_status(b.ws) == BAD
+    want = [t.clone() for t in before]
+    want[0][0] = -1
+    want[1][0] = 0
+    want[2][one] = want[2][two] = 0
+    n = int(before[4])
+    want[3][n:n + 2] = b.i32(sorted([one, two]))
+    want[4] += 2
+    assert all(torch.equal(x, y) for x, y in zip(want, _state(b)))
