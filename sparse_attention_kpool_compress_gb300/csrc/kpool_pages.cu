@@ -622,10 +622,18 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan(const kpool_page_po
     ptx::grid_dependents_launch();
     ptx::grid_dependency_wait();
     const int n = p.n_pages;
+    // (the count and the first lengths are held back, so that all loads are in flight at once)
+    const int fc = *p.free_count, len0 = threadIdx.x < p.n_seqs ? p.seq_lens[threadIdx.x] : 0;
     int mine = 0;
     for (int i = threadIdx.x; i < n; i += blockDim.x) mine += p.ref_count[i] > 0;
     int k;
     block_exclusive(mine, scratch, &k);
+    const int64_t room = static_cast<int64_t>(p.max_pages) * p.page_size;
+    bool bad = !in_range(fc, n + 1) || len0 < 0 || len0 > room;
+    for (int s = threadIdx.x + blockDim.x; s < p.n_seqs; s += blockDim.x) {
+        const int len = p.seq_lens[s];
+        bad |= len < 0 || len > room;
+    }
     int from = 0, to = 0;                  // movers and holes before this round
     for (int base = 0; base < n; base += kPlanPages * blockDim.x) {
         const int p0 = base + kPlanPages * threadIdx.x;
@@ -649,7 +657,14 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan(const kpool_page_po
         from += tm;
         to += th;
     }
-    __syncthreads();
+    if (__syncthreads_or(bad)) {           // (so far only the workspace was written)
+        if (threadIdx.x == 0) {
+            ws[W_STATUS] = KPOOL_STATUS_BAD_PAGE;
+            ws[W_COUNT] = 0;
+            ws[W_LIVE] = n;                // every page stays where it is
+        }
+        return;
+    }
     // as many pages move as there are holes: both are k less the referenced pages below k
     for (int i = threadIdx.x; i < from; i += blockDim.x) {
         const int s = l.a[i], d = l.b[i];

@@ -587,3 +587,36 @@ def test_a_freed_id_out_of_range_is_skipped(K, what):
     want[3][n:n + 2] = b.i32(sorted([one, two]))
     want[4] += 2
     assert all(torch.equal(x, y) for x, y in zip(want, _state(b)))
+
+
+@pytest.mark.parametrize("what", ["count", "negative count", "length", "negative length"])
+def test_a_refused_packing_changes_nothing(K, what):
+    b = _broken(K, what)
+    if "count" in what:
+        b.gpu.ref_count[b.gpu.page_table[0, 0].long()] = 0     # (a hole, so that there is something to move)
+    before = _state(b)
+    K.kpool_pages_compact(b.gpu, b.stores, workspace=b.ws)
+    assert K.kpool_read_status(b.ws) == BAD
+    assert all(torch.equal(x, y) for x, y in zip(before, _state(b)))
+
+
+@pytest.mark.parametrize("what", ["id", "negative id", "list"])
+def test_packing_with_an_id_out_of_range(K, what):
+    """A bad table entry is skipped, with the status; the free list is made anew, so that what it held does not matter."""
+    b = _broken(K, what)
+    before = _state(b)
+    b.host.compact()
+    K.kpool_pages_compact(b.gpu, b.stores, workspace=b.ws)
+    if what == "list":
+        b.check(0)
+    else:
+        b.host.table[0, 2] = before[0][0, 2].item()
+        b.check(BAD)
+
+
+def test_lengths_that_fill_the_table(K):
+    """The largest length that a table row has room for, and none, are packed like others."""
+    b = Both(K, n_seqs=3, n_pages=9, max_pages=3, page_size=8)
+    b.grow([0, 1], [24, 24])
+    b.free([0])
+    b.compact()
