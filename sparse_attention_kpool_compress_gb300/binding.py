@@ -530,10 +530,10 @@ class KPoolPages:
     kpool_page_pool).  kpool_pages_new makes an empty one.  `workspace` is the
     one that calls on this pool use unless they are given another (calls on a
     pool are ordered anyway); kpool_read_status(pages.workspace) tells how the
-    last of them went."""
+    last of them went.  (kpool_pages_copy is a call on stores, not on a pool.)"""
 
     __slots__ = ("page_table", "seq_lens", "ref_count", "free_list", "free_count", "page_size",
-                 "n_seqs", "n_pages", "workspace", "_index", "_c", "_at", "_ws")
+                 "n_seqs", "n_pages", "workspace", "_index", "_c", "_at", "_ws", "_most")
 
     def __init__(self, page_table, seq_lens, ref_count, free_list, free_count, page_size: int):
         arrays = dict(page_table=page_table, seq_lens=seq_lens, ref_count=ref_count,
@@ -559,9 +559,10 @@ class KPoolPages:
                         free_list.data_ptr(), free_count.data_ptr(), page_table.shape[0],
                         page_table.shape[1], ref_count.numel(), page_size))
         put("_at", ctypes.addressof(self._c))
-        # (enough for every list of at most n_pages items)
+        # (enough for every list that names each sequence once)
+        put("_most", max(self.n_pages, self.n_seqs))
         put("workspace", torch.zeros(
-            max(256, _lib.kpool_pages_workspace_size(self.n_pages, self.n_seqs, self.n_pages)),
+            max(256, _lib.kpool_pages_workspace_size(self._most, self.n_seqs, self.n_pages)),
             dtype=torch.uint8, device=page_table.device))
         put("_ws", (self.workspace, self.workspace.data_ptr(), self.workspace.numel()))
 
@@ -613,7 +614,10 @@ def kpool_pages_workspace_size(n: int, n_seqs: int, n_pages: int) -> int:
 
 
 def kpool_pages_copy(src, dst, stores, workspace=None):
-    """Page dst[i] becomes a copy of page src[i] in every store and layer."""
+    """Page dst[i] becomes a copy of page src[i] in every store and layer.  A
+    list that is refused is told by the workspace alone (kpool_read_status): give
+    one (256 bytes of uint8 up to 1024 pairs, else kpool_pages_workspace_size(n,
+    0, n_pages)) to see whether it was."""
     first = stores if isinstance(stores, torch.Tensor) else stores[0] if len(stores) else None
     if first is None:
         raise ValueError("a store is required")
@@ -636,11 +640,19 @@ def _status_words(index):
     return t, t.data_ptr(), 256
 
 
-def _pool_workspace(workspace, n, pages):
-    if workspace is None and n <= pages.n_pages:
-        return pages._ws
-    return _bytes(workspace, 0 if workspace is not None else
-                  _lib.kpool_pages_workspace_size(n, pages.n_seqs, pages.n_pages), pages._index)
+def _pool_call(pages, workspace, n, name, fn, *args):
+    """fn(*args, workspace, size, stream) over n items, in the pool's own workspace
+    unless the caller gives one."""
+    index = pages._index
+    if workspace is None and n <= pages._most:
+        _, ws, size = pages._ws
+        return _call(index, name, fn, *args, ws, size)
+    keep, ws, size = _bytes(workspace, 0 if workspace is not None else
+                            _lib.kpool_pages_workspace_size(n, pages.n_seqs, pages.n_pages), index)
+    _call(index, name, fn, *args, ws, size)
+    if workspace is None:
+        # a list with repetitions: how it went is told where the pool's calls tell it
+        pages.workspace[:16].copy_(keep[:16])
 
 
 def kpool_pages_fork(pages: KPoolPages, parents, children, stores=(), workspace=None):
@@ -649,9 +661,8 @@ def kpool_pages_fork(pages: KPoolPages, parents, children, stores=(), workspace=
     index, n = pages._index, parents.numel()
     a, b = _ints(parents, "parents", n, index), _ints(children, "children", n, index)
     st, n_stores = _stores(stores, pages.n_pages, index)
-    keep, ws, size = _pool_workspace(workspace, n, pages)
-    _call(index, "kpool_pages_fork", _lib.kpool_pages_fork, pages._at, a, b, n, st, n_stores, ws,
-          size)
+    _pool_call(pages, workspace, n, "kpool_pages_fork",
+               _lib.kpool_pages_fork, pages._at, a, b, n, st, n_stores)
 
 
 def kpool_pages_extend(pages: KPoolPages, seqs, n_new, workspace=None, out=None):
@@ -662,8 +673,8 @@ def kpool_pages_extend(pages: KPoolPages, seqs, n_new, workspace=None, out=None)
     if out is None:
         out = torch.empty(n, dtype=_I32, device=_devices(index))
     c = _ints(out, "out", n, index)
-    keep, ws, size = _pool_workspace(workspace, n, pages)
-    _call(index, "kpool_pages_extend", _lib.kpool_pages_extend, pages._at, a, b, n, c, ws, size)
+    _pool_call(pages, workspace, n, "kpool_pages_extend",
+               _lib.kpool_pages_extend, pages._at, a, b, n, c)
     return out
 
 
@@ -685,26 +696,23 @@ def kpool_pages_write(pages: KPoolPages, seqs, begin, cu_rows, rows, store, work
     if shape[-1] != width:
         raise ValueError("rows are %d wide, the store's %d" % (shape[-1], width))
     total = shape[-2]
-    keep, ws, size = _pool_workspace(workspace, n, pages)
-    _call(index, "kpool_pages_write", _lib.kpool_pages_write, pages._at, a, b, c, n, total,
-          rows.data_ptr(), total * width * rows.element_size(), st, ws, size)
+    _pool_call(pages, workspace, n, "kpool_pages_write", _lib.kpool_pages_write, pages._at, a, b, c, n,
+               total, rows.data_ptr(), total * width * rows.element_size(), st)
 
 
 def kpool_pages_free(pages: KPoolPages, seqs, workspace=None):
     """The listed sequences give up their pages."""
     index, n = pages._index, seqs.numel()
     a = _ints(seqs, "seqs", n, index)
-    keep, ws, size = _pool_workspace(workspace, n, pages)
-    _call(index, "kpool_pages_free", _lib.kpool_pages_free, pages._at, a, n, ws, size)
+    _pool_call(pages, workspace, n, "kpool_pages_free", _lib.kpool_pages_free, pages._at, a, n)
 
 
 def kpool_pages_compact(pages: KPoolPages, stores=(), workspace=None):
     """The k referenced pages move to the pages 0 .. k - 1, in every store."""
     index = pages._index
     st, n_stores = _stores(stores, pages.n_pages, index)
-    keep, ws, size = _pool_workspace(workspace, 0, pages)
-    _call(index, "kpool_pages_compact", _lib.kpool_pages_compact, pages._at, st, n_stores, ws,
-          size)
+    _pool_call(pages, workspace, 0, "kpool_pages_compact",
+               _lib.kpool_pages_compact, pages._at, st, n_stores)
 
 
 def kpool_shared_prefix_mla_workspace_size(Tq: int, H: int, B: int, G: int) -> int:

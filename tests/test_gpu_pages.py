@@ -620,3 +620,38 @@ def test_lengths_that_fill_the_table(K):
     b.grow([0, 1], [24, 24])
     b.free([0])
     b.compact()
+
+
+def test_the_status_of_lists_longer_than_the_pool(K):
+    """More sequences than pages, lists with repetitions: the pool's own workspace tells of the last call, whatever its
+    length."""
+    i = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    n = 300
+    p = K.kpool_pages_new(n, 4, 2, 8)
+    store = torch.zeros(4, 8, 16, dtype=torch.uint8, device="cuda")
+    every = i(list(range(n)))
+
+    def status(want):
+        assert K.kpool_read_status(p.workspace) == want
+
+    K.kpool_pages_extend(p, i([0, 1]), i([3, 8]))
+    status(0)
+    assert K.kpool_pages_extend(p, every, torch.ones_like(every)).eq(-1).all()
+    status(SHORT)                                  # 299 pages needed, 2 free
+    K.kpool_pages_fork(p, i([1] * 298), i(list(range(2, n))), store)
+    status(0)
+    K.kpool_pages_fork(p, i([0] * n), every, store)
+    status(BAD)
+    K.kpool_pages_extend(p, i([0]), i([0]))
+    status(0)
+    K.kpool_pages_free(p, i([0, 0] * n))           # longer than any list that could be carried out
+    status(BAD)
+    K.kpool_pages_write(p, i([0] * 3 * n), i([k % 3 for k in range(3 * n)]), i([min(k, 3) for k in range(3 * n + 1)]),
+                        torch.ones(3, 16, dtype=torch.uint8, device="cuda"), store)
+    status(0)
+    assert store[p.page_table[0, 0], :3].eq(1).all() and int(store.sum()) == 3 * 16
+    K.kpool_pages_extend(p, i([0] * 3 * n), i([0] * 3 * n))
+    status(BAD)
+    K.kpool_pages_free(p, every)
+    status(0)
+    assert p.free_count.item() == 4
