@@ -530,10 +530,15 @@ class KPoolPages:
     kpool_page_pool).  kpool_pages_new makes an empty one.  `workspace` is the
     one that calls on this pool use unless they are given another (calls on a
     pool are ordered anyway); kpool_read_status(pages.workspace) tells how the
-    last of them went.  (kpool_pages_copy is a call on stores, not on a pool.)"""
+    last of them went.  (kpool_pages_copy is a call on stores, not on a pool.)
+    Calls may run on another stream than the one that the pool was made on: the
+    first there waits until the workspace is made (in a capture, what begins it
+    has to; torch.cuda.graph does), and its memory goes to nobody else before
+    they have ended."""
 
     __slots__ = ("page_table", "seq_lens", "ref_count", "free_list", "free_count", "page_size",
-                 "n_seqs", "n_pages", "workspace", "_index", "_c", "_at", "_ws", "_most")
+                 "n_seqs", "n_pages", "workspace", "_index", "_c", "_at", "_ws", "_most",
+                 "_streams", "_made")
 
     def __init__(self, page_table, seq_lens, ref_count, free_list, free_count, page_size: int):
         arrays = dict(page_table=page_table, seq_lens=seq_lens, ref_count=ref_count,
@@ -565,6 +570,10 @@ class KPoolPages:
             max(256, _lib.kpool_pages_workspace_size(self._most, self.n_seqs, self.n_pages)),
             dtype=torch.uint8, device=page_table.device))
         put("_ws", (self.workspace, self.workspace.data_ptr(), self.workspace.numel()))
+        put("_streams", {_raw_stream(self._index)})
+        with torch.cuda.device(self._index):
+            put("_made", None if torch.cuda.is_current_stream_capturing() else
+                torch.cuda.current_stream().record_event())
 
     def __setattr__(self, name, value):
         raise AttributeError("a KPoolPages keeps its tensors: make another one")
@@ -640,10 +649,23 @@ def _status_words(index):
     return t, t.data_ptr(), 256
 
 
+def _join(pages):
+    """The pool's own workspace is used on a stream that it was not made on."""
+    with torch.cuda.device(pages._index):
+        stream = torch.cuda.current_stream()
+        pages.workspace.record_stream(stream)
+        if not torch.cuda.is_current_stream_capturing():
+            if pages._made is not None:
+                stream.wait_event(pages._made)
+            pages._streams.add(stream.cuda_stream)
+
+
 def _pool_call(pages, workspace, n, name, fn, *args):
     """fn(*args, workspace, size, stream) over n items, in the pool's own workspace
     unless the caller gives one."""
     index = pages._index
+    if workspace is None and _raw_stream(index) not in pages._streams:
+        _join(pages)
     if workspace is None and n <= pages._most:
         _, ws, size = pages._ws
         return _call(index, name, fn, *args, ws, size)

@@ -655,3 +655,51 @@ def test_the_status_of_lists_longer_than_the_pool(K):
     K.kpool_pages_free(p, every)
     status(0)
     assert p.free_count.item() == 4
+
+
+def test_a_pool_dropped_while_another_stream_uses_it(K):
+    """The pool's own workspace goes to nobody else before the side stream's calls have ended."""
+    i = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    p = K.kpool_pages_new(6, 40, 8, 8)
+    kept = [getattr(p, a) for a in ARRAYS]
+    seqs, more = i([1, 4, 2]), i([20, 3, 64])
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(40_000_000)              # some 20 ms
+        begin = K.kpool_pages_extend(p, seqs, more)
+        K.kpool_pages_free(p, seqs[:1])
+    size, at = p.workspace.numel(), p.workspace.data_ptr()
+    del p
+    others = [torch.full((size,), 255, dtype=torch.uint8, device="cuda") for _ in range(20)]
+    assert all(o.data_ptr() != at for o in others)
+    torch.cuda.synchronize()
+    assert begin.tolist() == [0, 0, 0] and kept[1].tolist() == [0, 0, 64, 0, 3, 0]
+    assert kept[4].item() == 40 - 9
+
+
+def test_a_pool_used_at_once_on_another_stream(K):
+    """The first call there waits until the workspace is made; so does one in a graph, which is captured then."""
+    i = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    made = K.kpool_pages_new(6, 40, 8, 8)
+    arrays = [getattr(made, a) for a in ARRAYS]
+    seqs, more = i([1, 4, 2]), i([20, 3, 64])
+    torch.cuda.synchronize()
+    side, passed = torch.cuda.Stream(), torch.cuda.Event()
+    torch.cuda._sleep(40_000_000)
+    p = K.KPoolPages(*arrays, 8)
+    passed.record()
+    with torch.cuda.stream(side):
+        K.kpool_pages_extend(p, seqs, more)
+    side.synchronize()
+    assert passed.query()
+    assert K.kpool_read_status(p.workspace) == 0
+    assert p.seq_lens.tolist() == [0, 20, 64, 0, 3, 0]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        K.kpool_pages_free(p, seqs)
+        K.kpool_pages_extend(p, seqs, more)
+    for _ in range(3):
+        graph.replay()
+    assert K.kpool_read_status(p.workspace) == 0
+    assert p.seq_lens.tolist() == [0, 20, 64, 0, 3, 0] and p.free_count.item() == 40 - 12
