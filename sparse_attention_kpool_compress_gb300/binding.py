@@ -468,7 +468,8 @@ class _Pool(ctypes.Structure):
 # The calls below are short on the GPU, so the host's part is kept short as well:
 # one combined test per tensor (the messages are made only when it fails), raw
 # pointers and streams, structures packed in one go.
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# (a CPU build of torch has no streams; the host-only calls work there)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _pack_store = struct.Struct("@Pqqiiii").pack
 _I32 = torch.int32
 

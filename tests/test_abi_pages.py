@@ -124,3 +124,15 @@ def test_tensors_are_checked(b):
         b.kpool_pages_copy(i32, i32, ())
     with pytest.raises(ValueError, match="CUDA"):
         b.kpool_pages_copy(i32, i32, [torch.zeros(2, 8, 16, 8)])
+
+
+def test_the_binding_imports_without_cuda_in_torch(b, monkeypatch):
+    """A CPU build of torch lacks the stream lookup: the calls that work on the host alone still do."""
+    import importlib.util
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    spec = importlib.util.spec_from_file_location("binding_without_cuda", b.__file__)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    cu, total = module.kpool_num_pools([0, 5, 13], 13, 4)
+    assert cu.tolist() == [0, 1, 3] and total == 3
+    assert module.kpool_pages_workspace_size(4, 4, 32) == b.kpool_pages_workspace_size(4, 4, 32) > 0
