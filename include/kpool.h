@@ -553,7 +553,8 @@ KPOOL_API int kpool_pages_extend(const kpool_page_pool *pool, const int32_t *seq
  *   cu_rows  int32 [n + 1]
  * A row outside its sequence's length (rows_per_page of every page_size
  * tokens), in a page that other sequences hold too, or with no sequence to go
- * to is left out, with KPOOL_STATUS_BAD_PAGE.  Two rows that go to one place
+ * to is left out, with KPOOL_STATUS_BAD_PAGE; so are the rows that cu_rows
+ * counts behind the `total` that there are.  Two rows that go to one place
  * leave a mixture of both.
  */
 KPOOL_API int kpool_pages_write(const kpool_page_pool *pool, const int32_t *seqs,

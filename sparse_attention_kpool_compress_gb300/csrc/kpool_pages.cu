@@ -478,6 +478,7 @@ __global__ void __launch_bounds__(kOne ? kWriteClusterThreads : kApplyThreads) w
     ptx::grid_dependents_launch();
     ptx::grid_dependency_wait();
     bool bad = false;
+    const int named = blockIdx.x == 0 && threadIdx.x == 0 ? cu_rows[n] : 0;
     if (kOne) {
         if (blockIdx.x == 0 && threadIdx.x == 0) ws[W_STATUS] = 0;
         ptx::cluster_arrive();
@@ -520,6 +521,7 @@ __global__ void __launch_bounds__(kOne ? kWriteClusterThreads : kApplyThreads) w
         for (int off = 2048 + lane * 16; off < g.row_bytes; off += 512)
             *reinterpret_cast<uint4 *>(dst + off) = __ldcs(reinterpret_cast<const uint4 *>(src + off));
     }
+    bad |= named > total;                  // rows that the list names and nobody brought
     if (kOne) ptx::cluster_wait();
     if (bad && lane == 0) atomicOr(ws + W_STATUS, KPOOL_STATUS_BAD_PAGE);
 }
@@ -808,14 +810,14 @@ int run_pages_write(const kpool_page_pool &p, const int32_t *seqs, const int32_t
                     void *ws, cudaStream_t s)
 {
     const int64_t tasks = total * g.n_layers;
-    if (n > 0 && tasks > 0 && tasks * 32 <= kCluster * kWriteClusterThreads) {
-        const int blocks = static_cast<int>((tasks * 32 + kWriteClusterThreads - 1) / kWriteClusterThreads);
+    if (n > 0 && tasks * 32 <= kCluster * kWriteClusterThreads) {
+        const int blocks = std::max(1, static_cast<int>((tasks * 32 + kWriteClusterThreads - 1) / kWriteClusterThreads));
         KPOOL_CUDA_CHECK(launch_clusters_after(blocks, write_kernel<true>, blocks, kWriteClusterThreads, s, p, seqs, begin, cu_rows, n, total,
                                       static_cast<const char *>(rows), rows_layer_stride, g, static_cast<int *>(ws)));
         return KPOOL_OK;
     }
     KPOOL_CUDA_CHECK(launch_after(clear_status, 1, 1, s, static_cast<int *>(ws)));
-    if (n == 0 || tasks == 0) return KPOOL_OK;
+    if (n == 0) return KPOOL_OK;
     // (more blocks than fit at once: a warp has one row's chain of lookups to wait for)
     const int64_t blocks = std::min<int64_t>((tasks * 32 + kApplyThreads - 1) / kApplyThreads, 1 << 20);
     KPOOL_CUDA_CHECK(launch_after(write_kernel<false>, static_cast<int>(blocks), kApplyThreads, s, p, seqs, begin, cu_rows, n, total,

@@ -703,3 +703,18 @@ def test_a_pool_used_at_once_on_another_stream(K):
         graph.replay()
     assert K.kpool_read_status(p.workspace) == 0
     assert p.seq_lens.tolist() == [0, 20, 64, 0, 3, 0] and p.free_count.item() == 40 - 12
+
+
+@pytest.mark.parametrize("there", [0, 1, 8, 127, 128, 129, 300])
+def test_fewer_rows_than_the_offsets_count(K, there):
+    """The rows that there are go to their places, and the status tells of the others."""
+    b = Both(K, n_seqs=3, n_pages=60, max_pages=50, page_size=8)
+    b.grow([0, 2], [there + 20, 5])
+    rows = b.rng.randint(0, 256, (2, there, 48)).astype(np.uint8)
+    gpu = torch.from_numpy(rows).cuda()
+    for cu, want in (([0, 2, there + 3], BAD), ([0, there, there + 1], BAD), ([0, 0, there], 0)):
+        K.kpool_pages_write(b.gpu, b.i32([2, 0]), b.i32([0, 0]), b.i32(cu), gpu, b.stores[0], workspace=b.ws)
+        if cu[1] > 5:
+            want = BAD                             # (sequence 2 has room for five)
+        b.host.write([2, 0], [0, 0], [min(c, there) for c in cu], rows, 0)
+        b.check(want, (there, cu))
