@@ -470,6 +470,7 @@ class _Pool(ctypes.Structure):
 # pointers and streams, structures packed in one go.
 # (a CPU build of torch has no streams; the host-only calls work there)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 _pack_store = struct.Struct("@Pqqiiii").pack
 _I32 = torch.int32
 
@@ -498,7 +499,7 @@ def _device_of(t, name):
 
 def _call(index, name, fn, *args):
     """fn(*args, stream) on device `index` and its current stream."""
-    if torch._C._cuda_getDevice() == index:
+    if _current_device() == index:
         rc = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
@@ -665,11 +666,18 @@ def _pool_call(pages, workspace, n, name, fn, *args):
     """fn(*args, workspace, size, stream) over n items, in the pool's own workspace
     unless the caller gives one."""
     index = pages._index
-    if workspace is None and _raw_stream(index) not in pages._streams:
-        _join(pages)
-    if workspace is None and n <= pages._most:
-        _, ws, size = pages._ws
-        return _call(index, name, fn, *args, ws, size)
+    if workspace is None:
+        stream = _raw_stream(index)
+        if stream not in pages._streams:
+            _join(pages)
+        if n <= pages._most:
+            _, ws, size = pages._ws
+            if _current_device() != index:
+                return _call(index, name, fn, *args, ws, size)
+            rc = fn(*args, ws, size, stream)
+            if rc:
+                raise KPoolError(rc, name)
+            return
     keep, ws, size = _bytes(workspace, 0 if workspace is not None else
                             _lib.kpool_pages_workspace_size(n, pages.n_seqs, pages.n_pages), index)
     _call(index, name, fn, *args, ws, size)
