@@ -489,7 +489,8 @@ KPOOL_API int kpool_sparse_mla_fwd_pools_at(const void *q, const void *kv, const
  * KPOOL_STATUS_NO_PAGES.  Either way the call changes nothing.  The same goes
  * for the last, partial page of a sequence that a call forks or extends; other
  * page ids out of range inside the used part of a page-table row are skipped,
- * with KPOOL_STATUS_BAD_PAGE.  No id is followed out of its array.  Calls on one
+ * with KPOOL_STATUS_BAD_PAGE.  No id is followed out of its array.  The lists of a
+ * call lie apart from the pool's arrays (n_new may be seq_lens).  Calls on one
  * pool are ordered by the caller (one stream, or events).
  * workspace: kpool_pages_workspace_size(n, n_seqs, n_pages) bytes, n the
  * listed items (0 for kpool_pages_compact), 256-byte aligned; its status word
@@ -536,7 +537,7 @@ KPOOL_API int kpool_pages_fork(const kpool_page_pool *pool, const int32_t *paren
 /*
  * kpool_pages_extend -- sequence seqs[i] grows by n_new[i] >= 0 tokens; the
  * pages that it lacks are popped from the free pages in list order.
- * begin_out[i] (int32 [n], apart from the lists) gets its length before the
+ * begin_out[i] (int32 [n], apart from the lists and the pool) gets its length before the
  * call, or -1 everywhere when the call is refused.  A sequence whose last, partial page is held by
  * others as well is refused (KPOOL_STATUS_BAD_PAGE): fork copies such pages.
  */

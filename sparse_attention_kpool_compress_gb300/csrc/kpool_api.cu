@@ -173,6 +173,18 @@ int check_items(int64_t n, std::initializer_list<const int32_t *> arrays)
     return KPOOL_OK;
 }
 
+// Does out[0, n) share memory with one of the pool's arrays?
+bool in_pool(const int32_t *out, int64_t n, const kpool_page_pool &p)
+{
+    const uintptr_t o0 = reinterpret_cast<uintptr_t>(out), o1 = o0 + 4 * n;
+    auto meets = [&](const int32_t *a, int64_t len) {
+        const uintptr_t a0 = reinterpret_cast<uintptr_t>(a);
+        return o0 < a0 + 4 * len && a0 < o1;
+    };
+    return meets(p.page_table, static_cast<int64_t>(p.n_seqs) * p.max_pages) || meets(p.seq_lens, p.n_seqs) ||
+           meets(p.ref_count, p.n_pages) || meets(p.free_list, p.n_pages) || meets(p.free_count, 1);
+}
+
 // A call without items: a clean status word and nothing else.
 int nothing_listed(void *ws, kpool_stream_t stream)
 {
@@ -825,6 +837,7 @@ int kpool_pages_extend(const kpool_page_pool *pool, const int32_t *seqs, const i
     if ((begin_out < seqs + n && seqs < begin_out + n) || (begin_out < n_new + n && n_new < begin_out + n))
         return fail(KPOOL_ERR_INVALID_ARG, "begin_out overlaps a list of the call");
     if ((rc = check_pages_workspace(workspace, workspace_bytes, n, pool->n_seqs, pool->n_pages))) return rc;
+    if (n > 0 && in_pool(begin_out, n, *pool)) return fail(KPOOL_ERR_INVALID_ARG, "begin_out overlaps the pool's arrays");
     if (n == 0) return nothing_listed(workspace, stream);
     return run_pages_extend(*pool, seqs, n_new, static_cast<int>(n), begin_out, workspace,
                             reinterpret_cast<cudaStream_t>(stream));

@@ -355,7 +355,8 @@ __global__ void __launch_bounds__(kApplyThreads) fork_apply(const __grid_constan
 }
 
 // ---- extend ------------------------------------------------------------------
-// lists: a = pages taken before item i's, b = pages held, c = pages to take
+// lists: a = pages taken before item i's, b = length afterwards, c = pages to take (n_new
+// is not read again once lengths change: it may be seq_lens itself)
 
 __global__ void __launch_bounds__(kPlanThreads) extend_kernel(const kpool_page_pool p, const int32_t *seqs,
                                                               const int32_t *n_new, int n, int32_t *begin,
@@ -376,7 +377,7 @@ __global__ void __launch_bounds__(kPlanThreads) extend_kernel(const kpool_page_p
     int64_t need = 0;
     for (int base = 0; base < n; base += blockDim.x) {
         const int i = base + threadIdx.x;
-        int had = 0, take = 0, len = -1;
+        int had = 0, take = 0, len = -1, to = 0;
         const int s = i < n ? seqs[i] : 0;
         if (!in_range(s, p.n_seqs)) bad = true;
         else if (i < n) {
@@ -386,7 +387,8 @@ __global__ void __launch_bounds__(kPlanThreads) extend_kernel(const kpool_page_p
             if (len < 0 || add < 0 || static_cast<int64_t>(len) + add > room) bad = true;
             else {
                 had = ceil_div(len, ps);
-                take = ceil_div(len + add, ps) - had;
+                to = len + add;
+                take = ceil_div(to, ps) - had;
                 if (add > 0 && len % ps != 0) {
                     // the rows go on in the last page, which must be the sequence's own
                     const int last = p.page_table[static_cast<int64_t>(s) * p.max_pages + had - 1];
@@ -398,7 +400,7 @@ __global__ void __launch_bounds__(kPlanThreads) extend_kernel(const kpool_page_p
         const int rank = block_exclusive(take, scratch, &total);
         if (i < n) {
             l.a[i] = static_cast<int>(min(need + rank, static_cast<int64_t>(INT_MAX)));
-            l.b[i] = had;
+            l.b[i] = to;
             l.c[i] = take;
             begin[i] = len;
         }
@@ -417,14 +419,14 @@ __global__ void __launch_bounds__(kPlanThreads) extend_kernel(const kpool_page_p
         const int lane = threadIdx.x & 31;
         for (int i = threadIdx.x >> 5; i < n; i += blockDim.x >> 5) {
             const int s = seqs[i], take = l.c[i];
-            int32_t *row = p.page_table + static_cast<int64_t>(s) * p.max_pages + l.b[i];
+            int32_t *row = p.page_table + static_cast<int64_t>(s) * p.max_pages + ceil_div(begin[i], ps);
             for (int j = lane; j < take; j += 32) {
                 const int k = l.a[i] + j;
                 const int page = k < blockDim.x ? top[k] : p.free_list[fc - 1 - k];
                 row[j] = page;
                 p.ref_count[page] = 1;
             }
-            if (lane == 0) p.seq_lens[s] = begin[i] + n_new[i];
+            if (lane == 0) p.seq_lens[s] = l.b[i];
         }
     } else {
         for (int i = threadIdx.x; i < n; i += blockDim.x) begin[i] = -1;

@@ -136,3 +136,18 @@ def test_the_binding_imports_without_cuda_in_torch(b, monkeypatch):
     cu, total = module.kpool_num_pools([0, 5, 13], 13, 4)
     assert cu.tolist() == [0, 1, 3] and total == 3
     assert module.kpool_pages_workspace_size(4, 4, 32) == b.kpool_pages_workspace_size(4, 4, 32) > 0
+
+
+@pytest.mark.parametrize("array, size", [("page_table", 32), ("seq_lens", 4), ("ref_count", 32), ("free_list", 32),
+                                         ("free_count", 1)])
+def test_an_output_in_the_pool_is_refused(b, array, size):
+    """begin_out on the last entry of each of the pool's arrays, and across the first."""
+    L = b._lib
+    keep, a = _fake()
+    at = {name: a + 4096 * (k + 1) for k, name in enumerate(("page_table", "seq_lens", "ref_count", "free_list",
+                                                             "free_count"))}
+    ws, lists = a + 65536, P(a + 32768)
+    for out in (at[array] + 4 * (size - 1), at[array] - 4):
+        rc = L.kpool_pages_extend(_pool(b, a, **at), lists, lists, 2, P(out), P(ws), 1 << 16, None)
+        assert rc == -1 and b"overlaps the pool" in L.kpool_last_error()
+    del keep

@@ -718,3 +718,17 @@ def test_fewer_rows_than_the_offsets_count(K, there):
             want = BAD                             # (sequence 2 has room for five)
         b.host.write([2, 0], [0, 0], [min(c, there) for c in cu], rows, 0)
         b.check(want, (there, cu))
+
+
+def test_growing_by_the_lengths_themselves(K):
+    """n_new is seq_lens: each sequence grows by what another one holds."""
+    n = 200
+    b = Both(K, n_seqs=n, n_pages=1400, max_pages=12, page_size=8, layers=1)
+    b.ws = torch.empty(K.kpool_pages_workspace_size(n, n, 1400), dtype=torch.uint8, device="cuda")
+    seqs = b.rng.permutation(n).tolist()
+    b.extend(list(range(n)), b.rng.randint(0, 25, n).tolist())
+    for _ in range(2):
+        more = b.host.lens.tolist()
+        begin = K.kpool_pages_extend(b.gpu, b.i32(seqs), b.gpu.seq_lens, workspace=b.ws)
+        assert b.host.extend(seqs, more) == (0, begin.tolist())
+        b.check(0)
