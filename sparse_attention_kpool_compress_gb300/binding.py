@@ -855,8 +855,10 @@ def kpool_indexer_forward_host(q, k, gate, ape, w, kpool: int, index_topk: int,
 
 
 def kpool_read_status(workspace) -> int:
+    """Status word of the last call that used `workspace` (waits for its device)."""
     v = ctypes.c_int(0)
-    _check(_lib.kpool_read_status(_ptr(workspace), ctypes.byref(v)), "kpool_read_status")
+    with torch.cuda.device(-1 if workspace is None else workspace.get_device()):
+        _check(_lib.kpool_read_status(_ptr(workspace), ctypes.byref(v)), "kpool_read_status")
     return int(v.value)
 
 

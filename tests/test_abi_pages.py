@@ -151,3 +151,35 @@ def test_an_output_in_the_pool_is_refused(b, array, size):
         rc = L.kpool_pages_extend(_pool(b, a, **at), lists, lists, 2, P(out), P(ws), 1 << 16, None)
         assert rc == -1 and b"overlaps the pool" in L.kpool_last_error()
     del keep
+
+
+def test_a_status_is_read_on_the_device_of_its_workspace(b, monkeypatch):
+    """The read waits for the current device: that has to be the workspace's, as in the calls themselves."""
+    current, read = [0], []
+
+    class Device:
+        def __init__(self, device):
+            self.index = device
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.index
+
+        def __exit__(self, *_):
+            current[0] = self.before
+
+    class Lib:
+        def kpool_read_status(self, workspace, out):
+            read.append((current[0], workspace.value))
+            return 0
+
+    class Workspace:
+        def get_device(self):
+            return 3
+
+        def data_ptr(self):
+            return 4096
+
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(b, "_lib", Lib())
+    assert b.kpool_read_status(Workspace()) == 0
+    assert read == [(3, 4096)] and current == [0]
