@@ -683,7 +683,8 @@ def _pool_call(pages, workspace, n, name, fn, *args):
     _call(index, name, fn, *args, ws, size)
     if workspace is None:
         # a list with repetitions: how it went is told where the pool's calls tell it
-        pages.workspace[:16].copy_(keep[:16])
+        with torch.inference_mode():               # (the pool may have been made in it)
+            pages.workspace[:16].copy_(keep[:16])
 
 
 def kpool_pages_fork(pages: KPoolPages, parents, children, stores=(), workspace=None):

@@ -732,3 +732,21 @@ def test_growing_by_the_lengths_themselves(K):
         begin = K.kpool_pages_extend(b.gpu, b.i32(seqs), b.gpu.seq_lens, workspace=b.ws)
         assert b.host.extend(seqs, more) == (0, begin.tolist())
         b.check(0)
+
+
+def test_a_pool_made_in_inference_mode(K):
+    """Used in it and behind it, with a list longer than the pool among the calls."""
+    i = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    with torch.inference_mode():
+        p = K.kpool_pages_new(3, 6, 4, 8)
+        K.kpool_pages_extend(p, i([0]), i([9]))
+    store = torch.zeros(6, 8, 16, dtype=torch.uint8, device="cuda")
+    K.kpool_pages_fork(p, i([0]), i([1]), store)
+    assert K.kpool_read_status(p.workspace) == 0
+    K.kpool_pages_free(p, i([0] * 7))
+    assert K.kpool_read_status(p.workspace) == BAD
+    with torch.inference_mode():
+        K.kpool_pages_free(p, i([1, 0] * 4))
+        assert K.kpool_read_status(p.workspace) == BAD
+        K.kpool_pages_free(p, i([1, 0]))
+    assert K.kpool_read_status(p.workspace) == 0 and p.free_count.item() == 6
