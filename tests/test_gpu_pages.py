@@ -750,3 +750,13 @@ def test_a_pool_made_in_inference_mode(K):
         assert K.kpool_read_status(p.workspace) == BAD
         K.kpool_pages_free(p, i([1, 0]))
     assert K.kpool_read_status(p.workspace) == 0 and p.free_count.item() == 6
+
+
+@pytest.mark.parametrize("rows", [1, 32, 33, 65, 97, 129, 161, 193, 225, 256])
+def test_writes_of_one_to_eight_blocks(K, rows):
+    """A single layer, 32 rows to a block of the cluster."""
+    b = Both(K, n_seqs=4, n_pages=80, max_pages=40, page_size=8, layers=1)
+    b.extend([3, 1], [rows, 3])
+    b.write([3, 1], [0, 1], [0, rows // 2, rows // 2 + 2] if rows > 3 else [0, rows, rows])
+    b.write([3, 1], [0, 3], [0, rows - 1, rows], want=BAD)
+    b.write([3], [0], [0, rows])
