@@ -23,9 +23,9 @@
 //
 // Bound: contents by HBM (each byte read and written once, 16-byte accesses,
 // four in flight per thread: copying 300 pages of four layers moves its 167 MB in
-// 23 us, 7.1 TB/s with what the L2 holds); small calls by their launches and a
-// handful of dependent loads (copy 2.4 us, fork 4.8, extend and write 6.6, free and
-// compact 11.2, in a graph).
+// 25 us alone, 6.7 TB/s, and in 30 in a graph of such calls); small calls by their
+// launches and a handful of dependent loads (in a graph copy takes 2.5 us, fork 5.7,
+// extend and write 7.0, free and compact 11.3).
 #include <algorithm>
 #include <climits>
 
@@ -199,7 +199,7 @@ __device__ void copy_pages(const Stores &st, const int *src, const int *dst, con
 // with a hash table in shared memory (about a microsecond each, side by side) and
 // so agree without a plan in front.  Against plan and apply, with a host that
 // allocates no marks: 5 pages 27 -> 17 us a call (3.5 -> 2.4 in a graph), 300 pages
-// of four layers 35 -> 34 (31 -> 30).
+// of four layers 35 -> 34 (31 -> 30 in a graph).
 __global__ void __launch_bounds__(kApplyThreads) copy_fused(const __grid_constant__ Stores st, const int32_t *src,
                                                             const int32_t *dst, int n, int n_pages, int *ws)
 {

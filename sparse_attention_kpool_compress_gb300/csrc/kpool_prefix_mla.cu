@@ -16,8 +16,8 @@
 //   attend    one CTA pair per piece of a unit, persistent: unnormalised
 //             softmax with a running maximum, FP32 partial rows and their
 //             log-sum-exp to the workspace.
-//   combine   one or four warps per row join its pieces, the shared ones and its
-//             own.
+//   combine   a block per row where rows are few, a warp per row otherwise: joins a
+//             row's pieces, the shared ones and its own.
 //
 // attend, per CTA pair.  The output of 128 rows x 512 columns fills all of one
 // SM's tensor memory, so two SMs share it: tcgen05.mma with cta_group::2,
@@ -26,9 +26,8 @@
 //   O  [64 x 512]  256 columns of tensor memory, and
 //   S  [64 x 256]  128 columns, twice, so that the scores of the next tile run
 //                  while the softmax works on this one.
-// Both products take N = 256, at which the pair form runs at full rate (66.7
-// cycles per 128 x 256 x 16 MMA measured, M = 128 N = 256; N = 128 takes the
-// same time).  Operand B is split: for the scores each CTA brings 128 of the
+// Both products take N = 256, at which the pair form runs at full rate (64
+// cycles per 128 x 256 x 16 MMA measured; N = 128 takes 49, for half the work).  Operand B is split: for the scores each CTA brings 128 of the
 // tile's 256 tokens (K-major), for the output 256 of the 512 latent columns of
 // all its tokens (MN-major).  Each product has a ring of four 16 KB chunks, each
 // feeding four MMAs.  (Keeping the quarter of a tile that both products use would
@@ -47,7 +46,7 @@
 //                of the issuer, while the softmax works: in the issuer's own loop
 //                the first and last chunks of a short span took 2 us: 16 samples
 //                over 8191 shared tokens 34.0 -> 32.7 us a call, 64 queries each
-//                over 8192 of their own 195 -> 183.)
+//                over 8192 of their own 195 -> 184.)
 // All loads and arrivals meet on CTA 0's barriers, where the issuers wait.  P
 // passes in four parts of 64 tokens, so that the output of a tile's first part
 // begins while the last one is exponentiated, and the next tile's P is written
@@ -1030,9 +1029,14 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 }
 
 // A block per row, a piece per warp at a time, then a sum over the warps: for few
-// rows, whose pieces may be many and are then all on their way at once (one
-// sequence of 131072 tokens, 74 pieces a row: 78 -> 52 us in all; 256 rows of two
-// pieces: 20.8 -> 21.3; 1680 rows of four: 33 -> 37, so only up to kBlockRows).
+// rows, whose pieces may be many and are then all on their way at once.  With many
+// rows the blocks do not fit at once, and rows have few pieces.  A call of 64 heads in
+// a graph, in us, this form against a warp per row:
+//   shared tokens   64 rows      256 rows     512 rows      1024 rows     2048 rows
+//   203             18.2 / 18.0  19.2 / 19.5  19.2 / 19.4   23.4 / 21.0   32.5 / 24.7
+//   8191            21.8 / 30.8  23.2 / 27.4  25.0 / 28.6   32.1 / 32.0   48.0 / 42.2
+//   131072          48.4 / 72.6  62.0 / 74.6  109.3 / 116.6 195 / 197     400 / 395
+// so up to kBlockRows rows, whatever the pieces.
 __global__ void __launch_bounds__(256) combine_block_kernel(const Params p)
 {
     constexpr int kWarps = 8;
