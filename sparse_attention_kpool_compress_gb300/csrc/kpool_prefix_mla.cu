@@ -27,12 +27,13 @@
 //   S  [64 x 256]  128 columns, twice, so that the scores of the next tile run
 //                  while the softmax works on this one.
 // Both products take N = 256, at which the pair form runs at full rate (64
-// cycles per 128 x 256 x 16 MMA measured; N = 128 takes 49, for half the work).  Operand B is split: for the scores each CTA brings 128 of the
-// tile's 256 tokens (K-major), for the output 256 of the 512 latent columns of
-// all its tokens (MN-major).  Each product has a ring of four 16 KB chunks, each
-// feeding four MMAs.  (Keeping the quarter of a tile that both products use would
-// need 64 KB that the 64 KB of queries, the 32 KB of P and the rings leave no
-// room for.)
+// cycles per 128 x 256 x 16 MMA measured; N = 128 takes 49, for half the work).
+// Operand B is split: for the scores each CTA brings 128 of the tile's 256
+// tokens (K-major), for the output 256 of the 512 latent columns of all its
+// tokens (MN-major).  Each product has a ring of four 16 KB chunks, each
+// feeding four MMAs.  (Keeping the quarter of a tile that both products use
+// would need 64 KB that the 64 KB of queries, the 32 KB of P and the rings
+// leave no room for.)
 //   warp 0       TMA producer of queries and scores chunks
 //   warp 1       issuer of the scores' MMAs (CTA 0)
 //   warp 2       issuer of the output's MMAs (CTA 0).  Two issuers, because one
