@@ -458,6 +458,57 @@ KPOOL_API int kpool_sparse_mla_fwd_pools_at(const void *q, const void *kv, const
                                             kpool_stream_t stream);
 
 /*
+ * Backward pass of the sparse attention: the gradients of the queries and of
+ * the latent rows, from those of o and lse, over the same lists J(t) (the
+ * probabilities are computed again from lse, nothing else is kept):
+ *     p_j     = exp(softmax_scale * q[t, h, :] . kv[j, :] - lse[t, h])
+ *     delta   = sum_d d_o[t, h, d] * o[t, h, d] - d_lse[t, h]
+ *     ds_j    = softmax_scale * p_j * (d_o[t, h, :] . kv[j, :] - delta)
+ *     dq[t, h, :] = sum_j ds_j kv[j, :]                              (BF16 out)
+ *     dkv[j, :]   = sum_{t, h: j in J(t)} ds_j q[t, h, :] + p_j d_o[t, h, :]
+ *                                                                    (BF16 out)
+ * A token that a row lists twice counts twice; a row with no token (lse = -inf)
+ * gets dq = 0; a latent row that nobody lists gets dkv = 0.  Arithmetic: FP32
+ * accumulation; p and ds are rounded to BF16 before they multiply the rows.
+ * The sums of dkv over queries are FP32 atomic additions, in an order that
+ * varies: the same call twice may differ by what FP32 sums in another order
+ * differ by (seen after the rounding to BF16 as an occasional last bit).
+ *   q, kv, tok_idx / pool_idx, ...   as the forward call was given them
+ *   o, lse       what the forward call wrote
+ *   d_o          bf16 [T, H, Dc], 16-byte aligned: gradient of o
+ *   d_lse        NULL (none), or fp32 [T, H]: gradient of lse
+ *   dq_out       bf16 [T, H, Dc];  dkv_out  bf16 [Tk, Dc]: overwritten, apart
+ *                from the inputs; 16-byte aligned
+ *   workspace    >= kpool_sparse_mla_bwd_workspace_size(T, Tk) bytes (the FP32
+ *                sums of dkv and some words), 256-byte aligned; its status
+ *                word (kpool_read_status) reports a pipeline timeout
+ * Supported shapes as the forward calls.  The three calls list tokens as
+ * kpool_sparse_mla_fwd, _pools and _pools_at do (Tk = T for _pools).
+ */
+KPOOL_API size_t kpool_sparse_mla_bwd_workspace_size(int64_t T, int64_t Tk);
+KPOOL_API int kpool_sparse_mla_bwd(const void *q, const void *kv, const int32_t *tok_idx, const void *o,
+                                   const float *lse, const void *d_o, const float *d_lse, int64_t T,
+                                   int64_t Tk, int W, int H, int Dc, float softmax_scale, void *dq_out,
+                                   void *dkv_out, void *workspace, size_t workspace_bytes,
+                                   kpool_stream_t stream);
+KPOOL_API int kpool_sparse_mla_bwd_pools(const void *q, const void *kv, const int32_t *pool_idx,
+                                         const int32_t *cu_seqlens, const int32_t *cu_pools, int n_docs,
+                                         const void *o, const float *lse, const void *d_o,
+                                         const float *d_lse, int64_t T, int H, int Dc, int kpool,
+                                         int index_topk, int always_select_tail, float softmax_scale,
+                                         void *dq_out, void *dkv_out, void *workspace,
+                                         size_t workspace_bytes, kpool_stream_t stream);
+KPOOL_API int kpool_sparse_mla_bwd_pools_at(const void *q, const void *kv, const int32_t *pool_idx,
+                                            const int32_t *cu_seqlens_q, const int32_t *q_start_pos,
+                                            const int32_t *cu_seqlens_k, const int32_t *cu_pools,
+                                            int n_docs, const void *o, const float *lse, const void *d_o,
+                                            const float *d_lse, int64_t Tq, int64_t Tk, int H, int Dc,
+                                            int kpool, int index_topk, int always_select_tail,
+                                            float softmax_scale, void *dq_out, void *dkv_out,
+                                            void *workspace, size_t workspace_bytes,
+                                            kpool_stream_t stream);
+
+/*
  * Paged cache.  A store keeps the cached rows of tokens in pages; sequences
  * list their pages, and sequences forked from one parent list the same whole
  * pages.  (The pages have no counterpart in the sources: a rollout, as in
@@ -630,6 +681,49 @@ KPOOL_API int kpool_shared_prefix_mla_fwd(
     void *o_out, float *lse_out, void *workspace, size_t workspace_bytes, kpool_stream_t stream);
 
 /*
+ * kpool_sparse_mla_fwd_pools_paged -- the sparse attention of a chunk of new
+ * tokens over a paged cache: kpool_sparse_mla_fwd_pools_at with the latent rows
+ * read through page tables.  Sequence b of the batch has the query rows
+ * cu_seqlens_q[b] .. cu_seqlens_q[b+1] - 1 (any number: one to decode, a few
+ * drafted ones, a piece of a prompt); its i-th query is at position
+ * q_start_pos[b] + i, below the sequence's length (the new tokens are in the
+ * cache already: q_start_pos is what kpool_pages_extend returned).  J(t) is the
+ * row's first min(n_c, Kp) pools and its causal tail, as there, pool p of
+ * sequence b being its tokens (p - cu_pools[b]) * kpool + s.
+ *   q            bf16 [Tq, H, Dc], 16-byte aligned
+ *   kv           bf16 [n_pages, page_size, Dc], pages kv_page_stride elements
+ *                apart (a multiple of 8, >= page_size * Dc, < 2^34); 16-byte
+ *                aligned.  Any page_size >= 1
+ *   page_table   int32 [n_rows, max_pages], seq_lens int32 [n_rows], as in
+ *                kpool_page_pool
+ *   seq_ids      int32 [B]: the table row of each sequence of the batch, or
+ *                NULL for rows 0 .. B - 1 (then n_rows >= B)
+ *   pool_idx     int32 [Tq, index_topk / kpool], as kpool_score_topk_at writes it
+ *   cu_pools     int32 [B + 1]: the pools of sequence b are numbered
+ *                cu_pools[b] .. cu_pools[b+1] - 1 (others are skipped)
+ *   o_out, lse_out   as kpool_sparse_mla_fwd
+ *   workspace    kpool_sparse_mla_paged_workspace_size(Tq, kpool, index_topk)
+ *                bytes, 256-byte aligned
+ * Latent rows that are listed must be finite; no other row is read.
+ * Device status: KPOOL_STATUS_BAD_SEQLENS when cu_seqlens_q is not 0 .. Tq
+ * non-decreasing; KPOOL_STATUS_BAD_PAGE when a table row, length, position or
+ * page id that the call uses is out of range (such tokens are skipped, a length
+ * is cut to its table's room, a position to the length; results of those rows
+ * are not valid); KPOOL_STATUS_TIMEOUT as for kpool_sparse_mla_fwd.
+ * Supported: H = 64, Dc = 512 (UNSUPPORTED otherwise), 1 <= kpool <= 64;
+ * softmax_scale finite and > 0; B up to 2^24.  Calls that may overlap need
+ * workspaces of their own.
+ */
+KPOOL_API size_t kpool_sparse_mla_paged_workspace_size(int64_t Tq, int kpool, int index_topk);
+KPOOL_API int kpool_sparse_mla_fwd_pools_paged(
+    const void *q, const void *kv, int64_t kv_page_stride, int n_pages, int page_size,
+    const int32_t *page_table, const int32_t *seq_lens, int n_rows, int max_pages,
+    const int32_t *seq_ids, const int32_t *pool_idx, const int32_t *cu_seqlens_q,
+    const int32_t *q_start_pos, const int32_t *cu_pools, int B, int64_t Tq, int H, int Dc, int kpool,
+    int index_topk, int always_select_tail, float softmax_scale, void *o_out, float *lse_out,
+    void *workspace, size_t workspace_bytes, kpool_stream_t stream);
+
+/*
  * kpool_read_status -- debug helper: synchronously copy the device status
  * word of a workspace (KPOOL_STATUS_* bits, 0 = clean) to *status_out.
  * Synchronises the whole device.
@@ -639,7 +733,8 @@ KPOOL_API int kpool_read_status(const void *workspace, int *status_out);
 /*
  * kpool_debug_set_wait_limit_ns -- test entry: the time limit of each wait
  * inside the scoring kernel (kpool_score_topk, _at, _noalloc, _dense and the
- * host-buffer pass), the sparse attention (kpool_sparse_mla_*) and the
+ * host-buffer pass), the sparse attention (kpool_sparse_mla_*, its backward
+ * pass and its paged form among them) and the
  * shared-prefix attention (kpool_shared_prefix_mla_fwd) for launches made
  * after this call, process-wide; ns = 0
  * restores the default of 2 s.  Returns the previous limit.  A wait that

@@ -65,6 +65,18 @@ _SIGS = {
                                         ctypes.c_float, _P, _P, _P, _SZ, _P]),
     "kpool_sparse_mla_fwd_pools_at": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _L, _L, _I, _I, _I,
                                            _I, _I, ctypes.c_float, _P, _P, _P, _SZ, _P]),
+    "kpool_sparse_mla_bwd_workspace_size": (_SZ, [_L, _L]),
+    "kpool_sparse_mla_bwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _L, _L, _I, _I, _I, ctypes.c_float,
+                                  _P, _P, _P, _SZ, _P]),
+    "kpool_sparse_mla_bwd_pools": (_I, [_P, _P, _P, _P, _P, _I, _P, _P, _P, _P, _L, _I, _I, _I,
+                                        _I, _I, ctypes.c_float, _P, _P, _P, _SZ, _P]),
+    "kpool_sparse_mla_bwd_pools_at": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _P, _P, _P, _P, _L, _L,
+                                           _I, _I, _I, _I, _I, ctypes.c_float, _P, _P, _P, _SZ,
+                                           _P]),
+    "kpool_sparse_mla_paged_workspace_size": (_SZ, [_L, _I, _I]),
+    "kpool_sparse_mla_fwd_pools_paged": (_I, [_P, _P, _L, _I, _I, _P, _P, _I, _I, _P, _P, _P, _P,
+                                              _P, _I, _L, _I, _I, _I, _I, _I, ctypes.c_float, _P,
+                                              _P, _P, _SZ, _P]),
     "kpool_pages_workspace_size": (_SZ, [_L, _I, _I]),
     "kpool_pages_copy": (_I, [_P, _P, _L, _I, _P, _I, _P, _SZ, _P]),
     "kpool_pages_fork": (_I, [_P, _P, _P, _L, _P, _I, _P, _SZ, _P]),
@@ -801,6 +813,149 @@ def kpool_shared_prefix_mla_fwd(q, kv, page_table, seq_lens, cu_seqlens_q, cu_gr
     _call(index, "kpool_shared_prefix_mla_fwd", _lib.kpool_shared_prefix_mla_fwd, q.data_ptr(),
           kv.data_ptr(), stride[0] if n_pages > 1 else page_size * Dc, n_pages, page_size, *lists,
           Tq, H, Dc, float(softmax_scale), o.data_ptr(), lse.data_ptr(), ws, size)
+    return o, lse
+
+
+# ---- sparse attention: backward pass, paged form --------------------------------
+
+def _like(t, name, shape, dtype, index):
+    """A contiguous tensor of this shape on CUDA device `index`: `t`, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=_devices(index))
+    if not (t.shape == shape and t.dtype is dtype and t.get_device() == index and t.is_contiguous()):
+        _need(t, name, dtype)
+        _same_device(index, **{name: t})
+        raise ValueError("%s must be %s (got %s)" % (name, tuple(shape), tuple(t.shape)))
+    return t
+
+
+def _list_rows(t, name, T, width, index):
+    """Address of the lists int32 [T, width] (width None: any), and their width."""
+    if t.dim() != 2 or t.shape[0] != T or (width is not None and t.shape[1] != width):
+        raise ValueError("%s must be [%d, %s] (got %s)" % (name, T, "W" if width is None else width, tuple(t.shape)))
+    return _ints(t, name, t.numel(), index), t.shape[1]
+
+
+def kpool_sparse_mla_bwd_workspace_size(T: int, Tk: int) -> int:
+    return int(_lib.kpool_sparse_mla_bwd_workspace_size(T, Tk))
+
+
+def _mla_bwd(name, fn, q, kv, lists, o, lse, d_o, d_lse, sizes, softmax_scale, workspace, dq, dkv):
+    """fn(q, kv, *lists, o, lse, d_o, d_lse, *sizes, scale, dq, dkv, workspace) -> (dq, dkv);
+    `lists` and `sizes` are made of the device index, T and Tk."""
+    index, bf16 = _device_of(q, "q"), torch.bfloat16
+    if q.dim() != 3 or kv.dim() != 2 or kv.shape[1] != q.shape[2]:
+        raise ValueError("q must be [T, H, Dc] and kv [Tk, Dc] (got %s and %s)" % (tuple(q.shape), tuple(kv.shape)))
+    T, H, Dc = q.shape
+    for t, n, shape, dtype in ((q, "q", q.shape, bf16), (kv, "kv", kv.shape, bf16), (o, "o", q.shape, bf16),
+                               (lse, "lse", (T, H), torch.float32), (d_o, "d_o", q.shape, bf16)):
+        _like(t, n, shape, dtype, index)
+    if d_lse is not None:
+        _like(d_lse, "d_lse", (T, H), torch.float32, index)
+    Tk = kv.shape[0]
+    lists = lists(index, T)
+    dq, dkv = _like(dq, "dq", q.shape, bf16, index), _like(dkv, "dkv", kv.shape, bf16, index)
+    keep, ws, size = _bytes(workspace, 0 if workspace is not None else
+                            _lib.kpool_sparse_mla_bwd_workspace_size(T, Tk), index)
+    _call(index, name, fn, q.data_ptr(), kv.data_ptr(), *lists, o.data_ptr(), lse.data_ptr(), d_o.data_ptr(),
+          None if d_lse is None else d_lse.data_ptr(), *sizes(T, Tk, H, Dc), float(softmax_scale), dq.data_ptr(),
+          dkv.data_ptr(), ws, size)
+    return dq, dkv
+
+
+def kpool_sparse_mla_bwd(q, kv, tok_idx, o, lse, d_o, softmax_scale: float, d_lse=None, workspace=None, dq=None,
+                         dkv=None):
+    """Gradients of kpool_sparse_mla_fwd: from d_o bf16 [T, 64, 512] (and d_lse
+    fp32 [T, 64], if lse is used) and the o and lse that it wrote -> (dq bf16
+    [T, 64, 512], dkv bf16 [Tk, 512])."""
+    width = []
+
+    def lists(index, T):
+        at, w = _list_rows(tok_idx, "tok_idx", T, None, index)
+        width.append(w)
+        return (at,)
+
+    return _mla_bwd("kpool_sparse_mla_bwd", _lib.kpool_sparse_mla_bwd, q, kv, lists, o, lse, d_o, d_lse,
+                    lambda T, Tk, H, Dc: (T, Tk, width[0], H, Dc), softmax_scale, workspace, dq, dkv)
+
+
+def kpool_sparse_mla_bwd_pools(q, kv, pool_idx, o, lse, d_o, kpool: int, index_topk: int, softmax_scale: float,
+                               cu_seqlens=None, cu_pools=None, always_select_tail: bool = True, d_lse=None,
+                               workspace=None, dq=None, dkv=None):
+    """Gradients of kpool_sparse_mla_fwd_pools (kv [T, 512]) -> (dq, dkv)."""
+    if (cu_seqlens is None) != (cu_pools is None):
+        raise ValueError("cu_seqlens and cu_pools go together")
+    if kv.shape[0] != q.shape[0]:
+        raise ValueError("kv must have the %d rows of q (got %d)" % (q.shape[0], kv.shape[0]))
+    n_docs = 1 if cu_seqlens is None else cu_seqlens.numel() - 1
+
+    def lists(index, T):
+        return (_list_rows(pool_idx, "pool_idx", T, index_topk // kpool, index)[0],
+                None if cu_seqlens is None else _ints(cu_seqlens, "cu_seqlens", n_docs + 1, index),
+                None if cu_pools is None else _ints(cu_pools, "cu_pools", n_docs + 1, index), n_docs)
+
+    return _mla_bwd("kpool_sparse_mla_bwd_pools", _lib.kpool_sparse_mla_bwd_pools, q, kv, lists, o, lse, d_o, d_lse,
+                    lambda T, Tk, H, Dc: (T, H, Dc, kpool, index_topk, int(bool(always_select_tail))), softmax_scale,
+                    workspace, dq, dkv)
+
+
+def kpool_sparse_mla_bwd_pools_at(q, kv, pool_idx, o, lse, d_o, kpool: int, index_topk: int, softmax_scale: float,
+                                  cu_seqlens_q, q_start_pos, cu_seqlens_k, cu_pools, always_select_tail: bool = True,
+                                  d_lse=None, workspace=None, dq=None, dkv=None):
+    """Gradients of kpool_sparse_mla_fwd_pools_at (keys kv [Tk, 512]) -> (dq, dkv)."""
+    n_docs = cu_seqlens_q.numel() - 1
+
+    def lists(index, T):
+        return (_list_rows(pool_idx, "pool_idx", T, index_topk // kpool, index)[0],
+                _ints(cu_seqlens_q, "cu_seqlens_q", n_docs + 1, index),
+                _ints(q_start_pos, "q_start_pos", n_docs, index), _ints(cu_seqlens_k, "cu_seqlens_k", n_docs + 1, index),
+                _ints(cu_pools, "cu_pools", n_docs + 1, index), n_docs)
+
+    return _mla_bwd("kpool_sparse_mla_bwd_pools_at", _lib.kpool_sparse_mla_bwd_pools_at, q, kv, lists, o, lse, d_o,
+                    d_lse, lambda T, Tk, H, Dc: (T, Tk, H, Dc, kpool, index_topk, int(bool(always_select_tail))),
+                    softmax_scale, workspace, dq, dkv)
+
+
+def kpool_sparse_mla_paged_workspace_size(Tq: int, kpool: int, index_topk: int) -> int:
+    return int(_lib.kpool_sparse_mla_paged_workspace_size(Tq, kpool, index_topk))
+
+
+def kpool_sparse_mla_fwd_pools_paged(q, kv, page_table, seq_lens, pool_idx, kpool: int, index_topk: int,
+                                     softmax_scale: float, cu_seqlens_q, q_start_pos, cu_pools, seq_ids=None,
+                                     always_select_tail: bool = True, workspace=None, o=None, lse=None):
+    """kpool_sparse_mla_fwd_pools_at over a paged cache: kv bf16 [n_pages,
+    page_size, 512] (one layer of a store), page_table and seq_lens as in
+    KPoolPages -> (o bf16 [Tq, 64, 512], lse fp32 [Tq, 64]).  q_start_pos is
+    what kpool_pages_extend returned for the new tokens."""
+    index, bf16 = _device_of(q, "q"), torch.bfloat16
+    if kv.dtype is not bf16:
+        raise TypeError("kv must be %s (got %s)" % (bf16, kv.dtype))
+    if q.dim() != 3 or kv.dim() != 3 or kv.shape[2] != q.shape[2]:
+        raise ValueError("q must be [Tq, H, Dc] and kv [n_pages, page_size, Dc] (got %s and %s)"
+                         % (tuple(q.shape), tuple(kv.shape)))
+    Tq, H, Dc = q.shape
+    n_pages, page_size, _ = kv.shape
+    stride = kv.stride()
+    if kv.get_device() != index or stride[2] != 1 or (stride[1] != Dc and page_size > 1):
+        _same_device(index, kv=kv)
+        raise ValueError("the rows of a page of kv must be contiguous")
+    _like(q, "q", q.shape, bf16, index)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [n_rows, max_pages]")
+    n_rows, max_pages = page_table.shape
+    B = cu_seqlens_q.numel() - 1
+    lists = (_ints(page_table, "page_table", n_rows * max_pages, index), _ints(seq_lens, "seq_lens", n_rows, index),
+             n_rows, max_pages, None if seq_ids is None else _ints(seq_ids, "seq_ids", B, index),
+             _list_rows(pool_idx, "pool_idx", Tq, index_topk // kpool, index)[0],
+             _ints(cu_seqlens_q, "cu_seqlens_q", B + 1, index), _ints(q_start_pos, "q_start_pos", B, index),
+             _ints(cu_pools, "cu_pools", B + 1, index), B)
+    o, lse = _like(o, "o", q.shape, bf16, index), _like(lse, "lse", (Tq, H), torch.float32, index)
+    keep, ws, size = _bytes(workspace, 0 if workspace is not None else
+                            _lib.kpool_sparse_mla_paged_workspace_size(Tq, kpool, index_topk), index)
+    # (the stride of a single page says nothing)
+    _call(index, "kpool_sparse_mla_fwd_pools_paged", _lib.kpool_sparse_mla_fwd_pools_paged, q.data_ptr(),
+          kv.data_ptr(), stride[0] if n_pages > 1 else page_size * Dc, n_pages, page_size, *lists, Tq, H, Dc, kpool,
+          index_topk, int(bool(always_select_tail)), float(softmax_scale), o.data_ptr(), lse.data_ptr(), ws, size)
     return o, lse
 
 

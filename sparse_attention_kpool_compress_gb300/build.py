@@ -14,8 +14,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libkpool.so")
 SOURCES = ["kpool_api.cu", "kpool_compress.cu", "kpool_expand.cu", "kpool_score.cu",
            "kpool_pipeline.cu", "kpool_project.cu", "kpool_mla.cu", "kpool_pages.cu",
-           "kpool_prefix_mla.cu"]
-HEADERS = ["kpool_internal.h", "kpool_ptx.cuh"]
+           "kpool_prefix_mla.cu", "kpool_mla_bwd.cu", "kpool_paged_mla.cu"]
+HEADERS = ["kpool_internal.h", "kpool_mla_rows.cuh", "kpool_ptx.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr"]

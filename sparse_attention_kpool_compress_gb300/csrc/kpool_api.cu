@@ -105,6 +105,33 @@ int check_mla_args(const void *q, const void *kv, int64_t T, int64_t Tk, int H, 
     return KPOOL_OK;
 }
 
+// What the backward calls add to the forward calls' arguments (o and lse are
+// checked there, as its outputs).
+int check_mla_grad(const void *d_o, const float *d_lse, int64_t T, int64_t Tk, const void *dq_out,
+                   const void *dkv_out, const void *workspace, size_t workspace_bytes)
+{
+    if (T > 0 && (!d_o || !dq_out)) return fail(KPOOL_ERR_INVALID_ARG, "d_o and dq_out are required");
+    if (Tk > 0 && !dkv_out) return fail(KPOOL_ERR_INVALID_ARG, "dkv_out is required");
+    if (!aligned(d_o, 16) || !aligned(dq_out, 16) || !aligned(dkv_out, 16) || !aligned(d_lse, 4))
+        return fail(KPOOL_ERR_INVALID_ARG, "d_o, dq_out and dkv_out must be 16-byte aligned");
+    const size_t need = sparse_mla_bwd_workspace_bytes(T, Tk);
+    if (!workspace || workspace_bytes < need || !aligned(workspace, 256))
+        return fail(KPOOL_ERR_WORKSPACE, "workspace of at least %zu bytes, 256-byte aligned, needed", need);
+    return KPOOL_OK;
+}
+
+// The selection's sizes.
+int check_selection(int64_t T, int kpool, int index_topk, const int32_t *pool_idx)
+{
+    int rc = check_common(T, kpool);
+    if (rc) return rc;
+    if (index_topk < 1 || index_topk % kpool != 0)
+        return fail(KPOOL_ERR_INVALID_ARG, "index_topk must be a positive multiple of kpool");
+    if (T > 0 && !pool_idx) return fail(KPOOL_ERR_INVALID_ARG, "pool_idx is required");
+    if (!aligned(pool_idx, 4)) return fail(KPOOL_ERR_INVALID_ARG, "pool_idx must be 4-byte aligned");
+    return KPOOL_OK;
+}
+
 // ---- paged cache -----------------------------------------------------------
 int check_pool(const kpool_page_pool *p)
 {
@@ -781,6 +808,133 @@ int kpool_sparse_mla_fwd_pools_at(const void *q, const void *kv, const int32_t *
     a.kpool = kpool; a.Kp = index_topk / kpool; a.tail = always_select_tail ? 1 : 0;
     a.scale = softmax_scale; a.o = o_out; a.lse = lse_out; a.workspace = workspace;
     return run_sparse_mla(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t kpool_sparse_mla_bwd_workspace_size(int64_t T, int64_t Tk)
+{
+    if (T < 0 || T > 0x7FFFFFFFLL || Tk < 0 || Tk > 0x7FFFFFFFLL) return 0;
+    return sparse_mla_bwd_workspace_bytes(T, Tk);
+}
+
+int kpool_sparse_mla_bwd(const void *q, const void *kv, const int32_t *tok_idx, const void *o, const float *lse,
+                         const void *d_o, const float *d_lse, int64_t T, int64_t Tk, int W, int H, int Dc,
+                         float softmax_scale, void *dq_out, void *dkv_out, void *workspace, size_t workspace_bytes,
+                         kpool_stream_t stream)
+{
+    clear_error();
+    KPOOL_NVTX_RANGE("kpool_sparse_mla_bwd");
+    int rc = check_mla_args(q, kv, T, Tk, H, Dc, softmax_scale, o, lse, workspace, workspace_bytes);
+    if (rc) return rc;
+    if ((rc = check_mla_grad(d_o, d_lse, T, Tk, dq_out, dkv_out, workspace, workspace_bytes))) return rc;
+    if (W < 0 || W > (1 << 20)) return fail(KPOOL_ERR_INVALID_ARG, "W out of range");
+    if (T > 0 && W > 0 && !tok_idx) return fail(KPOOL_ERR_INVALID_ARG, "tok_idx is required");
+    if (!aligned(tok_idx, 4)) return fail(KPOOL_ERR_INVALID_ARG, "tok_idx must be 4-byte aligned");
+    SparseMlaArgs a{};
+    a.q = q; a.kv = kv; a.tok_idx = tok_idx; a.T = T; a.Tk = Tk; a.W = W; a.n_docs = 1;
+    a.kpool = 1; a.scale = softmax_scale; a.o = const_cast<void *>(o); a.lse = const_cast<float *>(lse);
+    a.workspace = workspace;
+    // (a row of width 0 is never read)
+    if (W == 0) a.tok_idx = static_cast<const int32_t *>(workspace);
+    const SparseMlaGrad g{d_o, d_lse, dq_out, dkv_out};
+    return run_sparse_mla_bwd(a, g, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int kpool_sparse_mla_bwd_pools(const void *q, const void *kv, const int32_t *pool_idx, const int32_t *cu_seqlens,
+                               const int32_t *cu_pools, int n_docs, const void *o, const float *lse, const void *d_o,
+                               const float *d_lse, int64_t T, int H, int Dc, int kpool, int index_topk,
+                               int always_select_tail, float softmax_scale, void *dq_out, void *dkv_out,
+                               void *workspace, size_t workspace_bytes, kpool_stream_t stream)
+{
+    clear_error();
+    KPOOL_NVTX_RANGE("kpool_sparse_mla_bwd_pools");
+    int rc = check_mla_args(q, kv, T, T, H, Dc, softmax_scale, o, lse, workspace, workspace_bytes);
+    if (rc) return rc;
+    if ((rc = check_mla_grad(d_o, d_lse, T, T, dq_out, dkv_out, workspace, workspace_bytes))) return rc;
+    if ((rc = check_selection(T, kpool, index_topk, pool_idx))) return rc;
+    if ((rc = check_docs(cu_seqlens, cu_pools, n_docs, T, kpool, -1))) return rc;
+    SparseMlaArgs a{};
+    a.q = q; a.kv = kv; a.pool_idx = pool_idx; a.cu_seqlens = cu_seqlens; a.cu_pools = cu_pools;
+    a.n_docs = n_docs; a.T = T; a.Tk = T; a.kpool = kpool; a.Kp = index_topk / kpool;
+    a.tail = always_select_tail ? 1 : 0; a.scale = softmax_scale; a.o = const_cast<void *>(o);
+    a.lse = const_cast<float *>(lse); a.workspace = workspace;
+    const SparseMlaGrad g{d_o, d_lse, dq_out, dkv_out};
+    return run_sparse_mla_bwd(a, g, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int kpool_sparse_mla_bwd_pools_at(const void *q, const void *kv, const int32_t *pool_idx,
+                                  const int32_t *cu_seqlens_q, const int32_t *q_start_pos,
+                                  const int32_t *cu_seqlens_k, const int32_t *cu_pools, int n_docs, const void *o,
+                                  const float *lse, const void *d_o, const float *d_lse, int64_t Tq, int64_t Tk, int H,
+                                  int Dc, int kpool, int index_topk, int always_select_tail, float softmax_scale,
+                                  void *dq_out, void *dkv_out, void *workspace, size_t workspace_bytes,
+                                  kpool_stream_t stream)
+{
+    clear_error();
+    KPOOL_NVTX_RANGE("kpool_sparse_mla_bwd_pools_at");
+    int rc = check_mla_args(q, kv, Tq, Tk, H, Dc, softmax_scale, o, lse, workspace, workspace_bytes);
+    if (rc) return rc;
+    if ((rc = check_mla_grad(d_o, d_lse, Tq, Tk, dq_out, dkv_out, workspace, workspace_bytes))) return rc;
+    if ((rc = check_selection(Tq, kpool, index_topk, pool_idx))) return rc;
+    if (!cu_seqlens_q || !q_start_pos || !cu_seqlens_k || !cu_pools)
+        return fail(KPOOL_ERR_INVALID_ARG,
+                    "cu_seqlens_q, q_start_pos, cu_seqlens_k and cu_pools are required");
+    if (n_docs < 1) return fail(KPOOL_ERR_INVALID_ARG, "n_docs must be >= 1");
+    if (!aligned(cu_seqlens_q, 4) || !aligned(q_start_pos, 4) || !aligned(cu_seqlens_k, 4) || !aligned(cu_pools, 4))
+        return fail(KPOOL_ERR_INVALID_ARG, "index arrays must be 4-byte aligned");
+    SparseMlaArgs a{};
+    a.q = q; a.kv = kv; a.pool_idx = pool_idx; a.cu_seqlens = cu_seqlens_q; a.q_pos = q_start_pos;
+    a.cu_k = cu_seqlens_k; a.cu_pools = cu_pools; a.n_docs = n_docs; a.T = Tq; a.Tk = Tk;
+    a.kpool = kpool; a.Kp = index_topk / kpool; a.tail = always_select_tail ? 1 : 0;
+    a.scale = softmax_scale; a.o = const_cast<void *>(o); a.lse = const_cast<float *>(lse); a.workspace = workspace;
+    const SparseMlaGrad g{d_o, d_lse, dq_out, dkv_out};
+    return run_sparse_mla_bwd(a, g, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t kpool_sparse_mla_paged_workspace_size(int64_t Tq, int kpool, int index_topk)
+{
+    if (Tq < 0 || Tq > 0x7FFFFFFFLL || kpool < 1 || kpool > 64 || index_topk < 1 || index_topk % kpool != 0) return 0;
+    return paged_mla_workspace_bytes(Tq, index_topk / kpool, kpool);
+}
+
+int kpool_sparse_mla_fwd_pools_paged(const void *q, const void *kv, int64_t kv_page_stride, int n_pages, int page_size,
+                                     const int32_t *page_table, const int32_t *seq_lens, int n_rows, int max_pages,
+                                     const int32_t *seq_ids, const int32_t *pool_idx, const int32_t *cu_seqlens_q,
+                                     const int32_t *q_start_pos, const int32_t *cu_pools, int B, int64_t Tq, int H,
+                                     int Dc, int kpool, int index_topk, int always_select_tail, float softmax_scale,
+                                     void *o_out, float *lse_out, void *workspace, size_t workspace_bytes,
+                                     kpool_stream_t stream)
+{
+    clear_error();
+    KPOOL_NVTX_RANGE("kpool_sparse_mla_fwd_pools_paged");
+    int rc = check_mla_args(q, kv, Tq, 0, H, Dc, softmax_scale, o_out, lse_out, workspace, workspace_bytes);
+    if (rc) return rc;
+    if ((rc = check_selection(Tq, kpool, index_topk, pool_idx))) return rc;
+    if (B < 1 || B > (1 << 24)) return fail(KPOOL_ERR_INVALID_ARG, "B must be 1 .. 2^24");
+    if (n_rows < 1 || max_pages < 1 || max_pages > (1 << 20) || page_size < 1 ||
+        static_cast<int64_t>(max_pages) * page_size > 0x7FFFFFFFLL)
+        return fail(KPOOL_ERR_INVALID_ARG,
+                    "n_rows and page_size must be >= 1, max_pages 1 .. 2^20, max_pages * page_size < 2^31");
+    if (!seq_ids && n_rows < B) return fail(KPOOL_ERR_INVALID_ARG, "without seq_ids, n_rows must be >= B");
+    if (n_pages < 1 || n_pages > (1 << 28)) return fail(KPOOL_ERR_INVALID_ARG, "n_pages out of range");
+    if (kv_page_stride < static_cast<int64_t>(page_size) * Dc || kv_page_stride % 8 != 0 ||
+        kv_page_stride >= (int64_t(1) << 34))
+        return fail(KPOOL_ERR_INVALID_ARG, "kv_page_stride must be a multiple of 8 of at least a page's elements");
+    if (!kv || !page_table || !seq_lens || !cu_seqlens_q || !q_start_pos || !cu_pools)
+        return fail(KPOOL_ERR_INVALID_ARG,
+                    "kv, page_table, seq_lens, cu_seqlens_q, q_start_pos and cu_pools are required");
+    if (!aligned(page_table, 4) || !aligned(seq_lens, 4) || !aligned(seq_ids, 4) || !aligned(cu_seqlens_q, 4) ||
+        !aligned(q_start_pos, 4) || !aligned(cu_pools, 4))
+        return fail(KPOOL_ERR_INVALID_ARG, "index arrays must be 4-byte aligned");
+    const size_t need = paged_mla_workspace_bytes(Tq, index_topk / kpool, kpool);
+    if (workspace_bytes < need)
+        return fail(KPOOL_ERR_WORKSPACE, "workspace of at least %zu bytes, 256-byte aligned, needed", need);
+    PagedMlaArgs a{};
+    a.q = q; a.kv = kv; a.kv_page_stride = kv_page_stride; a.n_pages = n_pages; a.page_size = page_size;
+    a.page_table = page_table; a.seq_lens = seq_lens; a.n_rows = n_rows; a.max_pages = max_pages;
+    a.seq_ids = seq_ids; a.pool_idx = pool_idx; a.cu_q = cu_seqlens_q; a.q_pos = q_start_pos; a.cu_pools = cu_pools;
+    a.B = B; a.Tq = Tq; a.kpool = kpool; a.Kp = index_topk / kpool; a.tail = always_select_tail ? 1 : 0;
+    a.scale = softmax_scale; a.o = o_out; a.lse = lse_out; a.workspace = workspace;
+    return run_paged_mla(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t kpool_pages_workspace_size(int64_t n, int n_seqs, int n_pages)

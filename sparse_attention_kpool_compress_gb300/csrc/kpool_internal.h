@@ -148,6 +148,35 @@ struct SparseMlaArgs {
 size_t sparse_mla_workspace_bytes();
 int run_sparse_mla(const SparseMlaArgs &a, cudaStream_t s);
 
+// Its backward pass (kpool_mla_bwd.cu); o and lse of the arguments are what the
+// forward pass left, and are read.
+struct SparseMlaGrad {
+    const void *d_o;                    // bf16 [T, 64, 512]
+    const float *d_lse;                 // [T, 64] or NULL
+    void *dq, *dkv;                     // bf16 [T, 64, 512], bf16 [Tk, 512]
+};
+size_t sparse_mla_bwd_workspace_bytes(int64_t T, int64_t Tk);
+int run_sparse_mla_bwd(const SparseMlaArgs &a, const SparseMlaGrad &g, cudaStream_t s);
+
+// The sparse attention over a paged cache (kpool_paged_mla.cu).
+struct PagedMlaArgs {
+    const void *q, *kv;                 // bf16 [Tq, 64, 512], bf16 [n_pages, page_size, 512]
+    int64_t kv_page_stride;             // elements
+    int n_pages, page_size;
+    const int32_t *page_table, *seq_lens;
+    int n_rows, max_pages;
+    const int32_t *seq_ids, *pool_idx, *cu_q, *q_pos, *cu_pools;
+    int B;
+    int64_t Tq;
+    int kpool, Kp, tail;
+    float scale;
+    void *o;
+    float *lse;
+    void *workspace;
+};
+size_t paged_mla_workspace_bytes(int64_t Tq, int Kp, int kpool);
+int run_paged_mla(const PagedMlaArgs &a, cudaStream_t s);
+
 // Paged cache (kpool_pages.cu); arguments are validated by the caller.  Copies of up
 // to kPagesFusedCopy pages need a status word of workspace only.
 constexpr int kPagesFusedCopy = 1024;

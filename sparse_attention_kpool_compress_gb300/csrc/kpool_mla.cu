@@ -52,6 +52,7 @@
 #include <cmath>
 
 #include "kpool_internal.h"
+#include "kpool_mla_rows.cuh"
 #include "kpool_ptx.cuh"
 
 namespace kpool {
@@ -84,7 +85,6 @@ constexpr int kOParts = kDc / 128;      // O^T in 128-row (latent) parts of 64 c
 constexpr int kQChunk = kH * 128;       // 64 latent columns of the query block: 8 KiB
 constexpr float kRescale = 8.f;         // headroom of the reference maximum (log2)
 constexpr uint64_t kTimeoutNs = 2000000000ull;
-constexpr uint32_t kFull = 0xFFFFFFFFu;
 constexpr int kTmemCols = 512;          // S^T: 0..127, O^T: 128..383
 
 // shared memory (from a 1024-byte aligned base)
@@ -110,26 +110,15 @@ constexpr int kSmemBytes = kSmemUsed + 1024;         // alignment slack
 static_assert(kSmemBytes <= 232448, "shared memory over the per-block limit");
 
 struct Params {
+    RowLists rows;
     const uint16_t *q;          // bf16 [T, 64, 512]
     const uint16_t *kv;         // bf16 [Tk, 512]
-    const int32_t *tok;         // [T, W] or NULL (pool mode)
-    const int32_t *pool_idx;    // [T, Kp] (pool mode)
-    const int32_t *cu_seqlens, *q_pos, *cu_k, *cu_pools;
-    int n_docs;
-    int T, Tk, W, kp, Kp, tail;
     float c_scale;              // softmax scale * log2(e)
     uint16_t *o;                // bf16 [T, 64, 512]
     float *lse;                 // [T, 64]
     int *ws;                    // [0] row counter, [1] status
     uint64_t wait_limit_ns;
 };
-
-// What the loaders need to list the tokens of one row.
-struct RowMsg {
-    int64_t key0;               // first key token of the row's document
-    int t, n_slots, tau, pool_lo, pool_hi, n_sel, n_tail, pad;
-};
-static_assert(sizeof(RowMsg) <= 48, "RowMsg slot");
 
 // One block of a row, for the MMA issuer and the softmax warps.
 struct BInfo {
@@ -138,112 +127,15 @@ struct BInfo {
 };
 static_assert(sizeof(BInfo) == 32, "BInfo slot");
 
-struct Sync {
-    volatile uint32_t *abort_flag;
-    int *status;
-    uint64_t limit_ns;
-};
-
-// Bounded mbarrier wait (completion, then the CTA abort flag, then a timer
-// that raises the flag and KPOOL_STATUS_TIMEOUT).
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const Sync &sy)
-{
-    if (ptx::mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = ptx::globaltimer();
-    while (true) {
-        if (ptx::mbar_try_wait(bar, parity)) return true;
-        if (*sy.abort_flag) return false;
-        if (ptx::globaltimer() - t0 > sy.limit_ns) {
-            *sy.abort_flag = 1u;
-            atomicOr(sy.status, KPOOL_STATUS_TIMEOUT);
-            return false;
-        }
-    }
-}
-
-__device__ __forceinline__ bool wait_bar_warp(uint32_t bar, uint32_t parity, const Sync &sy)
-{
-    const bool ok = wait_bar(bar, parity, sy);
-    return __all_sync(kFull, ok);
-}
-
-// Document of row t (largest d with cu[d] <= t), one warp probing 32 evenly
-// spaced offsets per round.  Every lane gets the answer.
-__device__ __forceinline__ int doc_of_row(const int32_t *cu, int n_docs, int t, int lane)
-{
-    int lo = 0, hi = n_docs;
-    while (hi - lo > 1) {
-        const int step = (hi - lo + 31) / 32;
-        const int idx = lo + lane * step;
-        const bool le = idx < hi && cu[idx] <= t;
-        const unsigned m = __ballot_sync(kFull, le);
-        const int nlo = lo + (31 - __clz(m)) * step;
-        hi = min(hi, nlo + step);
-        lo = nlo;
-    }
-    return lo;
-}
-
-// Key token of slot j of the row (-1: none).  Pool mode lists the selected
-// pools' tokens in order, then the tail (the expansion of the selection).
-__device__ __forceinline__ int token_of(const Params &p, const RowMsg &m, int j)
-{
-    if (j >= m.n_slots) return -1;
-    if (p.tok != nullptr) {
-        const int v = __ldg(p.tok + static_cast<int64_t>(m.t) * p.W + j);
-        return (v >= 0 && v < p.Tk) ? v : -1;
-    }
-    const int npt = m.n_sel * p.kp;
-    int64_t v = -1;
-    if (j < npt) {
-        const int e = j / p.kp;
-        const int g = __ldg(p.pool_idx + static_cast<int64_t>(m.t) * p.Kp + e);
-        if (g >= m.pool_lo && g < m.pool_hi)
-            v = m.key0 + static_cast<int64_t>(g - m.pool_lo) * p.kp + (j - e * p.kp);
-    } else {
-        v = m.key0 + m.tau - m.n_tail + 1 + (j - npt);
-    }
-    return (v >= 0 && v < p.Tk) ? static_cast<int>(v) : -1;
-}
-
 // Warp 0: the next row's message (t = -1 when there is none or on abort).
 __device__ RowMsg next_row(const Params &p, int lane, bool go)
 {
-    RowMsg m{};
     int t = -1;
     if (lane == 0 && go) t = atomicAdd(p.ws, 1);
     t = __shfl_sync(kFull, t, 0);
-    m.t = (t >= 0 && t < p.T) ? t : -1;
-    if (m.t < 0) return m;
-    if (p.tok != nullptr) {
-        // extent of the listed tokens: one past the last valid entry
-        int last = -1;
-        const int32_t *row = p.tok + static_cast<int64_t>(m.t) * p.W;
-        for (int j = lane; j < p.W; j += 32) {
-            const int v = __ldg(row + j);
-            if (v >= 0 && v < p.Tk) last = j;
-        }
-        m.n_slots = __reduce_max_sync(kFull, last + 1);
-        return m;
-    }
-    int64_t doc_start = 0;
-    m.key0 = 0;
-    int pos0 = 0;
-    m.pool_lo = 0;
-    m.pool_hi = p.Tk / p.kp;
-    if (p.cu_seqlens != nullptr) {
-        const int d = doc_of_row(p.cu_seqlens, p.n_docs, m.t, lane);
-        doc_start = p.cu_seqlens[d];
-        m.key0 = p.cu_k != nullptr ? p.cu_k[d] : doc_start;
-        pos0 = p.q_pos != nullptr ? p.q_pos[d] : 0;
-        m.pool_lo = p.cu_pools[d];
-        m.pool_hi = p.cu_pools[d + 1];
-    }
-    m.tau = pos0 + static_cast<int>(m.t - doc_start);
-    const int nc = min((m.tau + 1) / p.kp, m.pool_hi - m.pool_lo);
-    m.n_sel = max(0, min(nc, p.Kp));
-    m.n_tail = p.tail ? (m.tau + 1) % p.kp : 0;
-    m.n_slots = m.n_sel * p.kp + m.n_tail;
+    if (t >= 0 && t < p.rows.T) return row_msg(p.rows, t, lane);
+    RowMsg m{};
+    m.t = -1;
     return m;
 }
 
@@ -323,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t my4 = 0;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    tk[k] = token_of(p, m, b * kBT + 4 * lane + k);
+                    tk[k] = token_of(p.rows, m, b * kBT + 4 * lane + k);
                     my4 |= (tk[k] >= 0 ? 1u : 0u) << k;
                 }
                 // validity word w (tokens 32w..32w+31) from lanes 8w..8w+7
@@ -748,19 +640,7 @@ int run_sparse_mla(const SparseMlaArgs &a, cudaStream_t s)
     Params p{};
     p.q = static_cast<const uint16_t *>(a.q);
     p.kv = static_cast<const uint16_t *>(a.kv);
-    p.tok = a.tok_idx;
-    p.pool_idx = a.pool_idx;
-    p.cu_seqlens = a.cu_seqlens;
-    p.q_pos = a.q_pos;
-    p.cu_k = a.cu_k;
-    p.cu_pools = a.cu_pools;
-    p.n_docs = a.n_docs;
-    p.T = static_cast<int>(a.T);
-    p.Tk = static_cast<int>(a.Tk);
-    p.W = a.W;
-    p.kp = a.kpool;
-    p.Kp = a.Kp;
-    p.tail = a.tail;
+    p.rows = row_lists(a);
     p.c_scale = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
     p.o = static_cast<uint16_t *>(a.o);
     p.lse = a.lse;
