@@ -9,7 +9,26 @@
 //   dq[t, h, :]  = sum_j ds_j c[j, :]
 //   dc[j, :]    += ds_j q[t, h, :] + p_j do[t, h, :]
 //
-// First form: a block per row, a warp per eight heads, lanes over the columns.
+// Design (one persistent CTA per SM, 24 warps, rows handed out by an atomic
+// counter, the last first).  Q and dO of a row are stacked, eight heads of one and
+// the same eight of the other in turn: X [128 x 512].  Per block of 64 listed tokens
+// C [64 x 512], in tensor memory:
+//   [S; dP]  [128 x 64]    = X . C^T                       (A, B K-major)
+//   dQ^T     [512 x 64]   += C^T . dS^T                    (A MN-major, B K-major)
+//   dC^T     [512 x 64]    = X^T . [dS; P]                 (A, B MN-major)
+// so every MMA has M = 128 and N = 64, one copy of X serves both orders, and so
+// does one tile [dS; P] [128 x 64].  Heads in eights put the score and the dP of a
+// (head, token) into one thread's registers (a 16x256b load has lanes r and r + 8),
+// so P and dS need no exchange; lse is known, so no maximum and no sum either.
+//   warp 0       control: per row X (TMA), per block a record with its token ids
+//   warp 1       MMA issuer (the loop in all lanes, one issues)
+//   warps 4-11   P and dS; after a row's last block, dQ
+//   warps 12-15  dC^T from tensor memory, added to the FP32 sums in L2
+//   warps 16-23  loaders: the tokens' latent rows by 16-byte cp.async, a pair of
+//                warps per slot of 128 columns
+// A row's block order is scores, dQ (which frees the slots one by one, so that the
+// next block's rows land while dC is computed), dC in four parts through three slots
+// of tensor memory.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -24,95 +43,474 @@ namespace {
 
 constexpr int kH = 64;                  // heads
 constexpr int kDc = 512;                // latent width
+constexpr int kBT = 64;                 // listed tokens per block
+constexpr int kThreads = 768;
+constexpr int kGradWarp0 = 4, kGradWarps = 8;      // P and dS, dQ
+constexpr int kSumWarp0 = kGradWarp0 + kGradWarps, kSumWarps = 4;
+constexpr int kLoaderWarp0 = kSumWarp0 + kSumWarps, kLoaderWarps = 8;
+static_assert(32 * (kLoaderWarp0 + kLoaderWarps) == kThreads, "warps");
+constexpr int kGroup = 8192;            // eight rows of X: 8 chunks of 64 columns, 1 KB each
+constexpr int kChunk = kBT * 128;       // 64 latent columns of a block
+constexpr int kSlots = 4;               // 128 columns each
+constexpr int kSlot = 2 * kChunk;
+constexpr int kParts = 4;               // dQ^T and dC^T in parts of 128 latent columns
+constexpr int kSumSlots = 3;
+constexpr int kInfoSlots = 4;
+constexpr uint64_t kTimeoutNs = 2000000000ull;
+constexpr int kTmemCols = 512;          // dQ^T: 0..255, [S; dP]: 256..319, dC^T parts: 320..511
+constexpr int kTmemS = 256, kTmemSum = 320;
 
+// shared memory (from a 1024-byte aligned base)
+constexpr int kOffX = 0;
+constexpr int kOffC = kOffX + 16 * kGroup;
+constexpr int kOffP = kOffC + kSlots * kSlot;          // [dS; P]: 16 groups of eight rows, 1 KB each
+constexpr int kOffInfo = kOffP + 128 * 128;
+constexpr int kOffTok = kOffInfo + kInfoSlots * 32;    // token ids [kInfoSlots][64]
+constexpr int kOffBar = kOffTok + kInfoSlots * kBT * 4;
+enum {
+    BX_FULL = 0, BX_EMPTY, BC_FULL, BC_EMPTY = BC_FULL + kSlots, BS_FULL = BC_EMPTY + kSlots, BP_FULL,
+    BQ_FULL, BQ_EMPTY, BD_FULL, BD_EMPTY = BD_FULL + kSumSlots, BI_FULL = BD_EMPTY + kSumSlots,
+    BI_EMPTY = BI_FULL + kInfoSlots, BDRAIN = BI_EMPTY + kInfoSlots, NBARS
+};
+constexpr int kOffMisc = kOffBar + NBARS * 8;          // [0] tmem base, [1] abort flag
+constexpr int kSmemBytes = kOffMisc + 16 + 1024;       // and alignment slack
+static_assert(kSmemBytes <= 232448, "shared memory over the per-block limit");
+
+// workspace: header (ints: row counter, status), {lse, delta} of each (row, head), sums
 struct Params {
     RowLists rows;
-    const uint16_t *q, *kv, *o, *d_o;
-    const float *lse, *d_lse;
+    const uint16_t *kv;
+    const float2 *stats;        // [T, 64]: lse * log2(e) (+inf: no token), delta
     uint16_t *dq;
     float *acc;                 // [Tk, 512]: the latent rows' gradients
-    float scale;
+    float scale, c_scale;       // softmax scale, and that * log2(e)
+    int *ws;
+    uint64_t wait_limit_ns;
 };
 
-__device__ __forceinline__ void load16(const uint16_t *row, int lane, float (&v)[16])
+// One block of a row.
+struct BInfo {
+    int t, b, nb, ksteps;
+    uint32_t mask[2];           // bit r of mask[r / 32]: listed token r is valid
+    int pad[2];
+};
+static_assert(sizeof(BInfo) == 32, "BInfo slot");
+
+// Operand tiles whose groups of eight rows lie `group` bytes apart.
+__device__ __forceinline__ uint64_t desc_k(uint32_t saddr, uint32_t group)
 {
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        const uint4 x = *reinterpret_cast<const uint4 *>(row + 256 * half + 8 * lane);
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[8 * half + 2 * i] = __uint_as_float(w[i] << 16);
-            v[8 * half + 2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    return (ptx::smem_desc_sw128(saddr) & ~(0x3FFFull << 32)) | (static_cast<uint64_t>(group >> 4) << 32);
+}
+
+__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t chunk, uint32_t group)
+{
+    return (ptx::smem_desc_mn_sw128(saddr, chunk) & ~(0x3FFFull << 32)) | (static_cast<uint64_t>(group >> 4) << 32);
+}
+
+// X: eight rows x all 512 columns of q or d_o, as eight chunks of 64 columns.
+__device__ __forceinline__ void load_group(uint32_t dst, const void *desc, uint32_t bar, int row)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(desc), "r"(bar), "r"(0), "r"(row), "r"(0)
+        : "memory");
+}
+
+__device__ __forceinline__ void red_add(float *to, uint32_t v)
+{
+    asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(to), "f"(__uint_as_float(v)) : "memory");
+}
+
+__device__ __forceinline__ void st_shared(uint32_t saddr, uint32_t v)
+{
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(saddr), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&b);
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    sparse_mla_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
+                          const __grid_constant__ Params p)
+{
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
+    const uint32_t sbase = ptx::smem_u32(smem);
+    const uint32_t sX = sbase + kOffX, sC = sbase + kOffC, sP = sbase + kOffP;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kOffBar);
+    auto bar = [&](int i) { return ptx::smem_u32(&bars[i]); };
+    uint32_t *misc = reinterpret_cast<uint32_t *>(smem + kOffMisc);
+    BInfo *info = reinterpret_cast<BInfo *>(smem + kOffInfo);
+    int *toks = reinterpret_cast<int *>(smem + kOffTok);
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        ptx::mbar_init(bar(BX_FULL), 1);
+        ptx::mbar_init(bar(BX_EMPTY), 1);
+        for (int i = 0; i < kSlots; ++i) {
+            ptx::mbar_init(bar(BC_FULL + i), 64);   // the slot's two loader warps
+            ptx::mbar_init(bar(BC_EMPTY + i), 1);
         }
+        ptx::mbar_init(bar(BS_FULL), 1);
+        ptx::mbar_init(bar(BP_FULL), kGradWarps);
+        ptx::mbar_init(bar(BQ_FULL), 1);
+        ptx::mbar_init(bar(BQ_EMPTY), kGradWarps);
+        for (int i = 0; i < kSumSlots; ++i) {
+            ptx::mbar_init(bar(BD_FULL + i), 1);
+            ptx::mbar_init(bar(BD_EMPTY + i), kSumWarps);
+        }
+        for (int i = 0; i < kInfoSlots; ++i) {
+            ptx::mbar_init(bar(BI_FULL + i), 1);
+            ptx::mbar_init(bar(BI_EMPTY + i), 1 + kGradWarps + kSumWarps + kLoaderWarps);
+        }
+        ptx::mbar_init(bar(BDRAIN), 1);
+        misc[1] = 0u;
+        ptx::fence_mbar_init();
     }
-}
-
-__device__ __forceinline__ float warp_dot(const float (&a)[16], const float (&b)[16])
-{
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) s = fmaf(a[i], b[i], s);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(kFull, s, d);
-    return s;
-}
-
-__global__ void __launch_bounds__(256) sparse_mla_bwd_kernel(const Params p)
-{
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int t = blockIdx.x;
-    const RowMsg m = row_msg(p.rows, t, lane);
-    const int64_t base = (static_cast<int64_t>(t) * kH + 8 * warp) * kDc;
-    float dq[8][16], lse[8], delta[8];
-#pragma unroll
-    for (int h = 0; h < 8; ++h) {
-        float a[16], b[16];
-        load16(p.o + base + h * kDc, lane, a);
-        load16(p.d_o + base + h * kDc, lane, b);
-        const int64_t at = static_cast<int64_t>(t) * kH + 8 * warp + h;
-        delta[h] = warp_dot(a, b) - (p.d_lse != nullptr ? p.d_lse[at] : 0.f);
-        lse[h] = p.lse[at];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) dq[h][i] = 0.f;
+    if (warp == 1) {
+        ptx::tmem_alloc(ptx::smem_u32(&misc[0]), kTmemCols);
+        ptx::tmem_relinquish();
+        ptx::tc_fence_before();
     }
-    for (int j = 0; j < m.n_slots; ++j) {
-        const int tok = token_of(p.rows, m, j);
-        if (tok < 0) continue;
-        float c[16], dc[16];
-        load16(p.kv + static_cast<int64_t>(tok) * kDc, lane, c);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) dc[i] = 0.f;
-#pragma unroll
-        for (int h = 0; h < 8; ++h) {
-            float a[16], b[16];
-            load16(p.q + base + h * kDc, lane, a);
-            load16(p.d_o + base + h * kDc, lane, b);
-            const float s = warp_dot(a, c) * p.scale, dp = warp_dot(b, c);
-            const float w = lse[h] == -INFINITY ? 0.f : expf(s - lse[h]);
-            const float ds = w * (dp - delta[h]) * p.scale;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                dq[h][i] = fmaf(ds, c[i], dq[h][i]);
-                dc[i] = fmaf(ds, a[i], fmaf(w, b[i], dc[i]));
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = misc[0];
+    const Sync sy{reinterpret_cast<volatile uint32_t *>(&misc[1]), p.ws + 1, p.wait_limit_ns};
+    // the statistics and the cleared sums and counter of the kernel in front
+    ptx::grid_dependency_wait();
+
+    if (warp == 0) {
+        // ---------------- control: rows, records, X ----------------
+        if (lane == 0) {
+            ptx::tma_prefetch_desc(&tm_q);
+            ptx::tma_prefetch_desc(&tm_do);
+        }
+        bool ok = true;
+        int g = 0;                      // blocks published
+        uint32_t x_ph = 0;
+        bool x_issued = false;
+        for (;;) {
+            int t = -1;
+            if (lane == 0 && ok && !*sy.abort_flag) t = p.rows.T - 1 - atomicAdd(p.ws, 1);
+            t = __shfl_sync(kFull, t, 0);
+            if (t < 0) break;
+            const RowMsg m = row_msg(p.rows, t, lane);
+            const int nb = max(1, (m.n_slots + kBT - 1) / kBT);
+            ok = wait_bar_warp(bar(BX_EMPTY), x_ph ^ 1, sy);
+            if (!ok) break;
+            if (lane == 0) ptx::mbar_arrive_expect_tx(bar(BX_FULL), 16 * kGroup);
+            __syncwarp();
+            if (lane < 16)
+                load_group(sX + lane * kGroup, (lane & 1) ? &tm_do : &tm_q, bar(BX_FULL), t * kH + 8 * (lane >> 1));
+            x_issued = true;
+            x_ph ^= 1;
+            for (int b = 0; b < nb && ok; ++b, ++g) {
+                const int t0 = token_of(p.rows, m, b * kBT + 2 * lane), t1 = token_of(p.rows, m, b * kBT + 2 * lane + 1);
+                // validity word w (tokens 32w .. 32w + 31) from lanes 16w .. 16w + 15
+                uint32_t mw = ((t0 >= 0 ? 1u : 0u) | (t1 >= 0 ? 2u : 0u)) << (2 * (lane & 15));
+                mw |= __shfl_xor_sync(kFull, mw, 1);
+                mw |= __shfl_xor_sync(kFull, mw, 2);
+                mw |= __shfl_xor_sync(kFull, mw, 4);
+                mw |= __shfl_xor_sync(kFull, mw, 8);
+                const int is = g % kInfoSlots;
+                ok = wait_bar_warp(bar(BI_EMPTY + is), ((g / kInfoSlots) & 1) ^ 1, sy);
+                if (!ok) break;
+                *reinterpret_cast<int2 *>(toks + is * kBT + 2 * lane) = make_int2(t0, t1);
+                if ((lane & 15) == 0) info[is].mask[lane >> 4] = mw;
+                if (lane == 0) {
+                    info[is].t = t;
+                    info[is].b = b;
+                    info[is].nb = nb;
+                    info[is].ksteps = max(1, (min(kBT, m.n_slots - b * kBT) + 15) / 16);
+                }
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(bar(BI_FULL + is));
             }
         }
-        float *to = p.acc + static_cast<int64_t>(tok) * kDc + 8 * lane;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) atomicAdd(to + (i >> 3) * 256 + (i & 7), dc[i]);
-    }
-#pragma unroll
-    for (int h = 0; h < 8; ++h)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const __nv_bfloat16 v = __float2bfloat16_rn(dq[h][i]);
-            p.dq[base + h * kDc + (i >> 3) * 256 + 8 * lane + (i & 7)] = *reinterpret_cast<const uint16_t *>(&v);
+        // end of the block stream for every consumer
+        const int is = g % kInfoSlots;
+        if (ok && wait_bar_warp(bar(BI_EMPTY + is), ((g / kInfoSlots) & 1) ^ 1, sy) && lane == 0) {
+            info[is].t = -1;
+            ptx::mbar_arrive(bar(BI_FULL + is));
         }
+        // no load of X may still be in flight when the CTA ends: a wait of its own,
+        // bounded by the default limit and blind to the abort flag
+        if (x_issued) {
+            const uint64_t t0 = ptx::globaltimer();
+            while (!ptx::mbar_try_wait(bar(BX_FULL), x_ph ^ 1))
+                if (ptx::globaltimer() - t0 > kTimeoutNs) break;
+        }
+    } else if (warp == 1) {
+        // ---------------- MMA issuer ----------------
+        constexpr uint32_t idesc = ptx::make_idesc(1u, 128, 64);
+        const bool one = ptx::elect_one();
+        int g = 0;
+        uint32_t c_ph = 0, x_ph = 0, q_ph = 0, nd = 0;      // nd: parts of dC so far
+        bool any = false;
+        for (;;) {
+            const int is = g % kInfoSlots;
+            if (!wait_bar_warp(bar(BI_FULL + is), (g / kInfoSlots) & 1, sy)) break;
+            const BInfo in = info[is];
+            __syncwarp();
+            if (one) ptx::mbar_arrive(bar(BI_EMPTY + is));
+            if (in.t < 0) break;
+            if (in.b == 0) {
+                if (!wait_bar_warp(bar(BX_FULL), x_ph, sy)) break;
+                x_ph ^= 1;
+            }
+            bool ok = true;
+            // (the last block's scores were read before its P was complete)
+            for (int sl = 0; sl < kSlots; ++sl) {
+                ok = wait_bar_warp(bar(BC_FULL + sl), c_ph, sy);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                if (one) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint64_t ad = desc_k(sX + (2 * sl + h) * 1024, kGroup);
+                        const uint64_t bd = desc_k(sC + sl * kSlot + h * kChunk, 1024);
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            ptx::mma_bf16(tmem + kTmemS, ad + 2 * kk, bd + 2 * kk, idesc, (sl | h | kk) != 0);
+                    }
+                }
+                any = true;
+            }
+            if (!ok) break;
+            if (one) ptx::mma_commit(bar(BS_FULL));
+            if (!wait_bar_warp(bar(BP_FULL), g & 1, sy)) break;
+            if (in.b == 0 && !wait_bar_warp(bar(BQ_EMPTY), q_ph ^ 1, sy)) break;
+            ptx::tc_fence_after();
+            if (one) {
+                for (int sl = 0; sl < kSlots; ++sl) {
+                    const uint64_t ad = desc_mn(sC + sl * kSlot, kChunk, 1024), bd = desc_k(sP, 2048);
+                    for (int kk = 0; kk < in.ksteps; ++kk)
+                        ptx::mma_bf16(tmem + sl * 64, ad + kk * 128, bd + 2 * kk, idesc | ptx::kIdescAMajorMN,
+                                      in.b > 0 || kk > 0);
+                    ptx::mma_commit(bar(BC_EMPTY + sl));
+                }
+                if (in.b == in.nb - 1) ptx::mma_commit(bar(BQ_FULL));
+            }
+            if (in.b == in.nb - 1) q_ph ^= 1;
+            for (int part = 0; part < kParts; ++part, ++nd) {
+                const uint32_t s = nd % kSumSlots;
+                ok = wait_bar_warp(bar(BD_EMPTY + s), ((nd / kSumSlots) & 1) ^ 1, sy);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                if (one) {
+                    const uint64_t ad = desc_mn(sX + part * 2048, 1024, kGroup), bd = desc_mn(sP, 1024, 1024);
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+                        ptx::mma_bf16(tmem + kTmemSum + s * 64, ad + kk * (2 * kGroup / 16), bd + kk * 128,
+                                      idesc | ptx::kIdescAMajorMN | ptx::kIdescBMajorMN, kk > 0);
+                    ptx::mma_commit(bar(BD_FULL + s));
+                }
+            }
+            if (!ok) break;
+            if (one && in.b == in.nb - 1) ptx::mma_commit(bar(BX_EMPTY));
+            c_ph ^= 1;
+            ++g;
+        }
+        if (any) {
+            if (one) ptx::mma_commit(bar(BDRAIN));
+            const uint64_t t0 = ptx::globaltimer();
+            while (!ptx::mbar_try_wait(bar(BDRAIN), 0))
+                if (ptx::globaltimer() - t0 > kTimeoutNs) break;
+        }
+    } else if (warp >= kGradWarp0 && warp < kSumWarp0) {
+        // ---------------- P and dS, dQ ----------------
+        const int sub = warp & 3, half = (warp - kGradWarp0) >> 2;
+        const int grp = 2 * sub + half;                    // heads 8 grp .. 8 grp + 7
+        const int head = 8 * grp + (lane >> 2);
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * sub) << 16);
+        const uint32_t s_at = lanes + (static_cast<uint32_t>(16 * half) << 16) + kTmemS;
+        // a thread has tokens 8 j + 2 (lane % 4) and the next, for j = 0 .. 7
+        const uint32_t row = sP + 2 * grp * 1024 + (lane >> 2) * 128 + (lane & 3) * 4;
+        float lse = 0.f, delta = 0.f;
+        uint32_t q_ph = 0;
+        for (int g = 0;; ++g) {
+            const int is = g % kInfoSlots;
+            if (!wait_bar_warp(bar(BI_FULL + is), (g / kInfoSlots) & 1, sy)) break;
+            const BInfo in = info[is];
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar(BI_EMPTY + is));
+            if (in.t < 0) break;
+            if (in.b == 0) {
+                const float2 st = p.stats[static_cast<int64_t>(in.t) * kH + head];
+                lse = st.x;
+                delta = st.y;
+            }
+            if (!wait_bar_warp(bar(BS_FULL), g & 1, sy)) break;
+            ptx::tc_fence_after();
+            uint32_t r[32];
+            ptx::tmem_ld16x256_x8(s_at, r);
+            ptx::tmem_ld_wait(r);
+            // (this block's scores come behind the last block's dC, which read [dS; P])
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t m = in.mask[j >> 2] >> (8 * (j & 3) + 2 * (lane & 3));
+                float w[2], ds[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float x = ptx::ex2_approx(fmaf(__uint_as_float(r[4 * j + e]), p.c_scale, -lse));
+                    const float y = x * ((__uint_as_float(r[4 * j + 2 + e]) - delta) * p.scale);
+                    const bool v = (m >> e) & 1u;
+                    w[e] = v ? x : 0.f;
+                    ds[e] = v ? y : 0.f;
+                }
+                const uint32_t at = row + ((j ^ (lane >> 2)) << 4);
+                st_shared(at, pack_bf16(ds[0], ds[1]));
+                st_shared(at + 1024, pack_bf16(w[0], w[1]));
+            }
+            ptx::tc_fence_before();
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar(BP_FULL));
+            if (in.b == in.nb - 1) {
+                if (!wait_bar_warp(bar(BQ_FULL), q_ph, sy)) break;
+                q_ph ^= 1;
+                ptx::tc_fence_after();
+                uint16_t *out = p.dq + static_cast<int64_t>(in.t) * kH * kDc + 32 * sub + lane;
+#pragma unroll 1
+                for (int part = 2 * half; part < 2 * half + 2; ++part)
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh) {
+                        uint32_t v[32];
+                        ptx::tmem_ld32(lanes + part * 64 + hh * 32, v);
+                        ptx::tmem_ld_wait(v);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const __nv_bfloat16 b = __float2bfloat16_rn(__uint_as_float(v[i]));
+                            out[static_cast<int64_t>(hh * 32 + i) * kDc + part * 128] = *reinterpret_cast<const uint16_t *>(&b);
+                        }
+                    }
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(bar(BQ_EMPTY));
+            }
+        }
+    } else if (warp >= kSumWarp0 && warp < kLoaderWarp0) {
+        // ---------------- sums of dC ----------------
+        const int sub = warp & 3;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * sub) << 16) + kTmemSum;
+        uint32_t nd = 0;
+        bool ok = true;
+        for (int g = 0; ok; ++g) {
+            const int is = g % kInfoSlots;
+            ok = wait_bar_warp(bar(BI_FULL + is), (g / kInfoSlots) & 1, sy);
+            if (!ok || info[is].t < 0) break;
+            const int4 *tk = reinterpret_cast<const int4 *>(toks + is * kBT);
+            for (int part = 0; part < kParts; ++part, ++nd) {
+                const uint32_t s = nd % kSumSlots;
+                ok = wait_bar_warp(bar(BD_FULL + s), (nd / kSumSlots) & 1, sy);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                float *to = p.acc + part * 128 + 32 * sub + lane;
+#pragma unroll 1
+                for (int hh = 0; hh < 2; ++hh) {
+                    uint32_t v[32];
+                    ptx::tmem_ld32(lanes + s * 64 + hh * 32, v);
+                    ptx::tmem_ld_wait(v);
+                    if (hh == 1) {
+                        ptx::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(bar(BD_EMPTY + s));
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int4 k = tk[8 * hh + i];
+                        if (k.x >= 0) red_add(to + static_cast<int64_t>(k.x) * kDc, v[4 * i]);
+                        if (k.y >= 0) red_add(to + static_cast<int64_t>(k.y) * kDc, v[4 * i + 1]);
+                        if (k.z >= 0) red_add(to + static_cast<int64_t>(k.z) * kDc, v[4 * i + 2]);
+                        if (k.w >= 0) red_add(to + static_cast<int64_t>(k.w) * kDc, v[4 * i + 3]);
+                    }
+                }
+            }
+            __syncwarp();
+            if (ok && lane == 0) ptx::mbar_arrive(bar(BI_EMPTY + is));
+        }
+    } else if (warp >= kLoaderWarp0) {
+        // ---------------- loaders ----------------
+        const int sl = (warp - kLoaderWarp0) >> 1;                 // the slot of this pair
+        const int t64 = ((warp - kLoaderWarp0) & 1) * 32 + lane;   // 0..63 within the pair
+        const int k = t64 & 15;                                    // 16-byte piece of the slot's 256 bytes
+        const char *kvb = reinterpret_cast<const char *>(p.kv) + sl * 256 + k * 16;
+        const uint32_t dst = sC + sl * kSlot + (k >> 3) * kChunk;
+        bool ok = true;
+        uint32_t c_ph = 0;
+        for (int g = 0;; ++g) {
+            const int is = g % kInfoSlots;
+            ok = wait_bar_warp(bar(BI_FULL + is), (g / kInfoSlots) & 1, sy);
+            if (!ok || info[is].t < 0) break;
+            ok = wait_bar_warp(bar(BC_EMPTY + sl), c_ph ^ 1, sy);
+            if (!ok) break;
+            const int *tk = toks + is * kBT;
+#pragma unroll
+            for (int i = 0; i < kBT / 4; ++i) {                    // rows t64 / 16 + 4 i
+                const int r = (t64 >> 4) + 4 * i;
+                const int tok = tk[r];
+                ptx::cp_async16(dst + r * 128 + (((k & 7) ^ (r & 7)) << 4),
+                                kvb + (tok >= 0 ? static_cast<int64_t>(tok) * (kDc * 2) : 0), tok >= 0 ? 16u : 0u);
+            }
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar(BI_EMPTY + is));   // token ids read
+            ptx::cp_async_commit();
+            ptx::cp_async_wait_all();
+            ptx::fence_proxy_async_smem();
+            ptx::mbar_arrive(bar(BC_FULL + sl));
+            c_ph ^= 1;
+        }
+        ptx::cp_async_wait_all();
+    }
+
+    __syncthreads();
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// In front: {lse, delta} of each (row, head), a warp each, and cleared sums and counter.
+__global__ void __launch_bounds__(256) stats_kernel(const uint4 *o, const uint4 *d_o, const float *lse,
+                                                    const float *d_lse, float2 *stats, int64_t n, float4 *acc,
+                                                    int64_t n_acc, int *ws)
+{
+    const int lane = threadIdx.x & 31;
+    const int64_t first = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+    if (first < 64) ws[first] = 0;
+    for (int64_t i = first; i < n_acc; i += step) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int64_t r = first >> 5; r < n; r += step >> 5) {
+        float s = 0.f;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const uint4 x = o[r * 64 + 32 * half + lane], y = d_o[r * 64 + 32 * half + lane];
+            const uint32_t a[4] = {x.x, x.y, x.z, x.w}, b[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                s = fmaf(__uint_as_float(a[i] << 16), __uint_as_float(b[i] << 16), s);
+                s = fmaf(__uint_as_float(a[i] & 0xFFFF0000u), __uint_as_float(b[i] & 0xFFFF0000u), s);
+            }
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(kFull, s, d);
+        if (lane == 0) {
+            const float l = lse[r];
+            // a row without tokens has no probability anywhere
+            stats[r] = make_float2(l == -INFINITY ? INFINITY : l * 1.4426950408889634f, s - (d_lse != nullptr ? d_lse[r] : 0.f));
+        }
+    }
 }
 
 // The sums of the latent rows' gradients, rounded to BF16: eight a thread.
 __global__ void __launch_bounds__(256) round_kernel(const float4 *acc, uint4 *out, int64_t n)
 {
+    ptx::grid_dependency_wait();
     const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
     for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < n; i += step) {
         const float4 a = acc[2 * i], b = acc[2 * i + 1];
@@ -127,39 +525,67 @@ __global__ void __launch_bounds__(256) round_kernel(const float4 *acc, uint4 *ou
     }
 }
 
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), int grid, int threads, int smem, cudaStream_t s, const A &...args)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+size_t stats_bytes(int64_t T) { return (static_cast<size_t>(T) * kH * sizeof(float2) + 255) / 256 * 256; }
+
 }  // namespace
 
 size_t sparse_mla_bwd_workspace_bytes(int64_t T, int64_t Tk)
 {
-    (void)T;
-    return 256 + static_cast<size_t>(Tk) * kDc * 4;
+    return 256 + stats_bytes(T) + static_cast<size_t>(Tk) * kDc * 4;
 }
 
 int run_sparse_mla_bwd(const SparseMlaArgs &a, const SparseMlaGrad &g, cudaStream_t s)
 {
     uint8_t *ws = static_cast<uint8_t *>(a.workspace);
-    KPOOL_CUDA_CHECK(cudaMemsetAsync(ws, 0, sparse_mla_bwd_workspace_bytes(a.T, a.Tk), s));
     Params p{};
     p.rows = row_lists(a);
-    p.q = static_cast<const uint16_t *>(a.q);
     p.kv = static_cast<const uint16_t *>(a.kv);
-    p.o = static_cast<const uint16_t *>(a.o);
-    p.d_o = static_cast<const uint16_t *>(g.d_o);
-    p.lse = a.lse;
-    p.d_lse = g.d_lse;
+    float2 *stats = reinterpret_cast<float2 *>(ws + 256);
+    p.stats = stats;
     p.dq = static_cast<uint16_t *>(g.dq);
-    p.acc = reinterpret_cast<float *>(ws + 256);
+    p.acc = reinterpret_cast<float *>(ws + 256 + stats_bytes(a.T));
     p.scale = a.scale;
+    p.c_scale = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
+    p.ws = reinterpret_cast<int *>(ws);
+    p.wait_limit_ns = get_wait_limit_ns();
+    const int sms = num_sms();
+    const int64_t rows = a.T * kH, n_acc = a.Tk * (kDc / 4);
+    const int64_t blocks = std::max<int64_t>(1, std::max((rows + 7) / 8, (n_acc + 1023) / 1024));
+    stats_kernel<<<static_cast<unsigned>(std::min<int64_t>(blocks, 8 * sms)), 256, 0, s>>>(
+        static_cast<const uint4 *>(a.o), static_cast<const uint4 *>(g.d_o), a.lse, g.d_lse, stats, rows,
+        reinterpret_cast<float4 *>(p.acc), n_acc, p.ws);
+    KPOOL_CUDA_CHECK(cudaGetLastError());
     if (a.T > 0) {
-        sparse_mla_bwd_kernel<<<static_cast<unsigned>(a.T), 256, 0, s>>>(p);
-        KPOOL_CUDA_CHECK(cudaGetLastError());
+        CUtensorMap mq, mdo;
+        int rc = encode_bf16_groups_tmap(&mq, a.q, static_cast<uint64_t>(rows));
+        if (rc) return rc;
+        rc = encode_bf16_groups_tmap(&mdo, g.d_o, static_cast<uint64_t>(rows));
+        if (rc) return rc;
+        KPOOL_CUDA_CHECK(cudaFuncSetAttribute(sparse_mla_bwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                              kSmemBytes));
+        KPOOL_CUDA_CHECK(launch_after(sparse_mla_bwd_kernel, static_cast<int>(std::min<int64_t>(sms, a.T)), kThreads,
+                                      kSmemBytes, s, mq, mdo, p));
     }
     const int64_t n = a.Tk * (kDc / 8);
-    if (n > 0) {
-        round_kernel<<<static_cast<unsigned>(std::min<int64_t>((n + 255) / 256, 8 * num_sms())), 256, 0, s>>>(
-            reinterpret_cast<const float4 *>(p.acc), static_cast<uint4 *>(g.dkv), n);
-        KPOOL_CUDA_CHECK(cudaGetLastError());
-    }
+    if (n > 0)
+        KPOOL_CUDA_CHECK(launch_after(round_kernel, static_cast<int>(std::min<int64_t>((n + 255) / 256, 8 * sms)), 256, 0,
+                                      s, reinterpret_cast<const float4 *>(p.acc), static_cast<uint4 *>(g.dkv), n));
     return KPOOL_OK;
 }
 

@@ -428,6 +428,22 @@ int encode_bf16_pages_tmap(CUtensorMap *m, const void *base, uint64_t cols, uint
     return KPOOL_OK;
 }
 
+int encode_bf16_groups_tmap(CUtensorMap *m, const void *base, uint64_t rows)
+{
+    EncodeTiledFnP enc = get_encode_p();
+    if (!enc) return fail(KPOOL_ERR_CUDA, "cuTensorMapEncodeTiled entry point unavailable");
+    const cuuint64_t gdim[3] = {64, rows, 8};
+    const cuuint64_t gstride[2] = {1024, 128};
+    const cuuint32_t box[3] = {64, 8, 8};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), gdim,
+                           gstride, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(KPOOL_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+    return KPOOL_OK;
+}
+
 int run_project_compress(const ProjectArgs &a, cudaStream_t s)
 {
     KPOOL_CUDA_CHECK(cudaMemsetAsync(a.status, 0, sizeof(int), s));

@@ -353,3 +353,25 @@ def test_refusals_with_tensors(K):
         ok(q=q[:, :32].contiguous(), o=q[:, :32].contiguous(), d_o=d_o[:, :32].contiguous(), lse=lse[:, :32].contiguous())
     with pytest.raises(K.KPoolError):
         ok(workspace=torch.zeros(256, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("limit_ns", [1, 3000])
+def test_expired_waits(K, limit_ns):
+    """With the wait limit lowered the call reports KPOOL_STATUS_TIMEOUT (1 ns) or finishes; the next call at
+    the default limit is clean and right."""
+    T, Tk = 400, 300
+    q, kv, d_o, _ = _inputs(T, Tk, 41)
+    tok = _lists(np.random.default_rng(1), T, Tk, 260, [260, 100, 0, 65])
+    o, lse = K.kpool_sparse_mla_fwd(q, kv, tok, SCALE)
+    ws = torch.zeros(K.kpool_sparse_mla_bwd_workspace_size(T, Tk), dtype=torch.uint8, device="cuda")
+    K.kpool_debug_set_wait_limit_ns(limit_ns)
+    try:
+        K.kpool_sparse_mla_bwd(q, kv, tok, o, lse, d_o, SCALE, workspace=ws)
+        status = K.kpool_read_status(ws)
+    finally:
+        assert K.kpool_debug_set_wait_limit_ns(0) == limit_ns
+    if limit_ns == 1:
+        assert status & K.STATUS_TIMEOUT
+    dq, dkv = K.kpool_sparse_mla_bwd(q, kv, tok, o, lse, d_o, SCALE, workspace=ws)
+    assert K.kpool_read_status(ws) == 0
+    Grads(q, kv, _rows_of(tok, Tk), o, lse, d_o, SCALE).check(dq, dkv)
