@@ -44,9 +44,9 @@ namespace {
 constexpr int kH = 64;                  // heads
 constexpr int kDc = 512;                // latent width
 constexpr int kBT = 64;                 // listed tokens per block
-constexpr int kThreads = 768;
+constexpr int kThreads = 896;
 constexpr int kGradWarp0 = 4, kGradWarps = 8;      // P and dS, dQ
-constexpr int kSumWarp0 = kGradWarp0 + kGradWarps, kSumWarps = 4;
+constexpr int kSumWarp0 = kGradWarp0 + kGradWarps, kSumWarps = 8;
 constexpr int kLoaderWarp0 = kSumWarp0 + kSumWarps, kLoaderWarps = 8;
 static_assert(32 * (kLoaderWarp0 + kLoaderWarps) == kThreads, "warps");
 constexpr int kGroup = 8192;            // eight rows of X: 8 chunks of 64 columns, 1 KB each
@@ -64,7 +64,9 @@ constexpr int kTmemS = 256, kTmemSum = 320;
 constexpr int kOffX = 0;
 constexpr int kOffC = kOffX + 16 * kGroup;
 constexpr int kOffP = kOffC + kSlots * kSlot;          // [dS; P]: 16 groups of eight rows, 1 KB each
-constexpr int kOffInfo = kOffP + 128 * 128;
+constexpr int kStage = 16 * 128;                       // 16 tokens x 32 columns of dC, a sums warp
+constexpr int kOffStage = kOffP + 128 * 128;
+constexpr int kOffInfo = kOffStage + kSumWarps * kStage;
 constexpr int kOffTok = kOffInfo + kInfoSlots * 32;    // token ids [kInfoSlots][64]
 constexpr int kOffBar = kOffTok + kInfoSlots * kBT * 4;
 enum {
@@ -79,7 +81,7 @@ static_assert(kSmemBytes <= 232448, "shared memory over the per-block limit");
 // workspace: header (ints: row counter, status), {lse, delta} of each (row, head), sums
 struct Params {
     RowLists rows;
-    const uint16_t *kv;
+    const uint16_t *q, *kv, *d_o;
     const float2 *stats;        // [T, 64]: lse * log2(e) (+inf: no token), delta
     uint16_t *dq;
     float *acc;                 // [Tk, 512]: the latent rows' gradients
@@ -117,9 +119,28 @@ __device__ __forceinline__ void load_group(uint32_t dst, const void *desc, uint3
         : "memory");
 }
 
-__device__ __forceinline__ void red_add(float *to, uint32_t v)
+__device__ __forceinline__ void prefetch_l2(const void *from, uint32_t bytes)
 {
-    asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(to), "f"(__uint_as_float(v)) : "memory");
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+
+__device__ __forceinline__ void red_add(float *to, const float4 &v)
+{
+    asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(to), "f"(v.x), "f"(v.y), "f"(v.z),
+                 "f"(v.w)
+                 : "memory");
 }
 
 __device__ __forceinline__ void st_shared(uint32_t saddr, uint32_t v)
@@ -162,11 +183,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::mbar_init(bar(BQ_EMPTY), kGradWarps);
         for (int i = 0; i < kSumSlots; ++i) {
             ptx::mbar_init(bar(BD_FULL + i), 1);
-            ptx::mbar_init(bar(BD_EMPTY + i), kSumWarps);
+            ptx::mbar_init(bar(BD_EMPTY + i), 4);       // a part goes to four of the sums warps
         }
         for (int i = 0; i < kInfoSlots; ++i) {
             ptx::mbar_init(bar(BI_FULL + i), 1);
-            ptx::mbar_init(bar(BI_EMPTY + i), 1 + kGradWarps + kSumWarps + kLoaderWarps);
+            ptx::mbar_init(bar(BI_EMPTY + i), 2 + kGradWarps + kSumWarps + kLoaderWarps);
         }
         ptx::mbar_init(bar(BDRAIN), 1);
         misc[1] = 0u;
@@ -185,31 +206,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::grid_dependency_wait();
 
     if (warp == 0) {
-        // ---------------- control: rows, records, X ----------------
-        if (lane == 0) {
-            ptx::tma_prefetch_desc(&tm_q);
-            ptx::tma_prefetch_desc(&tm_do);
-        }
+        // ---------------- control: rows and their blocks ----------------
         bool ok = true;
         int g = 0;                      // blocks published
-        uint32_t x_ph = 0;
-        bool x_issued = false;
-        for (;;) {
+        while (ok) {
             int t = -1;
-            if (lane == 0 && ok && !*sy.abort_flag) t = p.rows.T - 1 - atomicAdd(p.ws, 1);
+            if (lane == 0 && !*sy.abort_flag) t = p.rows.T - 1 - atomicAdd(p.ws, 1);
             t = __shfl_sync(kFull, t, 0);
             if (t < 0) break;
             const RowMsg m = row_msg(p.rows, t, lane);
             const int nb = max(1, (m.n_slots + kBT - 1) / kBT);
-            ok = wait_bar_warp(bar(BX_EMPTY), x_ph ^ 1, sy);
-            if (!ok) break;
-            if (lane == 0) ptx::mbar_arrive_expect_tx(bar(BX_FULL), 16 * kGroup);
-            __syncwarp();
-            if (lane < 16)
-                load_group(sX + lane * kGroup, (lane & 1) ? &tm_do : &tm_q, bar(BX_FULL), t * kH + 8 * (lane >> 1));
-            x_issued = true;
-            x_ph ^= 1;
-            for (int b = 0; b < nb && ok; ++b, ++g) {
+            for (int b = 0; b < nb; ++b, ++g) {
                 const int t0 = token_of(p.rows, m, b * kBT + 2 * lane), t1 = token_of(p.rows, m, b * kBT + 2 * lane + 1);
                 // validity word w (tokens 32w .. 32w + 31) from lanes 16w .. 16w + 15
                 uint32_t mw = ((t0 >= 0 ? 1u : 0u) | (t1 >= 0 ? 2u : 0u)) << (2 * (lane & 15));
@@ -238,9 +245,35 @@ __global__ void __launch_bounds__(kThreads, 1)
             info[is].t = -1;
             ptx::mbar_arrive(bar(BI_FULL + is));
         }
+    } else if (warp == 2) {
+        // ---------------- X ----------------
+        if (lane == 0) {
+            ptx::tma_prefetch_desc(&tm_q);
+            ptx::tma_prefetch_desc(&tm_do);
+        }
+        uint32_t x_ph = 0;
+        bool issued = false;
+        for (int g = 0;; ++g) {
+            const int is = g % kInfoSlots;
+            if (!wait_bar_warp(bar(BI_FULL + is), (g / kInfoSlots) & 1, sy)) break;
+            const int t = info[is].t, b = info[is].b;
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar(BI_EMPTY + is));
+            if (t < 0) break;
+            if (b > 0) continue;
+            // (known some blocks ahead: into L2 meanwhile)
+            if (lane < 2) prefetch_l2((lane ? p.d_o : p.q) + static_cast<int64_t>(t) * kH * kDc, kH * kDc * 2);
+            if (!wait_bar_warp(bar(BX_EMPTY), x_ph ^ 1, sy)) break;
+            if (lane == 0) ptx::mbar_arrive_expect_tx(bar(BX_FULL), 16 * kGroup);
+            __syncwarp();
+            if (lane < 16)
+                load_group(sX + lane * kGroup, (lane & 1) ? &tm_do : &tm_q, bar(BX_FULL), t * kH + 8 * (lane >> 1));
+            issued = true;
+            x_ph ^= 1;
+        }
         // no load of X may still be in flight when the CTA ends: a wait of its own,
         // bounded by the default limit and blind to the abort flag
-        if (x_issued) {
+        if (issued) {
             const uint64_t t0 = ptx::globaltimer();
             while (!ptx::mbar_try_wait(bar(BX_FULL), x_ph ^ 1))
                 if (ptx::globaltimer() - t0 > kTimeoutNs) break;
@@ -396,43 +429,49 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp >= kSumWarp0 && warp < kLoaderWarp0) {
         // ---------------- sums of dC ----------------
-        const int sub = warp & 3;
+        const int sub = warp & 3, set = (warp - kSumWarp0) >> 2;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * sub) << 16) + kTmemSum;
-        uint32_t nd = 0;
+        const uint32_t stage = sbase + kOffStage + (warp - kSumWarp0) * kStage;
         bool ok = true;
         for (int g = 0; ok; ++g) {
             const int is = g % kInfoSlots;
             ok = wait_bar_warp(bar(BI_FULL + is), (g / kInfoSlots) & 1, sy);
             if (!ok || info[is].t < 0) break;
-            const int4 *tk = reinterpret_cast<const int4 *>(toks + is * kBT);
-            for (int part = 0; part < kParts; ++part, ++nd) {
-                const uint32_t s = nd % kSumSlots;
+            // the tokens whose sums this lane adds to: 4 k + lane / 8
+            int tk[kBT / 4];
+#pragma unroll
+            for (int k = 0; k < kBT / 4; ++k) tk[k] = toks[is * kBT + 4 * k + (lane >> 3)];
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar(BI_EMPTY + is));
+            for (int part = set; part < kParts; part += 2) {
+                const uint32_t nd = static_cast<uint32_t>(g) * kParts + part, s = nd % kSumSlots;
                 ok = wait_bar_warp(bar(BD_FULL + s), (nd / kSumSlots) & 1, sy);
                 if (!ok) break;
                 ptx::tc_fence_after();
-                float *to = p.acc + part * 128 + 32 * sub + lane;
-#pragma unroll 1
-                for (int hh = 0; hh < 2; ++hh) {
-                    uint32_t v[32];
-                    ptx::tmem_ld32(lanes + s * 64 + hh * 32, v);
-                    ptx::tmem_ld_wait(v);
-                    if (hh == 1) {
+                float *to = p.acc + part * 128 + 32 * sub + 4 * (lane & 7);
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    uint32_t v[16];
+                    tmem_ld16(lanes + s * 64 + h * 16, v);
+                    if (h == 3) {
                         ptx::tc_fence_before();
                         __syncwarp();
                         if (lane == 0) ptx::mbar_arrive(bar(BD_EMPTY + s));
                     }
+                    // (lanes are latent columns: through shared memory, so that eight lanes
+                    // add 128 bytes of a token's row, 16 each)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int4 k = tk[8 * hh + i];
-                        if (k.x >= 0) red_add(to + static_cast<int64_t>(k.x) * kDc, v[4 * i]);
-                        if (k.y >= 0) red_add(to + static_cast<int64_t>(k.y) * kDc, v[4 * i + 1]);
-                        if (k.z >= 0) red_add(to + static_cast<int64_t>(k.z) * kDc, v[4 * i + 2]);
-                        if (k.w >= 0) red_add(to + static_cast<int64_t>(k.w) * kDc, v[4 * i + 3]);
+                    for (int i = 0; i < 16; ++i) st_shared(stage + i * 128 + lane * 4, v[i]);
+                    __syncwarp();
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float4 x = ptx::ld_shared_v4(stage + k * 512 + lane * 16);
+                        const int tok = tk[4 * h + k];
+                        if (tok >= 0) red_add(to + static_cast<int64_t>(tok) * kDc, x);
                     }
+                    __syncwarp();
                 }
             }
-            __syncwarp();
-            if (ok && lane == 0) ptx::mbar_arrive(bar(BI_EMPTY + is));
         }
     } else if (warp >= kLoaderWarp0) {
         // ---------------- loaders ----------------
@@ -555,7 +594,9 @@ int run_sparse_mla_bwd(const SparseMlaArgs &a, const SparseMlaGrad &g, cudaStrea
     uint8_t *ws = static_cast<uint8_t *>(a.workspace);
     Params p{};
     p.rows = row_lists(a);
+    p.q = static_cast<const uint16_t *>(a.q);
     p.kv = static_cast<const uint16_t *>(a.kv);
+    p.d_o = static_cast<const uint16_t *>(g.d_o);
     float2 *stats = reinterpret_cast<float2 *>(ws + 256);
     p.stats = stats;
     p.dq = static_cast<uint16_t *>(g.dq);
