@@ -26,9 +26,10 @@
 //   warps 12-15  dC^T from tensor memory, added to the FP32 sums in L2
 //   warps 16-23  loaders: the tokens' latent rows by 16-byte cp.async, a pair of
 //                warps per slot of 128 columns
-// A row's block order is scores, dQ (which frees the slots one by one, so that the
-// next block's rows land while dC is computed), dC in four parts through three slots
-// of tensor memory.
+// The MMAs' order is: a block's scores; the second half of the last block's dC,
+// while P and dS are made; dQ, which frees the slots one by one; the first half of
+// dC, while the next block's rows land.  dC goes in four parts through three slots of
+// tensor memory.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -70,7 +71,7 @@ constexpr int kOffInfo = kOffStage + kSumWarps * kStage;
 constexpr int kOffTok = kOffInfo + kInfoSlots * 32;    // token ids [kInfoSlots][64]
 constexpr int kOffBar = kOffTok + kInfoSlots * kBT * 4;
 enum {
-    BX_FULL = 0, BX_EMPTY, BC_FULL, BC_EMPTY = BC_FULL + kSlots, BS_FULL = BC_EMPTY + kSlots, BP_FULL,
+    BX_FULL = 0, BX_EMPTY, BC_FULL, BC_EMPTY = BC_FULL + kSlots, BS_FULL = BC_EMPTY + kSlots, BP_FULL, BP_EMPTY,
     BQ_FULL, BQ_EMPTY, BD_FULL, BD_EMPTY = BD_FULL + kSumSlots, BI_FULL = BD_EMPTY + kSumSlots,
     BI_EMPTY = BI_FULL + kInfoSlots, BDRAIN = BI_EMPTY + kInfoSlots, NBARS
 };
@@ -179,6 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ptx::mbar_init(bar(BS_FULL), 1);
         ptx::mbar_init(bar(BP_FULL), kGradWarps);
+        ptx::mbar_init(bar(BP_EMPTY), 1);
         ptx::mbar_init(bar(BQ_FULL), 1);
         ptx::mbar_init(bar(BQ_EMPTY), kGradWarps);
         for (int i = 0; i < kSumSlots; ++i) {
@@ -284,13 +286,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool one = ptx::elect_one();
         int g = 0;
         uint32_t c_ph = 0, x_ph = 0, q_ph = 0, nd = 0;      // nd: parts of dC so far
-        bool any = false;
+        bool any = false, rest = false;                     // rest: the last block's dC is half done
+        // two parts of dC^T = X^T . [dS; P]
+        auto two_parts = [&](int part0) {
+#pragma unroll 1
+            for (int part = part0; part < part0 + 2; ++part, ++nd) {
+                const uint32_t s = nd % kSumSlots;
+                if (!wait_bar_warp(bar(BD_EMPTY + s), ((nd / kSumSlots) & 1) ^ 1, sy)) return false;
+                ptx::tc_fence_after();
+                if (one) {
+                    const uint64_t ad = desc_mn(sX + part * 2048, 1024, kGroup), bd = desc_mn(sP, 1024, 1024);
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+                        ptx::mma_bf16(tmem + kTmemSum + s * 64, ad + kk * (2 * kGroup / 16), bd + kk * 128,
+                                      idesc | ptx::kIdescAMajorMN | ptx::kIdescBMajorMN, kk > 0);
+                    ptx::mma_commit(bar(BD_FULL + s));
+                }
+            }
+            if (part0 > 0 && one) ptx::mma_commit(bar(BP_EMPTY));
+            return true;
+        };
         for (;;) {
             const int is = g % kInfoSlots;
             if (!wait_bar_warp(bar(BI_FULL + is), (g / kInfoSlots) & 1, sy)) break;
             const BInfo in = info[is];
             __syncwarp();
             if (one) ptx::mbar_arrive(bar(BI_EMPTY + is));
+            if (rest && (in.t < 0 || in.b == 0)) {
+                // the row ends: X may go once its last block is done
+                if (!two_parts(2)) break;
+                if (one) ptx::mma_commit(bar(BX_EMPTY));
+                rest = false;
+            }
             if (in.t < 0) break;
             if (in.b == 0) {
                 if (!wait_bar_warp(bar(BX_FULL), x_ph, sy)) break;
@@ -316,6 +343,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!ok) break;
             if (one) ptx::mma_commit(bar(BS_FULL));
+            // the second half of the last block's dC while P and dS are made
+            if (rest && !two_parts(2)) break;
             if (!wait_bar_warp(bar(BP_FULL), g & 1, sy)) break;
             if (in.b == 0 && !wait_bar_warp(bar(BQ_EMPTY), q_ph ^ 1, sy)) break;
             ptx::tc_fence_after();
@@ -330,22 +359,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (in.b == in.nb - 1) ptx::mma_commit(bar(BQ_FULL));
             }
             if (in.b == in.nb - 1) q_ph ^= 1;
-            for (int part = 0; part < kParts; ++part, ++nd) {
-                const uint32_t s = nd % kSumSlots;
-                ok = wait_bar_warp(bar(BD_EMPTY + s), ((nd / kSumSlots) & 1) ^ 1, sy);
-                if (!ok) break;
-                ptx::tc_fence_after();
-                if (one) {
-                    const uint64_t ad = desc_mn(sX + part * 2048, 1024, kGroup), bd = desc_mn(sP, 1024, 1024);
-#pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        ptx::mma_bf16(tmem + kTmemSum + s * 64, ad + kk * (2 * kGroup / 16), bd + kk * 128,
-                                      idesc | ptx::kIdescAMajorMN | ptx::kIdescBMajorMN, kk > 0);
-                    ptx::mma_commit(bar(BD_FULL + s));
-                }
-            }
-            if (!ok) break;
-            if (one && in.b == in.nb - 1) ptx::mma_commit(bar(BX_EMPTY));
+            if (!two_parts(0)) break;
+            rest = true;
             c_ph ^= 1;
             ++g;
         }
@@ -383,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t r[32];
             ptx::tmem_ld16x256_x8(s_at, r);
             ptx::tmem_ld_wait(r);
-            // (this block's scores come behind the last block's dC, which read [dS; P])
+            uint32_t w2[8], ds2[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const uint32_t m = in.mask[j >> 2] >> (8 * (j & 3) + 2 * (lane & 3));
@@ -396,9 +411,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     w[e] = v ? x : 0.f;
                     ds[e] = v ? y : 0.f;
                 }
+                w2[j] = pack_bf16(w[0], w[1]);
+                ds2[j] = pack_bf16(ds[0], ds[1]);
+            }
+            // the last block's dC has read [dS; P]
+            if (!wait_bar_warp(bar(BP_EMPTY), (g & 1) ^ 1, sy)) break;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
                 const uint32_t at = row + ((j ^ (lane >> 2)) << 4);
-                st_shared(at, pack_bf16(ds[0], ds[1]));
-                st_shared(at + 1024, pack_bf16(w[0], w[1]));
+                st_shared(at, ds2[j]);
+                st_shared(at + 1024, w2[j]);
             }
             ptx::tc_fence_before();
             ptx::fence_proxy_async_smem();
