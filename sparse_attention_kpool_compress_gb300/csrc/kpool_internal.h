@@ -129,8 +129,8 @@ int encode_bf16_tmap(CUtensorMap *m, const void *base, uint64_t cols, uint64_t r
 // boxes of 64 columns x box_rows rows of one page.
 int encode_bf16_pages_tmap(CUtensorMap *m, const void *base, uint64_t cols, uint64_t rows, uint64_t pages,
                            uint64_t page_stride, uint32_t box_rows);
-// The same of rows of 512 columns: boxes of 8 rows, which land as eight chunks of
-// 64 columns (1 KB each) one after another.
+// The same of rows of 512 columns, [8 chunks of 64 columns][rows]: boxes of 8 rows
+// x two chunks (1 KB each, one after another).
 int encode_bf16_groups_tmap(CUtensorMap *m, const void *base, uint64_t rows);
 
 // Sparse attention over the selection (kpool_mla.cu): tok_idx mode when

@@ -55,6 +55,7 @@ constexpr int kChunk = kBT * 128;       // 64 latent columns of a block
 constexpr int kSlots = 4;               // 128 columns each
 constexpr int kSlot = 2 * kChunk;
 constexpr int kParts = 4;               // dQ^T and dC^T in parts of 128 latent columns
+constexpr int kFirst = 3;               // parts of dC^T before the next block's scores
 constexpr int kSumSlots = 3;
 constexpr int kInfoSlots = 4;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
@@ -71,7 +72,7 @@ constexpr int kOffInfo = kOffStage + kSumWarps * kStage;
 constexpr int kOffTok = kOffInfo + kInfoSlots * 32;    // token ids [kInfoSlots][64]
 constexpr int kOffBar = kOffTok + kInfoSlots * kBT * 4;
 enum {
-    BX_FULL = 0, BX_EMPTY, BC_FULL, BC_EMPTY = BC_FULL + kSlots, BS_FULL = BC_EMPTY + kSlots, BP_FULL, BP_EMPTY,
+    BX_FULL = 0, BX_EMPTY = BX_FULL + kParts, BC_FULL, BC_EMPTY = BC_FULL + kSlots, BS_FULL = BC_EMPTY + kSlots, BP_FULL, BP_EMPTY,
     BQ_FULL, BQ_EMPTY, BD_FULL, BD_EMPTY = BD_FULL + kSumSlots, BI_FULL = BD_EMPTY + kSumSlots,
     BI_EMPTY = BI_FULL + kInfoSlots, BDRAIN = BI_EMPTY + kInfoSlots, NBARS
 };
@@ -110,13 +111,13 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t chunk, uint
     return (ptx::smem_desc_mn_sw128(saddr, chunk) & ~(0x3FFFull << 32)) | (static_cast<uint64_t>(group >> 4) << 32);
 }
 
-// X: eight rows x all 512 columns of q or d_o, as eight chunks of 64 columns.
-__device__ __forceinline__ void load_group(uint32_t dst, const void *desc, uint32_t bar, int row)
+// X: eight rows x 128 columns of q or d_o, as two chunks of 64 columns.
+__device__ __forceinline__ void load_group(uint32_t dst, const void *desc, uint32_t bar, int row, int chunk)
 {
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
         " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
-        "l"(desc), "r"(bar), "r"(0), "r"(row), "r"(0)
+        "l"(desc), "r"(bar), "r"(0), "r"(row), "r"(chunk)
         : "memory");
 }
 
@@ -172,10 +173,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        ptx::mbar_init(bar(BX_FULL), 1);
+        for (int i = 0; i < kParts; ++i) ptx::mbar_init(bar(BX_FULL + i), 1);
         ptx::mbar_init(bar(BX_EMPTY), 1);
         for (int i = 0; i < kSlots; ++i) {
-            ptx::mbar_init(bar(BC_FULL + i), 64);   // the slot's two loader warps
+            ptx::mbar_init(bar(BC_FULL + i), 2);    // the slot's two loader warps
             ptx::mbar_init(bar(BC_EMPTY + i), 1);
         }
         ptx::mbar_init(bar(BS_FULL), 1);
@@ -185,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::mbar_init(bar(BQ_EMPTY), kGradWarps);
         for (int i = 0; i < kSumSlots; ++i) {
             ptx::mbar_init(bar(BD_FULL + i), 1);
-            ptx::mbar_init(bar(BD_EMPTY + i), 4);       // a part goes to four of the sums warps
+            ptx::mbar_init(bar(BD_EMPTY + i), kSumWarps);
         }
         for (int i = 0; i < kInfoSlots; ++i) {
             ptx::mbar_init(bar(BI_FULL + i), 1);
@@ -266,10 +267,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             // (known some blocks ahead: into L2 meanwhile)
             if (lane < 2) prefetch_l2((lane ? p.d_o : p.q) + static_cast<int64_t>(t) * kH * kDc, kH * kDc * 2);
             if (!wait_bar_warp(bar(BX_EMPTY), x_ph ^ 1, sy)) break;
-            if (lane == 0) ptx::mbar_arrive_expect_tx(bar(BX_FULL), 16 * kGroup);
+            // in pieces of 128 columns, as the scores take them
+            if (lane < kParts) ptx::mbar_arrive_expect_tx(bar(BX_FULL + lane), 16 * kGroup / kParts);
             __syncwarp();
             if (lane < 16)
-                load_group(sX + lane * kGroup, (lane & 1) ? &tm_do : &tm_q, bar(BX_FULL), t * kH + 8 * (lane >> 1));
+                for (int i = 0; i < kParts; ++i)
+                    load_group(sX + lane * kGroup + i * 2048, (lane & 1) ? &tm_do : &tm_q, bar(BX_FULL + i),
+                               t * kH + 8 * (lane >> 1), 2 * i);
             issued = true;
             x_ph ^= 1;
         }
@@ -277,8 +281,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // bounded by the default limit and blind to the abort flag
         if (issued) {
             const uint64_t t0 = ptx::globaltimer();
-            while (!ptx::mbar_try_wait(bar(BX_FULL), x_ph ^ 1))
-                if (ptx::globaltimer() - t0 > kTimeoutNs) break;
+            for (int i = 0; i < kParts; ++i)
+                while (!ptx::mbar_try_wait(bar(BX_FULL + i), x_ph ^ 1))
+                    if (ptx::globaltimer() - t0 > kTimeoutNs) break;
         }
     } else if (warp == 1) {
         // ---------------- MMA issuer ----------------
@@ -287,10 +292,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         int g = 0;
         uint32_t c_ph = 0, x_ph = 0, q_ph = 0, nd = 0;      // nd: parts of dC so far
         bool any = false, rest = false;                     // rest: the last block's dC is half done
-        // two parts of dC^T = X^T . [dS; P]
-        auto two_parts = [&](int part0) {
+        // parts of dC^T = X^T . [dS; P]
+        auto sum_parts = [&](int part0, int part1) {
 #pragma unroll 1
-            for (int part = part0; part < part0 + 2; ++part, ++nd) {
+            for (int part = part0; part < part1; ++part, ++nd) {
                 const uint32_t s = nd % kSumSlots;
                 if (!wait_bar_warp(bar(BD_EMPTY + s), ((nd / kSumSlots) & 1) ^ 1, sy)) return false;
                 ptx::tc_fence_after();
@@ -314,19 +319,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (one) ptx::mbar_arrive(bar(BI_EMPTY + is));
             if (rest && (in.t < 0 || in.b == 0)) {
                 // the row ends: X may go once its last block is done
-                if (!two_parts(2)) break;
+                if (!sum_parts(kFirst, kParts)) break;
                 if (one) ptx::mma_commit(bar(BX_EMPTY));
                 rest = false;
             }
             if (in.t < 0) break;
-            if (in.b == 0) {
-                if (!wait_bar_warp(bar(BX_FULL), x_ph, sy)) break;
-                x_ph ^= 1;
-            }
             bool ok = true;
             // (the last block's scores were read before its P was complete)
             for (int sl = 0; sl < kSlots; ++sl) {
-                ok = wait_bar_warp(bar(BC_FULL + sl), c_ph, sy);
+                ok = (in.b > 0 || wait_bar_warp(bar(BX_FULL + sl), x_ph, sy)) && wait_bar_warp(bar(BC_FULL + sl), c_ph, sy);
                 if (!ok) break;
                 ptx::tc_fence_after();
                 if (one) {
@@ -342,9 +343,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 any = true;
             }
             if (!ok) break;
+            if (in.b == 0) x_ph ^= 1;
             if (one) ptx::mma_commit(bar(BS_FULL));
             // the second half of the last block's dC while P and dS are made
-            if (rest && !two_parts(2)) break;
+            if (rest && !sum_parts(kFirst, kParts)) break;
             if (!wait_bar_warp(bar(BP_FULL), g & 1, sy)) break;
             if (in.b == 0 && !wait_bar_warp(bar(BQ_EMPTY), q_ph ^ 1, sy)) break;
             ptx::tc_fence_after();
@@ -359,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (in.b == in.nb - 1) ptx::mma_commit(bar(BQ_FULL));
             }
             if (in.b == in.nb - 1) q_ph ^= 1;
-            if (!two_parts(0)) break;
+            if (!sum_parts(0, kFirst)) break;
             rest = true;
             c_ph ^= 1;
             ++g;
@@ -451,31 +453,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp >= kSumWarp0 && warp < kLoaderWarp0) {
         // ---------------- sums of dC ----------------
-        const int sub = warp & 3, set = (warp - kSumWarp0) >> 2;
-        const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * sub) << 16) + kTmemSum;
+        // Four warps take the first 32 tokens of each part, four the others.
+        const int sub = warp & 3, tok0 = 32 * ((warp - kSumWarp0) >> 2);
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * sub) << 16) + kTmemSum + tok0;
         const uint32_t stage = sbase + kOffStage + (warp - kSumWarp0) * kStage;
+        uint32_t nd = 0;
         bool ok = true;
         for (int g = 0; ok; ++g) {
             const int is = g % kInfoSlots;
             ok = wait_bar_warp(bar(BI_FULL + is), (g / kInfoSlots) & 1, sy);
             if (!ok || info[is].t < 0) break;
             // the tokens whose sums this lane adds to: 4 k + lane / 8
-            int tk[kBT / 4];
+            int tk[8];
 #pragma unroll
-            for (int k = 0; k < kBT / 4; ++k) tk[k] = toks[is * kBT + 4 * k + (lane >> 3)];
+            for (int k = 0; k < 8; ++k) tk[k] = toks[is * kBT + tok0 + 4 * k + (lane >> 3)];
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(bar(BI_EMPTY + is));
-            for (int part = set; part < kParts; part += 2) {
-                const uint32_t nd = static_cast<uint32_t>(g) * kParts + part, s = nd % kSumSlots;
+            for (int part = 0; part < kParts; ++part, ++nd) {
+                const uint32_t s = nd % kSumSlots;
                 ok = wait_bar_warp(bar(BD_FULL + s), (nd / kSumSlots) & 1, sy);
                 if (!ok) break;
                 ptx::tc_fence_after();
                 float *to = p.acc + part * 128 + 32 * sub + 4 * (lane & 7);
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
+                for (int h = 0; h < 2; ++h) {
                     uint32_t v[16];
                     tmem_ld16(lanes + s * 64 + h * 16, v);
-                    if (h == 3) {
+                    if (h == 1) {
                         ptx::tc_fence_before();
                         __syncwarp();
                         if (lane == 0) ptx::mbar_arrive(bar(BD_EMPTY + s));
@@ -508,22 +512,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int is = g % kInfoSlots;
             ok = wait_bar_warp(bar(BI_FULL + is), (g / kInfoSlots) & 1, sy);
             if (!ok || info[is].t < 0) break;
+            int tk[kBT / 4];                                       // rows t64 / 16 + 4 i
+#pragma unroll
+            for (int i = 0; i < kBT / 4; ++i) tk[i] = toks[is * kBT + (t64 >> 4) + 4 * i];
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar(BI_EMPTY + is));
             ok = wait_bar_warp(bar(BC_EMPTY + sl), c_ph ^ 1, sy);
             if (!ok) break;
-            const int *tk = toks + is * kBT;
 #pragma unroll
-            for (int i = 0; i < kBT / 4; ++i) {                    // rows t64 / 16 + 4 i
+            for (int i = 0; i < kBT / 4; ++i) {
                 const int r = (t64 >> 4) + 4 * i;
-                const int tok = tk[r];
                 ptx::cp_async16(dst + r * 128 + (((k & 7) ^ (r & 7)) << 4),
-                                kvb + (tok >= 0 ? static_cast<int64_t>(tok) * (kDc * 2) : 0), tok >= 0 ? 16u : 0u);
+                                kvb + (tk[i] >= 0 ? static_cast<int64_t>(tk[i]) * (kDc * 2) : 0), tk[i] >= 0 ? 16u : 0u);
             }
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(bar(BI_EMPTY + is));   // token ids read
             ptx::cp_async_commit();
             ptx::cp_async_wait_all();
             ptx::fence_proxy_async_smem();
-            ptx::mbar_arrive(bar(BC_FULL + sl));
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar(BC_FULL + sl));
             c_ph ^= 1;
         }
         ptx::cp_async_wait_all();

@@ -434,7 +434,7 @@ int encode_bf16_groups_tmap(CUtensorMap *m, const void *base, uint64_t rows)
     if (!enc) return fail(KPOOL_ERR_CUDA, "cuTensorMapEncodeTiled entry point unavailable");
     const cuuint64_t gdim[3] = {64, rows, 8};
     const cuuint64_t gstride[2] = {1024, 128};
-    const cuuint32_t box[3] = {64, 8, 8};
+    const cuuint32_t box[3] = {64, 8, 2};
     const cuuint32_t estr[3] = {1, 1, 1};
     const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), gdim,
                            gstride, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
