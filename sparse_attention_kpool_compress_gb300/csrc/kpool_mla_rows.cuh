@@ -49,16 +49,22 @@ struct Sync {
     volatile uint32_t *abort_flag;
     int *status;
     uint64_t limit_ns;
+    bool poll = false;          // probes do not suspend the thread (a suspended one may outlast a short limit)
 };
+
+__device__ __forceinline__ bool probe_bar(uint32_t bar, uint32_t parity, const Sync &sy)
+{
+    return sy.poll ? ptx::mbar_test(bar, parity) : ptx::mbar_try_wait(bar, parity);
+}
 
 // Bounded mbarrier wait (completion, then the CTA abort flag, then a timer
 // that raises the flag and KPOOL_STATUS_TIMEOUT).
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const Sync &sy)
 {
-    if (ptx::mbar_try_wait(bar, parity)) return true;
+    if (probe_bar(bar, parity, sy)) return true;
     const uint64_t t0 = ptx::globaltimer();
     while (true) {
-        if (ptx::mbar_try_wait(bar, parity)) return true;
+        if (probe_bar(bar, parity, sy)) return true;
         if (*sy.abort_flag) return false;
         if (ptx::globaltimer() - t0 > sy.limit_ns) {
             *sy.abort_flag = 1u;

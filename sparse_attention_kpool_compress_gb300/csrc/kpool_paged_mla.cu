@@ -6,8 +6,29 @@
 //   s_j = scale * q[t, h, :] . c[j, :]
 //   o[t, h, :] = sum_j softmax_j(s) c[j, :],   lse[t, h] = ln sum_j exp(s_j)
 //
-// First form: a block per row, a warp per eight heads, lanes over the columns,
-// running maximum and sum.
+// Design (one persistent CTA per SM, 20 warps; a unit is a row, or a run of a row's
+// blocks where rows are few; units are handed out by an atomic counter).  Blocks of
+// 64 listed tokens C [64 x 512], two of them in shared memory, so that one is
+// multiplied while the other lands:
+//   S    [64 heads x 64]  = Q . C^T        (M = 64; A, B K-major)
+//   O^T  [512 x 64 heads] += C^T . P^T     (four parts of M = 128; A MN-major, B K-major)
+// The scores of a block run while the softmax works on the one before.  Tensor
+// memory: O^T 256 columns, S twice 64.
+//   warp 0       control: units, and per block a record with the places of its rows
+//   warp 1       issuer of the scores' MMAs (the loop in all lanes, one issues)
+//   warp 2       Q (TMA), ahead into L2
+//   warp 3       issuer of the output's MMAs
+//   warps 4-7    softmax: four threads share a row of 64 scores
+//   warps 8-11   output
+//   warps 12-19  loaders: 16-byte cp.async, a warp per block in flight and slot of
+//                128 columns
+// One reference maximum per head, raised (and O^T rescaled) only when a block's
+// scores exceed it by more than 8 in the base-2 exponent, so P <= 256; P goes to
+// shared memory in BF16 (the MMA's operand type), sums and statistics are FP32.
+//
+// Where rows are few (half the SMs or less), a row's blocks are cut into even runs,
+// FP32 outputs of the runs go to the workspace with their log-sums, and a second
+// kernel joins them.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -22,10 +43,54 @@ namespace {
 
 constexpr int kH = 64;                  // heads
 constexpr int kDc = 512;                // latent width
+constexpr int kBT = 64;                 // listed tokens per block
+constexpr int kThreads = 640;
+constexpr int kSoftWarps = 4;            // warps 4..7
+constexpr int kOutWarp0 = 8, kOutWarps = 4;
+// register split (setmaxnreg): 640 threads x 96 at launch
+constexpr int kRegsSoftmax = 152, kRegsOther = 72;
+static_assert(128 * kRegsSoftmax + 512 * kRegsOther <= 640 * 96, "register split above the launch's registers");
+constexpr int kLoaderWarp0 = 12;        // 8: two blocks x four slots
+constexpr int kChunk = kBT * 128;       // 64 latent columns of a block
+constexpr int kSlots = 4;               // 128 columns each
+constexpr int kSlot = 2 * kChunk;
+constexpr int kBlock = kSlots * kSlot;
+constexpr int kInfoSlots = 4;
+constexpr float kRescale = 8.f;         // headroom of the reference maximum (log2)
+constexpr int kMaxSplit = 16;           // runs of a row
+constexpr int kMaxSms = 160;             // that a workspace has room for
+constexpr int kPerUnit = 2;             // blocks that a run should have
+constexpr uint64_t kTimeoutNs = 2000000000ull;
+constexpr int kTmemCols = 512;          // O^T: 0..255, S: 256..319 and 320..383
+constexpr int kTmemS = 256;
+
+// shared memory (from a 1024-byte aligned base)
+constexpr int kOffQ = 0;                               // 8 chunks [64 heads x 64 columns]
+constexpr int kOffC = kOffQ + 8 * 8192;
+constexpr int kOffP = kOffC + 2 * kBlock;              // 2 x [64 heads x 64 tokens]
+constexpr int kOffInv = kOffP + 2 * 8192;              // 1 / sums of a unit [2][64]
+constexpr int kOffScale = kOffInv + 2 * kH * 4;        // rescale factors [64]
+constexpr int kOffInfo = kOffScale + kH * 4;
+constexpr int kOffAt = kOffInfo + kInfoSlots * 32;     // places of the rows [kInfoSlots][64] int64
+constexpr int kOffBar = kOffAt + kInfoSlots * kBT * 8;
+enum {
+    BQ_FULL = 0, BQ_EMPTY, BC_FULL, BC_EMPTY = BC_FULL + 2 * kSlots, BS_FULL = BC_EMPTY + 2 * kSlots,
+    BS_EMPTY = BS_FULL + 2, BP_FULL = BS_EMPTY + 2, BP_EMPTY = BP_FULL + 2, BO_FULL = BP_EMPTY + 2, BO_EMPTY,
+    BL_FULL, BL_EMPTY = BL_FULL + 2, BI_FULL = BL_EMPTY + 2, BI_EMPTY = BI_FULL + kInfoSlots,
+    BDRAIN = BI_EMPTY + kInfoSlots, NBARS = BDRAIN + 2
+};
+constexpr int kOffMisc = kOffBar + NBARS * 8;          // [0] tmem base, [1] abort flag
+constexpr int kSmemBytes = kOffMisc + 16 + 1024;       // and alignment slack
+static_assert(kSmemBytes <= 232448, "shared memory over the per-block limit");
 
 struct Params {
     PagedMlaArgs a;
-    int *status;
+    float c_scale;              // softmax scale * log2(e)
+    int split;                  // runs of a row (1: rows are whole)
+    int *ws;                    // [0] unit counter, [1] status
+    float *part_lse;            // [Tq * split, 64], base 2
+    float *part_o;              // [Tq * split, 64, 512]
+    uint64_t wait_limit_ns;
 };
 
 // What lists the tokens of one row.
@@ -61,17 +126,21 @@ __device__ __forceinline__ PagedRow paged_row(const PagedMlaArgs &p, int t, int 
     return m;
 }
 
-// Where slot j of the row lies in the pages, in elements (-1: no token there).
-__device__ __forceinline__ int64_t paged_at(const PagedMlaArgs &p, const PagedRow &m, int j, bool &bad)
+// The pool that slot j of the row is in (-1: none, or the tail).
+__device__ __forceinline__ int pool_of(const PagedMlaArgs &p, const PagedRow &m, int j)
+{
+    return j < m.n_sel * p.kpool ? p.pool_idx[static_cast<int64_t>(m.t) * p.Kp + j / p.kpool] : -1;
+}
+
+// Where slot j of the row, in pool g, lies in the pages, in elements (-1: no token there).
+__device__ __forceinline__ int64_t paged_at(const PagedMlaArgs &p, const PagedRow &m, int j, int g, bool &bad)
 {
     if (j >= m.n_slots) return -1;
     const int npt = m.n_sel * p.kpool;
     int64_t v;
     if (j < npt) {
-        const int e = j / p.kpool;
-        const int g = __ldg(p.pool_idx + static_cast<int64_t>(m.t) * p.Kp + e);
         if (g < m.pool_lo || g >= m.pool_hi) return -1;
-        v = static_cast<int64_t>(g - m.pool_lo) * p.kpool + (j - e * p.kpool);
+        v = static_cast<int64_t>(g - m.pool_lo) * p.kpool + j % p.kpool;
     } else {
         v = m.tau - m.n_tail + 1 + (j - npt);
     }
@@ -88,99 +157,571 @@ __device__ __forceinline__ int64_t paged_at(const PagedMlaArgs &p, const PagedRo
     return id * p.kv_page_stride + static_cast<int64_t>(static_cast<int>(v) - page * p.page_size) * kDc;
 }
 
-__device__ __forceinline__ void load16(const uint16_t *row, int lane, float (&v)[16])
+// One block of a unit.
+struct BInfo {
+    int unit, b, nb, ksteps;    // b-th of the unit's nb blocks
+    uint32_t mask[2];           // bit r of mask[r / 32]: listed token r is valid
+    int pad[2];
+};
+static_assert(sizeof(BInfo) == 32, "BInfo slot");
+
+__device__ __forceinline__ void prefetch_l2(const void *from, uint32_t bytes)
 {
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        const uint4 x = *reinterpret_cast<const uint4 *>(row + 256 * half + 8 * lane);
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[8 * half + 2 * i] = __uint_as_float(w[i] << 16);
-            v[8 * half + 2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ void st_shared(uint32_t saddr, uint32_t v)
+{
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(saddr), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&b);
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ Params p)
+{
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
+    const uint32_t sbase = ptx::smem_u32(smem);
+    const uint32_t sQ = sbase + kOffQ, sC = sbase + kOffC, sP = sbase + kOffP;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kOffBar);
+    auto bar = [&](int i) { return ptx::smem_u32(&bars[i]); };
+    uint32_t *misc = reinterpret_cast<uint32_t *>(smem + kOffMisc);
+    BInfo *info = reinterpret_cast<BInfo *>(smem + kOffInfo);
+    int64_t *ats = reinterpret_cast<int64_t *>(smem + kOffAt);
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        ptx::mbar_init(bar(BQ_FULL), 1);
+        ptx::mbar_init(bar(BQ_EMPTY), 1);
+        for (int i = 0; i < 2 * kSlots; ++i) {
+            ptx::mbar_init(bar(BC_FULL + i), 1);
+            ptx::mbar_init(bar(BC_EMPTY + i), 1);
         }
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(bar(BS_FULL + i), 1);
+            ptx::mbar_init(bar(BS_EMPTY + i), kSoftWarps);
+            ptx::mbar_init(bar(BP_FULL + i), kSoftWarps);
+            ptx::mbar_init(bar(BP_EMPTY + i), 1);
+            ptx::mbar_init(bar(BL_FULL + i), kSoftWarps);
+            ptx::mbar_init(bar(BL_EMPTY + i), kOutWarps);
+            ptx::mbar_init(bar(BDRAIN + i), 1);
+        }
+        ptx::mbar_init(bar(BO_FULL), 1);
+        ptx::mbar_init(bar(BO_EMPTY), kOutWarps);
+        for (int i = 0; i < kInfoSlots; ++i) {
+            ptx::mbar_init(bar(BI_FULL + i), 1);
+            // (even blocks go to four of the loaders, odd ones to the others)
+            ptx::mbar_init(bar(BI_EMPTY + i), 3 + kSoftWarps + kOutWarps + kSlots);
+        }
+        misc[1] = 0u;
+        ptx::fence_mbar_init();
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(ptx::smem_u32(&misc[0]), kTmemCols);
+        ptx::tmem_relinquish();
+        ptx::tc_fence_before();
+    }
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = misc[0];
+    const Sync sy{reinterpret_cast<volatile uint32_t *>(&misc[1]), p.ws + 1, p.wait_limit_ns, p.wait_limit_ns < 1000000u};
+    ptx::grid_dependents_launch();
+    ptx::grid_dependency_wait();        // the cleared counter and status
+
+    // the block records, one after another, for every role but the loaders
+    auto next_info = [&](int g, BInfo &in) {
+        const int is = g % kInfoSlots;
+        if (!wait_bar_warp(bar(BI_FULL + is), (g / kInfoSlots) & 1, sy)) return false;
+        in = info[is];
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(BI_EMPTY + is));
+        return in.unit >= 0;
+    };
+
+    if (warp < 4) {
+    ptx::setmaxnreg_dec<kRegsOther>();
+    if (warp == 0) {
+        // ---------------- control: units and their blocks ----------------
+        const int units = static_cast<int>(p.a.Tq) * p.split;
+        bool ok = true, bad = false;
+        int g = 0;                      // blocks published
+        while (ok) {
+            int u = -1;
+            if (lane == 0 && !*sy.abort_flag) u = atomicAdd(p.ws, 1);
+            u = __shfl_sync(kFull, u, 0);
+            if (u < 0 || u >= units) break;
+            const int t = u / p.split;
+            const PagedRow m = paged_row(p.a, t, lane);
+            bad |= m.bad;
+            const int all = (m.n_slots + kBT - 1) / kBT, per = (all + p.split - 1) / p.split;
+            const int b0 = (u - t * p.split) * per, nb = max(0, min(all - b0, per));
+            if (nb == 0) {
+                // nothing listed: what the output warps would write
+                float *l = p.split > 1 ? p.part_lse + static_cast<int64_t>(u) * kH : p.a.lse + static_cast<int64_t>(t) * kH;
+                l[lane] = l[32 + lane] = -INFINITY;
+                if (p.split == 1) {
+                    uint4 *o = static_cast<uint4 *>(p.a.o) + static_cast<int64_t>(t) * (kH * kDc / 8);
+                    for (int i = lane; i < kH * kDc / 8; i += 32) o[i] = make_uint4(0, 0, 0, 0);
+                }
+                continue;
+            }
+            const int j0 = b0 * kBT + 2 * lane;
+            int g0 = pool_of(p.a, m, j0), g1 = pool_of(p.a, m, j0 + 1);
+            for (int b = 0; b < nb; ++b, ++g) {
+                const int j = j0 + b * kBT;
+                const int64_t at0 = paged_at(p.a, m, j, g0, bad), at1 = paged_at(p.a, m, j + 1, g1, bad);
+                // (the next block's pools, so that only the pages' table is waited for there)
+                g0 = pool_of(p.a, m, j + kBT);
+                g1 = pool_of(p.a, m, j + kBT + 1);
+                // validity word w (tokens 32w .. 32w + 31) from lanes 16w .. 16w + 15
+                uint32_t mw = ((at0 >= 0 ? 1u : 0u) | (at1 >= 0 ? 2u : 0u)) << (2 * (lane & 15));
+                mw |= __shfl_xor_sync(kFull, mw, 1);
+                mw |= __shfl_xor_sync(kFull, mw, 2);
+                mw |= __shfl_xor_sync(kFull, mw, 4);
+                mw |= __shfl_xor_sync(kFull, mw, 8);
+                const int is = g % kInfoSlots;
+                ok = wait_bar_warp(bar(BI_EMPTY + is), ((g / kInfoSlots) & 1) ^ 1, sy);
+                if (!ok) break;
+                ats[is * kBT + 2 * lane] = at0;
+                ats[is * kBT + 2 * lane + 1] = at1;
+                if ((lane & 15) == 0) info[is].mask[lane >> 4] = mw;
+                if (lane == 0) {
+                    info[is].unit = u;
+                    info[is].b = b;
+                    info[is].nb = nb;
+                    info[is].ksteps = (min(kBT, m.n_slots - (b0 + b) * kBT) + 15) / 16;
+                }
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(bar(BI_FULL + is));
+            }
+        }
+        // end of the block stream, for the loaders of even and of odd blocks
+        for (int e = 0; e < 2 && ok; ++e, ++g) {
+            const int is = g % kInfoSlots;
+            ok = wait_bar_warp(bar(BI_EMPTY + is), ((g / kInfoSlots) & 1) ^ 1, sy);
+            if (ok && lane == 0) {
+                info[is].unit = -1;
+                ptx::mbar_arrive(bar(BI_FULL + is));
+            }
+        }
+        if (__any_sync(kFull, bad) && lane == 0) atomicOr(sy.status, KPOOL_STATUS_BAD_PAGE);
+    } else if (warp == 1) {
+        // ---------------- issuer of the scores ----------------
+        constexpr uint32_t idesc = ptx::make_idesc(1u, 64, 64);
+        const bool one = ptx::elect_one();
+        uint32_t q_ph = 0;
+        bool any = false;
+        BInfo in;
+        for (int g = 0; next_info(g, in); ++g) {
+            const int buf = g & 1;
+            const uint32_t ph = (g >> 1) & 1;
+            bool ok = in.b > 0 || wait_bar_warp(bar(BQ_FULL), q_ph, sy);
+            if (in.b == 0) q_ph ^= 1;
+            ok = ok && wait_bar_warp(bar(BS_EMPTY + buf), ph ^ 1, sy);
+            for (int sl = 0; sl < kSlots && ok; ++sl) {
+                ok = wait_bar_warp(bar(BC_FULL + buf * kSlots + sl), ph, sy);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                if (one) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint64_t ad = ptx::smem_desc_sw128(sQ + (2 * sl + h) * 8192);
+                        const uint64_t bd = ptx::smem_desc_sw128(sC + buf * kBlock + sl * kSlot + h * kChunk);
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            ptx::mma_bf16(tmem + kTmemS + buf * 64, ad + 2 * kk, bd + 2 * kk, idesc, (sl | h | kk) != 0);
+                    }
+                }
+                any = true;
+            }
+            if (!ok) break;
+            if (one) {
+                ptx::mma_commit(bar(BS_FULL + buf));
+                if (in.b == in.nb - 1) ptx::mma_commit(bar(BQ_EMPTY));
+            }
+        }
+        if (any) {
+            if (one) ptx::mma_commit(bar(BDRAIN));
+            const uint64_t t0 = ptx::globaltimer();
+            while (!ptx::mbar_try_wait(bar(BDRAIN), 0))
+                if (ptx::globaltimer() - t0 > kTimeoutNs) break;
+        }
+    } else if (warp == 2) {
+        // ---------------- Q ----------------
+        if (lane == 0) ptx::tma_prefetch_desc(&tm_q);
+        uint32_t q_ph = 0;
+        bool issued = false;
+        BInfo in;
+        for (int g = 0; next_info(g, in); ++g) {
+            if (in.b > 0) continue;
+            const int t = in.unit / p.split;
+            // (known some blocks ahead: into L2 meanwhile)
+            if (lane == 0)
+                prefetch_l2(static_cast<const uint16_t *>(p.a.q) + static_cast<int64_t>(t) * kH * kDc, kH * kDc * 2);
+            if (!wait_bar_warp(bar(BQ_EMPTY), q_ph ^ 1, sy)) break;
+            if (lane == 0) ptx::mbar_arrive_expect_tx(bar(BQ_FULL), 8 * 8192);
+            __syncwarp();
+            if (lane < 8) ptx::tma_load_2d(sQ + lane * 8192, &tm_q, bar(BQ_FULL), 64 * lane, t * kH);
+            issued = true;
+            q_ph ^= 1;
+        }
+        // no load of Q may still be in flight when the CTA ends: a wait of its own,
+        // bounded by the default limit and blind to the abort flag
+        if (issued) {
+            const uint64_t t0 = ptx::globaltimer();
+            while (!ptx::mbar_try_wait(bar(BQ_FULL), q_ph ^ 1))
+                if (ptx::globaltimer() - t0 > kTimeoutNs) break;
+        }
+    } else {
+        // ---------------- issuer of the output ----------------
+        constexpr uint32_t idesc = ptx::make_idesc(1u, 128, 64) | ptx::kIdescAMajorMN;
+        const bool one = ptx::elect_one();
+        uint32_t o_ph = 0;
+        bool any = false;
+        BInfo in;
+        for (int g = 0; next_info(g, in); ++g) {
+            const int buf = g & 1;
+            const uint32_t ph = (g >> 1) & 1;
+            bool ok = wait_bar_warp(bar(BP_FULL + buf), ph, sy);
+            if (in.b == 0) {
+                ok = ok && wait_bar_warp(bar(BO_EMPTY), o_ph ^ 1, sy);
+                o_ph ^= 1;
+            }
+            for (int sl = 0; sl < kSlots && ok; ++sl) ok = wait_bar_warp(bar(BC_FULL + buf * kSlots + sl), ph, sy);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            any = true;
+            if (one) {
+                const uint64_t bd = ptx::smem_desc_sw128(sP + buf * 8192);
+                for (int sl = 0; sl < kSlots; ++sl) {
+                    const uint64_t ad = ptx::smem_desc_mn_sw128(sC + buf * kBlock + sl * kSlot, kChunk);
+                    for (int kk = 0; kk < in.ksteps; ++kk)
+                        ptx::mma_bf16(tmem + sl * 64, ad + kk * 128, bd + 2 * kk, idesc, in.b > 0 || kk > 0);
+                    ptx::mma_commit(bar(BC_EMPTY + buf * kSlots + sl));
+                }
+                ptx::mma_commit(bar(BP_EMPTY + buf));
+                if (in.b == in.nb - 1) ptx::mma_commit(bar(BO_FULL));
+            }
+        }
+        if (any) {
+            if (one) ptx::mma_commit(bar(BDRAIN + 1));
+            const uint64_t t0 = ptx::globaltimer();
+            while (!ptx::mbar_try_wait(bar(BDRAIN + 1), 0))
+                if (ptx::globaltimer() - t0 > kTimeoutNs) break;
+        }
+    }
+    } else if (warp < kOutWarp0) {
+        ptx::setmaxnreg_inc<kRegsSoftmax>();
+        // ---------------- softmax ----------------
+        const int sub = warp & 3;
+        const int h0 = 16 * sub + (lane >> 2);             // this thread's heads: h0 and h0 + 8
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * sub) << 16);
+        const uint32_t row = sP + h0 * 128 + (lane & 3) * 4;
+        float *inv = reinterpret_cast<float *>(smem + kOffInv), *factor = reinterpret_cast<float *>(smem + kOffScale);
+        float m[2] = {0.f, 0.f}, l[2] = {0.f, 0.f};
+        int nu = 0;                                        // units so far
+        // the four warps meet once a block, and leave together
+        for (int g = 0;; ++g) {
+            const int buf = g & 1;
+            const uint32_t ph = (g >> 1) & 1;
+            BInfo in;
+            in.unit = -1;
+            const bool more = next_info(g, in);
+            bool ok = more && wait_bar_warp(bar(BS_FULL + buf), ph, sy);
+            float v[2][16];                                // scores of tokens 8 j + 2 (lane % 4) and the next
+            bool raise = false;
+            float top[2] = {-INFINITY, -INFINITY};
+            if (ok) {
+                ptx::tc_fence_after();
+                uint32_t r[32];
+                ptx::tmem_ld16x256_x8(lanes + kTmemS + buf * 64, r);
+                ptx::tmem_ld_wait(r);
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(bar(BS_EMPTY + buf));
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint32_t mk = in.mask[j >> 2] >> (8 * (j & 3) + 2 * (lane & 3));
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const float x = (mk >> e) & 1u ? __uint_as_float(r[4 * j + 2 * k + e]) * p.c_scale : -INFINITY;
+                            v[k][2 * j + e] = x;
+                            top[k] = fmaxf(top[k], x);
+                        }
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    top[k] = fmaxf(top[k], __shfl_xor_sync(kFull, top[k], 1));
+                    top[k] = fmaxf(top[k], __shfl_xor_sync(kFull, top[k], 2));
+                    if (in.b == 0) {
+                        m[k] = top[k];
+                        l[k] = 0.f;
+                    }
+                    raise |= top[k] > m[k] + kRescale;     // (from -inf too)
+                }
+            }
+            if (ptx::named_bar_or(1, 32 * kSoftWarps, !ok || raise)) {
+                // some warp leaves, or some head's reference rises
+                if (ptx::named_bar_or(2, 32 * kSoftWarps, !ok)) break;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float now = top[k] > m[k] + kRescale ? top[k] : m[k];
+                    const float f = now == m[k] ? 1.f : ptx::ex2_approx(m[k] - now);
+                    m[k] = now;
+                    l[k] *= f;
+                    if ((lane & 3) == 0) factor[h0 + 8 * k] = f;
+                }
+                // the last block's output MMAs are done (its P has been read)
+                ok = wait_bar_warp(bar(BP_EMPTY + (buf ^ 1)), ((g - 1) >> 1) & 1, sy);
+                if (ptx::named_bar_or(2, 32 * kSoftWarps, !ok)) break;
+                ptx::tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < 8; ++c) {
+                    uint32_t x[32];
+                    ptx::tmem_ld32(lanes + 32 * c, x);
+                    ptx::tmem_ld_wait(x);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        x[i] = __float_as_uint(__uint_as_float(x[i]) * factor[32 * (c & 1) + i]);
+                    ptx::tmem_st32(lanes + 32 * c, x);
+                }
+                ptx::tmem_st_wait();
+                ptx::named_bar_sync(2, 32 * kSoftWarps);   // the factors have been read
+            }
+            // P of two blocks ago has been read
+            ok = wait_bar_warp(bar(BP_EMPTY + buf), ph ^ 1, sy);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const float ref = m[k] == -INFINITY ? 0.f : m[k];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float a = ptx::ex2_approx(v[k][2 * j] - ref), b = ptx::ex2_approx(v[k][2 * j + 1] - ref);
+                    l[k] += a + b;
+                    if (ok) st_shared(row + buf * 8192 + k * 1024 + ((j ^ (lane >> 2)) << 4), pack_bf16(a, b));
+                }
+            }
+            ptx::tc_fence_before();
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (ok && lane == 0) ptx::mbar_arrive(bar(BP_FULL + buf));
+            if (ok && in.b == in.nb - 1) {
+                float *to = inv + (nu & 1) * kH;
+                ok = wait_bar_warp(bar(BL_EMPTY + (nu & 1)), ((nu >> 1) & 1) ^ 1, sy);
+                float *out = p.split > 1 ? p.part_lse + static_cast<int64_t>(in.unit) * kH
+                                         : p.a.lse + static_cast<int64_t>(in.unit) * kH;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    l[k] += __shfl_xor_sync(kFull, l[k], 1);
+                    l[k] += __shfl_xor_sync(kFull, l[k], 2);
+                    if (ok && (lane & 3) == 0) {
+                        // (no listed token: 0; NaN goes on)
+                        to[h0 + 8 * k] = l[k] != 0.f ? 1.f / l[k] : 0.f;
+                        const float lse = l[k] != 0.f ? m[k] + log2f(l[k]) : -INFINITY;
+                        out[h0 + 8 * k] = p.split > 1 ? lse : lse * 0.69314718055994531f;
+                    }
+                }
+                __syncwarp();
+                if (ok && lane == 0) ptx::mbar_arrive(bar(BL_FULL + (nu & 1)));
+                ++nu;
+            }
+        }
+    } else if (warp < kLoaderWarp0) {
+        ptx::setmaxnreg_dec<kRegsOther>();
+        // ---------------- output ----------------
+        const int sub = warp & 3;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * sub) << 16);
+        int nu = 0;
+        BInfo in;
+        for (int g = 0; next_info(g, in); ++g) {
+            if (in.b < in.nb - 1) continue;
+            if (!wait_bar_warp(bar(BL_FULL + (nu & 1)), (nu >> 1) & 1, sy)) break;
+            if (!wait_bar_warp(bar(BO_FULL), nu & 1, sy)) break;
+            ptx::tc_fence_after();
+            const float *inv = reinterpret_cast<const float *>(smem + kOffInv) + (nu & 1) * kH;
+            const int64_t at = static_cast<int64_t>(in.unit) * kH * kDc + 32 * sub + lane;
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+                uint32_t x[32];
+                ptx::tmem_ld32(lanes + 32 * c, x);
+                ptx::tmem_ld_wait(x);
+                if (c == 7) {
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(bar(BO_EMPTY));
+                }
+                const int64_t to = at + (c >> 1) * 128 + static_cast<int64_t>(32 * (c & 1)) * kDc;
+                if (p.split > 1) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        p.part_o[to + i * kDc] = __uint_as_float(x[i]) * inv[32 * (c & 1) + i];
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const __nv_bfloat16 b = __float2bfloat16_rn(__uint_as_float(x[i]) * inv[32 * (c & 1) + i]);
+                        static_cast<uint16_t *>(p.a.o)[to + i * kDc] = *reinterpret_cast<const uint16_t *>(&b);
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar(BL_EMPTY + (nu & 1)));
+            ++nu;
+        }
+    } else {
+        ptx::setmaxnreg_dec<kRegsOther>();
+        // ---------------- loaders ----------------
+        const int buf = (warp - kLoaderWarp0) >> 2, sl = warp & 3;
+        const int k = lane & 15;                           // 16-byte piece of the slot's 256 bytes
+        const char *kvb = static_cast<const char *>(p.a.kv) + sl * 256 + k * 16;
+        const uint32_t dst = sC + buf * kBlock + sl * kSlot + (k >> 3) * kChunk;
+        const int full = BC_FULL + buf * kSlots + sl, empty = BC_EMPTY + buf * kSlots + sl;
+        for (int g = buf;; g += 2) {
+            const int is = g % kInfoSlots;
+            const uint32_t ph = (g >> 1) & 1;
+            if (!wait_bar_warp(bar(BI_FULL + is), (g / kInfoSlots) & 1, sy) || info[is].unit < 0) break;
+            if (!wait_bar_warp(bar(empty), ph ^ 1, sy)) break;
+            const int64_t *at = ats + is * kBT + (lane >> 4);      // rows lane / 16 + 2 i
+#pragma unroll 16
+            for (int i = 0; i < kBT / 2; ++i) {
+                const int r = (lane >> 4) + 2 * i;
+                const int64_t x = at[2 * i];
+                ptx::cp_async16(dst + r * 128 + (((k & 7) ^ (r & 7)) << 4), kvb + (x >= 0 ? 2 * x : 0), x >= 0 ? 16u : 0u);
+            }
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar(BI_EMPTY + is));   // places read
+            ptx::cp_async_commit();
+            ptx::cp_async_wait_all();
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar(full));
+        }
+        ptx::cp_async_wait_all();
+    }
+
+    __syncthreads();
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, kTmemCols);
     }
 }
 
-__global__ void __launch_bounds__(256) paged_mla_kernel(const Params p)
+// In front: a cleared counter and status; cu_q has to be 0 .. Tq and non-decreasing.
+__global__ void __launch_bounds__(256) start_kernel(const int32_t *cu_q, int B, int64_t Tq, int *ws)
 {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int t = blockIdx.x;
-    const PagedRow m = paged_row(p.a, t, lane);
-    const int64_t base = (static_cast<int64_t>(t) * kH + 8 * warp) * kDc;
-    float o[8][16], top[8], sum[8];
-#pragma unroll
-    for (int h = 0; h < 8; ++h) {
-        top[h] = -INFINITY;
-        sum[h] = 0.f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) o[h][i] = 0.f;
-    }
-    bool bad = m.bad;
-    for (int j = 0; j < m.n_slots; ++j) {
-        const int64_t at = paged_at(p.a, m, j, bad);
-        if (at < 0) continue;
-        float c[16];
-        load16(static_cast<const uint16_t *>(p.a.kv) + at, lane, c);
-#pragma unroll
-        for (int h = 0; h < 8; ++h) {
-            float a[16], s = 0.f;
-            load16(static_cast<const uint16_t *>(p.a.q) + base + h * kDc, lane, a);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) s = fmaf(a[i], c[i], s);
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(kFull, s, d);
-            s *= p.a.scale;
-            const float now = fmaxf(top[h], s), keep = expf(top[h] - now), w = expf(s - now);
-            top[h] = now;
-            sum[h] = fmaf(sum[h], keep, w);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[h][i] = fmaf(o[h][i], keep, w * c[i]);
-        }
-    }
-#pragma unroll
-    for (int h = 0; h < 8; ++h) {
-        const float inv = sum[h] != 0.f ? 1.f / sum[h] : 0.f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const __nv_bfloat16 v = __float2bfloat16_rn(o[h][i] * inv);
-            static_cast<uint16_t *>(p.a.o)[base + h * kDc + (i >> 3) * 256 + 8 * lane + (i & 7)] =
-                *reinterpret_cast<const uint16_t *>(&v);
-        }
-        if (lane == 0)
-            p.a.lse[static_cast<int64_t>(t) * kH + 8 * warp + h] =
-                sum[h] != 0.f ? top[h] + logf(sum[h]) : -INFINITY;
-    }
-    if (bad) atomicOr(p.status, KPOOL_STATUS_BAD_PAGE);
-}
-
-// cu_q has to be 0 .. Tq and non-decreasing.
-__global__ void check_kernel(const int32_t *cu_q, int B, int64_t Tq, int *status)
-{
+    ptx::grid_dependents_launch();
     bool bad = cu_q[0] != 0 || cu_q[B] != Tq;
     for (int i = threadIdx.x; i < B; i += blockDim.x) bad |= cu_q[i] > cu_q[i + 1];
-    if (bad) atomicOr(status, KPOOL_STATUS_BAD_SEQLENS);
+    bad = __syncthreads_or(bad);
+    if (threadIdx.x < 64) ws[threadIdx.x] = threadIdx.x == 1 && bad ? KPOOL_STATUS_BAD_SEQLENS : 0;
+}
+
+// Joins the runs of a (row, head), a warp each: sum of 2^(lse_s - max) o_s over that of
+// 2^(lse_s - max).
+__global__ void __launch_bounds__(128) join_kernel(const Params p)
+{
+    const int lane = threadIdx.x & 31;
+    const int64_t r = (static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x) >> 5;
+    const int64_t t = r / kH, h = r % kH, u0 = t * p.split;
+    ptx::grid_dependency_wait();
+    const float mine = lane < p.split ? p.part_lse[(u0 + lane) * kH + h] : -INFINITY;
+    float top = mine;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
+    float w = ptx::ex2_approx(mine - (top == -INFINITY ? 0.f : top)), sum = w;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(kFull, sum, d);
+    const float inv = sum != 0.f ? 1.f / sum : 0.f;        // (0: no token; NaN goes on)
+    float4 acc[4];
+#pragma unroll
+    for (int v = 0; v < 4; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int s = 0; s < p.split; ++s) {
+        const float f = __shfl_sync(kFull, w, s) * inv;
+        if (f == 0.f) continue;                            // (an empty run has written no row)
+        const float4 *from = reinterpret_cast<const float4 *>(p.part_o + ((u0 + s) * kH + h) * kDc) + lane;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            const float4 y = from[32 * v];
+            acc[v].x = fmaf(y.x, f, acc[v].x);
+            acc[v].y = fmaf(y.y, f, acc[v].y);
+            acc[v].z = fmaf(y.z, f, acc[v].z);
+            acc[v].w = fmaf(y.w, f, acc[v].w);
+        }
+    }
+    uint2 *out = reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.a.o) + r * kDc) + lane;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) out[32 * v] = make_uint2(pack_bf16(acc[v].x, acc[v].y), pack_bf16(acc[v].z, acc[v].w));
+    if (lane == 0) p.a.lse[r] = sum != 0.f ? (top + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+}
+
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), int grid, int threads, int smem, cudaStream_t s, const A &...args)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Runs of a row, where rows are at most half of the SMs: as many as fill them, of at
+// least kPerUnit blocks in the longest rows.
+int runs(int64_t Tq, int Kp, int kpool, int sms)
+{
+    if (Tq == 0 || 2 * Tq > sms) return 1;
+    const int64_t blocks = (static_cast<int64_t>(Kp) * kpool + kpool - 1 + kBT - 1) / kBT;
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({sms / Tq, (blocks + kPerUnit - 1) / kPerUnit, kMaxSplit})));
 }
 
 }  // namespace
 
+// (The size must not depend on the device that a caller sizes its workspace on, so the
+// number of SMs is bounded there.)
 size_t paged_mla_workspace_bytes(int64_t Tq, int Kp, int kpool)
 {
-    (void)Tq;
-    (void)Kp;
-    (void)kpool;
-    return 256;
+    const int n = runs(Tq, Kp, kpool, kMaxSms);
+    return 256 + (n > 1 ? static_cast<size_t>(Tq) * n * kH * (kDc + 1) * 4 : 0);
 }
 
 int run_paged_mla(const PagedMlaArgs &a, cudaStream_t s)
 {
-    KPOOL_CUDA_CHECK(cudaMemsetAsync(a.workspace, 0, 256, s));
-    Params p{a, static_cast<int *>(a.workspace) + 1};
-    check_kernel<<<1, 256, 0, s>>>(a.cu_q, a.B, a.Tq, p.status);
+    uint8_t *ws = static_cast<uint8_t *>(a.workspace);
+    Params p{};
+    p.a = a;
+    p.c_scale = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
+    const int sms = std::min(num_sms(), kMaxSms);
+    p.split = runs(a.Tq, a.Kp, a.kpool, sms);
+    p.ws = reinterpret_cast<int *>(ws);
+    p.part_o = reinterpret_cast<float *>(ws + 256);
+    p.part_lse = p.part_o + a.Tq * p.split * kH * kDc;
+    p.wait_limit_ns = get_wait_limit_ns();
+    CUtensorMap mq;
+    if (a.Tq > 0) {
+        const int rc = encode_bf16_tmap(&mq, a.q, kDc, static_cast<uint64_t>(a.Tq) * kH, kH);
+        if (rc) return rc;
+        KPOOL_CUDA_CHECK(
+            cudaFuncSetAttribute(paged_mla_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes));
+    }
+    start_kernel<<<1, 256, 0, s>>>(a.cu_q, a.B, a.Tq, p.ws);
     KPOOL_CUDA_CHECK(cudaGetLastError());
     if (a.Tq == 0) return KPOOL_OK;
-    paged_mla_kernel<<<static_cast<unsigned>(a.Tq), 256, 0, s>>>(p);
-    KPOOL_CUDA_CHECK(cudaGetLastError());
+    KPOOL_CUDA_CHECK(launch_after(paged_mla_kernel, static_cast<int>(std::min<int64_t>(sms, a.Tq * p.split)), kThreads,
+                                  kSmemBytes, s, mq, p));
+    if (p.split > 1)
+        KPOOL_CUDA_CHECK(launch_after(join_kernel, static_cast<int>(a.Tq * (kH / 4)), 128, 0, s, p));
     return KPOOL_OK;
 }
 

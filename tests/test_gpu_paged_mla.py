@@ -348,3 +348,43 @@ def test_rollout_and_training_step(K):
                                                 _dev(np.arange(answers + 1) * steps), _dev([prompt] * answers), cu, cu_pools)
     assert torch.equal(dq2, dq[rows]) and torch.all(dq.view(answers, total, H, DC)[:, :prompt] == 0)
     assert torch.allclose(dkv2.float(), dkv.float(), rtol=2.0 ** -7, atol=1e-5)
+
+
+@pytest.mark.parametrize("limit_ns", [1, 3000])
+def test_expired_waits(K, limit_ns):
+    """With the wait limit lowered the call reports KPOOL_STATUS_TIMEOUT (1 ns) or finishes; the next call at
+    the default limit is clean and right, for whole rows and for rows that are cut."""
+    for c in (Case(16, [900] * 4, [60] * 4, 4, 100, 64), Case(17, [2500, 2200], [1, 2], 4, 512, 64)):
+        ws = c.workspace(K)
+        K.kpool_debug_set_wait_limit_ns(limit_ns)
+        try:
+            c.call(K, workspace=ws)
+            status = K.kpool_read_status(ws)
+        finally:
+            assert K.kpool_debug_set_wait_limit_ns(0) == limit_ns
+        if limit_ns == 1:
+            assert status & K.STATUS_TIMEOUT
+        o, lse = c.call(K, workspace=ws)
+        assert K.kpool_read_status(ws) == 0
+        c.check(o, lse, rows={0, 1, 2, 77, 239})
+
+
+def test_rising_scores(K):
+    """Scores that rise by more than the headroom (8 in base 2) from block to block: the reference maximum and
+    the output so far are rescaled at every block, cut rows and whole ones."""
+    for queries in ([1], [60, 60, 60]):
+        lens = [1400] * len(queries)
+        c = Case(18, lens, queries, 1, 1400, 64)
+        g = torch.Generator("cuda").manual_seed(4)
+        c.q.zero_()
+        c.q[:, :, 0] = torch.linspace(0.5, 1.5, H, device="cuda") / SCALE
+        for b in range(len(lens)):
+            x = torch.randn(1400, DC, generator=g, device="cuda") * 0.2
+            x[:, 0] = torch.arange(1400, device="cuda") * 0.15
+            c.flat[b] = x.to(torch.bfloat16)
+            row = b if c.ids is None else int(c.ids[b])
+            ids = c.table[row, :22].long()
+            c.kv[ids] = torch.cat([c.flat[b], torch.full((22 * 64 - 1400, DC), torch.nan, device="cuda",
+                                                         dtype=torch.bfloat16)]).view(22, 64, DC)
+        o, lse = c.call(K)
+        c.check(o, lse, rows={0, 59, 60, 100, 179})
