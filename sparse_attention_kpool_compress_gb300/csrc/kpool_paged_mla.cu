@@ -6,22 +6,20 @@
 //   s_j = scale * q[t, h, :] . c[j, :]
 //   o[t, h, :] = sum_j softmax_j(s) c[j, :],   lse[t, h] = ln sum_j exp(s_j)
 //
-// Design (one persistent CTA per SM, 20 warps; a unit is a row, or a run of a row's
-// blocks where rows are few; units are handed out by an atomic counter).  Blocks of
-// 64 listed tokens C [64 x 512], two of them in shared memory, so that one is
-// multiplied while the other lands:
-//   S    [64 heads x 64]  = Q . C^T        (M = 64; A, B K-major)
+// Design (one persistent CTA per SM, 24 warps; a unit is a row, or a run of a row's
+// blocks where rows are few; units are handed out by an atomic counter).  Per block of
+// 128 listed tokens C [128 x 512], in tensor memory:
+//   S    [64 heads x 128] = Q . C^T        (M = 64; A, B K-major)
 //   O^T  [512 x 64 heads] += C^T . P^T     (four parts of M = 128; A MN-major, B K-major)
-// The scores of a block run while the softmax works on the one before.  Tensor
-// memory: O^T 256 columns, S twice 64.
+// One block's rows are in shared memory at a time, in four slots of 128 columns: the
+// output's MMAs free the slots in order, and the next block's rows land in them.
 //   warp 0       control: units, and per block a record with the places of its rows
-//   warp 1       issuer of the scores' MMAs (the loop in all lanes, one issues)
+//   warp 1       MMA issuer (the loop in all lanes, one issues)
 //   warp 2       Q (TMA), ahead into L2
-//   warp 3       issuer of the output's MMAs
-//   warps 4-7    softmax: four threads share a row of 64 scores
-//   warps 8-11   output
-//   warps 12-19  loaders: 16-byte cp.async, a warp per block in flight and slot of
-//                128 columns
+//   warps 4-11   softmax: four warps have the first 64 tokens of a block, four the
+//                others; four threads share a head's 64 scores
+//   warps 12-15  output, while the next unit's first scores run
+//   warps 16-23  loaders: 16-byte cp.async, two warps a slot
 // One reference maximum per head, raised (and O^T rescaled) only when a block's
 // scores exceed it by more than 8 in the base-2 exponent, so P <= 256; P goes to
 // shared memory in BF16 (the MMA's operand type), sums and statistics are FP32.
@@ -43,48 +41,70 @@ namespace {
 
 constexpr int kH = 64;                  // heads
 constexpr int kDc = 512;                // latent width
-constexpr int kBT = 64;                 // listed tokens per block
-constexpr int kThreads = 640;
-constexpr int kSoftWarps = 4;            // warps 4..7
-constexpr int kOutWarp0 = 8, kOutWarps = 4;
-// register split (setmaxnreg): 640 threads x 96 at launch
-constexpr int kRegsSoftmax = 152, kRegsOther = 72;
-static_assert(128 * kRegsSoftmax + 512 * kRegsOther <= 640 * 96, "register split above the launch's registers");
-constexpr int kLoaderWarp0 = 12;        // 8: two blocks x four slots
+constexpr int kBT = 128;                // listed tokens per block
+constexpr int kThreads = 768;
+constexpr int kSoftWarps = 8;            // warps 4..11
+constexpr int kSoftThreads = 32 * kSoftWarps;
+constexpr int kOutWarp0 = 12, kOutWarps = 4;
+// register split (setmaxnreg): 768 threads x 80 at launch
+constexpr int kRegsSoftmax = 104, kRegsControl = 80, kRegsOther = 64;
+static_assert(kSoftThreads * kRegsSoftmax + 128 * kRegsControl + (kThreads - kSoftThreads - 128) * kRegsOther <= kThreads * 80,
+              "register split above the launch's registers");
+constexpr int kLoaderWarp0 = 16, kLoaderWarps = 8;
 constexpr int kChunk = kBT * 128;       // 64 latent columns of a block
 constexpr int kSlots = 4;               // 128 columns each
 constexpr int kSlot = 2 * kChunk;
-constexpr int kBlock = kSlots * kSlot;
 constexpr int kInfoSlots = 4;
 constexpr float kRescale = 8.f;         // headroom of the reference maximum (log2)
-constexpr int kMaxSplit = 16;           // runs of a row
+constexpr int kMaxSplit = 32;           // runs of a row
 constexpr int kMaxSms = 160;             // that a workspace has room for
-constexpr int kPerUnit = 2;             // blocks that a run should have
 constexpr uint64_t kTimeoutNs = 2000000000ull;
-constexpr int kTmemCols = 512;          // O^T: 0..255, S: 256..319 and 320..383
+constexpr int kTmemCols = 512;          // O^T: 0..255, S: 256..383
 constexpr int kTmemS = 256;
 
 // shared memory (from a 1024-byte aligned base)
 constexpr int kOffQ = 0;                               // 8 chunks [64 heads x 64 columns]
 constexpr int kOffC = kOffQ + 8 * 8192;
-constexpr int kOffP = kOffC + 2 * kBlock;              // 2 x [64 heads x 64 tokens]
+constexpr int kOffP = kOffC + kSlots * kSlot;          // 2 x [64 heads x 64 tokens]
 constexpr int kOffInv = kOffP + 2 * 8192;              // 1 / sums of a unit [2][64]
 constexpr int kOffScale = kOffInv + 2 * kH * 4;        // rescale factors [64]
-constexpr int kOffInfo = kOffScale + kH * 4;
-constexpr int kOffAt = kOffInfo + kInfoSlots * 32;     // places of the rows [kInfoSlots][64] int64
+constexpr int kOffTop = kOffScale + kH * 4;            // maxima, sums of the halves [2][64]
+constexpr int kOffInfo = kOffTop + 2 * kH * 4;
+constexpr int kOffAt = kOffInfo + kInfoSlots * 32;     // places of the rows [kInfoSlots][128] int64
 constexpr int kOffBar = kOffAt + kInfoSlots * kBT * 8;
 enum {
-    BQ_FULL = 0, BQ_EMPTY, BC_FULL, BC_EMPTY = BC_FULL + 2 * kSlots, BS_FULL = BC_EMPTY + 2 * kSlots,
-    BS_EMPTY = BS_FULL + 2, BP_FULL = BS_EMPTY + 2, BP_EMPTY = BP_FULL + 2, BO_FULL = BP_EMPTY + 2, BO_EMPTY,
-    BL_FULL, BL_EMPTY = BL_FULL + 2, BI_FULL = BL_EMPTY + 2, BI_EMPTY = BI_FULL + kInfoSlots,
-    BDRAIN = BI_EMPTY + kInfoSlots, NBARS = BDRAIN + 2
+    BQ_FULL = 0, BQ_EMPTY, BC_FULL, BC_EMPTY = BC_FULL + kSlots, BS_FULL = BC_EMPTY + kSlots, BP_FULL, BO_FULL,
+    BO_EMPTY, BL_FULL, BL_EMPTY = BL_FULL + 2, BI_FULL = BL_EMPTY + 2, BI_EMPTY = BI_FULL + kInfoSlots,
+    BDRAIN = BI_EMPTY + kInfoSlots, NBARS
 };
 constexpr int kOffMisc = kOffBar + NBARS * 8;          // [0] tmem base, [1] abort flag
 constexpr int kSmemBytes = kOffMisc + 16 + 1024;       // and alignment slack
 static_assert(kSmemBytes <= 232448, "shared memory over the per-block limit");
 
+// n / d for 0 <= n < 2^31, d >= 2: with 2^(s-1) < d <= 2^s and mul = floor(2^(31+s) / d) + 1,
+// mul * d exceeds 2^(31+s) by at most 2^s, so n * mul / 2^(31+s) exceeds n / d by less
+// than 1 / d.  (The control warp divides for every listed token; the compiler's own
+// divisions kept the loaders waiting: 2400 of 2900 cycles a block.)
+struct Divisor {
+    uint32_t mul, shift;        // mul = 0: d = 1
+};
+
+Divisor divisor(int d)
+{
+    if (d <= 1) return {0, 0};
+    int s = 1;
+    while (s < 31 && (int64_t(1) << s) < d) ++s;
+    return {static_cast<uint32_t>((uint64_t(1) << (31 + s)) / static_cast<uint32_t>(d) + 1), static_cast<uint32_t>(s - 1)};
+}
+
+__device__ __forceinline__ int divide(int n, const Divisor &d)
+{
+    return d.mul ? static_cast<int>(__umulhi(static_cast<uint32_t>(n), d.mul) >> d.shift) : n;
+}
+
 struct Params {
     PagedMlaArgs a;
+    Divisor by_pool, by_page;
     float c_scale;              // softmax scale * log2(e)
     int split;                  // runs of a row (1: rows are whole)
     int *ws;                    // [0] unit counter, [1] status
@@ -97,7 +117,7 @@ struct Params {
 struct PagedRow {
     const int32_t *table;       // its sequence's pages (NULL: no such sequence)
     int len;                    // tokens of the sequence, cut to its table's room
-    int t, n_slots, tau, pool_lo, pool_hi, n_sel, n_tail;
+    int t, n_slots, n_pooled, tau, pool_lo, pool_hi;
     bool bad;                   // a sequence or length out of range
 };
 
@@ -120,48 +140,45 @@ __device__ __forceinline__ PagedRow paged_row(const PagedMlaArgs &p, int t, int 
     m.bad |= tau < 0 || tau >= m.len;
     m.tau = static_cast<int>(max(int64_t(-1), min(tau, static_cast<int64_t>(m.len) - 1)));
     const int nc = min((m.tau + 1) / p.kpool, m.pool_hi - m.pool_lo);
-    m.n_sel = max(0, min(nc, p.Kp));
-    m.n_tail = p.tail ? (m.tau + 1) % p.kpool : 0;
-    m.n_slots = m.n_sel * p.kpool + m.n_tail;
+    m.n_pooled = max(0, min(nc, p.Kp)) * p.kpool;
+    m.n_slots = m.n_pooled + (p.tail ? (m.tau + 1) % p.kpool : 0);
     return m;
 }
 
 // The pool that slot j of the row is in (-1: none, or the tail).
-__device__ __forceinline__ int pool_of(const PagedMlaArgs &p, const PagedRow &m, int j)
+__device__ __forceinline__ int pool_of(const Params &p, const PagedRow &m, int j)
 {
-    return j < m.n_sel * p.kpool ? p.pool_idx[static_cast<int64_t>(m.t) * p.Kp + j / p.kpool] : -1;
+    return j < m.n_pooled ? p.a.pool_idx[static_cast<int64_t>(m.t) * p.a.Kp + divide(j, p.by_pool)] : -1;
 }
 
 // Where slot j of the row, in pool g, lies in the pages, in elements (-1: no token there).
-__device__ __forceinline__ int64_t paged_at(const PagedMlaArgs &p, const PagedRow &m, int j, int g, bool &bad)
+__device__ __forceinline__ int64_t paged_at(const Params &p, const PagedRow &m, int j, int g, bool &bad)
 {
     if (j >= m.n_slots) return -1;
-    const int npt = m.n_sel * p.kpool;
     int64_t v;
-    if (j < npt) {
+    if (j < m.n_pooled) {
         if (g < m.pool_lo || g >= m.pool_hi) return -1;
-        v = static_cast<int64_t>(g - m.pool_lo) * p.kpool + j % p.kpool;
+        v = static_cast<int64_t>(g - m.pool_lo) * p.a.kpool + (j - divide(j, p.by_pool) * p.a.kpool);
     } else {
-        v = m.tau - m.n_tail + 1 + (j - npt);
+        v = m.tau + 1 - (m.n_slots - j);
     }
     if (v >= m.len) {
         bad = true;
         return -1;
     }
-    const int page = static_cast<int>(v) / p.page_size;
+    const int page = divide(static_cast<int>(v), p.by_page);
     const int id = m.table[page];
-    if (id < 0 || id >= p.n_pages) {
+    if (id < 0 || id >= p.a.n_pages) {
         bad = true;
         return -1;
     }
-    return id * p.kv_page_stride + static_cast<int64_t>(static_cast<int>(v) - page * p.page_size) * kDc;
+    return id * p.a.kv_page_stride + static_cast<int64_t>(static_cast<int>(v) - page * p.a.page_size) * kDc;
 }
 
 // One block of a unit.
 struct BInfo {
     int unit, b, nb, ksteps;    // b-th of the unit's nb blocks
-    uint32_t mask[2];           // bit r of mask[r / 32]: listed token r is valid
-    int pad[2];
+    uint32_t mask[4];           // bit r of mask[r / 32]: listed token r is valid
 };
 static_assert(sizeof(BInfo) == 32, "BInfo slot");
 
@@ -199,25 +216,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         ptx::mbar_init(bar(BQ_FULL), 1);
         ptx::mbar_init(bar(BQ_EMPTY), 1);
-        for (int i = 0; i < 2 * kSlots; ++i) {
-            ptx::mbar_init(bar(BC_FULL + i), 1);
+        for (int i = 0; i < kSlots; ++i) {
+            ptx::mbar_init(bar(BC_FULL + i), 2);       // the slot's two loader warps
             ptx::mbar_init(bar(BC_EMPTY + i), 1);
         }
-        for (int i = 0; i < 2; ++i) {
-            ptx::mbar_init(bar(BS_FULL + i), 1);
-            ptx::mbar_init(bar(BS_EMPTY + i), kSoftWarps);
-            ptx::mbar_init(bar(BP_FULL + i), kSoftWarps);
-            ptx::mbar_init(bar(BP_EMPTY + i), 1);
-            ptx::mbar_init(bar(BL_FULL + i), kSoftWarps);
-            ptx::mbar_init(bar(BL_EMPTY + i), kOutWarps);
-            ptx::mbar_init(bar(BDRAIN + i), 1);
-        }
+        ptx::mbar_init(bar(BS_FULL), 1);
+        ptx::mbar_init(bar(BP_FULL), kSoftWarps);
         ptx::mbar_init(bar(BO_FULL), 1);
         ptx::mbar_init(bar(BO_EMPTY), kOutWarps);
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(bar(BL_FULL + i), 4);       // the softmax warps of the first half
+            ptx::mbar_init(bar(BL_EMPTY + i), kOutWarps);
+        }
+        ptx::mbar_init(bar(BDRAIN), 1);
         for (int i = 0; i < kInfoSlots; ++i) {
             ptx::mbar_init(bar(BI_FULL + i), 1);
-            // (even blocks go to four of the loaders, odd ones to the others)
-            ptx::mbar_init(bar(BI_EMPTY + i), 3 + kSoftWarps + kOutWarps + kSlots);
+            ptx::mbar_init(bar(BI_EMPTY + i), 2 + kSoftWarps + kOutWarps + kLoaderWarps);
         }
         misc[1] = 0u;
         ptx::fence_mbar_init();
@@ -245,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 
     if (warp < 4) {
-    ptx::setmaxnreg_dec<kRegsOther>();
+    ptx::setmaxnreg_dec<kRegsControl>();
     if (warp == 0) {
         // ---------------- control: units and their blocks ----------------
         const int units = static_cast<int>(p.a.Tq) * p.split;
@@ -271,26 +285,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 continue;
             }
-            const int j0 = b0 * kBT + 2 * lane;
-            int g0 = pool_of(p.a, m, j0), g1 = pool_of(p.a, m, j0 + 1);
+            const int j0 = b0 * kBT + 4 * lane;
             for (int b = 0; b < nb; ++b, ++g) {
-                const int j = j0 + b * kBT;
-                const int64_t at0 = paged_at(p.a, m, j, g0, bad), at1 = paged_at(p.a, m, j + 1, g1, bad);
-                // (the next block's pools, so that only the pages' table is waited for there)
-                g0 = pool_of(p.a, m, j + kBT);
-                g1 = pool_of(p.a, m, j + kBT + 1);
-                // validity word w (tokens 32w .. 32w + 31) from lanes 16w .. 16w + 15
-                uint32_t mw = ((at0 >= 0 ? 1u : 0u) | (at1 >= 0 ? 2u : 0u)) << (2 * (lane & 15));
+                int pool[4];
+                int64_t at[4];
+                uint32_t mw = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) pool[i] = pool_of(p, m, j0 + b * kBT + i);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    at[i] = paged_at(p, m, j0 + b * kBT + i, pool[i], bad);
+                    mw |= (at[i] >= 0 ? 1u : 0u) << i;
+                }
+                // validity word w (tokens 32w .. 32w + 31) from lanes 8w .. 8w + 7
+                mw <<= 4 * (lane & 7);
                 mw |= __shfl_xor_sync(kFull, mw, 1);
                 mw |= __shfl_xor_sync(kFull, mw, 2);
                 mw |= __shfl_xor_sync(kFull, mw, 4);
-                mw |= __shfl_xor_sync(kFull, mw, 8);
                 const int is = g % kInfoSlots;
                 ok = wait_bar_warp(bar(BI_EMPTY + is), ((g / kInfoSlots) & 1) ^ 1, sy);
                 if (!ok) break;
-                ats[is * kBT + 2 * lane] = at0;
-                ats[is * kBT + 2 * lane + 1] = at1;
-                if ((lane & 15) == 0) info[is].mask[lane >> 4] = mw;
+                longlong2 *to = reinterpret_cast<longlong2 *>(ats + is * kBT + 4 * lane);
+                to[0] = make_longlong2(at[0], at[1]);
+                to[1] = make_longlong2(at[2], at[3]);
+                if ((lane & 7) == 0) info[is].mask[lane >> 3] = mw;
                 if (lane == 0) {
                     info[is].unit = u;
                     info[is].b = b;
@@ -301,49 +319,63 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) ptx::mbar_arrive(bar(BI_FULL + is));
             }
         }
-        // end of the block stream, for the loaders of even and of odd blocks
-        for (int e = 0; e < 2 && ok; ++e, ++g) {
-            const int is = g % kInfoSlots;
-            ok = wait_bar_warp(bar(BI_EMPTY + is), ((g / kInfoSlots) & 1) ^ 1, sy);
-            if (ok && lane == 0) {
-                info[is].unit = -1;
-                ptx::mbar_arrive(bar(BI_FULL + is));
-            }
+        // end of the block stream for every consumer
+        const int is = g % kInfoSlots;
+        if (ok && wait_bar_warp(bar(BI_EMPTY + is), ((g / kInfoSlots) & 1) ^ 1, sy) && lane == 0) {
+            info[is].unit = -1;
+            ptx::mbar_arrive(bar(BI_FULL + is));
         }
         if (__any_sync(kFull, bad) && lane == 0) atomicOr(sy.status, KPOOL_STATUS_BAD_PAGE);
     } else if (warp == 1) {
-        // ---------------- issuer of the scores ----------------
-        constexpr uint32_t idesc = ptx::make_idesc(1u, 64, 64);
+        // ---------------- MMA issuer ----------------
+        constexpr uint32_t idesc_s = ptx::make_idesc(1u, 64, kBT);
+        constexpr uint32_t idesc_o = ptx::make_idesc(1u, 128, 64) | ptx::kIdescAMajorMN;
         const bool one = ptx::elect_one();
-        uint32_t q_ph = 0;
+        uint32_t q_ph = 0, o_ph = 0;
         bool any = false;
         BInfo in;
         for (int g = 0; next_info(g, in); ++g) {
-            const int buf = g & 1;
-            const uint32_t ph = (g >> 1) & 1;
             bool ok = in.b > 0 || wait_bar_warp(bar(BQ_FULL), q_ph, sy);
             if (in.b == 0) q_ph ^= 1;
-            ok = ok && wait_bar_warp(bar(BS_EMPTY + buf), ph ^ 1, sy);
+            // (the last block's scores were read before its P was complete)
             for (int sl = 0; sl < kSlots && ok; ++sl) {
-                ok = wait_bar_warp(bar(BC_FULL + buf * kSlots + sl), ph, sy);
+                ok = wait_bar_warp(bar(BC_FULL + sl), g & 1, sy);
                 if (!ok) break;
                 ptx::tc_fence_after();
                 if (one) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const uint64_t ad = ptx::smem_desc_sw128(sQ + (2 * sl + h) * 8192);
-                        const uint64_t bd = ptx::smem_desc_sw128(sC + buf * kBlock + sl * kSlot + h * kChunk);
+                        const uint64_t bd = ptx::smem_desc_sw128(sC + sl * kSlot + h * kChunk);
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            ptx::mma_bf16(tmem + kTmemS + buf * 64, ad + 2 * kk, bd + 2 * kk, idesc, (sl | h | kk) != 0);
+                            ptx::mma_bf16(tmem + kTmemS, ad + 2 * kk, bd + 2 * kk, idesc_s, (sl | h | kk) != 0);
                     }
                 }
                 any = true;
             }
             if (!ok) break;
             if (one) {
-                ptx::mma_commit(bar(BS_FULL + buf));
+                ptx::mma_commit(bar(BS_FULL));
                 if (in.b == in.nb - 1) ptx::mma_commit(bar(BQ_EMPTY));
+            }
+            ok = wait_bar_warp(bar(BP_FULL), g & 1, sy);
+            if (in.b == 0) {
+                ok = ok && wait_bar_warp(bar(BO_EMPTY), o_ph ^ 1, sy);
+                o_ph ^= 1;
+            }
+            if (!ok) break;
+            ptx::tc_fence_after();
+            if (one) {
+                const uint64_t bd = ptx::smem_desc_sw128(sP);
+                for (int sl = 0; sl < kSlots; ++sl) {
+                    const uint64_t ad = ptx::smem_desc_mn_sw128(sC + sl * kSlot, kChunk);
+                    for (int kk = 0; kk < in.ksteps; ++kk)
+                        ptx::mma_bf16(tmem + sl * 64, ad + kk * 128, bd + (kk >> 2) * 512 + (kk & 3) * 2, idesc_o,
+                                      in.b > 0 || kk > 0);
+                    ptx::mma_commit(bar(BC_EMPTY + sl));
+                }
+                if (in.b == in.nb - 1) ptx::mma_commit(bar(BO_FULL));
             }
         }
         if (any) {
@@ -378,158 +410,137 @@ __global__ void __launch_bounds__(kThreads, 1)
             while (!ptx::mbar_try_wait(bar(BQ_FULL), q_ph ^ 1))
                 if (ptx::globaltimer() - t0 > kTimeoutNs) break;
         }
-    } else {
-        // ---------------- issuer of the output ----------------
-        constexpr uint32_t idesc = ptx::make_idesc(1u, 128, 64) | ptx::kIdescAMajorMN;
-        const bool one = ptx::elect_one();
-        uint32_t o_ph = 0;
-        bool any = false;
-        BInfo in;
-        for (int g = 0; next_info(g, in); ++g) {
-            const int buf = g & 1;
-            const uint32_t ph = (g >> 1) & 1;
-            bool ok = wait_bar_warp(bar(BP_FULL + buf), ph, sy);
-            if (in.b == 0) {
-                ok = ok && wait_bar_warp(bar(BO_EMPTY), o_ph ^ 1, sy);
-                o_ph ^= 1;
-            }
-            for (int sl = 0; sl < kSlots && ok; ++sl) ok = wait_bar_warp(bar(BC_FULL + buf * kSlots + sl), ph, sy);
-            if (!ok) break;
-            ptx::tc_fence_after();
-            any = true;
-            if (one) {
-                const uint64_t bd = ptx::smem_desc_sw128(sP + buf * 8192);
-                for (int sl = 0; sl < kSlots; ++sl) {
-                    const uint64_t ad = ptx::smem_desc_mn_sw128(sC + buf * kBlock + sl * kSlot, kChunk);
-                    for (int kk = 0; kk < in.ksteps; ++kk)
-                        ptx::mma_bf16(tmem + sl * 64, ad + kk * 128, bd + 2 * kk, idesc, in.b > 0 || kk > 0);
-                    ptx::mma_commit(bar(BC_EMPTY + buf * kSlots + sl));
-                }
-                ptx::mma_commit(bar(BP_EMPTY + buf));
-                if (in.b == in.nb - 1) ptx::mma_commit(bar(BO_FULL));
-            }
-        }
-        if (any) {
-            if (one) ptx::mma_commit(bar(BDRAIN + 1));
-            const uint64_t t0 = ptx::globaltimer();
-            while (!ptx::mbar_try_wait(bar(BDRAIN + 1), 0))
-                if (ptx::globaltimer() - t0 > kTimeoutNs) break;
-        }
     }
     } else if (warp < kOutWarp0) {
         ptx::setmaxnreg_inc<kRegsSoftmax>();
         // ---------------- softmax ----------------
-        const int sub = warp & 3;
+        const int sub = warp & 3, half = (warp - 4) >> 2;
         const int h0 = 16 * sub + (lane >> 2);             // this thread's heads: h0 and h0 + 8
         const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * sub) << 16);
         const uint32_t row = sP + h0 * 128 + (lane & 3) * 4;
         float *inv = reinterpret_cast<float *>(smem + kOffInv), *factor = reinterpret_cast<float *>(smem + kOffScale);
+        float *halves = reinterpret_cast<float *>(smem + kOffTop);
         float m[2] = {0.f, 0.f}, l[2] = {0.f, 0.f};
         int nu = 0;                                        // units so far
-        // the four warps meet once a block, and leave together
+        // the warps meet once a block, and leave together
         for (int g = 0;; ++g) {
-            const int buf = g & 1;
-            const uint32_t ph = (g >> 1) & 1;
             BInfo in;
             in.unit = -1;
-            const bool more = next_info(g, in);
-            bool ok = more && wait_bar_warp(bar(BS_FULL + buf), ph, sy);
-            float v[2][16];                                // scores of tokens 8 j + 2 (lane % 4) and the next
-            bool raise = false;
-            float top[2] = {-INFINITY, -INFINITY};
-            if (ok) {
-                ptx::tc_fence_after();
+            bool ok = next_info(g, in) && wait_bar_warp(bar(BS_FULL), g & 1, sy);
+            const uint32_t mask[2] = {(half ? in.mask[2] : in.mask[0]) >> (2 * (lane & 3)),
+                                      (half ? in.mask[3] : in.mask[1]) >> (2 * (lane & 3))};
+            // v[k][2 j + e]: the score of token 64 half + 8 j + 2 (lane % 4) + e, base 2
+            auto load = [&](float (&v)[2][16]) {
                 uint32_t r[32];
-                ptx::tmem_ld16x256_x8(lanes + kTmemS + buf * 64, r);
+                ptx::tmem_ld16x256_x8(lanes + kTmemS + 64 * half, r);
                 ptx::tmem_ld_wait(r);
-                ptx::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(bar(BS_EMPTY + buf));
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const uint32_t mk = in.mask[j >> 2] >> (8 * (j & 3) + 2 * (lane & 3));
+                for (int j = 0; j < 8; ++j)
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const float x = (mk >> e) & 1u ? __uint_as_float(r[4 * j + 2 * k + e]) * p.c_scale : -INFINITY;
-                            v[k][2 * j + e] = x;
-                            top[k] = fmaxf(top[k], x);
-                        }
-                }
+                        for (int k = 0; k < 2; ++k)
+                            v[k][2 * j + e] = (mask[j >> 2] >> (8 * (j & 3) + e)) & 1u
+                                                  ? __uint_as_float(r[4 * j + 2 * k + e]) * p.c_scale : -INFINITY;
+            };
+            float w[2][16];                                // 2^(score - m)
+            bool over = false;
+            if (ok) {
+                ptx::tc_fence_after();
+                load(w);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    top[k] = fmaxf(top[k], __shfl_xor_sync(kFull, top[k], 1));
-                    top[k] = fmaxf(top[k], __shfl_xor_sync(kFull, top[k], 2));
-                    if (in.b == 0) {
-                        m[k] = top[k];
-                        l[k] = 0.f;
+                    // (a head without tokens so far has m = -inf, and any score exceeds it)
+                    const float ref = m[k] == -INFINITY ? 0.f : m[k], most = m[k] + kRescale;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        over |= w[k][i] > most;
+                        w[k][i] = ptx::ex2_approx(w[k][i] - ref);
                     }
-                    raise |= top[k] > m[k] + kRescale;     // (from -inf too)
                 }
             }
-            if (ptx::named_bar_or(1, 32 * kSoftWarps, !ok || raise)) {
-                // some warp leaves, or some head's reference rises
-                if (ptx::named_bar_or(2, 32 * kSoftWarps, !ok)) break;
+            if (ptx::named_bar_or(1, kSoftThreads, !ok || over || in.b == 0)) {
+                // some warp leaves, a unit begins, or some head's reference rises
+                if (ptx::named_bar_or(2, kSoftThreads, !ok)) break;
+                load(w);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    const float now = top[k] > m[k] + kRescale ? top[k] : m[k];
+                    float top = w[k][0];
+#pragma unroll
+                    for (int i = 1; i < 16; ++i) top = fmaxf(top, w[k][i]);
+                    top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
+                    if ((lane & 3) == 0) halves[half * kH + h0 + 8 * k] = top;
+                }
+                ptx::named_bar_sync(2, kSoftThreads);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float t = fmaxf(halves[h0 + 8 * k], halves[kH + h0 + 8 * k]);
+                    const float now = in.b == 0 || t > m[k] + kRescale ? t : m[k];
                     const float f = now == m[k] ? 1.f : ptx::ex2_approx(m[k] - now);
                     m[k] = now;
-                    l[k] *= f;
-                    if ((lane & 3) == 0) factor[h0 + 8 * k] = f;
+                    l[k] = in.b == 0 ? 0.f : l[k] * f;
+                    if (half == 0 && (lane & 3) == 0) factor[h0 + 8 * k] = f;
+                    const float ref = now == -INFINITY ? 0.f : now;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) w[k][i] = ptx::ex2_approx(w[k][i] - ref);
                 }
-                // the last block's output MMAs are done (its P has been read)
-                ok = wait_bar_warp(bar(BP_EMPTY + (buf ^ 1)), ((g - 1) >> 1) & 1, sy);
-                if (ptx::named_bar_or(2, 32 * kSoftWarps, !ok)) break;
-                ptx::tc_fence_after();
+                ptx::named_bar_sync(2, kSoftThreads);
+                if (in.b > 0) {
+                    // (the last block's output MMAs are done: this one's scores came behind them)
 #pragma unroll 1
-                for (int c = 0; c < 8; ++c) {
-                    uint32_t x[32];
-                    ptx::tmem_ld32(lanes + 32 * c, x);
-                    ptx::tmem_ld_wait(x);
+                    for (int c = 4 * half; c < 4 * half + 4; ++c) {
+                        uint32_t x[32];
+                        ptx::tmem_ld32(lanes + 32 * c, x);
+                        ptx::tmem_ld_wait(x);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        x[i] = __float_as_uint(__uint_as_float(x[i]) * factor[32 * (c & 1) + i]);
-                    ptx::tmem_st32(lanes + 32 * c, x);
-                }
-                ptx::tmem_st_wait();
-                ptx::named_bar_sync(2, 32 * kSoftWarps);   // the factors have been read
-            }
-            // P of two blocks ago has been read
-            ok = wait_bar_warp(bar(BP_EMPTY + buf), ph ^ 1, sy);
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const float ref = m[k] == -INFINITY ? 0.f : m[k];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float a = ptx::ex2_approx(v[k][2 * j] - ref), b = ptx::ex2_approx(v[k][2 * j + 1] - ref);
-                    l[k] += a + b;
-                    if (ok) st_shared(row + buf * 8192 + k * 1024 + ((j ^ (lane >> 2)) << 4), pack_bf16(a, b));
+                        for (int i = 0; i < 32; ++i)
+                            x[i] = __float_as_uint(__uint_as_float(x[i]) * factor[32 * (c & 1) + i]);
+                        ptx::tmem_st32(lanes + 32 * c, x);
+                    }
+                    ptx::tmem_st_wait();
+                    ptx::named_bar_sync(2, kSoftThreads);  // the factors have been read
                 }
             }
+            // (and have read P)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    st_shared(row + half * 8192 + k * 1024 + ((j ^ (lane >> 2)) << 4), pack_bf16(w[k][2 * j], w[k][2 * j + 1]));
             ptx::tc_fence_before();
             ptx::fence_proxy_async_smem();
             __syncwarp();
-            if (ok && lane == 0) ptx::mbar_arrive(bar(BP_FULL + buf));
-            if (ok && in.b == in.nb - 1) {
-                float *to = inv + (nu & 1) * kH;
+            if (lane == 0) ptx::mbar_arrive(bar(BP_FULL));
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) l[k] += w[k][i];
+            if (in.b == in.nb - 1) {
                 ok = wait_bar_warp(bar(BL_EMPTY + (nu & 1)), ((nu >> 1) & 1) ^ 1, sy);
-                float *out = p.split > 1 ? p.part_lse + static_cast<int64_t>(in.unit) * kH
-                                         : p.a.lse + static_cast<int64_t>(in.unit) * kH;
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     l[k] += __shfl_xor_sync(kFull, l[k], 1);
                     l[k] += __shfl_xor_sync(kFull, l[k], 2);
-                    if (ok && (lane & 3) == 0) {
-                        // (no listed token: 0; NaN goes on)
-                        to[h0 + 8 * k] = l[k] != 0.f ? 1.f / l[k] : 0.f;
-                        const float lse = l[k] != 0.f ? m[k] + log2f(l[k]) : -INFINITY;
-                        out[h0 + 8 * k] = p.split > 1 ? lse : lse * 0.69314718055994531f;
-                    }
+                    if (half == 1 && (lane & 3) == 0) halves[h0 + 8 * k] = l[k];
                 }
-                __syncwarp();
-                if (ok && lane == 0) ptx::mbar_arrive(bar(BL_FULL + (nu & 1)));
+                if (ptx::named_bar_or(2, kSoftThreads, !ok)) break;
+                if (half == 0) {
+                    float *out = p.split > 1 ? p.part_lse + static_cast<int64_t>(in.unit) * kH
+                                             : p.a.lse + static_cast<int64_t>(in.unit) * kH;
+                    if ((lane & 3) == 0)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const int h = h0 + 8 * k;
+                            const float sum = l[k] + halves[h];
+                            // (no listed token: 0; NaN goes on)
+                            inv[(nu & 1) * kH + h] = sum != 0.f ? 1.f / sum : 0.f;
+                            const float lse = sum != 0.f ? m[k] + log2f(sum) : -INFINITY;
+                            out[h] = p.split > 1 ? lse : lse * 0.69314718055994531f;
+                        }
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(bar(BL_FULL + (nu & 1)));
+                }
                 ++nu;
             }
         }
@@ -577,21 +588,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         ptx::setmaxnreg_dec<kRegsOther>();
         // ---------------- loaders ----------------
-        const int buf = (warp - kLoaderWarp0) >> 2, sl = warp & 3;
-        const int k = lane & 15;                           // 16-byte piece of the slot's 256 bytes
+        const int sl = (warp - kLoaderWarp0) >> 1;                 // the slot of this pair
+        const int t64 = ((warp - kLoaderWarp0) & 1) * 32 + lane;   // 0..63 within the pair
+        const int k = t64 & 15;                                    // 16-byte piece of the slot's 256 bytes
         const char *kvb = static_cast<const char *>(p.a.kv) + sl * 256 + k * 16;
-        const uint32_t dst = sC + buf * kBlock + sl * kSlot + (k >> 3) * kChunk;
-        const int full = BC_FULL + buf * kSlots + sl, empty = BC_EMPTY + buf * kSlots + sl;
-        for (int g = buf;; g += 2) {
+        const uint32_t dst = sC + sl * kSlot + (k >> 3) * kChunk;
+        for (int g = 0;; ++g) {
             const int is = g % kInfoSlots;
-            const uint32_t ph = (g >> 1) & 1;
             if (!wait_bar_warp(bar(BI_FULL + is), (g / kInfoSlots) & 1, sy) || info[is].unit < 0) break;
-            if (!wait_bar_warp(bar(empty), ph ^ 1, sy)) break;
-            const int64_t *at = ats + is * kBT + (lane >> 4);      // rows lane / 16 + 2 i
-#pragma unroll 16
-            for (int i = 0; i < kBT / 2; ++i) {
-                const int r = (lane >> 4) + 2 * i;
-                const int64_t x = at[2 * i];
+            if (!wait_bar_warp(bar(BC_EMPTY + sl), (g & 1) ^ 1, sy)) break;
+            const int64_t *at = ats + is * kBT + (t64 >> 4);       // rows t64 / 16 + 4 i
+#pragma unroll 8
+            for (int i = 0; i < kBT / 4; ++i) {
+                const int r = (t64 >> 4) + 4 * i;
+                const int64_t x = at[4 * i];
                 ptx::cp_async16(dst + r * 128 + (((k & 7) ^ (r & 7)) << 4), kvb + (x >= 0 ? 2 * x : 0), x >= 0 ? 16u : 0u);
             }
             __syncwarp();
@@ -600,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::cp_async_wait_all();
             ptx::fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(bar(full));
+            if (lane == 0) ptx::mbar_arrive(bar(BC_FULL + sl));
         }
         ptx::cp_async_wait_all();
     }
@@ -677,13 +687,12 @@ cudaError_t launch_after(void (*kernel)(P...), int grid, int threads, int smem, 
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// Runs of a row, where rows are at most half of the SMs: as many as fill them, of at
-// least kPerUnit blocks in the longest rows.
+// Runs of a row, where rows are at most half of the SMs: as many as fill them.
 int runs(int64_t Tq, int Kp, int kpool, int sms)
 {
     if (Tq == 0 || 2 * Tq > sms) return 1;
     const int64_t blocks = (static_cast<int64_t>(Kp) * kpool + kpool - 1 + kBT - 1) / kBT;
-    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({sms / Tq, (blocks + kPerUnit - 1) / kPerUnit, kMaxSplit})));
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({sms / Tq, blocks, kMaxSplit})));
 }
 
 }  // namespace
@@ -703,6 +712,8 @@ int run_paged_mla(const PagedMlaArgs &a, cudaStream_t s)
     p.a = a;
     p.c_scale = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
     const int sms = std::min(num_sms(), kMaxSms);
+    p.by_pool = divisor(a.kpool);
+    p.by_page = divisor(a.page_size);
     p.split = runs(a.Tq, a.Kp, a.kpool, sms);
     p.ws = reinterpret_cast<int *>(ws);
     p.part_o = reinterpret_cast<float *>(ws + 256);
