@@ -818,48 +818,63 @@ def kpool_shared_prefix_mla_fwd(q, kv, page_table, seq_lens, cu_seqlens_q, cu_gr
 
 # ---- sparse attention: backward pass, paged form --------------------------------
 
-def _like(t, name, shape, dtype, index):
-    """A contiguous tensor of this shape on CUDA device `index`: `t`, checked, or a new one."""
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=_devices(index))
-    if not (t.shape == shape and t.dtype is dtype and t.get_device() == index and t.is_contiguous()):
+def _fits(t, shape, dtype, index):
+    return t.dtype is dtype and t.get_device() == index and t.shape == shape and t.is_contiguous()
+
+
+def _refuse(t, name, shape, dtype, index):
+    """Says why `t` does not fit, if it does not."""
+    if not _fits(t, shape, dtype, index):
         _need(t, name, dtype)
         _same_device(index, **{name: t})
         raise ValueError("%s must be %s (got %s)" % (name, tuple(shape), tuple(t.shape)))
+
+
+def _output(t, name, shape, dtype, index):
+    """`t`, checked, or a new tensor."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=_devices(index))
+    _refuse(t, name, shape, dtype, index)
     return t
 
 
 def _list_rows(t, name, T, width, index):
     """Address of the lists int32 [T, width] (width None: any), and their width."""
-    if t.dim() != 2 or t.shape[0] != T or (width is not None and t.shape[1] != width):
-        raise ValueError("%s must be [%d, %s] (got %s)" % (name, T, "W" if width is None else width, tuple(t.shape)))
-    return _ints(t, name, t.numel(), index), t.shape[1]
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != T or (width is not None and shape[1] != width):
+        raise ValueError("%s must be [%d, %s] (got %s)" % (name, T, "W" if width is None else width, tuple(shape)))
+    return _ints(t, name, T * shape[1], index), shape[1]
 
 
 def kpool_sparse_mla_bwd_workspace_size(T: int, Tk: int) -> int:
     return int(_lib.kpool_sparse_mla_bwd_workspace_size(T, Tk))
 
 
-def _mla_bwd(name, fn, q, kv, lists, o, lse, d_o, d_lse, sizes, softmax_scale, workspace, dq, dkv):
-    """fn(q, kv, *lists, o, lse, d_o, d_lse, *sizes, scale, dq, dkv, workspace) -> (dq, dkv);
-    `lists` and `sizes` are made of the device index, T and Tk."""
-    index, bf16 = _device_of(q, "q"), torch.bfloat16
-    if q.dim() != 3 or kv.dim() != 2 or kv.shape[1] != q.shape[2]:
-        raise ValueError("q must be [T, H, Dc] and kv [Tk, Dc] (got %s and %s)" % (tuple(q.shape), tuple(kv.shape)))
-    T, H, Dc = q.shape
-    for t, n, shape, dtype in ((q, "q", q.shape, bf16), (kv, "kv", kv.shape, bf16), (o, "o", q.shape, bf16),
-                               (lse, "lse", (T, H), torch.float32), (d_o, "d_o", q.shape, bf16)):
-        _like(t, n, shape, dtype, index)
-    if d_lse is not None:
-        _like(d_lse, "d_lse", (T, H), torch.float32, index)
-    Tk = kv.shape[0]
-    lists = lists(index, T)
-    dq, dkv = _like(dq, "dq", q.shape, bf16, index), _like(dkv, "dkv", kv.shape, bf16, index)
+def _mla_sizes(q, kv):
+    """(device index, T, Tk, H, Dc) of q [T, H, Dc] and kv [Tk, Dc]."""
+    shape, rows = q.shape, kv.shape
+    if len(shape) != 3 or len(rows) != 2 or rows[1] != shape[2]:
+        raise ValueError("q must be [T, H, Dc] and kv [Tk, Dc] (got %s and %s)" % (tuple(shape), tuple(rows)))
+    return _device_of(q, "q"), shape[0], rows[0], shape[1], shape[2]
+
+
+def _mla_bwd(name, fn, index, q, kv, lists, o, lse, d_o, d_lse, sizes, softmax_scale, workspace, dq, dkv):
+    """fn(q, kv, *lists, o, lse, d_o, d_lse, *sizes, scale, dq, dkv, workspace) -> (dq, dkv)"""
+    bf16, f32, shape = torch.bfloat16, torch.float32, q.shape
+    T, heads = shape[0], shape[:2]
+    if not (_fits(q, shape, bf16, index) and _fits(kv, kv.shape, bf16, index) and _fits(o, shape, bf16, index)
+            and _fits(d_o, shape, bf16, index) and _fits(lse, heads, f32, index)
+            and (d_lse is None or _fits(d_lse, heads, f32, index))):
+        for t, n, want, dtype in ((q, "q", shape, bf16), (kv, "kv", kv.shape, bf16), (o, "o", shape, bf16),
+                                  (d_o, "d_o", shape, bf16), (lse, "lse", heads, f32),
+                                  (lse if d_lse is None else d_lse, "d_lse", heads, f32)):
+            _refuse(t, n, want, dtype, index)
+    dq, dkv = _output(dq, "dq", shape, bf16, index), _output(dkv, "dkv", kv.shape, bf16, index)
     keep, ws, size = _bytes(workspace, 0 if workspace is not None else
-                            _lib.kpool_sparse_mla_bwd_workspace_size(T, Tk), index)
+                            _lib.kpool_sparse_mla_bwd_workspace_size(T, kv.shape[0]), index)
     _call(index, name, fn, q.data_ptr(), kv.data_ptr(), *lists, o.data_ptr(), lse.data_ptr(), d_o.data_ptr(),
-          None if d_lse is None else d_lse.data_ptr(), *sizes(T, Tk, H, Dc), float(softmax_scale), dq.data_ptr(),
-          dkv.data_ptr(), ws, size)
+          None if d_lse is None else d_lse.data_ptr(), *sizes, float(softmax_scale), dq.data_ptr(), dkv.data_ptr(), ws,
+          size)
     return dq, dkv
 
 
@@ -868,34 +883,28 @@ def kpool_sparse_mla_bwd(q, kv, tok_idx, o, lse, d_o, softmax_scale: float, d_ls
     """Gradients of kpool_sparse_mla_fwd: from d_o bf16 [T, 64, 512] (and d_lse
     fp32 [T, 64], if lse is used) and the o and lse that it wrote -> (dq bf16
     [T, 64, 512], dkv bf16 [Tk, 512])."""
-    width = []
-
-    def lists(index, T):
-        at, w = _list_rows(tok_idx, "tok_idx", T, None, index)
-        width.append(w)
-        return (at,)
-
-    return _mla_bwd("kpool_sparse_mla_bwd", _lib.kpool_sparse_mla_bwd, q, kv, lists, o, lse, d_o, d_lse,
-                    lambda T, Tk, H, Dc: (T, Tk, width[0], H, Dc), softmax_scale, workspace, dq, dkv)
+    index, T, Tk, H, Dc = _mla_sizes(q, kv)
+    at, width = _list_rows(tok_idx, "tok_idx", T, None, index)
+    return _mla_bwd("kpool_sparse_mla_bwd", _lib.kpool_sparse_mla_bwd, index, q, kv, (at,), o, lse, d_o, d_lse,
+                    (T, Tk, width, H, Dc), softmax_scale, workspace, dq, dkv)
 
 
 def kpool_sparse_mla_bwd_pools(q, kv, pool_idx, o, lse, d_o, kpool: int, index_topk: int, softmax_scale: float,
                                cu_seqlens=None, cu_pools=None, always_select_tail: bool = True, d_lse=None,
                                workspace=None, dq=None, dkv=None):
     """Gradients of kpool_sparse_mla_fwd_pools (kv [T, 512]) -> (dq, dkv)."""
+    index, T, Tk, H, Dc = _mla_sizes(q, kv)
     if (cu_seqlens is None) != (cu_pools is None):
         raise ValueError("cu_seqlens and cu_pools go together")
-    if kv.shape[0] != q.shape[0]:
-        raise ValueError("kv must have the %d rows of q (got %d)" % (q.shape[0], kv.shape[0]))
-    n_docs = 1 if cu_seqlens is None else cu_seqlens.numel() - 1
-
-    def lists(index, T):
-        return (_list_rows(pool_idx, "pool_idx", T, index_topk // kpool, index)[0],
-                None if cu_seqlens is None else _ints(cu_seqlens, "cu_seqlens", n_docs + 1, index),
-                None if cu_pools is None else _ints(cu_pools, "cu_pools", n_docs + 1, index), n_docs)
-
-    return _mla_bwd("kpool_sparse_mla_bwd_pools", _lib.kpool_sparse_mla_bwd_pools, q, kv, lists, o, lse, d_o, d_lse,
-                    lambda T, Tk, H, Dc: (T, H, Dc, kpool, index_topk, int(bool(always_select_tail))), softmax_scale,
+    if Tk != T:
+        raise ValueError("kv must have the %d rows of q (got %d)" % (T, Tk))
+    at, n_docs = _list_rows(pool_idx, "pool_idx", T, index_topk // kpool, index)[0], 1
+    docs = (None, None)
+    if cu_seqlens is not None:
+        n_docs = cu_seqlens.numel() - 1
+        docs = (_ints(cu_seqlens, "cu_seqlens", n_docs + 1, index), _ints(cu_pools, "cu_pools", n_docs + 1, index))
+    return _mla_bwd("kpool_sparse_mla_bwd_pools", _lib.kpool_sparse_mla_bwd_pools, index, q, kv, (at, *docs, n_docs), o,
+                    lse, d_o, d_lse, (T, H, Dc, kpool, index_topk, 1 if always_select_tail else 0), softmax_scale,
                     workspace, dq, dkv)
 
 
@@ -903,17 +912,14 @@ def kpool_sparse_mla_bwd_pools_at(q, kv, pool_idx, o, lse, d_o, kpool: int, inde
                                   cu_seqlens_q, q_start_pos, cu_seqlens_k, cu_pools, always_select_tail: bool = True,
                                   d_lse=None, workspace=None, dq=None, dkv=None):
     """Gradients of kpool_sparse_mla_fwd_pools_at (keys kv [Tk, 512]) -> (dq, dkv)."""
-    n_docs = cu_seqlens_q.numel() - 1
-
-    def lists(index, T):
-        return (_list_rows(pool_idx, "pool_idx", T, index_topk // kpool, index)[0],
-                _ints(cu_seqlens_q, "cu_seqlens_q", n_docs + 1, index),
-                _ints(q_start_pos, "q_start_pos", n_docs, index), _ints(cu_seqlens_k, "cu_seqlens_k", n_docs + 1, index),
-                _ints(cu_pools, "cu_pools", n_docs + 1, index), n_docs)
-
-    return _mla_bwd("kpool_sparse_mla_bwd_pools_at", _lib.kpool_sparse_mla_bwd_pools_at, q, kv, lists, o, lse, d_o,
-                    d_lse, lambda T, Tk, H, Dc: (T, Tk, H, Dc, kpool, index_topk, int(bool(always_select_tail))),
-                    softmax_scale, workspace, dq, dkv)
+    index, T, Tk, H, Dc = _mla_sizes(q, kv)
+    n = cu_seqlens_q.numel() - 1
+    lists = (_list_rows(pool_idx, "pool_idx", T, index_topk // kpool, index)[0],
+             _ints(cu_seqlens_q, "cu_seqlens_q", n + 1, index), _ints(q_start_pos, "q_start_pos", n, index),
+             _ints(cu_seqlens_k, "cu_seqlens_k", n + 1, index), _ints(cu_pools, "cu_pools", n + 1, index), n)
+    return _mla_bwd("kpool_sparse_mla_bwd_pools_at", _lib.kpool_sparse_mla_bwd_pools_at, index, q, kv, lists, o, lse, d_o,
+                    d_lse, (T, Tk, H, Dc, kpool, index_topk, 1 if always_select_tail else 0), softmax_scale, workspace,
+                    dq, dkv)
 
 
 def kpool_sparse_mla_paged_workspace_size(Tq: int, kpool: int, index_topk: int) -> int:
@@ -930,16 +936,17 @@ def kpool_sparse_mla_fwd_pools_paged(q, kv, page_table, seq_lens, pool_idx, kpoo
     index, bf16 = _device_of(q, "q"), torch.bfloat16
     if kv.dtype is not bf16:
         raise TypeError("kv must be %s (got %s)" % (bf16, kv.dtype))
-    if q.dim() != 3 or kv.dim() != 3 or kv.shape[2] != q.shape[2]:
+    shape, pages = q.shape, kv.shape
+    if len(shape) != 3 or len(pages) != 3 or pages[2] != shape[2]:
         raise ValueError("q must be [Tq, H, Dc] and kv [n_pages, page_size, Dc] (got %s and %s)"
-                         % (tuple(q.shape), tuple(kv.shape)))
-    Tq, H, Dc = q.shape
-    n_pages, page_size, _ = kv.shape
+                         % (tuple(shape), tuple(pages)))
+    Tq, H, Dc = shape
+    n_pages, page_size, _ = pages
     stride = kv.stride()
     if kv.get_device() != index or stride[2] != 1 or (stride[1] != Dc and page_size > 1):
         _same_device(index, kv=kv)
         raise ValueError("the rows of a page of kv must be contiguous")
-    _like(q, "q", q.shape, bf16, index)
+    _refuse(q, "q", shape, bf16, index)
     if page_table.dim() != 2:
         raise ValueError("page_table must be [n_rows, max_pages]")
     n_rows, max_pages = page_table.shape
@@ -949,13 +956,13 @@ def kpool_sparse_mla_fwd_pools_paged(q, kv, page_table, seq_lens, pool_idx, kpoo
              _list_rows(pool_idx, "pool_idx", Tq, index_topk // kpool, index)[0],
              _ints(cu_seqlens_q, "cu_seqlens_q", B + 1, index), _ints(q_start_pos, "q_start_pos", B, index),
              _ints(cu_pools, "cu_pools", B + 1, index), B)
-    o, lse = _like(o, "o", q.shape, bf16, index), _like(lse, "lse", (Tq, H), torch.float32, index)
+    o, lse = _output(o, "o", shape, bf16, index), _output(lse, "lse", shape[:2], torch.float32, index)
     keep, ws, size = _bytes(workspace, 0 if workspace is not None else
                             _lib.kpool_sparse_mla_paged_workspace_size(Tq, kpool, index_topk), index)
     # (the stride of a single page says nothing)
     _call(index, "kpool_sparse_mla_fwd_pools_paged", _lib.kpool_sparse_mla_fwd_pools_paged, q.data_ptr(),
           kv.data_ptr(), stride[0] if n_pages > 1 else page_size * Dc, n_pages, page_size, *lists, Tq, H, Dc, kpool,
-          index_topk, int(bool(always_select_tail)), float(softmax_scale), o.data_ptr(), lse.data_ptr(), ws, size)
+          index_topk, 1 if always_select_tail else 0, float(softmax_scale), o.data_ptr(), lse.data_ptr(), ws, size)
     return o, lse
 
 

@@ -8,18 +8,19 @@
 //
 // Design (one persistent CTA per SM, 24 warps; a unit is a row, or a run of a row's
 // blocks where rows are few; units are handed out by an atomic counter).  Per block of
-// 128 listed tokens C [128 x 512], in tensor memory:
-//   S    [64 heads x 128] = Q . C^T        (M = 64; A, B K-major)
+// 80 listed tokens C [80 x 512], in tensor memory:
+//   S    [64 heads x 80]  = Q . C^T        (M = 64; A, B K-major)
 //   O^T  [512 x 64 heads] += C^T . P^T     (four parts of M = 128; A MN-major, B K-major)
-// One block's rows are in shared memory at a time, in four slots of 128 columns: the
-// output's MMAs free the slots in order, and the next block's rows land in them.
+// The rows go through a ring of seven slots of 128 columns, of which a block takes four:
+// the output's MMAs free them in order, and three quarters of the next block land while
+// this one's softmax runs.
 //   warp 0       control: units, and per block a record with the places of its rows
 //   warp 1       MMA issuer (the loop in all lanes, one issues)
 //   warp 2       Q (TMA), ahead into L2
-//   warps 4-11   softmax: four warps have the first 64 tokens of a block, four the
-//                others; four threads share a head's 64 scores
+//   warps 4-11   softmax: four warps have the first 40 tokens of a block, four the
+//                others; four threads share a head's 40 scores
 //   warps 12-15  output, while the next unit's first scores run
-//   warps 16-23  loaders: 16-byte cp.async, two warps a slot
+//   warps 16-23  loaders: 16-byte cp.async, two warps for each quarter of the columns
 // One reference maximum per head, raised (and O^T rescaled) only when a block's
 // scores exceed it by more than 8 in the base-2 exponent, so P <= 256; P goes to
 // shared memory in BF16 (the MMA's operand type), sums and statistics are FP32.
@@ -41,7 +42,7 @@ namespace {
 
 constexpr int kH = 64;                  // heads
 constexpr int kDc = 512;                // latent width
-constexpr int kBT = 128;                // listed tokens per block
+constexpr int kBT = 80;                 // listed tokens per block
 constexpr int kThreads = 768;
 constexpr int kSoftWarps = 8;            // warps 4..11
 constexpr int kSoftThreads = 32 * kSoftWarps;
@@ -52,28 +53,29 @@ static_assert(kSoftThreads * kRegsSoftmax + 128 * kRegsControl + (kThreads - kSo
               "register split above the launch's registers");
 constexpr int kLoaderWarp0 = 16, kLoaderWarps = 8;
 constexpr int kChunk = kBT * 128;       // 64 latent columns of a block
-constexpr int kSlots = 4;               // 128 columns each
+constexpr int kQuarters = 4;            // 128 columns each
+constexpr int kRing = 7;                // slots of a quarter of a block
 constexpr int kSlot = 2 * kChunk;
 constexpr int kInfoSlots = 4;
 constexpr float kRescale = 8.f;         // headroom of the reference maximum (log2)
 constexpr int kMaxSplit = 32;           // runs of a row
 constexpr int kMaxSms = 160;             // that a workspace has room for
 constexpr uint64_t kTimeoutNs = 2000000000ull;
-constexpr int kTmemCols = 512;          // O^T: 0..255, S: 256..383
+constexpr int kTmemCols = 512;          // O^T: 0..255, S: 256..335
 constexpr int kTmemS = 256;
 
 // shared memory (from a 1024-byte aligned base)
 constexpr int kOffQ = 0;                               // 8 chunks [64 heads x 64 columns]
 constexpr int kOffC = kOffQ + 8 * 8192;
-constexpr int kOffP = kOffC + kSlots * kSlot;          // 2 x [64 heads x 64 tokens]
+constexpr int kOffP = kOffC + kRing * kSlot;          // [64 heads x 64 tokens], and 16 tokens
 constexpr int kOffInv = kOffP + 2 * 8192;              // 1 / sums of a unit [2][64]
 constexpr int kOffScale = kOffInv + 2 * kH * 4;        // rescale factors [64]
 constexpr int kOffTop = kOffScale + kH * 4;            // maxima, sums of the halves [2][64]
 constexpr int kOffInfo = kOffTop + 2 * kH * 4;
-constexpr int kOffAt = kOffInfo + kInfoSlots * 32;     // places of the rows [kInfoSlots][128] int64
+constexpr int kOffAt = kOffInfo + kInfoSlots * 32;     // places of the rows [kInfoSlots][80] int64
 constexpr int kOffBar = kOffAt + kInfoSlots * kBT * 8;
 enum {
-    BQ_FULL = 0, BQ_EMPTY, BC_FULL, BC_EMPTY = BC_FULL + kSlots, BS_FULL = BC_EMPTY + kSlots, BP_FULL, BO_FULL,
+    BQ_FULL = 0, BQ_EMPTY, BC_FULL, BC_EMPTY = BC_FULL + kRing, BS_FULL = BC_EMPTY + kRing, BP_FULL, BO_FULL,
     BO_EMPTY, BL_FULL, BL_EMPTY = BL_FULL + 2, BI_FULL = BL_EMPTY + 2, BI_EMPTY = BI_FULL + kInfoSlots,
     BDRAIN = BI_EMPTY + kInfoSlots, NBARS
 };
@@ -178,13 +180,29 @@ __device__ __forceinline__ int64_t paged_at(const Params &p, const PagedRow &m, 
 // One block of a unit.
 struct BInfo {
     int unit, b, nb, ksteps;    // b-th of the unit's nb blocks
-    uint32_t mask[4];           // bit r of mask[r / 32]: listed token r is valid
+    uint32_t mask[3], pad;      // bit r of mask[r / 32]: listed token r is valid
 };
 static_assert(sizeof(BInfo) == 32, "BInfo slot");
 
 __device__ __forceinline__ void prefetch_l2(const void *from, uint32_t bytes)
 {
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"(bytes) : "memory");
+}
+
+// 16 lanes x 256 bits over 40 columns: for the columns 8 j + 2 (t % 4) and the next,
+// registers 4 j .. 4 j + 3 are (lane t / 4, both), (lane t / 4 + 8, both).
+__device__ __forceinline__ void tmem_ld_40(uint32_t taddr, uint32_t (&r)[20])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%20];\n\t"
+        "tcgen05.ld.sync.aligned.16x256b.x1.b32 {%16,%17,%18,%19}, [%21];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=&r"(r[0]), "=&r"(r[1]), "=&r"(r[2]), "=&r"(r[3]), "=&r"(r[4]), "=&r"(r[5]), "=&r"(r[6]), "=&r"(r[7]),
+          "=&r"(r[8]), "=&r"(r[9]), "=&r"(r[10]), "=&r"(r[11]), "=&r"(r[12]), "=&r"(r[13]), "=&r"(r[14]),
+          "=&r"(r[15]), "=&r"(r[16]), "=&r"(r[17]), "=&r"(r[18]), "=&r"(r[19])
+        : "r"(taddr), "r"(taddr + 32)
+        : "memory");
 }
 
 __device__ __forceinline__ void st_shared(uint32_t saddr, uint32_t v)
@@ -216,8 +234,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         ptx::mbar_init(bar(BQ_FULL), 1);
         ptx::mbar_init(bar(BQ_EMPTY), 1);
-        for (int i = 0; i < kSlots; ++i) {
-            ptx::mbar_init(bar(BC_FULL + i), 2);       // the slot's two loader warps
+        for (int i = 0; i < kRing; ++i) {
+            ptx::mbar_init(bar(BC_FULL + i), 2);       // two loader warps
             ptx::mbar_init(bar(BC_EMPTY + i), 1);
         }
         ptx::mbar_init(bar(BS_FULL), 1);
@@ -285,35 +303,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 continue;
             }
-            const int j0 = b0 * kBT + 4 * lane;
             for (int b = 0; b < nb; ++b, ++g) {
-                int pool[4];
-                int64_t at[4];
-                uint32_t mw = 0;
+                // lane's tokens 32 i + lane of the block
+                const int end = min(kBT, m.n_slots - (b0 + b) * kBT), j0 = (b0 + b) * kBT + lane;
+                int pool[3];
+                int64_t at[3];
+                uint32_t mask[3];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) pool[i] = pool_of(p, m, j0 + b * kBT + i);
+                for (int i = 0; i < 3; ++i) pool[i] = 32 * i + lane < end ? pool_of(p, m, j0 + 32 * i) : -1;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    at[i] = paged_at(p, m, j0 + b * kBT + i, pool[i], bad);
-                    mw |= (at[i] >= 0 ? 1u : 0u) << i;
+                for (int i = 0; i < 3; ++i) {
+                    at[i] = 32 * i + lane < end ? paged_at(p, m, j0 + 32 * i, pool[i], bad) : -1;
+                    mask[i] = __ballot_sync(kFull, at[i] >= 0);
                 }
-                // validity word w (tokens 32w .. 32w + 31) from lanes 8w .. 8w + 7
-                mw <<= 4 * (lane & 7);
-                mw |= __shfl_xor_sync(kFull, mw, 1);
-                mw |= __shfl_xor_sync(kFull, mw, 2);
-                mw |= __shfl_xor_sync(kFull, mw, 4);
                 const int is = g % kInfoSlots;
                 ok = wait_bar_warp(bar(BI_EMPTY + is), ((g / kInfoSlots) & 1) ^ 1, sy);
                 if (!ok) break;
-                longlong2 *to = reinterpret_cast<longlong2 *>(ats + is * kBT + 4 * lane);
-                to[0] = make_longlong2(at[0], at[1]);
-                to[1] = make_longlong2(at[2], at[3]);
-                if ((lane & 7) == 0) info[is].mask[lane >> 3] = mw;
+#pragma unroll
+                for (int i = 0; i < 3; ++i)
+                    if (32 * i + lane < kBT) ats[is * kBT + 32 * i + lane] = at[i];
                 if (lane == 0) {
                     info[is].unit = u;
                     info[is].b = b;
                     info[is].nb = nb;
-                    info[is].ksteps = (min(kBT, m.n_slots - (b0 + b) * kBT) + 15) / 16;
+                    info[is].ksteps = (end + 15) / 16;
+#pragma unroll
+                    for (int i = 0; i < 3; ++i) info[is].mask[i] = mask[i];
                 }
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(bar(BI_FULL + is));
@@ -338,15 +353,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = in.b > 0 || wait_bar_warp(bar(BQ_FULL), q_ph, sy);
             if (in.b == 0) q_ph ^= 1;
             // (the last block's scores were read before its P was complete)
-            for (int sl = 0; sl < kSlots && ok; ++sl) {
-                ok = wait_bar_warp(bar(BC_FULL + sl), g & 1, sy);
+            for (int sl = 0; sl < kQuarters && ok; ++sl) {
+                const uint32_t n = static_cast<uint32_t>(g) * kQuarters + sl, at = n % kRing;
+                ok = wait_bar_warp(bar(BC_FULL + at), (n / kRing) & 1, sy);
                 if (!ok) break;
                 ptx::tc_fence_after();
                 if (one) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const uint64_t ad = ptx::smem_desc_sw128(sQ + (2 * sl + h) * 8192);
-                        const uint64_t bd = ptx::smem_desc_sw128(sC + sl * kSlot + h * kChunk);
+                        const uint64_t bd = ptx::smem_desc_sw128(sC + at * kSlot + h * kChunk);
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
                             ptx::mma_bf16(tmem + kTmemS, ad + 2 * kk, bd + 2 * kk, idesc_s, (sl | h | kk) != 0);
@@ -368,12 +384,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::tc_fence_after();
             if (one) {
                 const uint64_t bd = ptx::smem_desc_sw128(sP);
-                for (int sl = 0; sl < kSlots; ++sl) {
-                    const uint64_t ad = ptx::smem_desc_mn_sw128(sC + sl * kSlot, kChunk);
+                for (int sl = 0; sl < kQuarters; ++sl) {
+                    const uint32_t at = (static_cast<uint32_t>(g) * kQuarters + sl) % kRing;
+                    const uint64_t ad = ptx::smem_desc_mn_sw128(sC + at * kSlot, kChunk);
                     for (int kk = 0; kk < in.ksteps; ++kk)
                         ptx::mma_bf16(tmem + sl * 64, ad + kk * 128, bd + (kk >> 2) * 512 + (kk & 3) * 2, idesc_o,
                                       in.b > 0 || kk > 0);
-                    ptx::mma_commit(bar(BC_EMPTY + sl));
+                    ptx::mma_commit(bar(BC_EMPTY + at));
                 }
                 if (in.b == in.nb - 1) ptx::mma_commit(bar(BO_FULL));
             }
@@ -427,23 +444,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             BInfo in;
             in.unit = -1;
             bool ok = next_info(g, in) && wait_bar_warp(bar(BS_FULL), g & 1, sy);
-            const uint32_t mask[2] = {(half ? in.mask[2] : in.mask[0]) >> (2 * (lane & 3)),
-                                      (half ? in.mask[3] : in.mask[1]) >> (2 * (lane & 3))};
-            // v[k][2 j + e]: the score of token 64 half + 8 j + 2 (lane % 4) + e, base 2
-            auto load = [&](float (&v)[2][16]) {
-                uint32_t r[32];
-                ptx::tmem_ld16x256_x8(lanes + kTmemS + 64 * half, r);
-                ptx::tmem_ld_wait(r);
+            // this half's 40 validity bits, from its thread's first token on
+            const uint32_t lo = (half ? in.mask[1] >> 8 | in.mask[2] << 24 : in.mask[0]) >> (2 * (lane & 3));
+            const uint32_t hi = (half ? in.mask[2] >> 8 : in.mask[1]) >> (2 * (lane & 3));
+            // v[k][2 j + e]: the score of token 40 half + 8 j + 2 (lane % 4) + e, base 2
+            auto load = [&](float (&v)[2][10]) {
+                uint32_t r[20];
+                tmem_ld_40(lanes + kTmemS + 40 * half, r);
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
+                for (int j = 0; j < 5; ++j)
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
 #pragma unroll
                         for (int k = 0; k < 2; ++k)
-                            v[k][2 * j + e] = (mask[j >> 2] >> (8 * (j & 3) + e)) & 1u
+                            v[k][2 * j + e] = (j < 4 ? lo >> (8 * j + e) : hi >> e) & 1u
                                                   ? __uint_as_float(r[4 * j + 2 * k + e]) * p.c_scale : -INFINITY;
             };
-            float w[2][16];                                // 2^(score - m)
+            float w[2][10];                                // 2^(score - m)
             bool over = false;
             if (ok) {
                 ptx::tc_fence_after();
@@ -453,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // (a head without tokens so far has m = -inf, and any score exceeds it)
                     const float ref = m[k] == -INFINITY ? 0.f : m[k], most = m[k] + kRescale;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
+                    for (int i = 0; i < 10; ++i) {
                         over |= w[k][i] > most;
                         w[k][i] = ptx::ex2_approx(w[k][i] - ref);
                     }
@@ -467,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int k = 0; k < 2; ++k) {
                     float top = w[k][0];
 #pragma unroll
-                    for (int i = 1; i < 16; ++i) top = fmaxf(top, w[k][i]);
+                    for (int i = 1; i < 10; ++i) top = fmaxf(top, w[k][i]);
                     top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
                     top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
                     if ((lane & 3) == 0) halves[half * kH + h0 + 8 * k] = top;
@@ -483,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (half == 0 && (lane & 3) == 0) factor[h0 + 8 * k] = f;
                     const float ref = now == -INFINITY ? 0.f : now;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) w[k][i] = ptx::ex2_approx(w[k][i] - ref);
+                    for (int i = 0; i < 10; ++i) w[k][i] = ptx::ex2_approx(w[k][i] - ref);
                 }
                 ptx::named_bar_sync(2, kSoftThreads);
                 if (in.b > 0) {
@@ -506,8 +523,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int k = 0; k < 2; ++k)
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    st_shared(row + half * 8192 + k * 1024 + ((j ^ (lane >> 2)) << 4), pack_bf16(w[k][2 * j], w[k][2 * j + 1]));
+                for (int j = 0; j < 5; ++j) {
+                    const int piece = 5 * half + j;        // eight tokens
+                    st_shared(row + (piece >> 3) * 8192 + k * 1024 + (((piece & 7) ^ (lane >> 2)) << 4),
+                              pack_bf16(w[k][2 * j], w[k][2 * j + 1]));
+                }
             ptx::tc_fence_before();
             ptx::fence_proxy_async_smem();
             __syncwarp();
@@ -515,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int k = 0; k < 2; ++k)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) l[k] += w[k][i];
+                for (int i = 0; i < 10; ++i) l[k] += w[k][i];
             if (in.b == in.nb - 1) {
                 ok = wait_bar_warp(bar(BL_EMPTY + (nu & 1)), ((nu >> 1) & 1) ^ 1, sy);
 #pragma unroll
@@ -588,17 +608,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         ptx::setmaxnreg_dec<kRegsOther>();
         // ---------------- loaders ----------------
-        const int sl = (warp - kLoaderWarp0) >> 1;                 // the slot of this pair
+        const int sl = (warp - kLoaderWarp0) >> 1;                 // the quarter of this pair
         const int t64 = ((warp - kLoaderWarp0) & 1) * 32 + lane;   // 0..63 within the pair
-        const int k = t64 & 15;                                    // 16-byte piece of the slot's 256 bytes
+        const int k = t64 & 15;                                    // 16-byte piece of the quarter's 256 bytes
         const char *kvb = static_cast<const char *>(p.a.kv) + sl * 256 + k * 16;
-        const uint32_t dst = sC + sl * kSlot + (k >> 3) * kChunk;
         for (int g = 0;; ++g) {
             const int is = g % kInfoSlots;
+            const uint32_t n = static_cast<uint32_t>(g) * kQuarters + sl, slot = n % kRing;
+            const uint32_t dst = sC + slot * kSlot + (k >> 3) * kChunk;
             if (!wait_bar_warp(bar(BI_FULL + is), (g / kInfoSlots) & 1, sy) || info[is].unit < 0) break;
-            if (!wait_bar_warp(bar(BC_EMPTY + sl), (g & 1) ^ 1, sy)) break;
+            if (!wait_bar_warp(bar(BC_EMPTY + slot), ((n / kRing) & 1) ^ 1, sy)) break;
             const int64_t *at = ats + is * kBT + (t64 >> 4);       // rows t64 / 16 + 4 i
-#pragma unroll 8
+#pragma unroll 10
             for (int i = 0; i < kBT / 4; ++i) {
                 const int r = (t64 >> 4) + 4 * i;
                 const int64_t x = at[4 * i];
@@ -610,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::cp_async_wait_all();
             ptx::fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(bar(BC_FULL + sl));
+            if (lane == 0) ptx::mbar_arrive(bar(BC_FULL + slot));
         }
         ptx::cp_async_wait_all();
     }

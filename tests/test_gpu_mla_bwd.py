@@ -351,6 +351,11 @@ def test_refusals_with_tensors(K):
             ok(**kw)
     with pytest.raises(K.KPoolError):
         ok(q=q[:, :32].contiguous(), o=q[:, :32].contiguous(), d_o=d_o[:, :32].contiguous(), lse=lse[:, :32].contiguous())
+    pools = torch.zeros(3, 2, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="rows of q"):
+        K.kpool_sparse_mla_bwd_pools(q, kv, pools, q, lse, d_o, 4, 8, 0.1)
+    with pytest.raises(ValueError, match="go together"):
+        K.kpool_sparse_mla_bwd_pools(q, kv[:3], pools, q, lse, d_o, 4, 8, 0.1, cu_seqlens=pools[0])
     with pytest.raises(K.KPoolError):
         ok(workspace=torch.zeros(256, dtype=torch.uint8, device="cuda"))
 
