@@ -12,15 +12,16 @@
 //   S    [64 heads x 80]  = Q . C^T        (M = 64; A, B K-major)
 //   O^T  [512 x 64 heads] += C^T . P^T     (four parts of M = 128; A MN-major, B K-major)
 // The rows go through a ring of seven slots of 128 columns, of which a block takes four:
-// the output's MMAs free them in order, and three quarters of the next block land while
-// this one's softmax runs.
+// the output's MMAs free them in order, and three quarters of the next block land, and
+// its scores are begun, while this one's softmax runs (S is there twice).
 //   warp 0       control: units, and per block a record with the places of its rows
 //   warp 1       MMA issuer (the loop in all lanes, one issues)
 //   warp 2       Q (TMA), ahead into L2
 //   warps 4-11   softmax: four warps have the first 40 tokens of a block, four the
 //                others; four threads share a head's 40 scores
 //   warps 12-15  output, while the next unit's first scores run
-//   warps 16-23  loaders: 16-byte cp.async, two warps for each quarter of the columns
+//   warps 16-23  loaders: 16-byte cp.async, all of them on each quarter, up to three
+//                quarters in flight
 // One reference maximum per head, raised (and O^T rescaled) only when a block's
 // scores exceed it by more than 8 in the base-2 exponent, so P <= 256; P goes to
 // shared memory in BF16 (the MMA's operand type), sums and statistics are FP32.
@@ -61,7 +62,7 @@ constexpr float kRescale = 8.f;         // headroom of the reference maximum (lo
 constexpr int kMaxSplit = 32;           // runs of a row
 constexpr int kMaxSms = 160;             // that a workspace has room for
 constexpr uint64_t kTimeoutNs = 2000000000ull;
-constexpr int kTmemCols = 512;          // O^T: 0..255, S: 256..335
+constexpr int kTmemCols = 512;          // O^T: 0..255, S: 256..335 and 336..415
 constexpr int kTmemS = 256;
 
 // shared memory (from a 1024-byte aligned base)
@@ -205,6 +206,13 @@ __device__ __forceinline__ void tmem_ld_40(uint32_t taddr, uint32_t (&r)[20])
         : "memory");
 }
 
+// All but the thread's last N groups of copies have landed.
+template <int N>
+__device__ __forceinline__ void cp_async_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 __device__ __forceinline__ void st_shared(uint32_t saddr, uint32_t v)
 {
     asm volatile("st.shared.b32 [%0], %1;" ::"r"(saddr), "r"(v) : "memory");
@@ -235,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::mbar_init(bar(BQ_FULL), 1);
         ptx::mbar_init(bar(BQ_EMPTY), 1);
         for (int i = 0; i < kRing; ++i) {
-            ptx::mbar_init(bar(BC_FULL + i), 2);       // two loader warps
+            ptx::mbar_init(bar(BC_FULL + i), kLoaderWarps);
             ptx::mbar_init(bar(BC_EMPTY + i), 1);
         }
         ptx::mbar_init(bar(BS_FULL), 1);
@@ -348,32 +356,55 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool one = ptx::elect_one();
         uint32_t q_ph = 0, o_ph = 0;
         bool any = false;
-        BInfo in;
-        for (int g = 0; next_info(g, in); ++g) {
+        // a quarter of block g's scores
+        auto scores = [&](int g, int sl) {
+            ptx::tc_fence_after();
+            if (one) {
+                const uint32_t at = (static_cast<uint32_t>(g) * kQuarters + sl) % kRing;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint64_t ad = ptx::smem_desc_sw128(sQ + (2 * sl + h) * 8192);
+                    const uint64_t bd = ptx::smem_desc_sw128(sC + at * kSlot + h * kChunk);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        ptx::mma_bf16(tmem + kTmemS + (g & 1) * kBT, ad + 2 * kk, bd + 2 * kk, idesc_s, (sl | h | kk) != 0);
+                }
+            }
+            any = true;
+        };
+        auto landed = [&](int g, int sl, uint32_t &at) {
+            const uint32_t n = static_cast<uint32_t>(g) * kQuarters + sl;
+            at = bar(BC_FULL + n % kRing);
+            return (n / kRing) & 1;
+        };
+        BInfo in, nx;
+        bool more = next_info(0, in);
+        int ahead = 0;                                     // quarters of this block's scores that are issued
+        for (int g = 0; more; ++g) {
+            uint32_t at;
             bool ok = in.b > 0 || wait_bar_warp(bar(BQ_FULL), q_ph, sy);
             if (in.b == 0) q_ph ^= 1;
-            // (the last block's scores were read before its P was complete)
-            for (int sl = 0; sl < kQuarters && ok; ++sl) {
-                const uint32_t n = static_cast<uint32_t>(g) * kQuarters + sl, at = n % kRing;
-                ok = wait_bar_warp(bar(BC_FULL + at), (n / kRing) & 1, sy);
-                if (!ok) break;
-                ptx::tc_fence_after();
-                if (one) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint64_t ad = ptx::smem_desc_sw128(sQ + (2 * sl + h) * 8192);
-                        const uint64_t bd = ptx::smem_desc_sw128(sC + at * kSlot + h * kChunk);
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            ptx::mma_bf16(tmem + kTmemS, ad + 2 * kk, bd + 2 * kk, idesc_s, (sl | h | kk) != 0);
-                    }
-                }
-                any = true;
+            // (the scores of two blocks ago were read before their P was complete)
+            for (int sl = ahead; sl < kQuarters && ok; ++sl) {
+                const uint32_t ph = landed(g, sl, at);
+                ok = wait_bar_warp(at, ph, sy);
+                if (ok) scores(g, sl);
             }
             if (!ok) break;
             if (one) {
                 ptx::mma_commit(bar(BS_FULL));
                 if (in.b == in.nb - 1) ptx::mma_commit(bar(BQ_EMPTY));
+            }
+            // while the softmax works on them, the next block's scores as far as it has landed
+            ahead = 0;
+            const bool known = __shfl_sync(kFull, ptx::mbar_test(bar(BI_FULL + (g + 1) % kInfoSlots), ((g + 1) / kInfoSlots) & 1), 0);
+            if (known) {
+                more = next_info(g + 1, nx);
+                for (; more && nx.b > 0 && ahead < kQuarters - 1; ++ahead) {
+                    const uint32_t ph = landed(g + 1, ahead, at);
+                    if (!__shfl_sync(kFull, ptx::mbar_test(at, ph), 0)) break;
+                    scores(g + 1, ahead);
+                }
             }
             ok = wait_bar_warp(bar(BP_FULL), g & 1, sy);
             if (in.b == 0) {
@@ -385,15 +416,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (one) {
                 const uint64_t bd = ptx::smem_desc_sw128(sP);
                 for (int sl = 0; sl < kQuarters; ++sl) {
-                    const uint32_t at = (static_cast<uint32_t>(g) * kQuarters + sl) % kRing;
-                    const uint64_t ad = ptx::smem_desc_mn_sw128(sC + at * kSlot, kChunk);
+                    const uint32_t slot = (static_cast<uint32_t>(g) * kQuarters + sl) % kRing;
+                    const uint64_t ad = ptx::smem_desc_mn_sw128(sC + slot * kSlot, kChunk);
                     for (int kk = 0; kk < in.ksteps; ++kk)
                         ptx::mma_bf16(tmem + sl * 64, ad + kk * 128, bd + (kk >> 2) * 512 + (kk & 3) * 2, idesc_o,
                                       in.b > 0 || kk > 0);
-                    ptx::mma_commit(bar(BC_EMPTY + at));
+                    ptx::mma_commit(bar(BC_EMPTY + slot));
                 }
                 if (in.b == in.nb - 1) ptx::mma_commit(bar(BO_FULL));
             }
+            if (!known) more = next_info(g + 1, nx);
+            in = nx;
         }
         if (any) {
             if (one) ptx::mma_commit(bar(BDRAIN));
@@ -450,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // v[k][2 j + e]: the score of token 40 half + 8 j + 2 (lane % 4) + e, base 2
             auto load = [&](float (&v)[2][10]) {
                 uint32_t r[20];
-                tmem_ld_40(lanes + kTmemS + 40 * half, r);
+                tmem_ld_40(lanes + kTmemS + (g & 1) * kBT + 40 * half, r);
 #pragma unroll
                 for (int j = 0; j < 5; ++j)
 #pragma unroll
@@ -608,30 +641,56 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         ptx::setmaxnreg_dec<kRegsOther>();
         // ---------------- loaders ----------------
-        const int sl = (warp - kLoaderWarp0) >> 1;                 // the quarter of this pair
-        const int t64 = ((warp - kLoaderWarp0) & 1) * 32 + lane;   // 0..63 within the pair
-        const int k = t64 & 15;                                    // 16-byte piece of the quarter's 256 bytes
-        const char *kvb = static_cast<const char *>(p.a.kv) + sl * 256 + k * 16;
-        for (int g = 0;; ++g) {
-            const int is = g % kInfoSlots;
-            const uint32_t n = static_cast<uint32_t>(g) * kQuarters + sl, slot = n % kRing;
-            const uint32_t dst = sC + slot * kSlot + (k >> 3) * kChunk;
-            if (!wait_bar_warp(bar(BI_FULL + is), (g / kInfoSlots) & 1, sy) || info[is].unit < 0) break;
-            if (!wait_bar_warp(bar(BC_EMPTY + slot), ((n / kRing) & 1) ^ 1, sy)) break;
-            const int64_t *at = ats + is * kBT + (t64 >> 4);       // rows t64 / 16 + 4 i
-#pragma unroll 10
-            for (int i = 0; i < kBT / 4; ++i) {
-                const int r = (t64 >> 4) + 4 * i;
-                const int64_t x = at[4 * i];
-                ptx::cp_async16(dst + r * 128 + (((k & 7) ^ (r & 7)) << 4), kvb + (x >= 0 ? 2 * x : 0), x >= 0 ? 16u : 0u);
+        const int tid = threadIdx.x - 32 * kLoaderWarp0;
+        const int k = tid & 15, r0 = tid >> 4;             // 16-byte piece of a quarter's 256 bytes; rows r0 + 16 i
+        const char *kvb = static_cast<const char *>(p.a.kv) + k * 16;
+        const uint32_t dst = sC + (k >> 3) * kChunk + r0 * 128 + (((k & 7) ^ (r0 & 7)) << 4);
+        int64_t at[kBT / 16];
+        uint32_t n = 0, done = 0;                          // quarters sent for, quarters landed
+        bool known = false, end = false, ok = true;
+        // has the phase completed?  Waits for it where nothing is in flight
+        auto ready = [&](uint32_t b, uint32_t ph) -> bool {
+            if (n != done) return __shfl_sync(kFull, ptx::mbar_test(b, ph), 0) != 0;
+            ok = wait_bar_warp(b, ph, sy);
+            return ok;
+        };
+        while (true) {
+            bool sent = false;
+            if (!end && n - done < 3) {
+                const int g = n / kQuarters, is = g % kInfoSlots;
+                if (!known && ready(bar(BI_FULL + is), (g / kInfoSlots) & 1)) {
+                    end = info[is].unit < 0;
+#pragma unroll
+                    for (int i = 0; i < kBT / 16; ++i) at[i] = ats[is * kBT + r0 + 16 * i];
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(bar(BI_EMPTY + is));
+                    known = !end;
+                }
+                const uint32_t slot = n % kRing;
+                if (known && ready(bar(BC_EMPTY + slot), ((n / kRing) & 1) ^ 1)) {
+                    const int64_t column = (n % kQuarters) * 256;
+#pragma unroll
+                    for (int i = 0; i < kBT / 16; ++i)
+                        ptx::cp_async16(dst + slot * kSlot + i * 2048, kvb + (at[i] >= 0 ? 2 * at[i] + column : 0),
+                                        at[i] >= 0 ? 16u : 0u);
+                    ptx::cp_async_commit();
+                    known = ++n % kQuarters != 0;
+                    sent = true;
+                }
             }
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(bar(BI_EMPTY + is));   // places read
-            ptx::cp_async_commit();
-            ptx::cp_async_wait_all();
+            if (!ok) break;
+            if (sent) continue;
+            if (n == done) {
+                if (end) break;
+                continue;
+            }
+            if (n - done == 3) cp_async_wait<2>();
+            else if (n - done == 2) cp_async_wait<1>();
+            else cp_async_wait<0>();
             ptx::fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(bar(BC_FULL + slot));
+            if (lane == 0) ptx::mbar_arrive(bar(BC_FULL + done % kRing));
+            ++done;
         }
         ptx::cp_async_wait_all();
     }
