@@ -72,7 +72,7 @@ constexpr int kOffInfo = kOffStage + kSumWarps * kStage;
 constexpr int kOffTok = kOffInfo + kInfoSlots * 32;    // token ids [kInfoSlots][64]
 constexpr int kOffBar = kOffTok + kInfoSlots * kBT * 4;
 enum {
-    BX_FULL = 0, BX_EMPTY = BX_FULL + kParts, BC_FULL, BC_EMPTY = BC_FULL + kSlots, BS_FULL = BC_EMPTY + kSlots, BP_FULL, BP_EMPTY,
+    BX_FULL = 0, BX_EMPTY = BX_FULL + kParts, BC_FULL = BX_EMPTY + kParts, BC_EMPTY = BC_FULL + kSlots, BS_FULL = BC_EMPTY + kSlots, BP_FULL, BP_EMPTY,
     BQ_FULL, BQ_EMPTY, BD_FULL, BD_EMPTY = BD_FULL + kSumSlots, BI_FULL = BD_EMPTY + kSumSlots,
     BI_EMPTY = BI_FULL + kInfoSlots, BDRAIN = BI_EMPTY + kInfoSlots, NBARS
 };
@@ -173,8 +173,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kParts; ++i) ptx::mbar_init(bar(BX_FULL + i), 1);
-        ptx::mbar_init(bar(BX_EMPTY), 1);
+        for (int i = 0; i < kParts; ++i) {
+            ptx::mbar_init(bar(BX_FULL + i), 1);
+            ptx::mbar_init(bar(BX_EMPTY + i), 1);
+        }
         for (int i = 0; i < kSlots; ++i) {
             ptx::mbar_init(bar(BC_FULL + i), 2);    // the slot's two loader warps
             ptx::mbar_init(bar(BC_EMPTY + i), 1);
@@ -254,8 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::tma_prefetch_desc(&tm_q);
             ptx::tma_prefetch_desc(&tm_do);
         }
-        uint32_t x_ph = 0;
-        bool issued = false;
+        int sent = 0;                   // pieces of X so far
         for (int g = 0;; ++g) {
             const int is = g % kInfoSlots;
             if (!wait_bar_warp(bar(BI_FULL + is), (g / kInfoSlots) & 1, sy)) break;
@@ -266,24 +267,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (b > 0) continue;
             // (known some blocks ahead: into L2 meanwhile)
             if (lane < 2) prefetch_l2((lane ? p.d_o : p.q) + static_cast<int64_t>(t) * kH * kDc, kH * kDc * 2);
-            if (!wait_bar_warp(bar(BX_EMPTY), x_ph ^ 1, sy)) break;
-            // in pieces of 128 columns, as the scores take them
-            if (lane < kParts) ptx::mbar_arrive_expect_tx(bar(BX_FULL + lane), 16 * kGroup / kParts);
-            __syncwarp();
-            if (lane < 16)
-                for (int i = 0; i < kParts; ++i)
+            // in pieces of 128 columns: the scores take them in turn, and the last block's dC has
+            // given them up in turn
+            bool ok = true;
+            for (int i = 0; i < kParts && ok; ++i) {
+                ok = wait_bar_warp(bar(BX_EMPTY + i), (sent / kParts & 1) ^ 1, sy);
+                if (!ok) break;
+                if (lane == 0) ptx::mbar_arrive_expect_tx(bar(BX_FULL + i), 16 * kGroup / kParts);
+                __syncwarp();
+                if (lane < 16)
                     load_group(sX + lane * kGroup + i * 2048, (lane & 1) ? &tm_do : &tm_q, bar(BX_FULL + i),
                                t * kH + 8 * (lane >> 1), 2 * i);
-            issued = true;
-            x_ph ^= 1;
+                ++sent;
+            }
+            if (!ok) break;
         }
-        // no load of X may still be in flight when the CTA ends: a wait of its own,
-        // bounded by the default limit and blind to the abort flag
-        if (issued) {
+        // no load of X may still be in flight when the CTA ends: a wait of its own for the
+        // last pieces, bounded by the default limit and blind to the abort flag
+        for (int n = max(0, sent - kParts); n < sent; ++n) {
             const uint64_t t0 = ptx::globaltimer();
-            for (int i = 0; i < kParts; ++i)
-                while (!ptx::mbar_try_wait(bar(BX_FULL + i), x_ph ^ 1))
-                    if (ptx::globaltimer() - t0 > kTimeoutNs) break;
+            while (!ptx::mbar_try_wait(bar(BX_FULL + n % kParts), n / kParts & 1))
+                if (ptx::globaltimer() - t0 > kTimeoutNs) break;
         }
     } else if (warp == 1) {
         // ---------------- MMA issuer ----------------
@@ -293,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t c_ph = 0, x_ph = 0, q_ph = 0, nd = 0;      // nd: parts of dC so far
         bool any = false, rest = false;                     // rest: the last block's dC is half done
         // parts of dC^T = X^T . [dS; P]
-        auto sum_parts = [&](int part0, int part1) {
+        auto sum_parts = [&](int part0, int part1, bool last) {
 #pragma unroll 1
             for (int part = part0; part < part1; ++part, ++nd) {
                 const uint32_t s = nd % kSumSlots;
@@ -306,6 +310,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ptx::mma_bf16(tmem + kTmemSum + s * 64, ad + kk * (2 * kGroup / 16), bd + kk * 128,
                                       idesc | ptx::kIdescAMajorMN | ptx::kIdescBMajorMN, kk > 0);
                     ptx::mma_commit(bar(BD_FULL + s));
+                    // (these columns of X have served the row)
+                    if (last) ptx::mma_commit(bar(BX_EMPTY + part));
                 }
             }
             if (part0 > 0 && one) ptx::mma_commit(bar(BP_EMPTY));
@@ -318,9 +324,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (one) ptx::mbar_arrive(bar(BI_EMPTY + is));
             if (rest && (in.t < 0 || in.b == 0)) {
-                // the row ends: X may go once its last block is done
-                if (!sum_parts(kFirst, kParts)) break;
-                if (one) ptx::mma_commit(bar(BX_EMPTY));
+                // the row ends: the next one's X waits for this
+                if (!sum_parts(kFirst, kParts, true)) break;
                 rest = false;
             }
             if (in.t < 0) break;
@@ -346,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (in.b == 0) x_ph ^= 1;
             if (one) ptx::mma_commit(bar(BS_FULL));
             // the second half of the last block's dC while P and dS are made
-            if (rest && !sum_parts(kFirst, kParts)) break;
+            if (rest && !sum_parts(kFirst, kParts, false)) break;
             if (!wait_bar_warp(bar(BP_FULL), g & 1, sy)) break;
             if (in.b == 0 && !wait_bar_warp(bar(BQ_EMPTY), q_ph ^ 1, sy)) break;
             ptx::tc_fence_after();
@@ -361,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (in.b == in.nb - 1) ptx::mma_commit(bar(BQ_FULL));
             }
             if (in.b == in.nb - 1) q_ph ^= 1;
-            if (!sum_parts(0, kFirst)) break;
+            if (!sum_parts(0, kFirst, in.b == in.nb - 1)) break;
             rest = true;
             c_ph ^= 1;
             ++g;
