@@ -860,18 +860,21 @@ def _mla_sizes(q, kv):
 
 def _mla_bwd(name, fn, index, q, kv, lists, o, lse, d_o, d_lse, sizes, softmax_scale, workspace, dq, dkv):
     """fn(q, kv, *lists, o, lse, d_o, d_lse, *sizes, scale, dq, dkv, workspace) -> (dq, dkv)"""
-    bf16, f32, shape = torch.bfloat16, torch.float32, q.shape
+    bf16, f32, shape, rows = torch.bfloat16, torch.float32, q.shape, kv.shape
     T, heads = shape[0], shape[:2]
-    if not (_fits(q, shape, bf16, index) and _fits(kv, kv.shape, bf16, index) and _fits(o, shape, bf16, index)
-            and _fits(d_o, shape, bf16, index) and _fits(lse, heads, f32, index)
-            and (d_lse is None or _fits(d_lse, heads, f32, index))):
-        for t, n, want, dtype in ((q, "q", shape, bf16), (kv, "kv", kv.shape, bf16), (o, "o", shape, bf16),
+    if not (q.dtype is bf16 and kv.dtype is bf16 and o.dtype is bf16 and d_o.dtype is bf16 and lse.dtype is f32
+            and q.is_contiguous() and kv.is_contiguous() and o.is_contiguous() and d_o.is_contiguous()
+            and lse.is_contiguous() and o.shape == shape and d_o.shape == shape and lse.shape == heads
+            and kv.get_device() == index and o.get_device() == index and d_o.get_device() == index
+            and lse.get_device() == index and (d_lse is None or _fits(d_lse, heads, f32, index))):
+        for t, n, want, dtype in ((q, "q", shape, bf16), (kv, "kv", rows, bf16), (o, "o", shape, bf16),
                                   (d_o, "d_o", shape, bf16), (lse, "lse", heads, f32),
                                   (lse if d_lse is None else d_lse, "d_lse", heads, f32)):
             _refuse(t, n, want, dtype, index)
-    dq, dkv = _output(dq, "dq", shape, bf16, index), _output(dkv, "dkv", kv.shape, bf16, index)
+    dq = torch.empty_like(q) if dq is None else _output(dq, "dq", shape, bf16, index)
+    dkv = torch.empty_like(kv) if dkv is None else _output(dkv, "dkv", rows, bf16, index)
     keep, ws, size = _bytes(workspace, 0 if workspace is not None else
-                            _lib.kpool_sparse_mla_bwd_workspace_size(T, kv.shape[0]), index)
+                            _lib.kpool_sparse_mla_bwd_workspace_size(T, rows[0]), index)
     _call(index, name, fn, q.data_ptr(), kv.data_ptr(), *lists, o.data_ptr(), lse.data_ptr(), d_o.data_ptr(),
           None if d_lse is None else d_lse.data_ptr(), *sizes, float(softmax_scale), dq.data_ptr(), dkv.data_ptr(), ws,
           size)
@@ -956,7 +959,8 @@ def kpool_sparse_mla_fwd_pools_paged(q, kv, page_table, seq_lens, pool_idx, kpoo
              _list_rows(pool_idx, "pool_idx", Tq, index_topk // kpool, index)[0],
              _ints(cu_seqlens_q, "cu_seqlens_q", B + 1, index), _ints(q_start_pos, "q_start_pos", B, index),
              _ints(cu_pools, "cu_pools", B + 1, index), B)
-    o, lse = _output(o, "o", shape, bf16, index), _output(lse, "lse", shape[:2], torch.float32, index)
+    o = torch.empty_like(q) if o is None else _output(o, "o", shape, bf16, index)
+    lse = _output(lse, "lse", shape[:2], torch.float32, index)
     keep, ws, size = _bytes(workspace, 0 if workspace is not None else
                             _lib.kpool_sparse_mla_paged_workspace_size(Tq, kpool, index_topk), index)
     # (the stride of a single page says nothing)

@@ -26,9 +26,11 @@
 // scores exceed it by more than 8 in the base-2 exponent, so P <= 256; P goes to
 // shared memory in BF16 (the MMA's operand type), sums and statistics are FP32.
 //
-// Where rows are few (half the SMs or less), a row's blocks are cut into even runs,
-// FP32 outputs of the runs go to the workspace with their log-sums, and a second
-// kernel joins them.
+// Where rows are few (half the SMs or less), a row's blocks are cut into even runs, one
+// for each CTA; FP32 outputs of the runs go to the workspace with their log-sums, and a
+// second kernel joins them (and the CTAs' status words, so that none has to be cleared
+// in front of the call: a launch less).  Otherwise a first kernel clears the counter and
+// the status.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -60,7 +62,7 @@ constexpr int kSlot = 2 * kChunk;
 constexpr int kInfoSlots = 4;
 constexpr float kRescale = 8.f;         // headroom of the reference maximum (log2)
 constexpr int kMaxSplit = 32;           // runs of a row
-constexpr int kMaxSms = 160;             // that a workspace has room for
+constexpr int kMaxSms = 160;            // that a workspace has room for
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr int kTmemCols = 512;          // O^T: 0..255, S: 256..335 and 336..415
 constexpr int kTmemS = 256;
@@ -105,12 +107,17 @@ __device__ __forceinline__ int divide(int n, const Divisor &d)
     return d.mul ? static_cast<int>(__umulhi(static_cast<uint32_t>(n), d.mul) >> d.shift) : n;
 }
 
+// workspace: header (ints: unit counter, status, each CTA's status where rows are cut),
+// outputs and log-sums of the runs
+constexpr int kHeadInts = 256, kHeadCtas = 64;
+static_assert(kHeadCtas + kMaxSms <= kHeadInts, "a status word for each CTA");
+
 struct Params {
     PagedMlaArgs a;
     Divisor by_pool, by_page;
     float c_scale;              // softmax scale * log2(e)
     int split;                  // runs of a row (1: rows are whole)
-    int *ws;                    // [0] unit counter, [1] status
+    int *ws;                    // header
     float *part_lse;            // [Tq * split, 64], base 2
     float *part_o;              // [Tq * split, 64, 512]
     uint64_t wait_limit_ns;
@@ -239,6 +246,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
 
+    int *status = p.split > 1 ? p.ws + kHeadCtas + blockIdx.x : p.ws + 1;
+
     if (threadIdx.x == 0) {
         ptx::mbar_init(bar(BQ_FULL), 1);
         ptx::mbar_init(bar(BQ_EMPTY), 1);
@@ -260,6 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mbar_init(bar(BI_EMPTY + i), 2 + kSoftWarps + kOutWarps + kLoaderWarps);
         }
         misc[1] = 0u;
+        if (p.split > 1) *status = 0;
         ptx::fence_mbar_init();
     }
     if (warp == 1) {
@@ -270,9 +280,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = misc[0];
-    const Sync sy{reinterpret_cast<volatile uint32_t *>(&misc[1]), p.ws + 1, p.wait_limit_ns, p.wait_limit_ns < 1000000u};
+    const Sync sy{reinterpret_cast<volatile uint32_t *>(&misc[1]), status, p.wait_limit_ns, p.wait_limit_ns < 1000000u};
     ptx::grid_dependents_launch();
-    ptx::grid_dependency_wait();        // the cleared counter and status
+    ptx::grid_dependency_wait();        // the cleared counter and status (whole rows)
 
     // the block records, one after another, for every role but the loaders
     auto next_info = [&](int g, BInfo &in) {
@@ -290,11 +300,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---------------- control: units and their blocks ----------------
         const int units = static_cast<int>(p.a.Tq) * p.split;
         bool ok = true, bad = false;
-        int g = 0;                      // blocks published
+        int g = 0, run = blockIdx.x;    // blocks published
         while (ok) {
             int u = -1;
-            if (lane == 0 && !*sy.abort_flag) u = atomicAdd(p.ws, 1);
-            u = __shfl_sync(kFull, u, 0);
+            if (p.split > 1) {
+                u = run;                // a CTA for each
+                run = -1;
+            } else {
+                if (lane == 0 && !*sy.abort_flag) u = atomicAdd(p.ws, 1);
+                u = __shfl_sync(kFull, u, 0);
+            }
             if (u < 0 || u >= units) break;
             const int t = u / p.split;
             const PagedRow m = paged_row(p.a, t, lane);
@@ -702,14 +717,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// In front: a cleared counter and status; cu_q has to be 0 .. Tq and non-decreasing.
+// The status that cu_q gives: it has to be 0 .. Tq and non-decreasing.  One block.
+__device__ __forceinline__ int status_of(const int32_t *cu_q, int B, int64_t Tq)
+{
+    bool bad = cu_q[0] != 0 || cu_q[B] != Tq;
+    for (int i = threadIdx.x; i < B; i += blockDim.x) bad |= cu_q[i] > cu_q[i + 1];
+    return __syncthreads_or(bad) ? KPOOL_STATUS_BAD_SEQLENS : 0;
+}
+
+// In front of whole rows: a cleared counter, and the status.
 __global__ void __launch_bounds__(256) start_kernel(const int32_t *cu_q, int B, int64_t Tq, int *ws)
 {
     ptx::grid_dependents_launch();
-    bool bad = cu_q[0] != 0 || cu_q[B] != Tq;
-    for (int i = threadIdx.x; i < B; i += blockDim.x) bad |= cu_q[i] > cu_q[i + 1];
-    bad = __syncthreads_or(bad);
-    if (threadIdx.x < 64) ws[threadIdx.x] = threadIdx.x == 1 && bad ? KPOOL_STATUS_BAD_SEQLENS : 0;
+    const int status = status_of(cu_q, B, Tq);
+    if (threadIdx.x < 2) ws[threadIdx.x] = threadIdx.x == 1 ? status : 0;
 }
 
 // Joins the runs of a (row, head), a warp each: sum of 2^(lse_s - max) o_s over that of
@@ -720,6 +741,13 @@ __global__ void __launch_bounds__(128) join_kernel(const Params p)
     const int64_t r = (static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x) >> 5;
     const int64_t t = r / kH, h = r % kH, u0 = t * p.split;
     ptx::grid_dependency_wait();
+    if (blockIdx.x == 0) {
+        int status = status_of(p.a.cu_q, p.a.B, p.a.Tq);
+        for (int u = threadIdx.x; u < p.a.Tq * p.split; u += 128) status |= p.ws[kHeadCtas + u];
+        status |= __syncthreads_or(status & KPOOL_STATUS_BAD_PAGE) ? KPOOL_STATUS_BAD_PAGE : 0;
+        status |= __syncthreads_or(status & KPOOL_STATUS_TIMEOUT) ? KPOOL_STATUS_TIMEOUT : 0;
+        if (threadIdx.x == 0) p.ws[1] = status;
+    }
     const float mine = lane < p.split ? p.part_lse[(u0 + lane) * kH + h] : -INFINITY;
     float top = mine;
 #pragma unroll
@@ -782,7 +810,7 @@ int runs(int64_t Tq, int Kp, int kpool, int sms)
 size_t paged_mla_workspace_bytes(int64_t Tq, int Kp, int kpool)
 {
     const int n = runs(Tq, Kp, kpool, kMaxSms);
-    return 256 + (n > 1 ? static_cast<size_t>(Tq) * n * kH * (kDc + 1) * 4 : 0);
+    return kHeadInts * 4 + (n > 1 ? static_cast<size_t>(Tq) * n * kH * (kDc + 1) * 4 : 0);
 }
 
 int run_paged_mla(const PagedMlaArgs &a, cudaStream_t s)
@@ -796,7 +824,7 @@ int run_paged_mla(const PagedMlaArgs &a, cudaStream_t s)
     p.by_page = divisor(a.page_size);
     p.split = runs(a.Tq, a.Kp, a.kpool, sms);
     p.ws = reinterpret_cast<int *>(ws);
-    p.part_o = reinterpret_cast<float *>(ws + 256);
+    p.part_o = reinterpret_cast<float *>(ws + kHeadInts * 4);
     p.part_lse = p.part_o + a.Tq * p.split * kH * kDc;
     p.wait_limit_ns = get_wait_limit_ns();
     CUtensorMap mq;
@@ -806,13 +834,17 @@ int run_paged_mla(const PagedMlaArgs &a, cudaStream_t s)
         KPOOL_CUDA_CHECK(
             cudaFuncSetAttribute(paged_mla_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes));
     }
+    if (p.split > 1) {
+        paged_mla_kernel<<<static_cast<unsigned>(a.Tq * p.split), kThreads, kSmemBytes, s>>>(mq, p);
+        KPOOL_CUDA_CHECK(cudaGetLastError());
+        KPOOL_CUDA_CHECK(launch_after(join_kernel, static_cast<int>(a.Tq * (kH / 4)), 128, 0, s, p));
+        return KPOOL_OK;
+    }
     start_kernel<<<1, 256, 0, s>>>(a.cu_q, a.B, a.Tq, p.ws);
     KPOOL_CUDA_CHECK(cudaGetLastError());
-    if (a.Tq == 0) return KPOOL_OK;
-    KPOOL_CUDA_CHECK(launch_after(paged_mla_kernel, static_cast<int>(std::min<int64_t>(sms, a.Tq * p.split)), kThreads,
-                                  kSmemBytes, s, mq, p));
-    if (p.split > 1)
-        KPOOL_CUDA_CHECK(launch_after(join_kernel, static_cast<int>(a.Tq * (kH / 4)), 128, 0, s, p));
+    if (a.Tq > 0)
+        KPOOL_CUDA_CHECK(launch_after(paged_mla_kernel, static_cast<int>(std::min<int64_t>(sms, a.Tq)), kThreads,
+                                      kSmemBytes, s, mq, p));
     return KPOOL_OK;
 }
 
