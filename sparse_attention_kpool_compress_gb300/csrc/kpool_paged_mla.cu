@@ -400,6 +400,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = in.b > 0 || wait_bar_warp(bar(BQ_FULL), q_ph, sy);
             if (in.b == 0) q_ph ^= 1;
             // (the scores of two blocks ago were read before their P was complete)
+            // (rolled loops: unrolled, 8192 queries over 65536 tokens take 3.51 ms, so 3.38)
+#pragma unroll 1
             for (int sl = ahead; sl < kQuarters && ok; ++sl) {
                 const uint32_t ph = landed(g, sl, at);
                 ok = wait_bar_warp(at, ph, sy);
@@ -415,6 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool known = __shfl_sync(kFull, ptx::mbar_test(bar(BI_FULL + (g + 1) % kInfoSlots), ((g + 1) / kInfoSlots) & 1), 0);
             if (known) {
                 more = next_info(g + 1, nx);
+#pragma unroll 1
                 for (; more && nx.b > 0 && ahead < kQuarters - 1; ++ahead) {
                     const uint32_t ph = landed(g + 1, ahead, at);
                     if (!__shfl_sync(kFull, ptx::mbar_test(at, ph), 0)) break;
