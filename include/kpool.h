@@ -480,8 +480,10 @@ KPOOL_API int kpool_sparse_mla_fwd_pools_at(const void *q, const void *kv, const
  *   dq_out       bf16 [T, H, Dc];  dkv_out  bf16 [Tk, Dc]: overwritten, apart
  *                from the inputs; 16-byte aligned
  *   workspace    >= kpool_sparse_mla_bwd_workspace_size(T, Tk) bytes (the FP32
- *                sums of dkv and some words), 256-byte aligned; its status
- *                word (kpool_read_status) reports a pipeline timeout
+ *                sums of dkv, and two words a row and head), 256-byte aligned;
+ *                its status word (kpool_read_status) reports a pipeline timeout
+ *                (KPOOL_STATUS_TIMEOUT: outputs invalid).  Calls that may
+ *                overlap need workspaces of their own
  * Supported shapes as the forward calls.  The three calls list tokens as
  * kpool_sparse_mla_fwd, _pools and _pools_at do (Tk = T for _pools).
  */
@@ -706,7 +708,9 @@ KPOOL_API int kpool_shared_prefix_mla_fwd(
  *                bytes, 256-byte aligned
  * Latent rows that are listed must be finite; no other row is read.
  * Device status: KPOOL_STATUS_BAD_SEQLENS when cu_seqlens_q is not 0 .. Tq
- * non-decreasing; KPOOL_STATUS_BAD_PAGE when a table row, length, position or
+ * non-decreasing (rows outside cu_seqlens_q[0] .. cu_seqlens_q[B] - 1 are left
+ * as they were, the others' results are not valid where it decreases);
+ * KPOOL_STATUS_BAD_PAGE when a table row, length, position or
  * page id that the call uses is out of range (such tokens are skipped, a length
  * is cut to its table's room, a position to the length; results of those rows
  * are not valid); KPOOL_STATUS_TIMEOUT as for kpool_sparse_mla_fwd.
@@ -734,10 +738,9 @@ KPOOL_API int kpool_read_status(const void *workspace, int *status_out);
  * kpool_debug_set_wait_limit_ns -- test entry: the time limit of each wait
  * inside the scoring kernel (kpool_score_topk, _at, _noalloc, _dense and the
  * host-buffer pass), the sparse attention (kpool_sparse_mla_*, its backward
- * pass and its paged form among them) and the
- * shared-prefix attention (kpool_shared_prefix_mla_fwd) for launches made
- * after this call, process-wide; ns = 0
- * restores the default of 2 s.  Returns the previous limit.  A wait that
+ * pass and its paged form among them) and the shared-prefix attention
+ * (kpool_shared_prefix_mla_fwd) for launches made after this call,
+ * process-wide; ns = 0 restores the default of 2 s.  Returns the previous limit.  A wait that
  * runs out sets KPOOL_STATUS_TIMEOUT in the call's status word and raises an
  * abort flag in its CTA: the CTA's roles stop waiting, let their in-flight
  * copies and MMAs land (bounded by 2 s whatever this limit), free their

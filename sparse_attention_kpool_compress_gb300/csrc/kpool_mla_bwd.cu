@@ -9,7 +9,7 @@
 //   dq[t, h, :]  = sum_j ds_j c[j, :]
 //   dc[j, :]    += ds_j q[t, h, :] + p_j do[t, h, :]
 //
-// Design (one persistent CTA per SM, 24 warps, rows handed out by an atomic
+// Design (one persistent CTA per SM, 28 warps, rows handed out by an atomic
 // counter, the last first).  Q and dO of a row are stacked, eight heads of one and
 // the same eight of the other in turn: X [128 x 512].  Per block of 64 listed tokens
 // C [64 x 512], in tensor memory:
@@ -20,16 +20,35 @@
 // does one tile [dS; P] [128 x 64].  Heads in eights put the score and the dP of a
 // (head, token) into one thread's registers (a 16x256b load has lanes r and r + 8),
 // so P and dS need no exchange; lse is known, so no maximum and no sum either.
-//   warp 0       control: per row X (TMA), per block a record with its token ids
+//   warp 0       control: rows, and per block a record with its token ids
 //   warp 1       MMA issuer (the loop in all lanes, one issues)
+//   warp 2       X (TMA), ahead into L2
 //   warps 4-11   P and dS; after a row's last block, dQ
-//   warps 12-15  dC^T from tensor memory, added to the FP32 sums in L2
-//   warps 16-23  loaders: the tokens' latent rows by 16-byte cp.async, a pair of
+//   warps 12-19  dC^T from tensor memory, added to the FP32 sums in L2
+//   warps 20-27  loaders: the tokens' latent rows by 16-byte cp.async, a pair of
 //                warps per slot of 128 columns
-// The MMAs' order is: a block's scores; the second half of the last block's dC,
-// while P and dS are made; dQ, which frees the slots one by one; the first half of
-// dC, while the next block's rows land.  dC goes in four parts through three slots of
-// tensor memory.
+// The MMAs' order is: a block's scores; the last part of the last block's dC, while P
+// and dS are made; dQ, which frees the slots one by one; three parts of dC, while the
+// next block's rows land.  dC goes in four parts through three slots of tensor memory.
+// P and dS are rounded to BF16, the type of the MMAs' operands (2^-8 of each at most);
+// everything that is summed, is summed in FP32.
+//
+// Two kernels more: in front, {lse, delta} of each (row, head) and cleared sums;
+// behind, the sums rounded to BF16.
+//
+// What bounds it: 10 * 64 * 512 FLOP a (row, token), and 2 KB added into L2 for each,
+// since a row's tokens are its own: no tile of keys meets enough queries to sum them on
+// chip first.  Additions reach 6.0 to 6.3 TB/s here where the sums fit L2 (64 MB; into
+// 256 MB 3.7), so 32768 rows of up to 2051 tokens take 22 ms for them and 11 for the
+// MMAs at the rate of a library product; the call takes 28.1 ms (757 TFLOP/s, 4.7 TB/s
+// of additions).  A block takes 8000 cycles: the tensor pipe 32%, the path to shared
+// memory 73% (operands 48%, and each dC value goes through it twice).  Steps on 8192
+// rows: four sums warps with 4-byte additions 9.8 ms; through shared memory with
+// 16-byte additions 7.5; eight such warps, X ahead into L2 6.8; the first parts of dC
+// moved behind dQ 6.65; X in quarters, token ids read ahead 6.47; X given up in quarters
+// 6.39.  Slower: bulk reductions from shared memory (8.0 to 8.6), direct 4-byte
+// additions by eight warps (6.7), waits polled by one lane (11.1) or without suspending
+// (9.3).
 #include <cuda_bf16.h>
 
 #include <algorithm>

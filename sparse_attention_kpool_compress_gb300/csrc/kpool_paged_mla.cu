@@ -131,6 +131,9 @@ struct PagedRow {
     bool bad;                   // a sequence or length out of range
 };
 
+// Does row t belong to a sequence of the batch?  Others are left as they were.
+__device__ __forceinline__ bool in_batch(const PagedMlaArgs &p, int t) { return t >= p.cu_q[0] && t < p.cu_q[p.B]; }
+
 __device__ __forceinline__ PagedRow paged_row(const PagedMlaArgs &p, int t, int lane)
 {
     PagedRow m{};
@@ -312,6 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (u < 0 || u >= units) break;
             const int t = u / p.split;
+            if (!in_batch(p.a, t)) continue;
             const PagedRow m = paged_row(p.a, t, lane);
             bad |= m.bad;
             const int all = (m.n_slots + kBT - 1) / kBT, per = (all + p.split - 1) / p.split;
@@ -751,6 +755,7 @@ __global__ void __launch_bounds__(128) join_kernel(const Params p)
         status |= __syncthreads_or(status & KPOOL_STATUS_TIMEOUT) ? KPOOL_STATUS_TIMEOUT : 0;
         if (threadIdx.x == 0) p.ws[1] = status;
     }
+    if (!in_batch(p.a, static_cast<int>(t))) return;
     const float mine = lane < p.split ? p.part_lse[(u0 + lane) * kH + h] : -INFINITY;
     float top = mine;
 #pragma unroll

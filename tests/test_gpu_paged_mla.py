@@ -182,6 +182,29 @@ def test_bad_pages_are_skipped(K):
     c.check(o, lse)
 
 
+@pytest.mark.parametrize("queries", [[1, 2, 1], [60, 50, 70]])
+def test_rows_outside_the_batch_stay(K, queries):
+    """A padded q: rows behind the last sequence (and in front of the first) are left as they were, told by
+    the status; the others are right.  Cut rows and whole ones."""
+    c = Case(19, [700, 400, 550], queries, 4, 100, 64)
+    n, pad = c.q.shape[0], 5
+    c.q = torch.cat([c.q, torch.full((pad, H, DC), torch.nan, device="cuda", dtype=torch.bfloat16)])
+    c.sel = torch.cat([c.sel, torch.full((pad, c.budget), 2 ** 31 - 1, device="cuda", dtype=torch.int32)])
+    ws = c.workspace(K)
+    o, lse = torch.full_like(c.q, 7.0), torch.full((n + pad, H), 7.0, device="cuda")
+    c.call(K, workspace=ws, o=o, lse=lse)
+    assert K.kpool_read_status(ws) == K.STATUS_BAD_SEQLENS
+    assert torch.all(o[n:] == 7) and torch.all(lse[n:] == 7)
+    c.check(o, lse, rows=set(range(0, n, max(1, n // 9))) | {n - 1})
+    # and the first sequence's first row taken out
+    o.fill_(7.0)
+    lse.fill_(7.0)
+    c.cu_q[0], c.pos[0] = 1, int(c.pos[0]) + 1
+    c.call(K, workspace=ws, o=o, lse=lse)
+    assert torch.all(o[0] == 7) and torch.all(lse[0] == 7) and torch.all(o[n:] == 7)
+    c.check(o, lse, rows={1, n - 1})
+
+
 def test_degenerate_batches(K):
     """No query rows, and rows whose masks leave nothing (o = 0, lse = -inf)."""
     c = Case(9, [50, 3], [0, 0], 4, 8, 16)
