@@ -24,7 +24,19 @@
 //                quarters in flight
 // One reference maximum per head, raised (and O^T rescaled) only when a block's
 // scores exceed it by more than 8 in the base-2 exponent, so P <= 256; P goes to
-// shared memory in BF16 (the MMA's operand type), sums and statistics are FP32.
+// shared memory in BF16 (the MMA's operand type: 2^-8 of each at most), sums and
+// statistics are FP32.
+//
+// What bounds it: 4 * 64 * 512 FLOP and 1 KB gathered, mostly from L2, a (row, token).
+// 8192 rows of 2051 tokens take 3.38 ms: 650 TFLOP/s, 5.1 TB/s (1.15 ms at the rate of a
+// library product).  The tensor pipe is 40% busy, shared memory's operands 43%: a block's
+// chain (its last quarter lands, scores, softmax, first quarter of the output) is longer
+// than its MMAs, and the next block's rows can only be three quarters there, next to the
+// 64 KB of Q.  Steps: 64-token blocks, two in flight, four softmax warps 4.40 ms (the
+// MMAs fell behind one another's latencies); divisions by multiplication in control 4.24;
+// 128-token blocks, one in flight 3.70; the ring of 80-token blocks 3.73, but 128 decode
+// steps 99 -> 87 us; all loader warps on each quarter 3.49 and 81 us; rolled issue loops
+// 3.38.  Slower: unrolled or shuffled-uniform MMA operands (3.73).
 //
 // Where rows are few (half the SMs or less), a row's blocks are cut into even runs, one
 // for each CTA; FP32 outputs of the runs go to the workspace with their log-sums, and a
@@ -803,7 +815,9 @@ cudaError_t launch_after(void (*kernel)(P...), int grid, int threads, int smem, 
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// Runs of a row, where rows are at most half of the SMs: as many as fill them.
+// Runs of a row, where rows are at most half of the SMs: as many as fill them.  (2049
+// tokens a row, us a call in a graph, cut and whole: 1 row 22 and 69, 8 rows 29 and 70,
+// 38 rows 37 and 73, 76 rows, in two runs each, 55 and 77.)
 int runs(int64_t Tq, int Kp, int kpool, int sms)
 {
     if (Tq == 0 || 2 * Tq > sms) return 1;
