@@ -34,7 +34,8 @@
 // everything that is summed, is summed in FP32.
 //
 // Two kernels more: in front, {lse, delta} of each (row, head) and cleared sums;
-// behind, the sums rounded to BF16.
+// behind, the sums rounded to BF16.  Where rows are few (half the SMs or less), a row's
+// blocks are cut into even runs, one for each CTA, whose FP32 dQ the last kernel adds up.
 //
 // What bounds it: 10 * 64 * 512 FLOP a (row, token), and 2 KB added into L2 for each,
 // since a row's tokens are its own: no tile of keys meets enough queries to sum them on
@@ -99,13 +100,21 @@ constexpr int kOffMisc = kOffBar + NBARS * 8;          // [0] tmem base, [1] abo
 constexpr int kSmemBytes = kOffMisc + 16 + 1024;       // and alignment slack
 static_assert(kSmemBytes <= 232448, "shared memory over the per-block limit");
 
-// workspace: header (ints: row counter, status), {lse, delta} of each (row, head), sums
+// workspace: header (ints: row counter, status; where rows are cut, whether a run has
+// blocks), {lse, delta} of each (row, head), the runs' dQ, sums
+constexpr int kHeadInts = 256, kHeadRuns = 64;
+constexpr int kMaxSms = 160;            // that a workspace has room for
+constexpr int kMaxSplit = 64;           // runs of a row
+static_assert(kHeadRuns + kMaxSms <= kHeadInts, "a word for each run");
+
 struct Params {
     RowLists rows;
     const uint16_t *q, *kv, *d_o;
     const float2 *stats;        // [T, 64]: lse * log2(e) (+inf: no token), delta
     uint16_t *dq;
     float *acc;                 // [Tk, 512]: the latent rows' gradients
+    int split;                  // runs of a row (1: rows are whole)
+    float *part;                // [T * split, 64, 512]: dQ of the runs
     float scale, c_scale;       // softmax scale, and that * log2(e)
     int *ws;
     uint64_t wait_limit_ns;
@@ -113,7 +122,7 @@ struct Params {
 
 // One block of a row.
 struct BInfo {
-    int t, b, nb, ksteps;
+    int t, b, nb, ksteps;       // b-th of nb blocks of a row, or of a run of row t
     uint32_t mask[2];           // bit r of mask[r / 32]: listed token r is valid
     int pad[2];
 };
@@ -175,6 +184,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&b);
 }
 
+template <bool kCut>
 __global__ void __launch_bounds__(kThreads, 1)
     sparse_mla_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
                           const __grid_constant__ Params p)
@@ -232,16 +242,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) {
         // ---------------- control: rows and their blocks ----------------
         bool ok = true;
-        int g = 0;                      // blocks published
+        int g = 0, run = blockIdx.x;    // blocks published; this CTA's run (of cut rows)
         while (ok) {
-            int t = -1;
-            if (lane == 0 && !*sy.abort_flag) t = p.rows.T - 1 - atomicAdd(p.ws, 1);
-            t = __shfl_sync(kFull, t, 0);
-            if (t < 0) break;
+            int t = -1, b0 = 0;
+            if (kCut) {
+                if (run < 0) break;
+                t = run / p.split;
+            } else {
+                if (lane == 0 && !*sy.abort_flag) t = p.rows.T - 1 - atomicAdd(p.ws, 1);
+                t = __shfl_sync(kFull, t, 0);
+                if (t < 0) break;
+            }
             const RowMsg m = row_msg(p.rows, t, lane);
-            const int nb = max(1, (m.n_slots + kBT - 1) / kBT);
+            int nb = max(1, (m.n_slots + kBT - 1) / kBT);
+            if (kCut) {
+                const int per = (nb + p.split - 1) / p.split;
+                b0 = (run - t * p.split) * per;
+                nb = max(0, min(nb - b0, per));
+                if (lane == 0) p.ws[kHeadRuns + run] = nb;
+                run = -1;
+            }
             for (int b = 0; b < nb; ++b, ++g) {
-                const int t0 = token_of(p.rows, m, b * kBT + 2 * lane), t1 = token_of(p.rows, m, b * kBT + 2 * lane + 1);
+                const int j0 = (b0 + b) * kBT;
+                const int t0 = token_of(p.rows, m, j0 + 2 * lane), t1 = token_of(p.rows, m, j0 + 2 * lane + 1);
                 // validity word w (tokens 32w .. 32w + 31) from lanes 16w .. 16w + 15
                 uint32_t mw = ((t0 >= 0 ? 1u : 0u) | (t1 >= 0 ? 2u : 0u)) << (2 * (lane & 15));
                 mw |= __shfl_xor_sync(kFull, mw, 1);
@@ -257,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     info[is].t = t;
                     info[is].b = b;
                     info[is].nb = nb;
-                    info[is].ksteps = max(1, (min(kBT, m.n_slots - b * kBT) + 15) / 16);
+                    info[is].ksteps = max(1, (min(kBT, m.n_slots - j0) + 15) / 16);
                 }
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(bar(BI_FULL + is));
@@ -466,8 +489,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ptx::tmem_ld_wait(v);
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
-                            const __nv_bfloat16 b = __float2bfloat16_rn(__uint_as_float(v[i]));
-                            out[static_cast<int64_t>(hh * 32 + i) * kDc + part * 128] = *reinterpret_cast<const uint16_t *>(&b);
+                            const int64_t at = static_cast<int64_t>(hh * 32 + i) * kDc + part * 128;
+                            if (kCut) {
+                                p.part[static_cast<int64_t>(blockIdx.x) * kH * kDc + 32 * sub + lane + at] = __uint_as_float(v[i]);
+                            } else {
+                                const __nv_bfloat16 b = __float2bfloat16_rn(__uint_as_float(v[i]));
+                                out[at] = *reinterpret_cast<const uint16_t *>(&b);
+                            }
                         }
                     }
                 ptx::tc_fence_before();
@@ -598,21 +626,31 @@ __global__ void __launch_bounds__(256) stats_kernel(const uint4 *o, const uint4 
     }
 }
 
-// The sums of the latent rows' gradients, rounded to BF16: eight a thread.
-__global__ void __launch_bounds__(256) round_kernel(const float4 *acc, uint4 *out, int64_t n)
+__device__ __forceinline__ uint4 round8(const float4 &a, const float4 &b)
+{
+    return make_uint4(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w), pack_bf16(b.x, b.y), pack_bf16(b.z, b.w));
+}
+
+// The sums of the latent rows' gradients, rounded to BF16, and the runs' dQ added up: eight
+// values a thread.
+__global__ void __launch_bounds__(256) round_kernel(const float4 *acc, uint4 *dkv, int64_t n, const float4 *part,
+                                                    uint4 *dq, int64_t n_dq, int split, const int *runs)
 {
     ptx::grid_dependency_wait();
     const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
-    for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < n; i += step) {
-        const float4 a = acc[2 * i], b = acc[2 * i + 1];
-        const float2 v[4] = {{a.x, a.y}, {a.z, a.w}, {b.x, b.y}, {b.z, b.w}};
-        uint32_t w[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const __nv_bfloat162 x = __floats2bfloat162_rn(v[k].x, v[k].y);
-            w[k] = *reinterpret_cast<const uint32_t *>(&x);
+    const int64_t first = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x;
+    for (int64_t i = first; i < n; i += step) dkv[i] = round8(acc[2 * i], acc[2 * i + 1]);
+    constexpr int kRow = kH * kDc / 8;
+    for (int64_t i = first; i < n_dq; i += step) {
+        const int64_t t = i / kRow, at = i % kRow;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+        for (int64_t r = t * split; r < (t + 1) * split; ++r) {
+            if (runs[r] == 0) break;                       // (runs without blocks come last)
+            const float4 x = part[2 * (r * kRow + at)], y = part[2 * (r * kRow + at) + 1];
+            a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
+            b.x += y.x; b.y += y.y; b.z += y.z; b.w += y.w;
         }
-        out[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        dq[i] = round8(a, b);
     }
 }
 
@@ -634,11 +672,25 @@ cudaError_t launch_after(void (*kernel)(P...), int grid, int threads, int smem, 
 
 size_t stats_bytes(int64_t T) { return (static_cast<size_t>(T) * kH * sizeof(float2) + 255) / 256 * 256; }
 
+// Runs of a row, where rows are at most half of the SMs: as many as fill them, and no more
+// than the longest list has blocks.  (2051 tokens a row, us a call in a graph, cut and
+// whole: 1 row 29 and 145, 16 rows 37 and 147, 38 rows 57 and 147, 76 rows, in two runs
+// each, 92 and 148.)
+int runs(int64_t T, int64_t slots, int sms)
+{
+    if (T == 0 || 2 * T > sms) return 1;
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({sms / T, (slots + kBT - 1) / kBT, kMaxSplit})));
+}
+
 }  // namespace
 
+// (Neither the device that a caller sizes its workspace on nor the lists' width is known
+// here: room for as many runs as there can be.)
 size_t sparse_mla_bwd_workspace_bytes(int64_t T, int64_t Tk)
 {
-    return 256 + stats_bytes(T) + static_cast<size_t>(Tk) * kDc * 4;
+    const int64_t n = T * runs(T, int64_t(kMaxSplit) * kBT, kMaxSms);
+    return kHeadInts * 4 + stats_bytes(T) + (n > T ? static_cast<size_t>(n) * kH * kDc * 4 : 0) +
+           static_cast<size_t>(Tk) * kDc * 4;
 }
 
 int run_sparse_mla_bwd(const SparseMlaArgs &a, const SparseMlaGrad &g, cudaStream_t s)
@@ -649,15 +701,19 @@ int run_sparse_mla_bwd(const SparseMlaArgs &a, const SparseMlaGrad &g, cudaStrea
     p.q = static_cast<const uint16_t *>(a.q);
     p.kv = static_cast<const uint16_t *>(a.kv);
     p.d_o = static_cast<const uint16_t *>(g.d_o);
-    float2 *stats = reinterpret_cast<float2 *>(ws + 256);
+    float2 *stats = reinterpret_cast<float2 *>(ws + kHeadInts * 4);
     p.stats = stats;
     p.dq = static_cast<uint16_t *>(g.dq);
-    p.acc = reinterpret_cast<float *>(ws + 256 + stats_bytes(a.T));
+    const int sms = std::min(num_sms(), kMaxSms);
+    // (pools list a token once at most)
+    p.split = runs(a.T, a.tok_idx != nullptr ? a.W : std::min<int64_t>(a.Tk, static_cast<int64_t>(a.Kp) * a.kpool + a.kpool - 1),
+                   sms);
+    p.part = reinterpret_cast<float *>(ws + kHeadInts * 4 + stats_bytes(a.T));
+    p.acc = p.part + (p.split > 1 ? a.T * p.split * kH * kDc : 0);
     p.scale = a.scale;
     p.c_scale = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
     p.ws = reinterpret_cast<int *>(ws);
     p.wait_limit_ns = get_wait_limit_ns();
-    const int sms = num_sms();
     const int64_t rows = a.T * kH, n_acc = a.Tk * (kDc / 4);
     const int64_t blocks = std::max<int64_t>(1, std::max((rows + 7) / 8, (n_acc + 1023) / 1024));
     stats_kernel<<<static_cast<unsigned>(std::min<int64_t>(blocks, 8 * sms)), 256, 0, s>>>(
@@ -670,15 +726,17 @@ int run_sparse_mla_bwd(const SparseMlaArgs &a, const SparseMlaGrad &g, cudaStrea
         if (rc) return rc;
         rc = encode_bf16_groups_tmap(&mdo, g.d_o, static_cast<uint64_t>(rows));
         if (rc) return rc;
-        KPOOL_CUDA_CHECK(cudaFuncSetAttribute(sparse_mla_bwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                              kSmemBytes));
-        KPOOL_CUDA_CHECK(launch_after(sparse_mla_bwd_kernel, static_cast<int>(std::min<int64_t>(sms, a.T)), kThreads,
-                                      kSmemBytes, s, mq, mdo, p));
+        const auto kernel = p.split > 1 ? sparse_mla_bwd_kernel<true> : sparse_mla_bwd_kernel<false>;
+        KPOOL_CUDA_CHECK(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes));
+        KPOOL_CUDA_CHECK(launch_after(kernel, static_cast<int>(p.split > 1 ? a.T * p.split : std::min<int64_t>(sms, a.T)),
+                                      kThreads, kSmemBytes, s, mq, mdo, p));
     }
-    const int64_t n = a.Tk * (kDc / 8);
-    if (n > 0)
-        KPOOL_CUDA_CHECK(launch_after(round_kernel, static_cast<int>(std::min<int64_t>((n + 255) / 256, 8 * sms)), 256, 0,
-                                      s, reinterpret_cast<const float4 *>(p.acc), static_cast<uint4 *>(g.dkv), n));
+    const int64_t n = a.Tk * (kDc / 8), n_dq = p.split > 1 ? a.T * (kH * kDc / 8) : 0;
+    if (std::max(n, n_dq) > 0)
+        KPOOL_CUDA_CHECK(launch_after(
+            round_kernel, static_cast<int>(std::min<int64_t>((std::max(n, n_dq) + 255) / 256, 8 * sms)), 256, 0, s,
+            reinterpret_cast<const float4 *>(p.acc), static_cast<uint4 *>(g.dkv), n, reinterpret_cast<const float4 *>(p.part),
+            static_cast<uint4 *>(g.dq), n_dq, p.split, static_cast<const int *>(p.ws + kHeadRuns)));
     return KPOOL_OK;
 }
 

@@ -369,7 +369,8 @@ def test_rollout_and_training_step(K):
     rows = (torch.arange(answers, device="cuda")[:, None] * total + prompt + torch.arange(steps, device="cuda")).view(-1)
     dq2, dkv2 = K.kpool_sparse_mla_bwd_pools_at(qf[rows], kvf, sel[rows], o[rows], lse[rows], d_o[rows], kp, topk, SCALE,
                                                 _dev(np.arange(answers + 1) * steps), _dev([prompt] * answers), cu, cu_pools)
-    assert torch.equal(dq2, dq[rows]) and torch.all(dq.view(answers, total, H, DC)[:, :prompt] == 0)
+    # (few rows are cut into runs, whose sums are joined in FP32)
+    assert torch.allclose(dq2.float(), dq[rows].float(), rtol=2.0 ** -7, atol=1e-6) and torch.all(dq.view(answers, total, H, DC)[:, :prompt] == 0)
     assert torch.allclose(dkv2.float(), dkv.float(), rtol=2.0 ** -7, atol=1e-5)
 
 
