@@ -480,7 +480,7 @@ KPOOL_API int kpool_sparse_mla_fwd_pools_at(const void *q, const void *kv, const
  *   dq_out       bf16 [T, H, Dc];  dkv_out  bf16 [Tk, Dc]: overwritten, apart
  *                from the inputs; 16-byte aligned
  *   workspace    >= kpool_sparse_mla_bwd_workspace_size(T, Tk) bytes (the FP32
- *                sums of dkv, and two words a row and head), 256-byte aligned;
+ *                sums of dkv; for few rows partial dq too), 256-byte aligned;
  *                its status word (kpool_read_status) reports a pipeline timeout
  *                (KPOOL_STATUS_TIMEOUT: outputs invalid).  Calls that may
  *                overlap need workspaces of their own

@@ -23,7 +23,8 @@
 //   warp 0       control: rows, and per block a record with its token ids
 //   warp 1       MMA issuer (the loop in all lanes, one issues)
 //   warp 2       X (TMA), ahead into L2
-//   warps 4-11   P and dS; after a row's last block, dQ
+//   warps 4-11   lse and delta of a row, while X lands; P and dS; after a row's last
+//                block, dQ
 //   warps 12-19  dC^T from tensor memory, added to the FP32 sums in L2
 //   warps 20-27  loaders: the tokens' latent rows by 16-byte cp.async, a pair of
 //                warps per slot of 128 columns
@@ -33,21 +34,21 @@
 // P and dS are rounded to BF16, the type of the MMAs' operands (2^-8 of each at most);
 // everything that is summed, is summed in FP32.
 //
-// Two kernels more: in front, {lse, delta} of each (row, head) and cleared sums;
-// behind, the sums rounded to BF16.  Where rows are few (half the SMs or less), a row's
+// Two kernels more: in front, cleared sums; behind, the sums rounded to BF16.  Where rows are few (half the SMs or less), a row's
 // blocks are cut into even runs, one for each CTA, whose FP32 dQ the last kernel adds up.
 //
 // What bounds it: 10 * 64 * 512 FLOP a (row, token), and 2 KB added into L2 for each,
 // since a row's tokens are its own: no tile of keys meets enough queries to sum them on
 // chip first.  Additions reach 6.0 to 6.3 TB/s here where the sums fit L2 (64 MB; into
 // 256 MB 3.7), so 32768 rows of up to 2051 tokens take 22 ms for them and 11 for the
-// MMAs at the rate of a library product; the call takes 28.1 ms (757 TFLOP/s, 4.7 TB/s
+// MMAs at the rate of a library product; the call takes 27.9 ms (764 TFLOP/s, 4.8 TB/s
 // of additions).  A block takes 8000 cycles: the tensor pipe 32%, the path to shared
 // memory 73% (operands 48%, and each dC value goes through it twice).  Steps on 8192
 // rows: four sums warps with 4-byte additions 9.8 ms; through shared memory with
 // 16-byte additions 7.5; eight such warps, X ahead into L2 6.8; the first parts of dC
 // moved behind dQ 6.65; X in quarters, token ids read ahead 6.47; X given up in quarters
-// 6.39.  Slower: bulk reductions from shared memory (8.0 to 8.6), direct 4-byte
+// 6.40; lse and delta in this kernel instead of one in front 6.34 (3001 packed tokens 431
+// -> 401 us).  Slower: bulk reductions from shared memory (8.0 to 8.6), direct 4-byte
 // additions by eight warps (6.7), waits polled by one lane (11.1) or without suspending
 // (9.3).
 #include <cuda_bf16.h>
@@ -100,8 +101,8 @@ constexpr int kOffMisc = kOffBar + NBARS * 8;          // [0] tmem base, [1] abo
 constexpr int kSmemBytes = kOffMisc + 16 + 1024;       // and alignment slack
 static_assert(kSmemBytes <= 232448, "shared memory over the per-block limit");
 
-// workspace: header (ints: row counter, status; where rows are cut, whether a run has
-// blocks), {lse, delta} of each (row, head), the runs' dQ, sums
+// workspace: header (ints: row counter, status; where rows are cut, the blocks of a run),
+// the runs' dQ, sums
 constexpr int kHeadInts = 256, kHeadRuns = 64;
 constexpr int kMaxSms = 160;            // that a workspace has room for
 constexpr int kMaxSplit = 64;           // runs of a row
@@ -109,8 +110,8 @@ static_assert(kHeadRuns + kMaxSms <= kHeadInts, "a word for each run");
 
 struct Params {
     RowLists rows;
-    const uint16_t *q, *kv, *d_o;
-    const float2 *stats;        // [T, 64]: lse * log2(e) (+inf: no token), delta
+    const uint16_t *q, *kv, *o, *d_o;
+    const float *lse, *d_lse;
     uint16_t *dq;
     float *acc;                 // [Tk, 512]: the latent rows' gradients
     int split;                  // runs of a row (1: rows are whole)
@@ -171,6 +172,19 @@ __device__ __forceinline__ void red_add(float *to, const float4 &v)
     asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(to), "f"(v.x), "f"(v.y), "f"(v.z),
                  "f"(v.w)
                  : "memory");
+}
+
+// Sum of the products of eight BF16 pairs.
+__device__ __forceinline__ float dot8(const uint4 &x, const uint4 &y)
+{
+    const uint32_t a[4] = {x.x, x.y, x.z, x.w}, b[4] = {y.x, y.y, y.z, y.w};
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        s = fmaf(__uint_as_float(a[i] << 16), __uint_as_float(b[i] << 16), s);
+        s = fmaf(__uint_as_float(a[i] & 0xFFFF0000u), __uint_as_float(b[i] & 0xFFFF0000u), s);
+    }
+    return s;
 }
 
 __device__ __forceinline__ void st_shared(uint32_t saddr, uint32_t v)
@@ -236,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tc_fence_after();
     const uint32_t tmem = misc[0];
     const Sync sy{reinterpret_cast<volatile uint32_t *>(&misc[1]), p.ws + 1, p.wait_limit_ns};
-    // the statistics and the cleared sums and counter of the kernel in front
+    // the cleared sums and counter of the kernel in front
     ptx::grid_dependency_wait();
 
     if (warp == 0) {
@@ -308,7 +322,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (t < 0) break;
             if (b > 0) continue;
             // (known some blocks ahead: into L2 meanwhile)
-            if (lane < 2) prefetch_l2((lane ? p.d_o : p.q) + static_cast<int64_t>(t) * kH * kDc, kH * kDc * 2);
+            if (lane < 3)
+                prefetch_l2((lane == 0 ? p.q : lane == 1 ? p.d_o : p.o) + static_cast<int64_t>(t) * kH * kDc, kH * kDc * 2);
             // in pieces of 128 columns: the scores take them in turn, and the last block's dC has
             // given them up in turn
             bool ok = true;
@@ -438,9 +453,32 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) ptx::mbar_arrive(bar(BI_EMPTY + is));
             if (in.t < 0) break;
             if (in.b == 0) {
-                const float2 st = p.stats[static_cast<int64_t>(in.t) * kH + head];
-                lse = st.x;
-                delta = st.y;
+                // the row's statistics, while X lands: every lane sums this warp's heads in turn
+                const int64_t row0 = static_cast<int64_t>(in.t) * kH;
+                const float l = p.lse[row0 + head];
+                lse = l == -INFINITY ? INFINITY : l * 1.4426950408889634f;     // (no token: no probability)
+                delta = p.d_lse != nullptr ? -p.d_lse[row0 + head] : 0.f;
+                const uint4 *o = reinterpret_cast<const uint4 *>(p.o) + (row0 + 8 * grp) * 64 + lane;
+                const uint4 *d = reinterpret_cast<const uint4 *>(p.d_o) + (row0 + 8 * grp) * 64 + lane;
+#pragma unroll 1
+                for (int h = 0; h < 8; h += 2) {
+                    uint4 x[4], y[4];                      // two heads, two halves each
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        x[i] = o[h * 64 + 32 * i];
+                        y[i] = d[h * 64 + 32 * i];
+                    }
+                    float v[2];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) v[k] = dot8(x[2 * k], y[2 * k]) + dot8(x[2 * k + 1], y[2 * k + 1]);
+#pragma unroll
+                    for (int w = 16; w > 0; w >>= 1) {
+                        v[0] += __shfl_xor_sync(kFull, v[0], w);
+                        v[1] += __shfl_xor_sync(kFull, v[1], w);
+                    }
+                    if ((lane >> 2) == h) delta += v[0];
+                    if ((lane >> 2) == h + 1) delta += v[1];
+                }
             }
             if (!wait_bar_warp(bar(BS_FULL), g & 1, sy)) break;
             ptx::tc_fence_after();
@@ -594,36 +632,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// In front: {lse, delta} of each (row, head), a warp each, and cleared sums and counter.
-__global__ void __launch_bounds__(256) stats_kernel(const uint4 *o, const uint4 *d_o, const float *lse,
-                                                    const float *d_lse, float2 *stats, int64_t n, float4 *acc,
-                                                    int64_t n_acc, int *ws)
+// In front: cleared sums, counter and status.
+__global__ void __launch_bounds__(256) clear_kernel(float4 *acc, int64_t n, int *ws)
 {
-    const int lane = threadIdx.x & 31;
     const int64_t first = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x;
     const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+    ptx::grid_dependents_launch();
     if (first < 64) ws[first] = 0;
-    for (int64_t i = first; i < n_acc; i += step) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int64_t r = first >> 5; r < n; r += step >> 5) {
-        float s = 0.f;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const uint4 x = o[r * 64 + 32 * half + lane], y = d_o[r * 64 + 32 * half + lane];
-            const uint32_t a[4] = {x.x, x.y, x.z, x.w}, b[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                s = fmaf(__uint_as_float(a[i] << 16), __uint_as_float(b[i] << 16), s);
-                s = fmaf(__uint_as_float(a[i] & 0xFFFF0000u), __uint_as_float(b[i] & 0xFFFF0000u), s);
-            }
-        }
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(kFull, s, d);
-        if (lane == 0) {
-            const float l = lse[r];
-            // a row without tokens has no probability anywhere
-            stats[r] = make_float2(l == -INFINITY ? INFINITY : l * 1.4426950408889634f, s - (d_lse != nullptr ? d_lse[r] : 0.f));
-        }
-    }
+    for (int64_t i = first; i < n; i += step) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 }
 
 __device__ __forceinline__ uint4 round8(const float4 &a, const float4 &b)
@@ -670,8 +686,6 @@ cudaError_t launch_after(void (*kernel)(P...), int grid, int threads, int smem, 
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-size_t stats_bytes(int64_t T) { return (static_cast<size_t>(T) * kH * sizeof(float2) + 255) / 256 * 256; }
-
 // Runs of a row, where rows are at most half of the SMs: as many as fill them, and no more
 // than the longest list has blocks.  (2051 tokens a row, us a call in a graph, cut and
 // whole: 1 row 29 and 145, 16 rows 37 and 147, 38 rows 57 and 147, 76 rows, in two runs
@@ -689,7 +703,7 @@ int runs(int64_t T, int64_t slots, int sms)
 size_t sparse_mla_bwd_workspace_bytes(int64_t T, int64_t Tk)
 {
     const int64_t n = T * runs(T, int64_t(kMaxSplit) * kBT, kMaxSms);
-    return kHeadInts * 4 + stats_bytes(T) + (n > T ? static_cast<size_t>(n) * kH * kDc * 4 : 0) +
+    return kHeadInts * 4 + (n > T ? static_cast<size_t>(n) * kH * kDc * 4 : 0) +
            static_cast<size_t>(Tk) * kDc * 4;
 }
 
@@ -700,24 +714,23 @@ int run_sparse_mla_bwd(const SparseMlaArgs &a, const SparseMlaGrad &g, cudaStrea
     p.rows = row_lists(a);
     p.q = static_cast<const uint16_t *>(a.q);
     p.kv = static_cast<const uint16_t *>(a.kv);
+    p.o = static_cast<const uint16_t *>(a.o);
     p.d_o = static_cast<const uint16_t *>(g.d_o);
-    float2 *stats = reinterpret_cast<float2 *>(ws + kHeadInts * 4);
-    p.stats = stats;
+    p.lse = a.lse;
+    p.d_lse = g.d_lse;
     p.dq = static_cast<uint16_t *>(g.dq);
     const int sms = std::min(num_sms(), kMaxSms);
     // (pools list a token once at most)
     p.split = runs(a.T, a.tok_idx != nullptr ? a.W : std::min<int64_t>(a.Tk, static_cast<int64_t>(a.Kp) * a.kpool + a.kpool - 1),
                    sms);
-    p.part = reinterpret_cast<float *>(ws + kHeadInts * 4 + stats_bytes(a.T));
+    p.part = reinterpret_cast<float *>(ws + kHeadInts * 4);
     p.acc = p.part + (p.split > 1 ? a.T * p.split * kH * kDc : 0);
     p.scale = a.scale;
     p.c_scale = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
     p.ws = reinterpret_cast<int *>(ws);
     p.wait_limit_ns = get_wait_limit_ns();
     const int64_t rows = a.T * kH, n_acc = a.Tk * (kDc / 4);
-    const int64_t blocks = std::max<int64_t>(1, std::max((rows + 7) / 8, (n_acc + 1023) / 1024));
-    stats_kernel<<<static_cast<unsigned>(std::min<int64_t>(blocks, 8 * sms)), 256, 0, s>>>(
-        static_cast<const uint4 *>(a.o), static_cast<const uint4 *>(g.d_o), a.lse, g.d_lse, stats, rows,
+    clear_kernel<<<static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>((n_acc + 1023) / 1024, 8 * sms))), 256, 0, s>>>(
         reinterpret_cast<float4 *>(p.acc), n_acc, p.ws);
     KPOOL_CUDA_CHECK(cudaGetLastError());
     if (a.T > 0) {
