@@ -433,12 +433,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool known = __shfl_sync(kFull, ptx::mbar_test(bar(BI_FULL + (g + 1) % kInfoSlots), ((g + 1) / kInfoSlots) & 1), 0);
             if (known) {
                 more = next_info(g + 1, nx);
+                // (quarters land in order: the last one says it of the others)
+                int here = more && nx.b > 0 ? kQuarters - 1 : 0;
 #pragma unroll 1
-                for (; more && nx.b > 0 && ahead < kQuarters - 1; ++ahead) {
-                    const uint32_t ph = landed(g + 1, ahead, at);
-                    if (!__shfl_sync(kFull, ptx::mbar_test(at, ph), 0)) break;
-                    scores(g + 1, ahead);
+                for (; here > 0; --here) {
+                    const uint32_t ph = landed(g + 1, here - 1, at);
+                    if (__shfl_sync(kFull, ptx::mbar_test(at, ph), 0)) break;
                 }
+#pragma unroll 1
+                for (; ahead < here; ++ahead) scores(g + 1, ahead);
             }
             ok = wait_bar_warp(bar(BP_FULL), g & 1, sy);
             if (in.b == 0) {
