@@ -28,7 +28,7 @@
 // statistics are FP32.
 //
 // What bounds it: 4 * 64 * 512 FLOP and 1 KB gathered, mostly from L2, a (row, token).
-// 8192 rows of 2051 tokens take 3.38 ms: 650 TFLOP/s, 5.1 TB/s (1.15 ms at the rate of a
+// 8192 rows of 2051 tokens take 3.16 ms: 697 TFLOP/s, 5.4 TB/s (1.15 ms at the rate of a
 // library product).  The tensor pipe is 40% busy, shared memory's operands 43%: a block's
 // chain (its last quarter lands, scores, softmax, first quarter of the output) is longer
 // than its MMAs, and the next block's rows can only be three quarters there, next to the
@@ -36,7 +36,8 @@
 // MMAs fell behind one another's latencies); divisions by multiplication in control 4.24;
 // 128-token blocks, one in flight 3.70; the ring of 80-token blocks 3.73, but 128 decode
 // steps 99 -> 87 us; all loader warps on each quarter 3.49 and 81 us; rolled issue loops
-// 3.38.  Slower: unrolled or shuffled-uniform MMA operands (3.73).
+// 3.38; one look for all quarters that have landed 3.23; whole blocks' output MMAs
+// unrolled 3.16.  Slower: unrolled or shuffled-uniform MMA operands (3.73).
 //
 // Where rows are few (half the SMs or less), a row's blocks are cut into even runs, one
 // for each CTA; FP32 outputs of the runs go to the workspace with their log-sums, and a
@@ -455,9 +456,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int sl = 0; sl < kQuarters; ++sl) {
                     const uint32_t slot = (static_cast<uint32_t>(g) * kQuarters + sl) % kRing;
                     const uint64_t ad = ptx::smem_desc_mn_sw128(sC + slot * kSlot, kChunk);
-                    for (int kk = 0; kk < in.ksteps; ++kk)
+                    auto step = [&](int kk) {
                         ptx::mma_bf16(tmem + sl * 64, ad + kk * 128, bd + (kk >> 2) * 512 + (kk & 3) * 2, idesc_o,
                                       in.b > 0 || kk > 0);
+                    };
+                    if (in.ksteps == kBT / 16) {           // (whole blocks unrolled: 3.23 -> 3.16 ms)
+#pragma unroll
+                        for (int kk = 0; kk < kBT / 16; ++kk) step(kk);
+                    } else {
+                        for (int kk = 0; kk < in.ksteps; ++kk) step(kk);
+                    }
                     ptx::mma_commit(bar(BC_EMPTY + slot));
                 }
                 if (in.b == in.nb - 1) ptx::mma_commit(bar(BO_FULL));
