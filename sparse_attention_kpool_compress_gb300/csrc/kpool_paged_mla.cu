@@ -29,7 +29,7 @@
 //
 // What bounds it: 4 * 64 * 512 FLOP and 1 KB gathered, mostly from L2, a (row, token).
 // 8192 rows of 2051 tokens take 3.16 ms: 697 TFLOP/s, 5.4 TB/s (1.15 ms at the rate of a
-// library product).  The tensor pipe is 40% busy, shared memory's operands 43%: a block's
+// library product).  The tensor pipe is 43% busy, shared memory's operands 46%: a block's
 // chain (its last quarter lands, scores, softmax, first quarter of the output) is longer
 // than its MMAs, and the next block's rows can only be three quarters there, next to the
 // 64 KB of Q.  Steps: 64-token blocks, two in flight, four softmax warps 4.40 ms (the
