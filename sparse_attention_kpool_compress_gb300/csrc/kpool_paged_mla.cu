@@ -60,7 +60,7 @@ constexpr int kH = 64;                  // heads
 constexpr int kDc = 512;                // latent width
 constexpr int kBT = 80;                 // listed tokens per block
 constexpr int kThreads = 768;
-constexpr int kSoftWarps = 8;            // warps 4..11
+constexpr int kSoftWarps = 8;           // warps 4..11
 constexpr int kSoftThreads = 32 * kSoftWarps;
 constexpr int kOutWarp0 = 12, kOutWarps = 4;
 // register split (setmaxnreg): 768 threads x 80 at launch
@@ -83,7 +83,7 @@ constexpr int kTmemS = 256;
 // shared memory (from a 1024-byte aligned base)
 constexpr int kOffQ = 0;                               // 8 chunks [64 heads x 64 columns]
 constexpr int kOffC = kOffQ + 8 * 8192;
-constexpr int kOffP = kOffC + kRing * kSlot;          // [64 heads x 64 tokens], and 16 tokens
+constexpr int kOffP = kOffC + kRing * kSlot;           // [64 heads x 64 tokens], and 16 tokens
 constexpr int kOffInv = kOffP + 2 * 8192;              // 1 / sums of a unit [2][64]
 constexpr int kOffScale = kOffInv + 2 * kH * 4;        // rescale factors [64]
 constexpr int kOffTop = kOffScale + kH * 4;            // maxima, sums of the halves [2][64]
