@@ -480,8 +480,10 @@ KPOOL_API int kpool_sparse_mla_fwd_pools_at(const void *q, const void *kv, const
  *   dq_out       bf16 [T, H, Dc];  dkv_out  bf16 [Tk, Dc]: overwritten, apart
  *                from the inputs; 16-byte aligned
  *   workspace    >= kpool_sparse_mla_bwd_workspace_size(T, Tk) bytes (the FP32
- *                sums of dkv; for few rows partial dq too), 256-byte aligned;
- *                its status word (kpool_read_status) reports a pipeline timeout
+ *                sums of dkv, and the partial dq that few rows need), 256-byte
+ *                aligned.  That size never shrinks as T or Tk grows: one
+ *                workspace for the largest call serves every smaller one.
+ *                Its status word (kpool_read_status) reports a pipeline timeout
  *                (KPOOL_STATUS_TIMEOUT: outputs invalid).  Calls that may
  *                overlap need workspaces of their own
  * Supported shapes as the forward calls.  The three calls list tokens as
@@ -704,8 +706,10 @@ KPOOL_API int kpool_shared_prefix_mla_fwd(
  *   cu_pools     int32 [B + 1]: the pools of sequence b are numbered
  *                cu_pools[b] .. cu_pools[b+1] - 1 (others are skipped)
  *   o_out, lse_out   as kpool_sparse_mla_fwd
- *   workspace    kpool_sparse_mla_paged_workspace_size(Tq, kpool, index_topk)
- *                bytes, 256-byte aligned
+ *   workspace    >= kpool_sparse_mla_paged_workspace_size(Tq, kpool,
+ *                index_topk) bytes, 256-byte aligned.  That size never shrinks
+ *                as Tq or index_topk grows (few rows need the most): one
+ *                workspace for the largest batch serves every smaller one
  * Latent rows that are listed must be finite; no other row is read.
  * Device status: KPOOL_STATUS_BAD_SEQLENS when cu_seqlens_q is not 0 .. Tq
  * non-decreasing (rows outside cu_seqlens_q[0] .. cu_seqlens_q[B] - 1 are left

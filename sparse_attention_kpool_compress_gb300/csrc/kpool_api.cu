@@ -114,7 +114,7 @@ int check_mla_grad(const void *d_o, const float *d_lse, int64_t T, int64_t Tk, c
     if (Tk > 0 && !dkv_out) return fail(KPOOL_ERR_INVALID_ARG, "dkv_out is required");
     if (!aligned(d_o, 16) || !aligned(dq_out, 16) || !aligned(dkv_out, 16) || !aligned(d_lse, 4))
         return fail(KPOOL_ERR_INVALID_ARG, "d_o, dq_out and dkv_out must be 16-byte aligned");
-    const size_t need = sparse_mla_bwd_workspace_bytes(T, Tk);
+    const size_t need = sparse_mla_bwd_workspace_need(T, Tk);
     if (!workspace || workspace_bytes < need || !aligned(workspace, 256))
         return fail(KPOOL_ERR_WORKSPACE, "workspace of at least %zu bytes, 256-byte aligned, needed", need);
     return KPOOL_OK;
@@ -925,7 +925,7 @@ int kpool_sparse_mla_fwd_pools_paged(const void *q, const void *kv, int64_t kv_p
     if (!aligned(page_table, 4) || !aligned(seq_lens, 4) || !aligned(seq_ids, 4) || !aligned(cu_seqlens_q, 4) ||
         !aligned(q_start_pos, 4) || !aligned(cu_pools, 4))
         return fail(KPOOL_ERR_INVALID_ARG, "index arrays must be 4-byte aligned");
-    const size_t need = paged_mla_workspace_bytes(Tq, index_topk / kpool, kpool);
+    const size_t need = paged_mla_workspace_need(Tq, index_topk / kpool, kpool);
     if (workspace_bytes < need)
         return fail(KPOOL_ERR_WORKSPACE, "workspace of at least %zu bytes, 256-byte aligned, needed", need);
     PagedMlaArgs a{};

@@ -158,7 +158,8 @@ struct SparseMlaGrad {
     const float *d_lse;                 // [T, 64] or NULL
     void *dq, *dkv;                     // bf16 [T, 64, 512], bf16 [Tk, 512]
 };
-size_t sparse_mla_bwd_workspace_bytes(int64_t T, int64_t Tk);
+size_t sparse_mla_bwd_workspace_need(int64_t T, int64_t Tk);    // of this call
+size_t sparse_mla_bwd_workspace_bytes(int64_t T, int64_t Tk);   // of any call of T rows or fewer
 int run_sparse_mla_bwd(const SparseMlaArgs &a, const SparseMlaGrad &g, cudaStream_t s);
 
 // The sparse attention over a paged cache (kpool_paged_mla.cu).
@@ -177,7 +178,8 @@ struct PagedMlaArgs {
     float *lse;
     void *workspace;
 };
-size_t paged_mla_workspace_bytes(int64_t Tq, int Kp, int kpool);
+size_t paged_mla_workspace_need(int64_t Tq, int Kp, int kpool);     // of this call
+size_t paged_mla_workspace_bytes(int64_t Tq, int Kp, int kpool);    // of any call of Tq rows or fewer
 int run_paged_mla(const PagedMlaArgs &a, cudaStream_t s);
 
 // Paged cache (kpool_pages.cu); arguments are validated by the caller.  Copies of up

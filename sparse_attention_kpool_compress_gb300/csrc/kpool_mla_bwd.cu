@@ -700,11 +700,21 @@ int runs(int64_t T, int64_t slots, int sms)
 
 // (Neither the device that a caller sizes its workspace on nor the lists' width is known
 // here: room for as many runs as there can be.)
-size_t sparse_mla_bwd_workspace_bytes(int64_t T, int64_t Tk)
+size_t sparse_mla_bwd_workspace_need(int64_t T, int64_t Tk)
 {
     const int64_t n = T * runs(T, int64_t(kMaxSplit) * kBT, kMaxSms);
     return kHeadInts * 4 + (n > T ? static_cast<size_t>(n) * kH * kDc * 4 : 0) +
            static_cast<size_t>(Tk) * kDc * 4;
+}
+
+// (Few rows need more than many, which are not cut: the most that T rows or fewer need, so
+// that a workspace for the largest batch serves the smaller ones.)
+size_t sparse_mla_bwd_workspace_bytes(int64_t T, int64_t Tk)
+{
+    size_t most = sparse_mla_bwd_workspace_need(T, Tk);
+    for (int64_t t = std::min<int64_t>(T, kMaxSms / 2); t > 0; --t)
+        most = std::max(most, sparse_mla_bwd_workspace_need(t, Tk));
+    return most;
 }
 
 int run_sparse_mla_bwd(const SparseMlaArgs &a, const SparseMlaGrad &g, cudaStream_t s)

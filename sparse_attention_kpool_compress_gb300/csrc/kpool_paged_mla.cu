@@ -840,10 +840,20 @@ int runs(int64_t Tq, int Kp, int kpool, int sms)
 
 // (The size must not depend on the device that a caller sizes its workspace on, so the
 // number of SMs is bounded there.)
-size_t paged_mla_workspace_bytes(int64_t Tq, int Kp, int kpool)
+size_t paged_mla_workspace_need(int64_t Tq, int Kp, int kpool)
 {
     const int n = runs(Tq, Kp, kpool, kMaxSms);
     return kHeadInts * 4 + (n > 1 ? static_cast<size_t>(Tq) * n * kH * (kDc + 1) * 4 : 0);
+}
+
+// (Few rows need more than many, which are not cut: the most that Tq rows or fewer need, so
+// that a workspace for the largest batch serves the smaller ones.)
+size_t paged_mla_workspace_bytes(int64_t Tq, int Kp, int kpool)
+{
+    size_t most = paged_mla_workspace_need(Tq, Kp, kpool);
+    for (int64_t t = std::min<int64_t>(Tq, kMaxSms / 2); t > 0; --t)
+        most = std::max(most, paged_mla_workspace_need(t, Kp, kpool));
+    return most;
 }
 
 int run_paged_mla(const PagedMlaArgs &a, cudaStream_t s)
