@@ -45,11 +45,16 @@ struct RowMsg {
 };
 static_assert(sizeof(RowMsg) <= 48, "RowMsg slot");
 
+// Limits below this are waited for by probes that do not suspend the thread: a suspended
+// one may see nothing until its barrier completes, so that a limit of 1 ns was not told of
+// by calls whose waits are short (backward pass, 1 to 77 rows).
+constexpr uint64_t kPollBelowNs = 1000000ull;
+
 struct Sync {
     volatile uint32_t *abort_flag;
     int *status;
     uint64_t limit_ns;
-    bool poll = false;          // probes do not suspend the thread (a suspended one may outlast a short limit)
+    bool poll = false;          // probes do not suspend the thread
 };
 
 __device__ __forceinline__ bool probe_bar(uint32_t bar, uint32_t parity, const Sync &sy)

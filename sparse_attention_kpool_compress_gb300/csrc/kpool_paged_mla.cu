@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = misc[0];
-    const Sync sy{reinterpret_cast<volatile uint32_t *>(&misc[1]), status, p.wait_limit_ns, p.wait_limit_ns < 1000000u};
+    const Sync sy{reinterpret_cast<volatile uint32_t *>(&misc[1]), status, p.wait_limit_ns, p.wait_limit_ns < kPollBelowNs};
     ptx::grid_dependents_launch();
     ptx::grid_dependency_wait();        // the cleared counter and status (whole rows)
 
