@@ -331,8 +331,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!in_batch(p.a, t)) continue;
             const PagedRow m = paged_row(p.a, t, lane);
             bad |= m.bad;
-            // (a row may list up to 2^31 - 1 tokens: nothing is added to their number)
-            const int all = m.n_slots / kBT + (m.n_slots % kBT != 0), per = (all + p.split - 1) / p.split;
+            // (a row may list up to 2^31 - 1 tokens: rounded up without a sign)
+            const int all = static_cast<int>((static_cast<uint32_t>(m.n_slots) + kBT - 1) / kBT);
+            const int per = (all + p.split - 1) / p.split;
             const int b0 = (u - t * p.split) * per, nb = max(0, min(all - b0, per));
             if (nb == 0) {
                 // nothing listed: what the output warps would write
