@@ -34,18 +34,24 @@
 // P and dS are rounded to BF16, the type of the MMAs' operands (2^-8 of each at most);
 // everything that is summed, is summed in FP32.
 //
-// Two kernels more: in front, cleared sums; behind, the sums rounded to BF16.  Where rows are few (half the SMs or less), a row's
-// blocks are cut into even runs, one for each CTA, whose FP32 dQ the last kernel adds up.
+// Two kernels more: in front, cleared sums; behind, the sums rounded to BF16.  Where rows
+// are few (half the SMs or less), a row's blocks are cut into even runs, one for each CTA,
+// whose FP32 dQ the last kernel adds up.
 //
-// What bounds it: 10 * 64 * 512 FLOP a (row, token), and 2 KB added into L2 for each,
-// since a row's tokens are its own: no tile of keys meets enough queries to sum them on
-// chip first.  Additions reach 6.0 to 6.3 TB/s here where the sums fit L2 (64 MB; into
-// 256 MB 3.7), so 32768 rows of up to 2051 tokens take 22 ms for them and 11 for the
-// MMAs at the rate of a library product; the call takes 27.9 ms (764 TFLOP/s, 4.8 TB/s
-// of additions).  A block takes 8000 cycles: the tensor pipe 32%, the path to shared
-// memory 73% (operands 48%, and each dC value goes through it twice).  Steps on 8192
-// rows: four sums warps with 4-byte additions 9.8 ms; through shared memory with
-// 16-byte additions 7.5; eight such warps, X ahead into L2 6.8; the first parts of dC
+// What bounds it: three costs that overlap in part.  10 * 64 * 512 FLOP a (row, token), in
+// MMAs of N = 64 that take 48 cycles for their operands where the tensor pipe needs 32: 80
+// of them are 3860 of a block's 8000 cycles.  2 KB added into L2 for each (row, token), at 6.0
+// to 6.3 TB/s where the sums fit L2 (64 MB; random rows of 256 MB 3.7).  The path to shared
+// memory, 73% busy (operands 48%; each dC value goes through it twice).  32768 rows of up to
+// 2051 tokens take 27.9 ms (764 TFLOP/s, 4.8 TB/s of additions), of which the MMAs as they
+// are take 13.4 and the additions alone 22; 131072 rows run at the same rate where
+// neighbours choose much the same pools (114 ms), and at 4.3 TB/s with pools chosen at random
+// (127 ms).  What neighbours have in common could be summed on chip before it is added: lists
+// nest below the budget, and beyond it two rows of that choice list 57% (4096 keys) to 68%
+// (32768) of the tokens of two rows apart.  This kernel adds each row by itself: two rows' X
+// (256 KB) do not fit a CTA.
+// Steps on 8192 rows: four sums warps with 4-byte additions 9.8 ms; through shared memory
+// with 16-byte additions 7.5; eight such warps, X ahead into L2 6.8; the first parts of dC
 // moved behind dQ 6.65; X in quarters, token ids read ahead 6.47; X given up in quarters
 // 6.40; lse and delta in this kernel instead of one in front 6.34 (3001 packed tokens 431
 // -> 401 us).  Slower: bulk reductions from shared memory (8.0 to 8.6), direct 4-byte
@@ -354,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool one = ptx::elect_one();
         int g = 0;
         uint32_t c_ph = 0, x_ph = 0, q_ph = 0, nd = 0;      // nd: parts of dC so far
-        bool any = false, rest = false;                     // rest: the last block's dC is half done
+        bool any = false, rest = false;                     // rest: the last block's dC lacks its last part
         // parts of dC^T = X^T . [dS; P]
         auto sum_parts = [&](int part0, int part1, bool last) {
 #pragma unroll 1
@@ -409,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             if (in.b == 0) x_ph ^= 1;
             if (one) ptx::mma_commit(bar(BS_FULL));
-            // the second half of the last block's dC while P and dS are made
+            // the last part of the last block's dC while P and dS are made
             if (rest && !sum_parts(kFirst, kParts, false)) break;
             if (!wait_bar_warp(bar(BP_FULL), g & 1, sy)) break;
             if (in.b == 0 && !wait_bar_warp(bar(BQ_EMPTY), q_ph ^ 1, sy)) break;
@@ -689,7 +695,8 @@ cudaError_t launch_after(void (*kernel)(P...), int grid, int threads, int smem, 
 }
 
 // Runs of a row, where rows are at most half of the SMs: as many as fill them, and no more
-// than the longest list has blocks.  (2051 tokens a row, us a call in a graph, cut and
+// than the longest list has blocks.  More rows are whole, one to a CTA at a time, so that a
+// last round that is not full costs a whole one (76 rows 88 us, 77 to 152 148, 153 275).  (2051 tokens a row, us a call in a graph, cut and
 // whole: 1 row 29 and 145, 16 rows 37 and 147, 38 rows 57 and 147, 76 rows, in two runs
 // each, 92 and 148.)
 int runs(int64_t T, int64_t slots, int sms)

@@ -37,7 +37,8 @@
 // 128-token blocks, one in flight 3.70; the ring of 80-token blocks 3.73, but 128 decode
 // steps 99 -> 87 us; all loader warps on each quarter 3.49 and 81 us; rolled issue loops
 // 3.38; one look for all quarters that have landed 3.23; whole blocks' output MMAs
-// unrolled 3.16.  Slower: unrolled or shuffled-uniform MMA operands (3.73).
+// unrolled 3.16.  Slower: the scores' loops unrolled (3.53), the MMAs' operands made uniform
+// by a shuffle (3.73).
 //
 // Where rows are few (half the SMs or less), a row's blocks are cut into even runs, one
 // for each CTA; FP32 outputs of the runs go to the workspace with their log-sums, and a
@@ -419,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = in.b > 0 || wait_bar_warp(bar(BQ_FULL), q_ph, sy);
             if (in.b == 0) q_ph ^= 1;
             // (the scores of two blocks ago were read before their P was complete)
-            // (rolled loops: unrolled, 8192 queries over 65536 tokens take 3.51 ms, so 3.38)
+            // (rolled loops: unrolled, 8192 queries over 65536 tokens take 3.53 ms, so 3.15)
 #pragma unroll 1
             for (int sl = ahead; sl < kQuarters && ok; ++sl) {
                 const uint32_t ph = landed(g, sl, at);
@@ -828,7 +829,9 @@ cudaError_t launch_after(void (*kernel)(P...), int grid, int threads, int smem, 
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// Runs of a row, where rows are at most half of the SMs: as many as fill them.  (2049
+// Runs of a row, where rows are at most half of the SMs: as many as fill them.  More rows
+// are whole, one to a CTA at a time, so that a last round that is not full costs a whole
+// one (76 rows 52 us, 77 to 152 73 to 79, 153 133).  (2049
 // tokens a row, us a call in a graph, cut and whole: 1 row 22 and 69, 8 rows 29 and 70,
 // 38 rows 37 and 73, 76 rows, in two runs each, 55 and 77.)
 int runs(int64_t Tq, int Kp, int kpool, int sms)
